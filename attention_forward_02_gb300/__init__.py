@@ -5,22 +5,42 @@ log-sum-exp for contiguous [B, H, N, d] fp16/bf16 CUDA tensors by calling the
 C ABI (include/fa.h) of the in-tree CUDA library on the current torch stream;
 ``fa_bwd`` computes the gradients of q, k, v from the forward's o and lse;
 ``fa_decode`` runs a few query rows per head against a long KV sequence
-(split-KV).
+(split-KV).  ``FACache`` is a paged KV cache held in 8 bits with a scale for each
+page and head: ``fa_cache_write`` appends tokens to it, ``fa_cache_read`` reads
+them back, ``fa_decode_cache`` attends to it (grouped query heads, ragged
+lengths) and ``fa_cache_select`` chooses the pages that it reads.
 PyTorch only supplies device memory and the stream; every step of the
 computation runs in the library's kernel.  There is no CPU or eager fallback:
 without the built library, or off a CUDA device, calls raise ``FAError``.
 """
-from ._lib import (FA_BF16, FA_FP16, FAError, fa1_fwd_raw, fa1_fwd_workspace_size,
-                   fa_abi_version, fa_bwd_raw, fa_bwd_workspace_size, fa_decode_raw,
-                   fa_decode_workspace_size, fa_fwd_raw, fa_last_device_status,
+from ._lib import (FA_BF16, FA_E4M3, FA_FP16, FA_INT8, CacheDesc, FAError, fa1_fwd_raw,
+                   fa1_fwd_workspace_size, fa_abi_version, fa_bwd_raw, fa_bwd_workspace_size,
+                   fa_cache_read_raw, fa_cache_select_raw, fa_cache_select_workspace_size,
+                   fa_cache_write_raw, fa_decode_cache_raw, fa_decode_cache_workspace_size,
+                   fa_decode_raw, fa_decode_workspace_size, fa_fwd_raw, fa_last_device_status,
                    fa_selftest_bounds_check, fa_selftest_wait_timeout, fa_status_str, lib_path,
                    load, load_checked)
+
+_CACHE_NAMES = ("FACache", "fa_cache_write", "fa_cache_read", "fa_cache_select", "fa_decode_cache")
 
 __all__ = ["fa_fwd", "fa_fwd_raw", "fa1_fwd", "fa1_fwd_raw", "fa1_fwd_workspace_size",
            "fa_bwd", "fa_bwd_raw", "fa_bwd_workspace_size",
            "fa_decode", "fa_decode_raw", "fa_decode_workspace_size",
+           "FACache", "fa_cache_write", "fa_cache_read", "fa_cache_select", "fa_decode_cache",
+           "fa_cache_write_raw", "fa_cache_read_raw", "fa_cache_select_raw", "fa_decode_cache_raw",
+           "fa_cache_select_workspace_size", "fa_decode_cache_workspace_size", "CacheDesc",
            "fa_last_device_status", "fa_selftest_wait_timeout", "fa_selftest_bounds_check",
            "fa_status_str", "fa_abi_version", "FAError", "load", "load_checked", "lib_path"]
+
+
+def __getattr__(name):
+    # the cache's module needs torch at its import, this one does not
+    if name in _CACHE_NAMES:
+        from . import cache
+        for n in _CACHE_NAMES:
+            globals()[n] = getattr(cache, n)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 
 def _dtype_code(t):

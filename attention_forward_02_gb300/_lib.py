@@ -18,15 +18,28 @@ FA_ERR_TIMEOUT = 5
 FA_ERR_BOUNDS = 6
 FA_FP16 = 0
 FA_BF16 = 1
+FA_E4M3 = 0
+FA_INT8 = 1
 
 # every symbol include/fa.h declares
 EXPORTS = ("fa_fwd", "fa1_fwd_workspace_size", "fa1_fwd", "fa1_fwd_noalloc", "fa_bwd_workspace_size",
-           "fa_bwd", "fa_decode_workspace_size", "fa_decode", "fa_last_device_status",
+           "fa_bwd", "fa_decode_workspace_size", "fa_decode", "fa_cache_write", "fa_cache_read",
+           "fa_decode_cache_workspace_size", "fa_decode_cache", "fa_cache_select_workspace_size",
+           "fa_cache_select", "fa_last_device_status",
            "fa_selftest_wait_timeout", "fa_selftest_bounds_check", "fa_checked_build",
            "fa_status_str", "fa_abi_version")
 
 _lib = None
 _lib_checked = None
+
+
+class CacheDesc(ctypes.Structure):
+    """fa_cache_t of include/fa.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_mean", ctypes.c_void_p),
+                ("k_mean_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int),
+                ("heads", ctypes.c_int), ("page", ctypes.c_int), ("d", ctypes.c_int),
+                ("format", ctypes.c_int)]
 
 
 class FAError(RuntimeError):
@@ -82,6 +95,21 @@ def _open(path):
     lib.fa_decode_workspace_size.argtypes = [i, i, i, i, i]
     lib.fa_decode.restype = i
     lib.fa_decode.argtypes = [vp, vp, vp, vp, vp, vp, ctypes.c_size_t, i, i, i, i, i, f, i, i, vp]
+    ll, cp = ctypes.c_longlong, ctypes.POINTER(CacheDesc)
+    lib.fa_cache_write.restype = i
+    lib.fa_cache_write.argtypes = [cp, vp, vp, ll, ll, ll, ll, vp, vp, vp, ll, i, i, i, i, vp]
+    lib.fa_cache_read.restype = i
+    lib.fa_cache_read.argtypes = [cp, vp, vp, vp, vp, ll, i, i, i, i, vp]
+    lib.fa_decode_cache_workspace_size.restype = ctypes.c_size_t
+    lib.fa_decode_cache_workspace_size.argtypes = [i, i, i, i, i]
+    lib.fa_decode_cache.restype = i
+    lib.fa_decode_cache.argtypes = [cp, vp, ll, ll, ll, vp, vp, vp, vp, ll, i, vp, i, vp,
+                                    ctypes.c_size_t, i, i, i, f, i, i, vp]
+    lib.fa_cache_select_workspace_size.restype = ctypes.c_size_t
+    lib.fa_cache_select_workspace_size.argtypes = [i, i, i, i]
+    lib.fa_cache_select.restype = i
+    lib.fa_cache_select.argtypes = [cp, vp, ll, ll, ll, vp, vp, ll, i, vp, i, i, i, vp,
+                                    ctypes.c_size_t, i, i, i, i, i, vp]
     lib.fa_last_device_status.restype = i
     lib.fa_last_device_status.argtypes = [vp]
     lib.fa_selftest_wait_timeout.restype = i
@@ -134,6 +162,35 @@ def fa_decode_raw(q, k, v, o, lse, ws, ws_bytes, B, H, Nq, Nk, d, scale, causal,
     """Direct call of the decoding entry point; returns the status."""
     return load().fa_decode(q, k, v, o, lse, ws, ws_bytes, B, H, Nq, Nk, d, scale, causal, dtype,
                             stream)
+
+
+def fa_cache_write_raw(*args):
+    """Direct call of the cache-writing entry point (arguments as in include/fa.h, the cache a
+    CacheDesc); returns the status."""
+    return load().fa_cache_write(*args)
+
+
+def fa_cache_read_raw(*args):
+    """Direct call of the cache-reading entry point; returns the status."""
+    return load().fa_cache_read(*args)
+
+
+def fa_decode_cache_workspace_size(B, Hq, Hkv, Nq, d):
+    return load().fa_decode_cache_workspace_size(B, Hq, Hkv, Nq, d)
+
+
+def fa_decode_cache_raw(*args):
+    """Direct call of the decoding entry point over the cache; returns the status."""
+    return load().fa_decode_cache(*args)
+
+
+def fa_cache_select_workspace_size(B, Hkv, Nq, max_pages):
+    return load().fa_cache_select_workspace_size(B, Hkv, Nq, max_pages)
+
+
+def fa_cache_select_raw(*args):
+    """Direct call of the page-selecting entry point; returns the status."""
+    return load().fa_cache_select(*args)
 
 
 def fa_last_device_status(stream=None):

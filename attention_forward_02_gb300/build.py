@@ -1,11 +1,11 @@
 """Build the sm_103a CUDA library in-tree (attention_forward_02_gb300/_build/).
 
-Three translation units (forward, backward, decoding), one -gencode
+Four translation units (forward, backward, decoding, the paged cache), one -gencode
 (compute_103a -> sm_103a), static cudart, no link against libcuda (the TMA
 encoder is fetched through the runtime's driver entry-point query).  The same
-three units are compiled a second time with FA_BOUNDS_CHECK into the checked
+units are compiled a second time with FA_BOUNDS_CHECK into the checked
 build (libfa_gb300_checked.so, device-side address checks; a test build).  All
-six compile in parallel.
+of them compile in parallel.
 """
 import os
 import shutil
@@ -22,9 +22,10 @@ LIB = os.path.join(OUT_DIR, LIB_NAME)
 # The same sources with the device-side address checks compiled in
 # (FA_BOUNDS_CHECK; see include/fa.h): a test build, never the product path.
 LIB_CHECKED = os.path.join(OUT_DIR, "libfa_gb300_checked.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("fa_fwd.cu", "fa_bwd.cu", "fa_decode.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("fa_fwd.cu", "fa_bwd.cu", "fa_decode.cu", "fa_cache.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_fwd_kernel.cuh", "fa1_fwd_kernel.cuh",
                                                   "fa_bwd_kernel.cuh", "fa_decode_kernel.cuh", "fa_decode_tc_kernel.cuh",
+                                                  "fa_cache_kernel.cuh", "fa_cache_decode_kernel.cuh",
                                                   "fa_common.cuh",
                                                   "fa_host.h", "sm100_ptx.cuh")] + [
     os.path.join(INCLUDE, "fa.h")]

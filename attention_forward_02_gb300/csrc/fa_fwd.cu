@@ -424,10 +424,11 @@ fa_status_t fa_last_device_status(void *stream)
         return FA_ERR_CUDA;
     if (cudaMemcpyToSymbol(fa::g_fa_status, &zero, sizeof(zero)) != cudaSuccess)
         return FA_ERR_CUDA;
-    unsigned int bwd_word = 0, dec_word = 0;
-    if (fa_host::take_bwd_status(&bwd_word) != FA_OK || fa_host::take_decode_status(&dec_word) != FA_OK)
+    unsigned int bwd_word = 0, dec_word = 0, cache_word = 0;
+    if (fa_host::take_bwd_status(&bwd_word) != FA_OK || fa_host::take_decode_status(&dec_word) != FA_OK ||
+        fa_host::take_cache_status(&cache_word) != FA_OK)
         return FA_ERR_CUDA;
-    word |= bwd_word | dec_word;
+    word |= bwd_word | dec_word | cache_word;
     if (word & fa::kStatusSelftest)
         return FA_ERR_CUDA;  // a self-test did not behave as required
     if (word & fa::kStatusBounds)

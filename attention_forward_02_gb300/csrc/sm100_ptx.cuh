@@ -21,7 +21,8 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p)
 // Device status word, one per device and translation unit (the host side of
 // each unit reads and clears its own): bit 0 = a bounded wait expired, bit 1 =
 // the wait self-test misbehaved, bit 2 = an address check of the checked build
-// failed.
+// failed, or a page number, length or offset in device memory lay outside the
+// paged cache (both builds).
 static __device__ unsigned int g_fa_status;
 constexpr unsigned int kStatusTimeout = 1u;
 constexpr unsigned int kStatusSelftest = 2u;

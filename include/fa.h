@@ -35,7 +35,7 @@
 extern "C" {
 #endif
 
-#define FA_ABI_VERSION 4
+#define FA_ABI_VERSION 5
 
 #if defined(__GNUC__)
 #define FA_API __attribute__((visibility("default")))
@@ -54,9 +54,11 @@ typedef enum {
     FA_ERR_CUDA = 4,        /* a CUDA runtime/driver call or the launch failed */
     FA_ERR_TIMEOUT = 5,     /* a kernel wait gave up (reported by
                                fa_last_device_status after the stream drained) */
-    FA_ERR_BOUNDS = 6       /* checked build only: a device-side address check
-                               failed and the access was skipped (reported by
-                               fa_last_device_status) */
+    FA_ERR_BOUNDS = 6       /* a page number, length or offset in device memory
+                               pointed outside the cache or the new tokens and
+                               was skipped or cut; in the checked build also an
+                               address check that failed, its access skipped
+                               (reported by fa_last_device_status) */
 } fa_status_t;
 
 /* Element type of Q, K, V and O (all four share it); accumulation is fp32. */
@@ -232,9 +234,170 @@ FA_API fa_status_t fa_decode(const void *q, const void *k, const void *v, void *
                              int d, float scale, int causal, fa_dtype_t dtype, void *stream);
 
 /*
+ * The 8-bit paged KV cache.
+ *
+ * K and V of many sequences lie in pages of `page` tokens.  A page holds, for
+ * every KV head, `page` x d 8-bit codes of K and of V, and one scale for each
+ * of the two: the value of a code c is c * scale.  Scales are powers of two,
+ * at least 2^-60, as fa_cache_write sets them, so encoding, decoding and moving
+ * codes to another scale round nothing but the 8-bit code itself.  The pages of
+ * sequence b are page_table[b][0], page_table[b][1], ...: the token at position
+ * t lies in slot t % page of page_table[b][t / page].  Lengths and page tables
+ * are read on the device when the call runs, so that a captured graph follows
+ * them; a batch may mix any lengths, 0 among them.
+ *
+ * "3.6 어텐션 I — 메모리 문제·FlashAttention 원리", section 3.6.9, has decoding
+ * bound by the bytes of K and V; 8 bits halve them against fa_decode's 16.
+ */
+typedef enum {
+    FA_E4M3 = 0, /* 1-4-3 floats up to 448, NaN kept; a page's scale 2^e has the
+                    smallest e with amax <= 448 2^e */
+    FA_INT8 = 1  /* -127 .. 127, NaN becomes 0; smallest e with amax <= 127 2^e */
+} fa_code_t;
+
+typedef struct {
+    void *k, *v;               /* [num_pages, heads, page, d] codes, 16-byte aligned */
+    float *k_scale, *v_scale;  /* [num_pages, heads] */
+    signed char *k_mean;       /* [num_pages, heads, d], 16-byte aligned, or NULL: the mean
+                                  key of a complete page is k_mean * k_mean_scale */
+    float *k_mean_scale;       /* [num_pages, heads], or NULL (with k_mean) */
+    int num_pages;             /* >= 1 */
+    int heads;                 /* KV heads */
+    int page;                  /* tokens a page: 16, 32, 64 or 128 */
+    int d;                     /* head dimension: 32, 64, 96 or 128 */
+    int format;                /* fa_code_t */
+} fa_cache_t;
+
+/*
+ * fa_cache_write -- append new tokens to the sequences' caches (asynchronous).
+ *
+ * Sequence b has seq_lens[b] tokens already; its new ones, rows cu_seqlens[b]
+ * .. cu_seqlens[b+1] - 1 of k and v, go to the positions from there on.  (The
+ * caller adds the counts to seq_lens afterwards.)  For each touched page and
+ * head, K and V apart, with amax the largest finite magnitude written to it:
+ *  - a page whose first slot is written gets its scale from amax alone;
+ *  - a page that held tokens before keeps its scale, or takes amax's if that is
+ *    larger; its old codes are then moved to the new scale (rounded to nearest);
+ *  - code = x / scale rounded to nearest even; infinities saturate.
+ * Slots behind the last token keep what they held.  Where k_mean is set and a
+ * page is complete afterwards, its summary for fa_cache_select is written: the
+ * mean over the slots of each channel (codes that are NaN count as 0), as int8
+ * with a power-of-two scale of its own.
+ *
+ *  cache   : the cache (host struct; its buffers on the device).
+ *  k, v    : new rows, element (t, h, c) at t * token_stride + h * head_stride
+ *            + c (strides in elements, multiples of 8); 16-byte aligned; must
+ *            not overlap the cache.  Read only.
+ *  cu_seqlens : [B + 1] int32 on the device, ascending, 0 .. T, or NULL: T / B
+ *            tokens for every sequence (T a multiple of B).  Rows from
+ *            cu_seqlens[B] on are ignored.
+ *  seq_lens: [B] int32 on the device: tokens before the write.
+ *  page_table : [B, max_pages] int32 on the device, rows table_stride apart.
+ *            A page being written belongs to one sequence of the batch.
+ *  B, T    : sequences (at most 65,535) and rows of k and v; 0 is an empty problem.
+ *  dtype   : type of k and v.
+ * A token whose position lies behind the page table, or whose page number is
+ * not in 0 .. num_pages - 1, is skipped and reported as FA_ERR_BOUNDS by
+ * fa_last_device_status.
+ */
+FA_API fa_status_t fa_cache_write(const fa_cache_t *cache, const void *k, const void *v,
+                                  long long k_token_stride, long long k_head_stride,
+                                  long long v_token_stride, long long v_head_stride,
+                                  const int *cu_seqlens, const int *seq_lens,
+                                  const int *page_table, long long table_stride, int max_pages,
+                                  int B, int T, fa_dtype_t dtype, void *stream);
+
+/*
+ * fa_cache_read -- read the first N positions of every sequence back into
+ * 16-bit tensors (asynchronous): code * scale rounded to nearest.  Positions
+ * from seq_lens[b] on, and those of a bad page, become zeros, so that the
+ * result can serve as K and V of fa_fwd or fa_decode.
+ *
+ *  k, v    : contiguous [B, heads, N, d] of `dtype`, 16-byte aligned; must not
+ *            overlap each other or the cache.  Written.
+ *  Other arguments as for fa_cache_write (seq_lens: tokens in the cache).
+ */
+FA_API fa_status_t fa_cache_read(const fa_cache_t *cache, void *k, void *v, const int *seq_lens,
+                                 const int *page_table, long long table_stride, int max_pages,
+                                 int B, int N, fa_dtype_t dtype, void *stream);
+
+/*
+ * fa_decode_cache_workspace_size -- bytes of device workspace fa_decode_cache
+ * needs (an fp32 (m, l, O[d]) per query row of the parts that no block of the
+ * launch covers alone; it does not depend on the lengths).  0 for invalid sizes.
+ */
+FA_API size_t fa_decode_cache_workspace_size(int B, int Hq, int Hkv, int Nq, int d);
+
+/*
+ * fa_decode_cache -- decoding attention over the cache (asynchronous): as
+ * fa_decode, with Nq (1 .. 16) query rows a head, seq_lens[b] keys, and Hq =
+ * G * heads query heads, head hq reading KV head hq / G.  causal = 1 puts the
+ * queries at the end of the sequence: query i sees keys 0 .. seq_lens[b] - Nq + i.
+ * A row that sees no key gets O = 0 and LSE = -infinity.
+ *
+ *  q       : element (b, h, i, c) at b * q_batch_stride + h * q_head_stride +
+ *            i * q_row_stride + c (elements, multiples of 8); 16-byte aligned.
+ *  o       : contiguous [B, Hq, Nq, d] of `dtype`, 16-byte aligned.
+ *  lse     : [B, Hq, Nq] fp32, or NULL.
+ *  seq_lens: [B] int32 on the device: keys, the queries' own among them.  A
+ *            length behind the page table is cut to it, a negative one is 0.
+ *  pages   : NULL, or [B, heads, Nq, slots] int32: query i of KV head h sees
+ *            only keys of the pages (numbers within the sequence) listed there.
+ *            The first min(slots, pages of its context) entries count; negative
+ *            ones are skipped; no page is listed twice (fa_cache_select's order
+ *            or any other).
+ *  workspace: device, 16-byte aligned, >= fa_decode_cache_workspace_size bytes;
+ *            contents do not matter.  Calls that share it must not run concurrently.
+ * Keys of a bad page number are left out and reported as FA_ERR_BOUNDS.
+ * Outputs must not overlap each other or any input.
+ */
+FA_API fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_batch_stride,
+                                   long long q_head_stride, long long q_row_stride, void *o,
+                                   float *lse, const int *seq_lens, const int *page_table,
+                                   long long table_stride, int max_pages, const int *pages,
+                                   int slots, void *workspace, size_t workspace_bytes, int B,
+                                   int Hq, int Nq, float scale, int causal, fa_dtype_t dtype,
+                                   void *stream);
+
+/*
+ * fa_cache_select_workspace_size -- bytes of device workspace fa_cache_select
+ * needs: a 32-bit score for every query, KV head and page.  0 for invalid sizes.
+ */
+FA_API size_t fa_cache_select_workspace_size(int B, int Hkv, int Nq, int max_pages);
+
+/*
+ * fa_cache_select -- choose the pages that fa_decode_cache reads for each query
+ * and KV head (asynchronous).
+ *
+ * With c the keys that query i sees (as in fa_decode_cache) and n = ceil(c /
+ * page): where n <= slots every page is chosen.  Else the first keep_first and
+ * the last keep_last, and of the others those with the largest score
+ *   max over the G query heads of q8 . k_mean * q8_scale * k_mean_scale,
+ * q8 the head's query row in int8 (its scale as for FA_INT8 codes, NaN as 0).
+ * The product is summed in whole numbers and the scales are powers of two, so
+ * that scores, and the choice, depend on no order of summation; equal scores go
+ * to the lower page.  Pages are written ascending, then -1 up to `slots`.
+ *
+ *  cache   : with k_mean and k_mean_scale set.
+ *  pages   : [B, heads, Nq, slots] int32, written.
+ *  slots   : >= keep_first + keep_last; keep_first >= 0, keep_last >= 1.
+ *  workspace: device, 16-byte aligned, >= fa_cache_select_workspace_size bytes.
+ *  Other arguments as for fa_decode_cache.  A page with a bad number scores
+ *  lowest and is reported as FA_ERR_BOUNDS.
+ */
+FA_API fa_status_t fa_cache_select(const fa_cache_t *cache, const void *q, long long q_batch_stride,
+                                   long long q_head_stride, long long q_row_stride,
+                                   const int *seq_lens, const int *page_table,
+                                   long long table_stride, int max_pages, int *pages, int slots,
+                                   int keep_first, int keep_last, void *workspace,
+                                   size_t workspace_bytes, int B, int Hq, int Nq, int causal,
+                                   fa_dtype_t dtype, void *stream);
+
+/*
  * fa_last_device_status -- synchronise `stream`, read and clear the device
- * status word of the current device.  Returns FA_ERR_BOUNDS if a kernel of
- * the checked build (below) failed an address check, else FA_ERR_TIMEOUT if
+ * status word of the current device.  Returns FA_ERR_BOUNDS if a kernel met a
+ * page number, length or offset outside the cache, or one of the checked build
+ * (below) failed an address check, else FA_ERR_TIMEOUT if
  * any kernel launched since the last call gave up on a wait, FA_ERR_CUDA if
  * the stream reports an error, else FA_OK.  Not for use during CUDA graph
  * capture.
