@@ -32,12 +32,54 @@ struct CacheState {
 };
 CacheState g_cache[kMaxDevices];
 
+template <int D, int NT>
+cudaError_t set_smem_attr()
+{
+    using namespace fa::cache;
+    const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, NT, __half, E4M3>, a, DecCfg<D, NT>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, NT, __half, I8>, a, DecCfg<D, NT>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, NT, __nv_bfloat16, E4M3>, a, DecCfg<D, NT>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, NT, __nv_bfloat16, I8>, a, DecCfg<D, NT>::SMEM);
+    return e;
+}
+
+template <int D>
+cudaError_t set_smem_attrs()
+{
+    const cudaError_t e = set_smem_attr<D, 1>();
+    return e == cudaSuccess ? set_smem_attr<D, 2>() : e;
+}
+
 void init_cache(CacheState &st)
 {
     void *p = nullptr;
     st.err = cudaGetSymbolAddress(&p, fa::g_fa_status);
     st.status = static_cast<unsigned int *>(p);
+    if (st.err == cudaSuccess) st.err = set_smem_attrs<32>();
+    if (st.err == cudaSuccess) st.err = set_smem_attrs<64>();
+    if (st.err == cudaSuccess) st.err = set_smem_attrs<96>();
+    if (st.err == cudaSuccess) st.err = set_smem_attrs<128>();
 }
+
+// How query rows of one KV head (R of them) are laid out: 8-row tiles a warp,
+// warps along the rows (the others take keys), rows a block.
+struct Shape {
+    int tiles, row_warps, rows_block;
+};
+Shape shape_of(int R)
+{
+    if (R <= 8)
+        return {1, 1, 8};
+    const int row_warps = R <= 16 ? 1 : R <= 32 ? 2 : 4;
+    return {2, row_warps, 16 * row_warps};
+}
+
+// Bytes of the plan at the workspace's start (a 64-bit number, and one a sequence).
+size_t plan_bytes(int B) { return (static_cast<size_t>(B) + 2) / 2 * 16; }
 
 // The current device's status word and SM count.
 fa_status_t device(CacheState **out, int *num_sms)
@@ -288,7 +330,8 @@ size_t fa_decode_cache_workspace_size(int B, int Hq, int Hkv, int Nq, int d)
     if (B < 0 || Hq < 0 || Hkv < 1 || Hq % Hkv != 0 || Nq < 1 || Nq > kMaxNq ||
         (d != 32 && d != 64 && d != 96 && d != 128))
         return 0;
-    return 16;
+    const Shape shape = shape_of(Hq / Hkv * Nq);
+    return plan_bytes(B) + static_cast<size_t>(2 * fa::cache::kMaxBlocks) * shape.rows_block * (d + 2) * 4;
 }
 
 fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_batch_stride, long long q_head_stride,
@@ -330,19 +373,56 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
         if (any_overlap(out[i], own, kCacheRanges) || any_overlap(out[i], in, 4) || any_overlap(out[i], out, i))
             return FA_ERR_INVALID_ARG;
     CacheState *st = nullptr;
-    if ((s = device(&st, nullptr)) != FA_OK)
+    int sms = 0;
+    if ((s = device(&st, &sms)) != FA_OK)
         return s;
     const Cache c = device_cache(cache);
     const Batch batch = {seq_lens, page_table, table_stride, max_pages, cache->num_pages, st->status};
     const Queries qs = {q, q_batch_stride, q_head_stride, q_row_stride, Hq / cache->heads, Nq, causal};
-    const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    fa::cache::Work w = {};
+    w.cache = c;
+    w.batch = batch;
+    w.q = qs;
+    w.pages = pages;
+    w.slots = slots;
+    w.B = B;
+    w.R = qs.G * (pages ? 1 : Nq);
+    const Shape shape = shape_of(w.R);
+    w.groups = (w.R + shape.rows_block - 1) / shape.rows_block;
+    w.row_warps = shape.row_warps;
+    w.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    w.plan = static_cast<long long *>(workspace);
+    const size_t part_rows = static_cast<size_t>(2 * fa::cache::kMaxBlocks) * shape.rows_block;
+    w.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan_bytes(B));
+    w.part_m = w.part_o + part_rows * cache->d;
+    w.part_l = w.part_m + part_rows;
+    const int log2_step = shape.row_warps == 1 ? 6 : shape.row_warps == 2 ? 5 : 4;
+    // no more blocks than units there can be
+    const long long most = static_cast<long long>(B) * (pages ? Nq : 1) * cache->heads * w.groups *
+                           (((static_cast<long long>(pages && slots < max_pages ? slots : max_pages) * cache->page - 1) >>
+                             log2_step) + 1);
+    const long long resident = static_cast<long long>(sms) * (shape.tiles == 1 ? 3 : 2);
+    long long blocks = resident < fa::cache::kMaxBlocks ? resident : fa::cache::kMaxBlocks;
+    if (most < blocks)
+        blocks = most;
     return by_dim(cache->d, [&](auto dim) {
         return by_types(dtype, cache->format, [&](auto t, auto code) {
+            constexpr int D = decltype(dim)::value;
             using T = decltype(t);
-            fa::cache::fa_cache_decode_kernel<decltype(dim)::value, T, decltype(code)>
-                <<<static_cast<unsigned>((rows + 3) / 4), 128, 0, cs>>>(c, batch, qs, pages, slots, static_cast<T *>(o), lse,
-                                                                        rows, Hq, scale_log2);
+            using C = decltype(code);
+            if (shape.tiles == 1)
+                fa::cache::fa_cache_decode_kernel<D, 1, T, C>
+                    <<<static_cast<unsigned>(blocks), fa::cache::kDecThreads, fa::cache::DecCfg<D, 1>::SMEM, cs>>>(
+                        w, static_cast<T *>(o), lse);
+            else
+                fa::cache::fa_cache_decode_kernel<D, 2, T, C>
+                    <<<static_cast<unsigned>(blocks), fa::cache::kDecThreads, fa::cache::DecCfg<D, 2>::SMEM, cs>>>(
+                        w, static_cast<T *>(o), lse);
+            if (cudaGetLastError() != cudaSuccess)
+                return FA_ERR_CUDA;
+            fa::cache::fa_cache_combine_kernel<D, T><<<static_cast<unsigned>(rows), fa::cache::kCombineThreads, 0, cs>>>(
+                w, static_cast<T *>(o), lse, log2_step, shape.rows_block);
             return launched();
         });
     });

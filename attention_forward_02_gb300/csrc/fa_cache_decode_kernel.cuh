@@ -1,6 +1,40 @@
 // fa_cache_decode_kernel.cuh -- decoding attention over the 8-bit paged cache
 // on sm_103a: O = softmax(scale q K^T) V with K = k_scale * codes, V likewise,
 // over all keys of a sequence or over listed pages only.
+//
+// What bounds it: with up to 16 query rows a KV head the work is 4 * 16 flops
+// for two code bytes, far below the ridge, so the time is that of reading the
+// codes once from HBM.  All else has to stay under it: per SM about 23 bytes a
+// clock arrive, so a warp's 16 keys of d = 128 (4 KB) may take some 170 clocks
+// of the SM, issue slots of four schedulers among them.
+//
+// The products run on the tensor cores in fp16 with fp32 sums: codes convert to
+// fp16 exactly, in registers, straight into the operand layout of
+// mma.m16n8k16, with keys as the 16 rows and query rows as the 8 columns:
+//     S^T = K Q^T   (16 keys x d) (d x 8 queries)
+//     O^T += V^T P^T  (d x 16 keys) (16 keys x 8 queries)
+// A matrix instruction fed from shared memory would need 8-bit Q and P, or a
+// round trip of the converted tile through shared memory; here nothing is
+// exchanged between threads but P^T, transposed by movmatrix.  The order of d
+// inside the first product, and of the rows of O^T in the second, is free, so a
+// thread takes consecutive bytes of a row: every byte of a key is loaded by
+// exactly the thread that multiplies it.  That makes the ring of cp.async
+// copies in shared memory private to each thread: no barrier, no transaction
+// count, conflict-free 16-byte reads, and the wait is the thread's own.
+//
+// Query rows are scaled by a power of two to a row maximum in [2^14, 2^15)
+// before they become fp16: a bf16 row keeps every bit that fp32 sums would see.
+// P is rounded to fp16 (2^-12) as P * v_scale against a reference m that
+// includes v_scale's exponent, m >= s_j + log2 v_scale_j - 8 for every key j,
+// so that no product with a V scale overflows and V scales of any size mix.
+// m moves (and O, l are rescaled) only when a score outgrows it by 2^8.
+//
+// Work is dealt in units of 64 keys (16 a warp) of one (sequence, KV head, row
+// group): the blocks of a persistent grid take equal runs of the concatenated
+// units of all sequences, whatever their lengths, which are read from device
+// memory.  A run may begin and end inside a segment; those parts (at most two a
+// block) go to the workspace as (m, l, O) and fa_cache_combine_kernel merges
+// them, in a fixed order.
 #pragma once
 
 #include "fa_cache_kernel.cuh"
@@ -8,83 +42,735 @@
 namespace fa {
 namespace cache {
 
-// One warp a query row: 32 keys at a time, lane l the score of key l, then all
-// lanes the columns l, l + 32, ... of P V.
-template <int D, typename T, typename C>
-__global__ void __launch_bounds__(128)
-    fa_cache_decode_kernel(Cache cache, Batch batch, Queries q, const int *__restrict__ pages, int slots,
-                           T *__restrict__ out, float *__restrict__ lse, long long rows, int Hq, float scale_log2)
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kTile = 16;         // keys a warp and step
+constexpr int kMaxBlocks = 640;   // of the persistent grid
+constexpr int kCombineThreads = 128;
+
+// One 16-key tile of K and V a stage, in thread-private pieces.
+template <int D, int NT>
+struct DecCfg {
+    static constexpr int KV = D % 64 == 0 ? 16 : 8;   // bytes of one K copy
+    static constexpr int KC = D / 4 / KV;             // K copies a thread and key
+    static constexpr int WPC = KV / 4;                // words a K copy
+    static constexpr int VV = D == 96 ? 4 : D / 8;    // bytes of one V copy
+    static constexpr int VC = D / 8 / VV;             // V copies a thread and key
+    static constexpr int STAGE = 2 * kTile * D;       // bytes
+    static constexpr int STAGES = 12288 / STAGE;      // 3 at d = 128
+    static constexpr int META = 32;
+    static constexpr int ROWS = 8 * NT;               // query rows a warp
+    static constexpr int OROW = D + 4;                // floats of a row of the merge
+    static constexpr int RING_OFF = 0;
+    static constexpr int META_OFF = kDecWarps * STAGES * STAGE;
+    static constexpr int MERGE_OFF = META_OFF + kDecWarps * STAGES * META;
+    static constexpr int ML_OFF = MERGE_OFF + kDecWarps * ROWS * OROW * 4;
+    static constexpr int SMEM = ML_OFF + kDecWarps * ROWS * 8;
+};
+
+// What a warp knows of a tile when it computes it (written with its copies).
+struct __align__(16) TileMeta {
+    float k_scale, v_scale;
+    int key0;    // position of the tile's first key
+    int flags;   // below
+    int b, i, head, group;
+};
+static_assert(sizeof(TileMeta) == 32, "tile record");
+constexpr int kFirst = 1, kLast = 2, kHeadPart = 4, kTailPart = 8, kSkip = 16;
+
+struct Work {
+    Cache cache;
+    Batch batch;
+    Queries q;
+    const int *pages;  // listed pages, or NULL
+    int slots;
+    int B, R, groups;  // rows of a segment (G Nq, or G with listed pages), row groups
+    int row_warps;     // warps along the rows (1, 2, 4), the others along the keys
+    float scale_log2;
+    // workspace: [0] blocks' share, [1 + b] first unit of sequence b; then the parts
+    long long *plan;
+    float *part_o, *part_m, *part_l;  // [2 blocks][rows][D], [2 blocks][rows]
+};
+
+// Units of query i's segment of a sequence of `len` keys (all queries' with no list).
+__device__ __forceinline__ int units_of(const Work &w, int len, int i, int log2_step)
 {
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= rows)
+    int keys = len;
+    if (w.pages) {
+        const int n = (context(w.q, len, i) + w.cache.page - 1) >> w.cache.log2_page;
+        keys = min(n, w.slots) << w.cache.log2_page;
+    }
+    return keys > 0 ? ((keys - 1) >> log2_step) + 1 : 0;
+}
+__device__ __forceinline__ long long units_of_sequence(const Work &w, int b, int log2_step)
+{
+    const int len = w.batch.length(b, w.cache.log2_page);
+    long long n = 0;
+    for (int i = 0; i < (w.pages ? w.q.Nq : 1); ++i)
+        n += units_of(w, len, i, log2_step);
+    return n * w.cache.heads * w.groups;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// Copy of `BYTES` (4, 8, 16) to shared memory, zeros where `live` is false.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool live)
+{
+    if (!smem_ok(dst, BYTES, BYTES))
         return;
-    const int i = static_cast<int>(row % q.Nq), hq = static_cast<int>(row / q.Nq % Hq);
-    const int b = static_cast<int>(row / q.Nq / Hq), h = hq / q.G;
-    const int ctx = context(q, batch.length(b, cache.log2_page), i);
-    const int n = (ctx + cache.page - 1) >> cache.log2_page;
-    const int count = pages ? min(n, slots) : n;
-    const int *list = pages ? pages + ((static_cast<long long>(b) * cache.heads + h) * q.Nq + i) * slots : nullptr;
-    const T *src = static_cast<const T *>(q.q) + b * q.batch_stride + hq * q.head_stride + i * q.row_stride;
-    float m = -INFINITY, l = 0.f, o[D / 32];
+    const int n = live ? BYTES : 0;
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n)
+                     : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <int WORDS>
+__device__ __forceinline__ void load_words(uint32_t (&w)[WORDS], uint32_t addr)
+{
+    if (!smem_ok(addr, 4 * WORDS, 4 * WORDS)) {
+        for (int i = 0; i < WORDS; ++i)
+            w[i] = 0;
+        return;
+    }
+    if (WORDS == 4)
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1 % WORDS]), "=r"(w[2 % WORDS]), "=r"(w[3 % WORDS])
+                     : "r"(addr)
+                     : "memory");
+    else if (WORDS == 2)
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1 % WORDS]) : "r"(addr) : "memory");
+    else
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+}
+
+// Bytes of a word that are e4m3 NaN codes, as their top bits.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+template <int D, int NT, typename T, typename C>
+__global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
+    fa_cache_decode_kernel(const __grid_constant__ Work w, T *__restrict__ out, float *__restrict__ lse)
+{
+    using F = DecCfg<D, NT>;
+    constexpr int S = F::STAGES;
+    constexpr int KW = D / 16;  // words of a key's codes a thread holds = steps of the first product
+    constexpr int VW = D / 32;  // words of a key's V a thread holds
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ long long scan[kDecWarps + 1];
+    __shared__ long long begin[2];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    const int key_warps = kDecWarps / w.row_warps;
+    const int wk = warp % key_warps, wr = warp / key_warps;
+    const int log2_step = key_warps == 4 ? 6 : key_warps == 2 ? 5 : 4;
+    const int rows_block = F::ROWS * w.row_warps;
+
+    // ---- this block's run of units ----
+    long long total, share, first_unit;
+    int b;
+    {
+        const int each = (w.B + kDecThreads - 1) / kDecThreads;
+        const int b0 = min(w.B, t * each), b1 = min(w.B, b0 + each);
+        long long sum = 0;
+        for (int x = b0; x < b1; ++x)
+            sum += units_of_sequence(w, x, log2_step);
+        long long incl = sum;
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c)
-        o[c] = 0.f;
-    for (int s = 0; s < count; ++s) {
-        const int at = list ? list[s] : s;
-        if (at < 0)
-            continue;
-        const int p = at < n ? batch.page(b, at) : -1;
-        if (p < 0) {
-            batch.bad();
-            continue;
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off)
+                incl += y;
         }
-        const size_t ph = static_cast<size_t>(p) * cache.heads + h;
-        const uint8_t *k = cache.k + ph * cache.page * D, *v = cache.v + ph * cache.page * D;
-        const float ks = cache.k_scale[ph] * scale_log2, vs = cache.v_scale[ph];
-        const int keys = min(cache.page, ctx - (at << cache.log2_page));
-        for (int j0 = 0; j0 < keys; j0 += 32) {
-            float x = -INFINITY;
-            if (j0 + lane < keys) {
-                float dot = 0.f;
-                for (int c = 0; c < D; c += 4) {
-                    float f[4];
-                    decode4<C>(*reinterpret_cast<const uint32_t *>(k + (j0 + lane) * D + c), f);
-                    const uint2 w = *reinterpret_cast<const uint2 *>(src + c);
-                    const float2 a = DTypeTraits<T>::unpack(w.x), e = DTypeTraits<T>::unpack(w.y);
-                    dot = fmaf(a.x, f[0], fmaf(a.y, f[1], fmaf(e.x, f[2], fmaf(e.y, f[3], dot))));
-                }
-                x = dot * ks;
+        if (lane == 31)
+            scan[warp] = incl;
+        __syncthreads();
+        total = 0;
+        for (int x = 0; x < kDecWarps; ++x) {
+            if (x < warp)
+                incl += scan[x];
+            total += scan[x];
+        }
+        share = (total + gridDim.x - 1) / gridDim.x;
+        if (share < 1)
+            share = 1;
+        first_unit = share * blockIdx.x;
+        long long at = incl - sum;
+        if (blockIdx.x == 0) {
+            if (t == 0)
+                w.plan[0] = share;
+            long long y = at;
+            for (int x = b0; x < b1; ++x) {
+                w.plan[1 + x] = y;
+                y += units_of_sequence(w, x, log2_step);
             }
-            float top = x;
-            for (int off = 16; off > 0; off >>= 1)
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            const float m_new = fmaxf(m, top);
-            const float ref = m_new == -INFINITY ? 0.f : m_new;
-            const float alpha = exp2f(m - ref), e = exp2f(x - ref);
-            m = m_new;
-            l = l * alpha + e;
-            for (int c = 0; c < D / 32; ++c)
-                o[c] *= alpha;
-            for (int j = 0; j < 32 && j0 + j < keys; ++j) {
-                const float w = __shfl_sync(0xffffffffu, e, j) * vs;
-                for (int c = 0; c < D / 32; ++c) {
-                    float f[4];
-                    decode4<C>(v[(j0 + j) * D + c * 32 + lane], f);
-                    o[c] = fmaf(w, f[0], o[c]);
+        }
+        if (first_unit >= at && first_unit < incl) {
+            int x = b0;
+            for (; x + 1 < b1; ++x) {
+                const long long n = units_of_sequence(w, x, log2_step);
+                if (first_unit < at + n)
+                    break;
+                at += n;
+            }
+            begin[0] = x;
+            begin[1] = first_unit - at;
+        }
+        __syncthreads();
+        if (first_unit >= total)
+            return;
+        b = static_cast<int>(begin[0]);
+    }
+    long long left = min(share, total - first_unit);  // units still to load
+    const long long all = left;                       // units of this block
+
+    // ---- the side that loads: a walk over segments, units, pages ----
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t ring = sbase + F::RING_OFF + warp * (S * F::STAGE);
+    TileMeta *meta = reinterpret_cast<TileMeta *>(smem + F::META_OFF) + warp * S;
+    int i = 0, head = 0, group = 0, len = 0, ctx = 0, units = 0, unit = 0;
+    int held = 0, held_count = 0;  // lane l: page number of the l-th next tile (-1: none); tiles so covered
+    int held_key = 0;              // ... and its first key
+    long long off = begin[1];
+    auto open_sequence = [&]() { len = b < w.B ? w.batch.length(b, w.cache.log2_page) : 0; };
+    auto open_query = [&]() {
+        ctx = w.pages ? context(w.q, len, i) : len;
+        units = units_of(w, len, i, log2_step);
+    };
+    open_sequence();
+    open_query();
+    while (i + 1 < w.q.Nq && off >= static_cast<long long>(units) * w.cache.heads * w.groups) {
+        off -= static_cast<long long>(units) * w.cache.heads * w.groups;
+        ++i;
+        open_query();
+    }
+    {
+        const int seg = static_cast<int>(off / units);
+        unit = static_cast<int>(off % units);
+        head = seg / w.groups;
+        group = seg % w.groups;
+    }
+    bool opened = true;  // the next tile is this block's first of its segment
+    int slot = 0;        // ring slot of the next load
+    auto load = [&]() {
+        if (left > 0) {
+            if (held_count == 0) {
+                // page numbers of the next 32 tiles of this segment
+                held_count = static_cast<int>(min(static_cast<long long>(min(32, units - unit)), left));
+                const int key = ((unit + lane) << log2_step) + wk * kTile;
+                int at = key >> w.cache.log2_page;
+                held = -1;
+                held_key = key;
+                if (lane < held_count) {
+                    if (w.pages) {
+                        const int n = (ctx + w.cache.page - 1) >> w.cache.log2_page;
+                        const int entry =
+                            at < min(n, w.slots)
+                                ? w.pages[((static_cast<long long>(b) * w.cache.heads + head) * w.q.Nq + i) * w.slots + at]
+                                : -1;
+                        if (entry >= n)
+                            w.batch.bad();
+                        at = entry < n ? entry : -1;
+                        held_key = at * w.cache.page + (key & (w.cache.page - 1));
+                    }
+                    if (at >= 0 && held_key < ctx) {
+                        held = w.batch.page(b, at);
+                        if (held < 0)
+                            w.batch.bad();
+                    }
+                }
+            }
+            const int p = __shfl_sync(0xffffffffu, held, 0), key0 = __shfl_sync(0xffffffffu, held_key, 0);
+            held = __shfl_down_sync(0xffffffffu, held, 1);
+            held_key = __shfl_down_sync(0xffffffffu, held_key, 1);
+            --held_count;
+            const bool live = p >= 0;
+            const size_t ph = live ? static_cast<size_t>(p) * w.cache.heads + head : 0;
+            const size_t base = live ? (ph * w.cache.page + (key0 & (w.cache.page - 1))) * D : 0;
+            const uint8_t *k = w.cache.k + base, *v = w.cache.v + base;
+            const uint32_t dst = ring + slot * F::STAGE + lane * F::KV;
+            const int seen = live ? ctx - key0 : 0;  // keys of the tile that exist
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int x = 0; x < F::KC; ++x) {
+                    const bool in = g + 8 * r < seen;
+                    copy_async<F::KV>(dst + (r * F::KC + x) * 32 * F::KV,
+                                      in ? k + (g + 8 * r) * D + (c + 4 * x) * F::KV : w.cache.k, in);
+                }
+            const uint32_t vdst = ring + slot * F::STAGE + kTile * D + lane * F::VV;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int x = 0; x < F::VC; ++x) {
+                    const int key = 2 * c + (r & 1) + 8 * (r >> 1);
+                    const bool in = key < seen;
+                    copy_async<F::VV>(vdst + (r * F::VC + x) * 32 * F::VV,
+                                      in ? v + key * D + (g + 8 * x) * F::VV : w.cache.v, in);
+                }
+            --left;
+            ++unit;
+            const bool ended = unit == units || left == 0;
+            TileMeta *m = meta + slot;
+            if (lane == 0) {
+                int flags = (opened ? kFirst : 0) | (ended ? kLast : 0) | (live ? 0 : kSkip);
+                if (ended) {
+                    // did this block see the segment from its first to its last unit?
+                    const bool before = all - left < unit;  // it began before this block's run
+                    if (before)
+                        flags |= kHeadPart;
+                    else if (unit < units)
+                        flags |= kTailPart;
+                }
+                m->key0 = key0;
+                m->flags = flags;
+                m->b = b;
+                m->i = i;
+                m->head = head;
+                m->group = group;
+                if (live) {
+                    copy_async<4>(smem_u32(&m->k_scale), w.cache.k_scale + ph, true);
+                    copy_async<4>(smem_u32(&m->v_scale), w.cache.v_scale + ph, true);
+                } else {
+                    m->k_scale = m->v_scale = 1.f;
+                }
+            }
+            opened = ended;
+            if (unit == units && left > 0) {  // on to the next segment
+                unit = 0;
+                if (++group == w.groups) {
+                    group = 0;
+                    if (++head == w.cache.heads) {
+                        head = 0;
+                        do {
+                            if (++i >= (w.pages ? w.q.Nq : 1)) {
+                                i = 0;
+                                ++b;
+                                open_sequence();
+                            }
+                            open_query();
+                        } while (units == 0 && b < w.B);
+                    }
+                }
+            }
+        }
+        slot = slot + 1 == S ? 0 : slot + 1;
+        copy_commit();
+    };
+#pragma unroll
+    for (int x = 0; x < S; ++x)
+        load();
+
+    // ---- the side that computes ----
+    uint32_t qb[NT][KW][2];  // Q^T operand: query g of each 8, its d in the order of the thread's K words
+    float qf[NT][2];         // per query 2 c, 2 c + 1: scale to log2 units
+    int lim[NT][2];          // ... keys that it sees
+    float m[NT][2], l[NT][2], acc[D / 16][NT][4];
+    int least = 0;           // keys that all rows see
+    int at = 0;              // ring slot
+    for (long long done = 0; done < all; ++done) {
+        copy_wait<S - 1>();
+        __syncwarp();
+        const TileMeta info = meta[at];
+        uint32_t kw[2][KW], vw[4][VW];
+        {
+            const uint32_t src = ring + at * F::STAGE + lane * F::KV;
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int x = 0; x < F::KC; ++x) {
+                    uint32_t y[F::WPC];
+                    load_words<F::WPC>(y, src + (r * F::KC + x) * 32 * F::KV);
+#pragma unroll
+                    for (int u = 0; u < F::WPC; ++u)
+                        kw[r][x * F::WPC + u] = y[u];
+                }
+            const uint32_t vsrc = ring + at * F::STAGE + kTile * D + lane * F::VV;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int x = 0; x < F::VC; ++x) {
+                    uint32_t y[F::VV / 4];
+                    load_words<F::VV / 4>(y, vsrc + (r * F::VC + x) * 32 * F::VV);
+#pragma unroll
+                    for (int u = 0; u < F::VV / 4; ++u)
+                        vw[r][x * (F::VV / 4) + u] = y[u];
+                }
+        }
+        __syncwarp();
+        at = at + 1 == S ? 0 : at + 1;
+        load();  // into the slot just read
+
+        if (info.flags & kFirst) {
+            const int n = w.batch.length(info.b, w.cache.log2_page);
+            least = w.pages ? context(w.q, n, info.i) : context(w.q, n, 0);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int row = info.group * rows_block + wr * F::ROWS + nt * 8 + g;
+                const int hq = w.pages ? row : row / w.q.Nq, qi = w.pages ? info.i : row % w.q.Nq;
+                const T *src = static_cast<const T *>(w.q.q) + info.b * w.q.batch_stride +
+                               static_cast<long long>(info.head * w.q.G + hq) * w.q.head_stride + qi * w.q.row_stride;
+                float top = 0.f;
+#pragma unroll
+                for (int s = 0; s < KW; ++s) {
+                    const int d = F::KV * (c + 4 * (s / F::WPC)) + 4 * (s % F::WPC);
+                    uint2 x = make_uint2(0, 0);
+                    if (row < w.R)
+                        x = *reinterpret_cast<const uint2 *>(src + d);
+                    qb[nt][s][0] = x.x;
+                    qb[nt][s][1] = x.y;
+                    const float2 y = DTypeTraits<T>::unpack(x.x), z = DTypeTraits<T>::unpack(x.y);
+                    const float f[4] = {fabsf(y.x), fabsf(y.y), fabsf(z.x), fabsf(z.y)};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (f[u] <= 3.402823466e38f)
+                            top = fmaxf(top, f[u]);
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int e = top > 0.f ? max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -100) : 0;
+                const float by = pow2f(-e);
+#pragma unroll
+                for (int s = 0; s < KW; ++s)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const float2 y = DTypeTraits<T>::unpack(qb[nt][s][u]);
+                        qb[nt][s][u] = DTypeTraits<__half>::pack(y.x * by, y.y * by);
+                    }
+                const int limit = context(w.q, n, qi);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    qf[nt][u] = pow2f(__shfl_sync(0xffffffffu, e, 8 * c + 4 * u)) * w.scale_log2;
+                    lim[nt][u] = __shfl_sync(0xffffffffu, limit, 8 * c + 4 * u);
+                    m[nt][u] = -INFINITY;
+                    l[nt][u] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        acc[j][nt][u] = 0.f;
+            }
+        }
+
+        if (!(info.flags & kSkip)) {
+            // ---- S^T = K Q^T ----
+            float s[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    s[nt][u] = 0.f;
+#pragma unroll
+            for (int x = 0; x < KW; ++x) {
+                uint32_t a0, a1, a2, a3;
+                C::halves(kw[0][x], a0, a2);
+                C::halves(kw[1][x], a1, a3);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(s[nt], a0, a1, a2, a3, qb[nt][x][0], qb[nt][x][1]);
+            }
+            // ---- log2 units, masks; does any score outgrow its reference? ----
+            const float ev = static_cast<float>(static_cast<int>(__float_as_uint(info.v_scale) >> 23) - 127);
+            bool grown = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float f0 = info.k_scale * qf[nt][0], f1 = info.k_scale * qf[nt][1];
+                s[nt][0] *= f0;
+                s[nt][1] *= f1;
+                s[nt][2] *= f0;
+                s[nt][3] *= f1;
+            }
+            const bool masked = info.key0 + kTile > least;
+            if (masked) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (info.key0 + g + 8 * (u >> 1) >= lim[nt][u & 1])
+                            s[nt][u] = -INFINITY;
+                if (C::kUnit != 1) {
+                    // NaN codes of V at keys that some rows do not see: 0 * NaN
+                    // must not reach those rows, so the rows that do see such a
+                    // key get their NaN here and the code becomes 0
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int x = 0; x < VW; ++x)
+                            any |= nan_bytes(vw[r][x]);
+                    if (__any_sync(0xffffffffu, any != 0)) {
+#pragma unroll 1
+                        for (int key = 0; key < kTile; ++key) {
+                            const int r = (key & 1) + 2 * (key >> 3), from = (lane & ~3) | ((key & 7) >> 1);
+#pragma unroll
+                            for (int x = 0; x < VW; ++x) {
+                                const uint32_t own = r == 0 ? vw[0][x] : r == 1 ? vw[1][x] : r == 2 ? vw[2][x] : vw[3][x];
+                                const uint32_t bits = nan_bytes(__shfl_sync(0xffffffffu, own, from));
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                        for (int u = 0; u < 2; ++u)
+                                            if ((bits >> (8 * e + 7) & 1u) && info.key0 + key < lim[nt][u])
+                                                acc[2 * x + (e >> 1)][nt][(e & 1) * 2 + u] = __int_as_float(0x7FC00000);
+                            }
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+#pragma unroll
+                            for (int x = 0; x < VW; ++x) {
+                                const uint32_t bits = nan_bytes(vw[r][x]);
+                                vw[r][x] &= ~((bits >> 7) * 0xFFu);
+                            }
+                    }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    grown = grown || s[nt][u] + ev > m[nt][u & 1] + 8.f;
+            if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float top = fmaxf(s[nt][u], s[nt][u + 2]) + ev;
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        const float next = fmaxf(m[nt][u], top);
+                        const float alpha = next == m[nt][u] ? 1.f : ex2(m[nt][u] - next);
+                        m[nt][u] = next;
+                        l[nt][u] *= alpha;
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            acc[j][nt][u] *= alpha;
+                            acc[j][nt][u + 2] *= alpha;
+                        }
+                    }
+            }
+            // ---- P, and O^T += V^T P^T ----
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float r0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], r1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+                const float p0 = ex2(s[nt][0] - r0), p1 = ex2(s[nt][1] - r1);
+                const float p2 = ex2(s[nt][2] - r0), p3 = ex2(s[nt][3] - r1);
+                l[nt][0] += p0 + p2;
+                l[nt][1] += p1 + p3;
+                pb[nt][0] = transpose8(DTypeTraits<__half>::pack(p0 * info.v_scale, p1 * info.v_scale));
+                pb[nt][1] = transpose8(DTypeTraits<__half>::pack(p2 * info.v_scale, p3 * info.v_scale));
+            }
+#pragma unroll
+            for (int x = 0; x < VW; ++x) {
+                // four columns of V: bytes of keys 2 c, 2 c + 1 and 2 c + 8, 2 c + 9 side by side
+                uint32_t a[4][2];  // column, key pair
+                C::halves(__byte_perm(vw[0][x], vw[1][x], 0x5140), a[0][0], a[1][0]);
+                C::halves(__byte_perm(vw[0][x], vw[1][x], 0x7362), a[2][0], a[3][0]);
+                C::halves(__byte_perm(vw[2][x], vw[3][x], 0x5140), a[0][1], a[1][1]);
+                C::halves(__byte_perm(vw[2][x], vw[3][x], 0x7362), a[2][1], a[3][1]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_f16(acc[2 * x][nt], a[0][0], a[1][0], a[0][1], a[1][1], pb[nt][0], pb[nt][1]);
+                    mma_f16(acc[2 * x + 1][nt], a[2][0], a[3][0], a[2][1], a[3][1], pb[nt][0], pb[nt][1]);
+                }
+            }
+        }
+
+        if (info.flags & kLast) {
+            // ---- merge the warps of each row group; write the rows, or the block's part ----
+            float *mo = reinterpret_cast<float *>(smem + F::MERGE_OFF);
+            float *mm = reinterpret_cast<float *>(smem + F::ML_OFF), *ml = mm + kDecWarps * F::ROWS;
+            __syncthreads();  // the segment before has been read
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float sum = l[nt][u];
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                    const int row = warp * F::ROWS + nt * 8 + 2 * c + u;
+                    if (g == 0) {
+                        mm[row] = m[nt][u];
+                        ml[row] = sum;
+                    }
+#pragma unroll
+                    for (int x = 0; x < VW; ++x) {
+                        // V words lie D / 8 bytes apart a thread, or 4 (d = 96)
+                        const int d = F::VV * (g + 8 * (x / (F::VV / 4))) + 4 * (x % (F::VV / 4));
+                        *reinterpret_cast<float4 *>(mo + row * F::OROW + d) =
+                            make_float4(acc[2 * x][nt][u], acc[2 * x][nt][u + 2], acc[2 * x + 1][nt][u],
+                                        acc[2 * x + 1][nt][u + 2]);
+                    }
+                }
+            __syncthreads();
+            const bool part = info.flags & (kHeadPart | kTailPart);
+            const long long seg_row =
+                w.pages ? 0 : (static_cast<long long>(info.b) * w.cache.heads + info.head) * w.R;
+            const long long place = 2ll * blockIdx.x + (info.flags & kTailPart ? 1 : 0);
+            for (int x = t; x < rows_block * (D / 2); x += kDecThreads) {
+                const int row = x / (D / 2), d = 2 * (x % (D / 2));
+                const int abs_row = info.group * rows_block + row;
+                if (abs_row >= w.R)
+                    break;
+                const int from = (row / F::ROWS) * key_warps * F::ROWS + row % F::ROWS;  // of its first warp
+                float top = -INFINITY;
+                for (int y = 0; y < key_warps; ++y)
+                    top = fmaxf(top, mm[from + y * F::ROWS]);
+                float2 o = make_float2(0.f, 0.f);
+                float sum = 0.f;
+                const float ref = top == -INFINITY ? 0.f : top;
+                for (int y = 0; y < key_warps; ++y) {
+                    const float f = ex2(mm[from + y * F::ROWS] - ref);
+                    const float2 z = *reinterpret_cast<const float2 *>(mo + (from + y * F::ROWS) * F::OROW + d);
+                    o.x = fmaf(z.x, f, o.x);
+                    o.y = fmaf(z.y, f, o.y);
+                    sum = fmaf(ml[from + y * F::ROWS], f, sum);
+                }
+                if (part) {
+                    const long long pr = place * rows_block + row;
+                    *reinterpret_cast<float2 *>(w.part_o + pr * D + d) = o;
+                    if (d == 0) {
+                        w.part_m[pr] = top;
+                        w.part_l[pr] = sum;
+                    }
+                } else {
+                    const long long orow =
+                        w.pages ? ((static_cast<long long>(info.b) * w.cache.heads + info.head) * w.q.G + abs_row) * w.q.Nq +
+                                      info.i
+                                : seg_row + abs_row;
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    *reinterpret_cast<uint32_t *>(out + orow * D + d) = DTypeTraits<T>::pack(o.x * inv, o.y * inv);
+                    if (d == 0 && lse != nullptr)
+                        lse[orow] = sum == 0.f ? -INFINITY : (ref + __log2f(sum)) * 0.6931471805599453f;
                 }
             }
         }
     }
-    for (int off = 16; off > 0; off >>= 1)
-        l += __shfl_xor_sync(0xffffffffu, l, off);
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    for (int c = 0; c < D / 32; ++c) {
-        const uint32_t r = DTypeTraits<T>::pack(o[c] * inv, 0.f);
-        reinterpret_cast<uint16_t *>(out)[row * D + c * 32 + lane] = static_cast<uint16_t>(r);
+    copy_wait<0>();
+}
+
+// Merges the parts of every segment that more than one block has, a block a
+// query row; writes the rows of segments without keys.
+template <int D, typename T>
+__global__ void __launch_bounds__(kCombineThreads)
+    fa_cache_combine_kernel(const __grid_constant__ Work w, T *__restrict__ out, float *__restrict__ lse, int log2_step,
+                            int rows_block)
+{
+    constexpr int WARPS = kCombineThreads / 32;
+    __shared__ float red_o[WARPS][D];
+    __shared__ float red_m[WARPS], red_l[WARPS];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    // block = ((b * queries + i) * heads + head) * R + row
+    const int queries = w.pages ? w.q.Nq : 1;
+    long long x = blockIdx.x;
+    const int row = static_cast<int>(x % w.R);
+    x /= w.R;
+    const int head = static_cast<int>(x % w.cache.heads);
+    x /= w.cache.heads;
+    const int i = static_cast<int>(x % queries), b = static_cast<int>(x / queries);
+    const int group = row / rows_block;
+    const int len = w.batch.length(b, w.cache.log2_page);
+    const int units = units_of(w, len, i, log2_step);
+    const long long orow =
+        w.pages ? ((static_cast<long long>(b) * w.cache.heads + head) * w.q.G + row) * w.q.Nq + i
+                : (static_cast<long long>(b) * w.cache.heads + head) * w.R + row;
+    if (units == 0) {
+        for (int d = 2 * t; d < D; d += 2 * kCombineThreads)
+            *reinterpret_cast<uint32_t *>(out + orow * D + d) = 0;
+        if (t == 0 && lse != nullptr)
+            lse[orow] = -INFINITY;
+        return;
     }
-    if (lse != nullptr && lane == 0)
-        lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    const long long share = w.plan[0];
+    long long first = w.plan[1 + b];
+    for (int y = 0; y < i; ++y)
+        first += static_cast<long long>(units_of(w, len, y, log2_step)) * w.cache.heads * w.groups;
+    first += (static_cast<long long>(head) * w.groups + group) * units;
+    const int x0 = static_cast<int>(first / share), x1 = static_cast<int>((first + units - 1) / share);
+    if (x0 == x1)
+        return;  // one block had it all, and has written it
+    const int in_block = row % rows_block;
+    // a block's place: its head part if the segment began before its run
+    auto place = [&](int y) -> long long {
+        return (2ll * y + (y * share > first ? 0 : 1)) * rows_block + in_block;
+    };
+    float top = -INFINITY;
+    for (int y = x0 + t; y <= x1; y += kCombineThreads)
+        top = fmaxf(top, w.part_m[place(y)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0)
+        red_m[warp] = top;
+    __syncthreads();
+    top = red_m[0];
+    for (int y = 1; y < WARPS; ++y)
+        top = fmaxf(top, red_m[y]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    // warp v: blocks x0 + v, + WARPS, ...; lane: columns 4 lane .. 4 lane + 3
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int y = x0 + warp; y <= x1; y += WARPS) {
+        const long long p = place(y);
+        const float f = ex2(w.part_m[p] - ref);
+        sum = fmaf(w.part_l[p], f, sum);
+        if (4 * lane < D) {
+            const float4 z = *reinterpret_cast<const float4 *>(w.part_o + p * D + 4 * lane);
+            o.x = fmaf(z.x, f, o.x);
+            o.y = fmaf(z.y, f, o.y);
+            o.z = fmaf(z.z, f, o.z);
+            o.w = fmaf(z.w, f, o.w);
+        }
+    }
+    if (4 * lane < D)
+        *reinterpret_cast<float4 *>(&red_o[warp][4 * lane]) = o;
+    if (lane == 0)
+        red_l[warp] = sum;
+    __syncthreads();
+    sum = 0.f;
+    for (int y = 0; y < WARPS; ++y)
+        sum += red_l[y];
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    for (int d = 2 * t; d < D; d += 2 * kCombineThreads) {
+        float2 z = make_float2(0.f, 0.f);
+        for (int y = 0; y < WARPS; ++y) {
+            z.x += red_o[y][d];
+            z.y += red_o[y][d + 1];
+        }
+        *reinterpret_cast<uint32_t *>(out + orow * D + d) = DTypeTraits<T>::pack(z.x * inv, z.y * inv);
+    }
+    if (t == 0 && lse != nullptr)
+        lse[orow] = sum == 0.f ? -INFINITY : (ref + __log2f(sum)) * 0.6931471805599453f;
 }
 
 }  // namespace cache
