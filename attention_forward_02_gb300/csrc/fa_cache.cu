@@ -78,14 +78,36 @@ Shape shape_of(int R)
     return {2, row_warps, 16 * row_warps};
 }
 
+// A code buffer as [num_pages * heads, page, d] bytes: boxes of `box` rows of
+// `width` columns, each row swizzled by its width.
+fa_status_t encode_codes(fa_host::EncodeTiledFn encode, CUtensorMap *map, void *codes, const fa_cache_t *c, int width,
+                         int box)
+{
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c->d), static_cast<cuuint64_t>(c->page),
+                                static_cast<cuuint64_t>(c->num_pages) * c->heads};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c->d), static_cast<cuuint64_t>(c->page) * c->d};
+    const cuuint32_t extent[3] = {static_cast<cuuint32_t>(width), static_cast<cuuint32_t>(box), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUtensorMapSwizzle swizzle = width == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                       : width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                     : CU_TENSOR_MAP_SWIZZLE_32B;
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, codes, dims, strides, extent, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? FA_OK
+               : FA_ERR_CUDA;
+}
+
 // Bytes of the plan at the workspace's start (a 64-bit number, and one a sequence).
 size_t plan_bytes(int B) { return (static_cast<size_t>(B) + 2) / 2 * 16; }
 
 // The current device's status word and SM count.
-fa_status_t device(CacheState **out, int *num_sms)
+fa_status_t device(CacheState **out, int *num_sms, fa_host::EncodeTiledFn *encoder = nullptr)
 {
     fa_host::EncodeTiledFn encode = nullptr;
     const fa_status_t s = fa_host::encoder(&encode, num_sms);
+    if (encoder)
+        *encoder = encode;
     if (s != FA_OK)
         return s;
     int dev = -1;
@@ -120,6 +142,8 @@ fa_status_t check_cache(const fa_cache_t *c, Range (&r)[kCacheRanges])
 {
     if (!c || c->num_pages < 1 || c->heads < 1)
         return FA_ERR_INVALID_ARG;
+    if (static_cast<long long>(c->num_pages) * c->heads > 0x7fffffffLL)
+        return FA_ERR_UNSUPPORTED;
     if ((c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) ||
         (c->d != 32 && c->d != 64 && c->d != 96 && c->d != 128) || (c->format != FA_E4M3 && c->format != FA_INT8) ||
         c->heads > kMaxBatch / 2)
@@ -374,7 +398,8 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
             return FA_ERR_INVALID_ARG;
     CacheState *st = nullptr;
     int sms = 0;
-    if ((s = device(&st, &sms)) != FA_OK)
+    fa_host::EncodeTiledFn encode = nullptr;
+    if ((s = device(&st, &sms, &encode)) != FA_OK)
         return s;
     const Cache c = device_cache(cache);
     const Batch batch = {seq_lens, page_table, table_stride, max_pages, cache->num_pages, st->status};
@@ -397,11 +422,18 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
     w.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan_bytes(B));
     w.part_m = w.part_o + part_rows * cache->d;
     w.part_l = w.part_m + part_rows;
-    const int log2_step = shape.row_warps == 1 ? 6 : shape.row_warps == 2 ? 5 : 4;
+    const int box = cache->page < fa::cache::kStep ? cache->page : fa::cache::kStep;
+    w.log2_box = box == 64 ? 6 : box == 32 ? 5 : 4;
+    fa::cache::Maps maps = {};
+    const int width[2] = {cache->d == 96 ? 64 : cache->d, 32};
+    for (int i = 0; i < (cache->d == 96 ? 2 : 1); ++i)
+        if ((s = encode_codes(encode, &maps.k[i], cache->k, cache, width[i], box)) != FA_OK ||
+            (s = encode_codes(encode, &maps.v[i], cache->v, cache, width[i], box)) != FA_OK)
+            return s;
     // no more blocks than units there can be
+    const long long keys = static_cast<long long>(pages && slots < max_pages ? slots : max_pages) * cache->page;
     const long long most = static_cast<long long>(B) * (pages ? Nq : 1) * cache->heads * w.groups *
-                           (((static_cast<long long>(pages && slots < max_pages ? slots : max_pages) * cache->page - 1) >>
-                             log2_step) + 1);
+                           ((keys - 1) / fa::cache::kStep + 1);
     const long long resident = static_cast<long long>(sms) * (shape.tiles == 1 ? 3 : 2);
     long long blocks = resident < fa::cache::kMaxBlocks ? resident : fa::cache::kMaxBlocks;
     if (most < blocks)
@@ -414,15 +446,15 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
             if (shape.tiles == 1)
                 fa::cache::fa_cache_decode_kernel<D, 1, T, C>
                     <<<static_cast<unsigned>(blocks), fa::cache::kDecThreads, fa::cache::DecCfg<D, 1>::SMEM, cs>>>(
-                        w, static_cast<T *>(o), lse);
+                        maps, w, static_cast<T *>(o), lse);
             else
                 fa::cache::fa_cache_decode_kernel<D, 2, T, C>
                     <<<static_cast<unsigned>(blocks), fa::cache::kDecThreads, fa::cache::DecCfg<D, 2>::SMEM, cs>>>(
-                        w, static_cast<T *>(o), lse);
+                        maps, w, static_cast<T *>(o), lse);
             if (cudaGetLastError() != cudaSuccess)
                 return FA_ERR_CUDA;
             fa::cache::fa_cache_combine_kernel<D, T><<<static_cast<unsigned>(rows), fa::cache::kCombineThreads, 0, cs>>>(
-                w, static_cast<T *>(o), lse, log2_step, shape.rows_block);
+                w, static_cast<T *>(o), lse, shape.rows_block);
             return launched();
         });
     });

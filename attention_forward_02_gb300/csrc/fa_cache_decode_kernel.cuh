@@ -17,10 +17,12 @@
 // round trip of the converted tile through shared memory; here nothing is
 // exchanged between threads but P^T, transposed by movmatrix.  The order of d
 // inside the first product, and of the rows of O^T in the second, is free, so a
-// thread takes consecutive bytes of a row: every byte of a key is loaded by
-// exactly the thread that multiplies it.  That makes the ring of cp.async
-// copies in shared memory private to each thread: no barrier, no transaction
-// count, conflict-free 16-byte reads, and the wait is the thread's own.
+// thread takes consecutive bytes of a row: 16-byte shared reads, free of bank
+// conflicts under the swizzle that TMA writes (d = 128; a few two-way ones below).
+//
+// One warp loads: it looks up page numbers and scales, 32 pages at a time, and
+// copies 64 keys of K and V a stage into a ring.  Four warps compute, 16 keys
+// each, or, with more than 16 query rows a head, fewer keys and more rows.
 //
 // Query rows are scaled by a power of two to a row maximum in [2^14, 2^15)
 // before they become fp16: a bf16 row keeps every bit that fp32 sums would see.
@@ -42,41 +44,88 @@
 namespace fa {
 namespace cache {
 
-constexpr int kDecWarps = 4;
-constexpr int kDecThreads = 32 * kDecWarps;
-constexpr int kTile = 16;         // keys a warp and step
+constexpr int kDecWarps = 4;      // that compute
+constexpr int kDecThreads = 32 * (kDecWarps + 1);
+constexpr int kTile = 16;         // keys of one product
+constexpr int kStep = 64;         // keys of a stage: a unit of work
+constexpr int kLog2Step = 6;
+constexpr int kSubs = kStep / kTile;
 constexpr int kMaxBlocks = 640;   // of the persistent grid
 constexpr int kCombineThreads = 128;
 
-// One 16-key tile of K and V a stage, in thread-private pieces.
+// A code row of d bytes is held in one or two column parts, each with the TMA
+// swizzle of its width: 32, 64, 128, or 64 + 32.
 template <int D, int NT>
 struct DecCfg {
-    static constexpr int KV = D % 64 == 0 ? 16 : 8;   // bytes of one K copy
-    static constexpr int KC = D / 4 / KV;             // K copies a thread and key
-    static constexpr int WPC = KV / 4;                // words a K copy
-    static constexpr int VV = D == 96 ? 4 : D / 8;    // bytes of one V copy
-    static constexpr int VC = D / 8 / VV;             // V copies a thread and key
-    static constexpr int STAGE = 2 * kTile * D;       // bytes
-    static constexpr int STAGES = 12288 / STAGE;      // 3 at d = 128
-    static constexpr int META = 32;
-    static constexpr int ROWS = 8 * NT;               // query rows a warp
-    static constexpr int OROW = D + 4;                // floats of a row of the merge
+    static constexpr int PARTS = D == 96 ? 2 : 1;
+    static constexpr int W0 = D == 96 ? 64 : D, W1 = D - W0;  // widths
+    static constexpr int HALF = kStep * D;                    // K or V of a stage, bytes
+    static constexpr int STAGE = 2 * HALF;
+    static constexpr int RING = NT == 1 ? 49152 : 65536;      // bytes; 3 blocks an SM, or 2
+    static constexpr int STAGES = RING / STAGE < 8 ? RING / STAGE : 8;  // 3 or 4 at d = 128
+    static constexpr int ROWS = 8 * NT;                       // query rows a warp
+    static constexpr int OROW = D + 4;                        // floats of a row of the merge
     static constexpr int RING_OFF = 0;
-    static constexpr int META_OFF = kDecWarps * STAGES * STAGE;
-    static constexpr int MERGE_OFF = META_OFF + kDecWarps * STAGES * META;
+    static constexpr int META_OFF = STAGES * STAGE;
+    static constexpr int MERGE_OFF = META_OFF + STAGES * 80;
     static constexpr int ML_OFF = MERGE_OFF + kDecWarps * ROWS * OROW * 4;
-    static constexpr int SMEM = ML_OFF + kDecWarps * ROWS * 8;
+    static constexpr int BAR_OFF = ML_OFF + kDecWarps * ROWS * 8;
+    static constexpr int FLAG_OFF = BAR_OFF + 16 * STAGES + 8;  // full, empty, merge
+    static constexpr int SMEM = FLAG_OFF + 16 + 1024;  // and room to align the ring
+    static_assert(STAGES * STAGE % 16 == 0 && STAGE % 1024 == 0, "alignment of the ring");
 };
 
-// What a warp knows of a tile when it computes it (written with its copies).
-struct __align__(16) TileMeta {
-    float k_scale, v_scale;
-    int key0;    // position of the tile's first key
-    int flags;   // below
-    int b, i, head, group;
+// What the computing warps know of a stage.
+struct __align__(16) StageMeta {
+    float k_scale[kSubs], v_scale[kSubs];
+    int key0[kSubs];  // position of the 16-key tile's first key; -1: nothing to see
+    int flags, b, i, head, group, pad[3];
 };
-static_assert(sizeof(TileMeta) == 32, "tile record");
-constexpr int kFirst = 1, kLast = 2, kHeadPart = 4, kTailPart = 8, kSkip = 16;
+static_assert(sizeof(StageMeta) == 80, "stage record");
+constexpr int kFirst = 1, kLast = 2, kHeadPart = 4, kTailPart = 8;
+
+// Where a thread (g = lane / 4, c = lane % 4) finds its bytes of a 16-key tile in
+// a part W bytes wide: of K, 4 words (2 if W = 32) ... of rows g and g + 8; of V,
+// W / 32 words of the rows 2 c, 2 c + 1, + 8.  Swizzle of a row of W bytes: its
+// 16-byte chunk number XOR bits of the row (TMA's 128-, 64- and 32-byte swizzles).
+template <int W>
+__device__ __forceinline__ uint32_t k_offset(int g, int c, int x)
+{
+    if (W == 128)
+        return g * 128 + (((2 * c + x) ^ g) << 4);
+    if (W == 64)
+        return g * 64 + ((c ^ ((g >> 1) & 3)) << 4);
+    return g * 32 + (((c >> 1) ^ ((g >> 2) & 1)) << 4) + (c & 1) * 8;
+}
+template <int W>
+__device__ __forceinline__ uint32_t v_offset(int g, int c, int odd)
+{
+    const int row = 2 * c + odd;
+    if (W == 128)
+        return row * 128 + ((g ^ row) << 4);
+    if (W == 64)
+        return row * 64 + (((g >> 1) ^ c) << 4) + (g & 1) * 8;
+    return row * 32 + (((g >> 2) ^ (c >> 1)) << 4) + (g & 3) * 4;
+}
+// Column of a thread's K word s, and of its V word x (each 4 consecutive columns).
+template <int D>
+__device__ __forceinline__ int k_column(int c, int s)
+{
+    if (D == 128)
+        return 32 * c + 4 * s;
+    if (D == 64)
+        return 16 * c + 4 * s;
+    if (D == 32)
+        return 8 * c + 4 * s;
+    return s < 4 ? 16 * c + 4 * s : 64 + 8 * c + 4 * (s - 4);
+}
+template <int D>
+__device__ __forceinline__ int v_column(int g, int x)
+{
+    if (D == 96)
+        return x < 2 ? 8 * g + 4 * x : 64 + 4 * g;
+    return g * (D / 8) + 4 * x;
+}
 
 struct Work {
     Cache cache;
@@ -86,6 +135,7 @@ struct Work {
     int slots;
     int B, R, groups;  // rows of a segment (G Nq, or G with listed pages), row groups
     int row_warps;     // warps along the rows (1, 2, 4), the others along the keys
+    int log2_box;      // keys of one copy: 64, or a page if that is smaller
     float scale_log2;
     // workspace: [0] blocks' share, [1 + b] first unit of sequence b; then the parts
     long long *plan;
@@ -93,21 +143,21 @@ struct Work {
 };
 
 // Units of query i's segment of a sequence of `len` keys (all queries' with no list).
-__device__ __forceinline__ int units_of(const Work &w, int len, int i, int log2_step)
+__device__ __forceinline__ int units_of(const Work &w, int len, int i)
 {
     int keys = len;
     if (w.pages) {
         const int n = (context(w.q, len, i) + w.cache.page - 1) >> w.cache.log2_page;
         keys = min(n, w.slots) << w.cache.log2_page;
     }
-    return keys > 0 ? ((keys - 1) >> log2_step) + 1 : 0;
+    return keys > 0 ? ((keys - 1) >> kLog2Step) + 1 : 0;
 }
-__device__ __forceinline__ long long units_of_sequence(const Work &w, int b, int log2_step)
+__device__ __forceinline__ long long units_of_sequence(const Work &w, int b)
 {
     const int len = w.batch.length(b, w.cache.log2_page);
     long long n = 0;
     for (int i = 0; i < (w.pages ? w.q.Nq : 1); ++i)
-        n += units_of(w, len, i, log2_step);
+        n += units_of(w, len, i);
     return n * w.cache.heads * w.groups;
 }
 
@@ -131,40 +181,21 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x)
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// Copy of `BYTES` (4, 8, 16) to shared memory, zeros where `live` is false.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool live)
-{
-    if (!smem_ok(dst, BYTES, BYTES))
-        return;
-    const int n = live ? BYTES : 0;
-    if (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n)
-                     : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 template <int WORDS>
-__device__ __forceinline__ void load_words(uint32_t (&w)[WORDS], uint32_t addr)
+__device__ __forceinline__ void load_words(uint32_t *w, uint32_t addr)
 {
     if (!smem_ok(addr, 4 * WORDS, 4 * WORDS)) {
         for (int i = 0; i < WORDS; ++i)
             w[i] = 0;
         return;
     }
-    if (WORDS == 4)
+    if constexpr (WORDS == 4)
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1 % WORDS]), "=r"(w[2 % WORDS]), "=r"(w[3 % WORDS])
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                      : "r"(addr)
                      : "memory");
-    else if (WORDS == 2)
-        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1 % WORDS]) : "r"(addr) : "memory");
+    else if constexpr (WORDS == 2)
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
     else
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
 }
@@ -172,53 +203,71 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[WORDS], uint32_t addr)
 // Bytes of a word that are e4m3 NaN codes, as their top bits.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
+struct Maps {
+    CUtensorMap k[2], v[2];  // of the column parts
+};
+
 template <int D, int NT, typename T, typename C>
 __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
-    fa_cache_decode_kernel(const __grid_constant__ Work w, T *__restrict__ out, float *__restrict__ lse)
+    fa_cache_decode_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Work w, T *__restrict__ out,
+                           float *__restrict__ lse)
 {
     using F = DecCfg<D, NT>;
     constexpr int S = F::STAGES;
     constexpr int KW = D / 16;  // words of a key's codes a thread holds = steps of the first product
     constexpr int VW = D / 32;  // words of a key's V a thread holds
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
     __shared__ long long scan[kDecWarps + 1];
     __shared__ long long begin[2];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (sbase - raw);
+    auto full = [&](int s) -> uint32_t { return sbase + F::BAR_OFF + 8u * s; };
+    auto empty = [&](int s) -> uint32_t { return sbase + F::BAR_OFF + 8u * (S + s); };
+    const uint32_t merged = sbase + F::BAR_OFF + 16u * S;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + F::FLAG_OFF);
+    StageMeta *meta = reinterpret_cast<StageMeta *>(smem + F::META_OFF);
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int g = lane >> 2, c = lane & 3;
-    const int key_warps = kDecWarps / w.row_warps;
-    const int wk = warp % key_warps, wr = warp / key_warps;
-    const int log2_step = key_warps == 4 ? 6 : key_warps == 2 ? 5 : 4;
     const int rows_block = F::ROWS * w.row_warps;
 
+    if (t == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), kDecWarps);
+        }
+        mbar_init(merged, kDecWarps);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+
     // ---- this block's run of units ----
-    long long total, share, first_unit;
-    int b;
+    int all;      // units of this block
+    int b;        // its first sequence
+    long long off;  // ... and the unit of that sequence it begins with
     {
         const int each = (w.B + kDecThreads - 1) / kDecThreads;
         const int b0 = min(w.B, t * each), b1 = min(w.B, b0 + each);
         long long sum = 0;
         for (int x = b0; x < b1; ++x)
-            sum += units_of_sequence(w, x, log2_step);
+            sum += units_of_sequence(w, x);
         long long incl = sum;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off)
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
                 incl += y;
         }
         if (lane == 31)
             scan[warp] = incl;
         __syncthreads();
-        total = 0;
-        for (int x = 0; x < kDecWarps; ++x) {
+        long long total = 0;
+        for (int x = 0; x < kDecWarps + 1; ++x) {
             if (x < warp)
                 incl += scan[x];
             total += scan[x];
         }
-        share = (total + gridDim.x - 1) / gridDim.x;
-        if (share < 1)
-            share = 1;
-        first_unit = share * blockIdx.x;
+        const long long share = max(1ll, (total + gridDim.x - 1) / gridDim.x);
+        const long long first_unit = share * blockIdx.x;
         long long at = incl - sum;
         if (blockIdx.x == 0) {
             if (t == 0)
@@ -226,13 +275,13 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
             long long y = at;
             for (int x = b0; x < b1; ++x) {
                 w.plan[1 + x] = y;
-                y += units_of_sequence(w, x, log2_step);
+                y += units_of_sequence(w, x);
             }
         }
         if (first_unit >= at && first_unit < incl) {
             int x = b0;
             for (; x + 1 < b1; ++x) {
-                const long long n = units_of_sequence(w, x, log2_step);
+                const long long n = units_of_sequence(w, x);
                 if (first_unit < at + n)
                     break;
                 at += n;
@@ -244,123 +293,111 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
         if (first_unit >= total)
             return;
         b = static_cast<int>(begin[0]);
+        off = begin[1];
+        all = static_cast<int>(min(share, total - first_unit));
     }
-    long long left = min(share, total - first_unit);  // units still to load
-    const long long all = left;                       // units of this block
 
-    // ---- the side that loads: a walk over segments, units, pages ----
-    const uint32_t sbase = smem_u32(smem);
-    const uint32_t ring = sbase + F::RING_OFF + warp * (S * F::STAGE);
-    TileMeta *meta = reinterpret_cast<TileMeta *>(smem + F::META_OFF) + warp * S;
-    int i = 0, head = 0, group = 0, len = 0, ctx = 0, units = 0, unit = 0;
-    int held = 0, held_count = 0;  // lane l: page number of the l-th next tile (-1: none); tiles so covered
-    int held_key = 0;              // ... and its first key
-    long long off = begin[1];
-    auto open_sequence = [&]() { len = b < w.B ? w.batch.length(b, w.cache.log2_page) : 0; };
-    auto open_query = [&]() {
-        ctx = w.pages ? context(w.q, len, i) : len;
-        units = units_of(w, len, i, log2_step);
-    };
-    open_sequence();
-    open_query();
-    while (i + 1 < w.q.Nq && off >= static_cast<long long>(units) * w.cache.heads * w.groups) {
-        off -= static_cast<long long>(units) * w.cache.heads * w.groups;
-        ++i;
+    if (warp == kDecWarps) {
+        // ---------------- the warp that loads ----------------
+        int i = 0, len = 0, ctx = 0, units = 0;
+        auto open_query = [&]() {
+            len = b < w.B ? w.batch.length(b, w.cache.log2_page) : 0;
+            ctx = w.pages ? context(w.q, len, i) : len;
+            units = units_of(w, len, i);
+        };
+        const int per_unit = w.cache.heads * w.groups;
         open_query();
-    }
-    {
-        const int seg = static_cast<int>(off / units);
-        unit = static_cast<int>(off % units);
-        head = seg / w.groups;
-        group = seg % w.groups;
-    }
-    bool opened = true;  // the next tile is this block's first of its segment
-    int slot = 0;        // ring slot of the next load
-    auto load = [&]() {
-        if (left > 0) {
-            if (held_count == 0) {
-                // page numbers of the next 32 tiles of this segment
-                held_count = static_cast<int>(min(static_cast<long long>(min(32, units - unit)), left));
-                const int key = ((unit + lane) << log2_step) + wk * kTile;
-                int at = key >> w.cache.log2_page;
-                held = -1;
-                held_key = key;
-                if (lane < held_count) {
-                    if (w.pages) {
-                        const int n = (ctx + w.cache.page - 1) >> w.cache.log2_page;
-                        const int entry =
-                            at < min(n, w.slots)
-                                ? w.pages[((static_cast<long long>(b) * w.cache.heads + head) * w.q.Nq + i) * w.slots + at]
-                                : -1;
-                        if (entry >= n)
-                            w.batch.bad();
-                        at = entry < n ? entry : -1;
-                        held_key = at * w.cache.page + (key & (w.cache.page - 1));
-                    }
-                    if (at >= 0 && held_key < ctx) {
-                        held = w.batch.page(b, at);
-                        if (held < 0)
-                            w.batch.bad();
-                    }
+        while (i + 1 < w.q.Nq && off >= static_cast<long long>(units) * per_unit) {
+            off -= static_cast<long long>(units) * per_unit;
+            ++i;
+            open_query();
+        }
+        int head = static_cast<int>(off / units) / w.groups, group = static_cast<int>(off / units) % w.groups;
+        int unit = static_cast<int>(off % units);
+        const int log2_boxes = kLog2Step - w.log2_box;  // copies of a stage: 1, 2 or 4
+        const int box = 1 << w.log2_box, batch_units = 32 >> log2_boxes;
+        const uint64_t policy = l2_policy_evict_first();
+        bool opened = true, ok = true;  // opened: the next unit is this block's first of its segment
+        int done = 0;
+        while (done < all && ok) {
+            // lane l: page and scales of the l-th of the next 32 copies of this segment
+            const int here = min(min(batch_units, units - unit), all - done);
+            const int key = (unit << kLog2Step) + lane * box;
+            int at = key >> w.cache.log2_page, key0 = key, p = -1;
+            float ks = 1.f, vs = 1.f;
+            if ((lane >> log2_boxes) < here) {
+                if (w.pages) {
+                    const int n = (ctx + w.cache.page - 1) >> w.cache.log2_page;
+                    const int entry =
+                        at < min(n, w.slots)
+                            ? w.pages[((static_cast<long long>(b) * w.cache.heads + head) * w.q.Nq + i) * w.slots + at]
+                            : -1;
+                    if (entry >= n)
+                        w.batch.bad();
+                    at = entry < n ? entry : -1;
+                    key0 = at * w.cache.page + (key & (w.cache.page - 1));
+                }
+                if (at >= 0 && key0 < ctx) {
+                    p = w.batch.page(b, at);
+                    if (p < 0)
+                        w.batch.bad();
                 }
             }
-            const int p = __shfl_sync(0xffffffffu, held, 0), key0 = __shfl_sync(0xffffffffu, held_key, 0);
-            held = __shfl_down_sync(0xffffffffu, held, 1);
-            held_key = __shfl_down_sync(0xffffffffu, held_key, 1);
-            --held_count;
-            const bool live = p >= 0;
-            const size_t ph = live ? static_cast<size_t>(p) * w.cache.heads + head : 0;
-            const size_t base = live ? (ph * w.cache.page + (key0 & (w.cache.page - 1))) * D : 0;
-            const uint8_t *k = w.cache.k + base, *v = w.cache.v + base;
-            const uint32_t dst = ring + slot * F::STAGE + lane * F::KV;
-            const int seen = live ? ctx - key0 : 0;  // keys of the tile that exist
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int x = 0; x < F::KC; ++x) {
-                    const bool in = g + 8 * r < seen;
-                    copy_async<F::KV>(dst + (r * F::KC + x) * 32 * F::KV,
-                                      in ? k + (g + 8 * r) * D + (c + 4 * x) * F::KV : w.cache.k, in);
-                }
-            const uint32_t vdst = ring + slot * F::STAGE + kTile * D + lane * F::VV;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int x = 0; x < F::VC; ++x) {
-                    const int key = 2 * c + (r & 1) + 8 * (r >> 1);
-                    const bool in = key < seen;
-                    copy_async<F::VV>(vdst + (r * F::VC + x) * 32 * F::VV,
-                                      in ? v + key * D + (g + 8 * x) * F::VV : w.cache.v, in);
-                }
-            --left;
-            ++unit;
-            const bool ended = unit == units || left == 0;
-            TileMeta *m = meta + slot;
-            if (lane == 0) {
-                int flags = (opened ? kFirst : 0) | (ended ? kLast : 0) | (live ? 0 : kSkip);
-                if (ended) {
-                    // did this block see the segment from its first to its last unit?
-                    const bool before = all - left < unit;  // it began before this block's run
-                    if (before)
-                        flags |= kHeadPart;
-                    else if (unit < units)
-                        flags |= kTailPart;
-                }
-                m->key0 = key0;
-                m->flags = flags;
-                m->b = b;
-                m->i = i;
-                m->head = head;
-                m->group = group;
-                if (live) {
-                    copy_async<4>(smem_u32(&m->k_scale), w.cache.k_scale + ph, true);
-                    copy_async<4>(smem_u32(&m->v_scale), w.cache.v_scale + ph, true);
-                } else {
-                    m->k_scale = m->v_scale = 1.f;
-                }
+            const int ph = p * w.cache.heads + head;
+            if (p >= 0) {
+                ks = w.cache.k_scale[ph];
+                vs = w.cache.v_scale[ph];
             }
-            opened = ended;
-            if (unit == units && left > 0) {  // on to the next segment
+            for (int u = 0; u < here; ++u, ++done) {
+                const int s = done % S;
+                if (done >= S && !(ok = wait_warp(empty(s), ((done / S) - 1) & 1, abort_flag)))
+                    break;
+                const bool mine = (lane >> log2_boxes) == u;
+                const bool ended = unit + 1 == units || done + 1 == all;
+                const int row0 = (lane & ((1 << log2_boxes) - 1)) << w.log2_box;  // of the stage
+                StageMeta *m = meta + s;
+                if (mine)
+                    for (int y = 0; y < box / kTile; ++y) {
+                        const int k0 = key0 + y * kTile, sub = row0 / kTile + y;
+                        m->key0[sub] = p >= 0 && k0 < ctx ? k0 : -1;
+                        m->k_scale[sub] = ks;
+                        m->v_scale[sub] = vs;
+                    }
+                const unsigned live = __ballot_sync(0xffffffffu, mine && p >= 0);
+                if (lane == 0) {
+                    int flags = (opened ? kFirst : 0) | (ended ? kLast : 0);
+                    if (ended) {
+                        // did this block have the segment from its first to its last unit?
+                        if (unit > done)
+                            flags |= kHeadPart;  // it began before this block's run
+                        else if (unit + 1 < units)
+                            flags |= kTailPart;
+                    }
+                    m->flags = flags;
+                    m->b = b;
+                    m->i = i;
+                    m->head = head;
+                    m->group = group;
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_expect_tx(full(s), __popc(live) * 2 * box * D);
+                __syncwarp();
+                if (mine && p >= 0) {
+                    const uint32_t dst = sbase + F::RING_OFF + s * F::STAGE + row0 * F::W0;
+                    const int y = key0 & (w.cache.page - 1);
+                    tma_load_3d(dst, &maps.k[0], full(s), 0, y, ph, policy);
+                    tma_load_3d(dst + F::HALF, &maps.v[0], full(s), 0, y, ph, policy);
+                    if (F::PARTS == 2) {
+                        const uint32_t dst1 = sbase + F::RING_OFF + s * F::STAGE + kStep * F::W0 + row0 * F::W1;
+                        tma_load_3d(dst1, &maps.k[1], full(s), F::W0, y, ph, policy);
+                        tma_load_3d(dst1 + F::HALF, &maps.v[1], full(s), F::W0, y, ph, policy);
+                    }
+                }
+                opened = ended;
+                ++unit;
+            }
+            if (unit == units && done < all) {  // on to the next segment
                 unit = 0;
                 if (++group == w.groups) {
                     group = 0;
@@ -370,7 +407,6 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
                             if (++i >= (w.pages ? w.q.Nq : 1)) {
                                 i = 0;
                                 ++b;
-                                open_sequence();
                             }
                             open_query();
                         } while (units == 0 && b < w.B);
@@ -378,66 +414,57 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
                 }
             }
         }
-        slot = slot + 1 == S ? 0 : slot + 1;
-        copy_commit();
-    };
-#pragma unroll
-    for (int x = 0; x < S; ++x)
-        load();
+        // the computing warps wait for every copy; after a failed wait this one does
+        if (!ok)
+            for (int s = 0; s < S; ++s)
+                if (done > s)
+                    drain_bounded(full(s), ((done - 1 - s) / S) & 1);
+        return;
+    }
 
-    // ---- the side that computes ----
+    // ---------------- the warps that compute ----------------
+    const int g = lane >> 2, c = lane & 3;
+    const int key_warps = kDecWarps / w.row_warps;
+    const int wk = warp % key_warps, wr = warp / key_warps;
     uint32_t qb[NT][KW][2];  // Q^T operand: query g of each 8, its d in the order of the thread's K words
     float qf[NT][2];         // per query 2 c, 2 c + 1: scale to log2 units
     int lim[NT][2];          // ... keys that it sees
     float m[NT][2], l[NT][2], acc[D / 16][NT][4];
-    int least = 0;           // keys that all rows see
-    int at = 0;              // ring slot
-    for (long long done = 0; done < all; ++done) {
-        copy_wait<S - 1>();
+    int least = 0, most = 0;  // keys that all rows see, that any row sees
+    int b_seg = 0, i_seg = 0, head = 0, group = 0;  // the segment's
+    uint32_t merges = 0;
+    // a barrier of the computing warps whose wait is bounded
+    auto meet = [&]() -> bool {
         __syncwarp();
-        const TileMeta info = meta[at];
-        uint32_t kw[2][KW], vw[4][VW];
-        {
-            const uint32_t src = ring + at * F::STAGE + lane * F::KV;
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int x = 0; x < F::KC; ++x) {
-                    uint32_t y[F::WPC];
-                    load_words<F::WPC>(y, src + (r * F::KC + x) * 32 * F::KV);
-#pragma unroll
-                    for (int u = 0; u < F::WPC; ++u)
-                        kw[r][x * F::WPC + u] = y[u];
-                }
-            const uint32_t vsrc = ring + at * F::STAGE + kTile * D + lane * F::VV;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int x = 0; x < F::VC; ++x) {
-                    uint32_t y[F::VV / 4];
-                    load_words<F::VV / 4>(y, vsrc + (r * F::VC + x) * 32 * F::VV);
-#pragma unroll
-                    for (int u = 0; u < F::VV / 4; ++u)
-                        vw[r][x * (F::VV / 4) + u] = y[u];
-                }
-        }
-        __syncwarp();
-        at = at + 1 == S ? 0 : at + 1;
-        load();  // into the slot just read
+        if (lane == 0)
+            mbar_arrive(merged);
+        return wait_warp(merged, merges++ & 1u, abort_flag);
+    };
+    for (int done = 0; done < all; ++done) {
+        const int slot = done % S;
+        if (!wait_warp(full(slot), (done / S) & 1, abort_flag))
+            return;
+        const StageMeta *info = meta + slot;
+        const int flags = info->flags;
 
-        if (info.flags & kFirst) {
-            const int n = w.batch.length(info.b, w.cache.log2_page);
-            least = w.pages ? context(w.q, n, info.i) : context(w.q, n, 0);
+        if (flags & kFirst) {
+            b_seg = info->b;
+            i_seg = info->i;
+            head = info->head;
+            group = info->group;
+            const int n = w.batch.length(b_seg, w.cache.log2_page);
+            least = w.pages ? context(w.q, n, i_seg) : context(w.q, n, 0);
+            most = w.pages ? least : n;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const int row = info.group * rows_block + wr * F::ROWS + nt * 8 + g;
-                const int hq = w.pages ? row : row / w.q.Nq, qi = w.pages ? info.i : row % w.q.Nq;
-                const T *src = static_cast<const T *>(w.q.q) + info.b * w.q.batch_stride +
-                               static_cast<long long>(info.head * w.q.G + hq) * w.q.head_stride + qi * w.q.row_stride;
+                const int row = group * rows_block + wr * F::ROWS + nt * 8 + g;
+                const int hq = w.pages ? row : row / w.q.Nq, qi = w.pages ? i_seg : row % w.q.Nq;
+                const T *src = static_cast<const T *>(w.q.q) + b_seg * w.q.batch_stride +
+                               static_cast<long long>(head * w.q.G + hq) * w.q.head_stride + qi * w.q.row_stride;
                 float top = 0.f;
 #pragma unroll
                 for (int s = 0; s < KW; ++s) {
-                    const int d = F::KV * (c + 4 * (s / F::WPC)) + 4 * (s % F::WPC);
+                    const int d = k_column<D>(c, s);
                     uint2 x = make_uint2(0, 0);
                     if (row < w.R)
                         x = *reinterpret_cast<const uint2 *>(src + d);
@@ -477,7 +504,56 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
             }
         }
 
-        if (!(info.flags & kSkip)) {
+        for (int sub = wk; sub < kSubs; sub += key_warps) {
+            const int key0 = info->key0[sub];
+            const bool last_sub = sub + key_warps >= kSubs;
+            if (key0 < 0) {
+                if (last_sub) {
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(empty(slot));
+                }
+                continue;
+            }
+            const float k_scale = info->k_scale[sub], v_scale = info->v_scale[sub];
+            uint32_t kw[2][KW], vw[4][VW];
+            {
+                const uint32_t k0 = sbase + F::RING_OFF + slot * F::STAGE + sub * kTile * F::W0, v0 = k0 + F::HALF;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    if constexpr (D == 128) {
+                        load_words<4>(&kw[r][0], k0 + k_offset<128>(g, c, 0) + r * 1024);
+                        load_words<4>(&kw[r][4], k0 + k_offset<128>(g, c, 1) + r * 1024);
+                    } else if constexpr (D == 32) {
+                        load_words<2>(&kw[r][0], k0 + k_offset<32>(g, c, 0) + r * 256);
+                    } else {
+                        load_words<4>(&kw[r][0], k0 + k_offset<64>(g, c, 0) + r * 512);
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    if constexpr (D == 128)
+                        load_words<4>(&vw[r][0], v0 + v_offset<128>(g, c, r & 1) + (r >> 1) * 1024);
+                    else if constexpr (D == 32)
+                        load_words<1>(&vw[r][0], v0 + v_offset<32>(g, c, r & 1) + (r >> 1) * 256);
+                    else
+                        load_words<2>(&vw[r][0], v0 + v_offset<64>(g, c, r & 1) + (r >> 1) * 512);
+                }
+                if constexpr (D == 96) {
+                    const uint32_t k1 = sbase + F::RING_OFF + slot * F::STAGE + kStep * F::W0 + sub * kTile * 32;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        load_words<2>(&kw[r][4], k1 + k_offset<32>(g, c, 0) + r * 256);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        load_words<1>(&vw[r][2], k1 + F::HALF + v_offset<32>(g, c, r & 1) + (r >> 1) * 256);
+                }
+            }
+            if (last_sub) {  // the stage's codes are in registers
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(empty(slot));
+            }
             // ---- S^T = K Q^T ----
             float s[NT][4];
 #pragma unroll
@@ -495,24 +571,31 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
                     mma_f16(s[nt], a0, a1, a2, a3, qb[nt][x][0], qb[nt][x][1]);
             }
             // ---- log2 units, masks; does any score outgrow its reference? ----
-            const float ev = static_cast<float>(static_cast<int>(__float_as_uint(info.v_scale) >> 23) - 127);
+            const float ev = static_cast<float>(static_cast<int>(__float_as_uint(v_scale) >> 23) - 127);
             bool grown = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float f0 = info.k_scale * qf[nt][0], f1 = info.k_scale * qf[nt][1];
+                const float f0 = k_scale * qf[nt][0], f1 = k_scale * qf[nt][1];
                 s[nt][0] *= f0;
                 s[nt][1] *= f1;
                 s[nt][2] *= f0;
                 s[nt][3] *= f1;
             }
-            const bool masked = info.key0 + kTile > least;
+            const bool masked = key0 + kTile > least;
             if (masked) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        if (info.key0 + g + 8 * (u >> 1) >= lim[nt][u & 1])
+                        if (key0 + g + 8 * (u >> 1) >= lim[nt][u & 1])
                             s[nt][u] = -INFINITY;
+                // codes behind the last key are whatever the page held
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (key0 + 2 * c + (r & 1) + 8 * (r >> 1) >= most)
+#pragma unroll
+                        for (int x = 0; x < VW; ++x)
+                            vw[r][x] = 0;
                 if (C::kUnit != 1) {
                     // NaN codes of V at keys that some rows do not see: 0 * NaN
                     // must not reach those rows, so the rows that do see such a
@@ -537,7 +620,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
                                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                         for (int u = 0; u < 2; ++u)
-                                            if ((bits >> (8 * e + 7) & 1u) && info.key0 + key < lim[nt][u])
+                                            if ((bits >> (8 * e + 7) & 1u) && key0 + key < lim[nt][u])
                                                 acc[2 * x + (e >> 1)][nt][(e & 1) * 2 + u] = __int_as_float(0x7FC00000);
                             }
                         }
@@ -585,8 +668,8 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
                 const float p2 = ex2(s[nt][2] - r0), p3 = ex2(s[nt][3] - r1);
                 l[nt][0] += p0 + p2;
                 l[nt][1] += p1 + p3;
-                pb[nt][0] = transpose8(DTypeTraits<__half>::pack(p0 * info.v_scale, p1 * info.v_scale));
-                pb[nt][1] = transpose8(DTypeTraits<__half>::pack(p2 * info.v_scale, p3 * info.v_scale));
+                pb[nt][0] = transpose8(DTypeTraits<__half>::pack(p0 * v_scale, p1 * v_scale));
+                pb[nt][1] = transpose8(DTypeTraits<__half>::pack(p2 * v_scale, p3 * v_scale));
             }
 #pragma unroll
             for (int x = 0; x < VW; ++x) {
@@ -604,11 +687,12 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
             }
         }
 
-        if (info.flags & kLast) {
+        if (flags & kLast) {
             // ---- merge the warps of each row group; write the rows, or the block's part ----
             float *mo = reinterpret_cast<float *>(smem + F::MERGE_OFF);
             float *mm = reinterpret_cast<float *>(smem + F::ML_OFF), *ml = mm + kDecWarps * F::ROWS;
-            __syncthreads();  // the segment before has been read
+            if (!meet())  // the segment before has been read
+                return;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -624,21 +708,21 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
                     }
 #pragma unroll
                     for (int x = 0; x < VW; ++x) {
-                        // V words lie D / 8 bytes apart a thread, or 4 (d = 96)
-                        const int d = F::VV * (g + 8 * (x / (F::VV / 4))) + 4 * (x % (F::VV / 4));
+                        const int d = v_column<D>(g, x);
                         *reinterpret_cast<float4 *>(mo + row * F::OROW + d) =
                             make_float4(acc[2 * x][nt][u], acc[2 * x][nt][u + 2], acc[2 * x + 1][nt][u],
                                         acc[2 * x + 1][nt][u + 2]);
                     }
                 }
-            __syncthreads();
-            const bool part = info.flags & (kHeadPart | kTailPart);
+            if (!meet())
+                return;
+            const bool part = flags & (kHeadPart | kTailPart);
             const long long seg_row =
-                w.pages ? 0 : (static_cast<long long>(info.b) * w.cache.heads + info.head) * w.R;
-            const long long place = 2ll * blockIdx.x + (info.flags & kTailPart ? 1 : 0);
-            for (int x = t; x < rows_block * (D / 2); x += kDecThreads) {
+                w.pages ? 0 : (static_cast<long long>(b_seg) * w.cache.heads + head) * w.R;
+            const long long place = 2ll * blockIdx.x + (flags & kTailPart ? 1 : 0);
+            for (int x = t; x < rows_block * (D / 2); x += 32 * kDecWarps) {
                 const int row = x / (D / 2), d = 2 * (x % (D / 2));
-                const int abs_row = info.group * rows_block + row;
+                const int abs_row = group * rows_block + row;
                 if (abs_row >= w.R)
                     break;
                 const int from = (row / F::ROWS) * key_warps * F::ROWS + row % F::ROWS;  // of its first warp
@@ -664,8 +748,8 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
                     }
                 } else {
                     const long long orow =
-                        w.pages ? ((static_cast<long long>(info.b) * w.cache.heads + info.head) * w.q.G + abs_row) * w.q.Nq +
-                                      info.i
+                        w.pages ? ((static_cast<long long>(b_seg) * w.cache.heads + head) * w.q.G + abs_row) * w.q.Nq +
+                                      i_seg
                                 : seg_row + abs_row;
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
                     *reinterpret_cast<uint32_t *>(out + orow * D + d) = DTypeTraits<T>::pack(o.x * inv, o.y * inv);
@@ -675,15 +759,13 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
             }
         }
     }
-    copy_wait<0>();
 }
 
 // Merges the parts of every segment that more than one block has, a block a
 // query row; writes the rows of segments without keys.
 template <int D, typename T>
 __global__ void __launch_bounds__(kCombineThreads)
-    fa_cache_combine_kernel(const __grid_constant__ Work w, T *__restrict__ out, float *__restrict__ lse, int log2_step,
-                            int rows_block)
+    fa_cache_combine_kernel(const __grid_constant__ Work w, T *__restrict__ out, float *__restrict__ lse, int rows_block)
 {
     constexpr int WARPS = kCombineThreads / 32;
     __shared__ float red_o[WARPS][D];
@@ -699,7 +781,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     const int i = static_cast<int>(x % queries), b = static_cast<int>(x / queries);
     const int group = row / rows_block;
     const int len = w.batch.length(b, w.cache.log2_page);
-    const int units = units_of(w, len, i, log2_step);
+    const int units = units_of(w, len, i);
     const long long orow =
         w.pages ? ((static_cast<long long>(b) * w.cache.heads + head) * w.q.G + row) * w.q.Nq + i
                 : (static_cast<long long>(b) * w.cache.heads + head) * w.R + row;
@@ -713,7 +795,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     const long long share = w.plan[0];
     long long first = w.plan[1 + b];
     for (int y = 0; y < i; ++y)
-        first += static_cast<long long>(units_of(w, len, y, log2_step)) * w.cache.heads * w.groups;
+        first += static_cast<long long>(units_of(w, len, y)) * w.cache.heads * w.groups;
     first += (static_cast<long long>(head) * w.groups + group) * units;
     const int x0 = static_cast<int>(first / share), x1 = static_cast<int>((first + units - 1) / share);
     if (x0 == x1)
