@@ -95,7 +95,7 @@ def _open(path):
     lib.fa_decode_workspace_size.argtypes = [i, i, i, i, i]
     lib.fa_decode.restype = i
     lib.fa_decode.argtypes = [vp, vp, vp, vp, vp, vp, ctypes.c_size_t, i, i, i, i, i, f, i, i, vp]
-    ll, cp = ctypes.c_longlong, ctypes.POINTER(CacheDesc)
+    ll, cp = ctypes.c_longlong, ctypes.c_void_p  # a CacheDesc by reference, or its bytes
     lib.fa_cache_write.restype = i
     lib.fa_cache_write.argtypes = [cp, vp, vp, ll, ll, ll, ll, vp, vp, vp, ll, i, i, i, i, vp]
     lib.fa_cache_read.restype = i

@@ -17,12 +17,13 @@ whatever they hold then.  What they hold cannot be checked by the call: a page
 number or length outside the cache is left out, and
 ``fa_last_device_status`` reports it.
 """
-from ctypes import byref
+from contextlib import nullcontext
+from struct import Struct
 from typing import NamedTuple, Optional
 
 import torch
 
-from ._lib import (FA_BF16, FA_E4M3, FA_FP16, FA_INT8, CacheDesc, FAError, fa_cache_read_raw,
+from ._lib import (FA_BF16, FA_E4M3, FA_FP16, FA_INT8, FAError, fa_cache_read_raw,
                    fa_cache_select_raw, fa_cache_select_workspace_size, fa_cache_write_raw,
                    fa_decode_cache_raw, fa_decode_cache_workspace_size)
 
@@ -55,98 +56,126 @@ class FACache(NamedTuple):
         return cls(k, v, ks, vs, mean, ms)
 
 
+# fa_cache_t of include/fa.h: six pointers, five ints
+_DESC = Struct("6Q5i4x").pack
+
+
 def _describe(cache):
-    """The checked CacheDesc of a cache."""
-    if not isinstance(cache, FACache):
+    """The checked fa_cache_t of a cache (as bytes, for ctypes), its KV heads, head dimension and device number."""
+    if type(cache) is not FACache:
         raise FAError(1, "cache must be an FACache")
-    k, v, ks, vs, mean, ms = cache
-    if not isinstance(k, torch.Tensor) or k.dim() != 4 or k.dtype not in _FORMATS:
-        raise FAError(1, "the cache's k must be [num_pages, heads, page, d] of float8_e4m3fn or int8")
-    num_pages, heads, page, d = k.shape
-    device, pair = k.device, (num_pages, heads)
-    wanted = ((k, "k", k.shape, k.dtype), (v, "v", k.shape, k.dtype),
-              (ks, "k_scale", pair, torch.float32), (vs, "v_scale", pair, torch.float32))
-    if mean is not None or ms is not None:
-        wanted += ((mean, "k_mean", (num_pages, heads, d), torch.int8),
-                   (ms, "k_mean_scale", pair, torch.float32))
-    for t, name, shape, dtype in wanted:
-        if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device or t.shape != shape
-                or t.dtype != dtype or not t.is_contiguous()):
-            raise FAError(1, "the cache's %s must be a contiguous CUDA tensor %s of %s on %s"
-                          % (name, tuple(shape), dtype, device))
-    return CacheDesc(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
-                     mean.data_ptr() if mean is not None else None,
-                     ms.data_ptr() if ms is not None else None, num_pages, heads, page, d,
-                     _FORMATS[k.dtype])
+    try:
+        k, v, ks, vs, mean, ms = cache
+        shape, dtype, index = k.shape, k.dtype, k.get_device()
+        num_pages, heads, page, d = shape
+        pair = (num_pages, heads)
+        fmt = _FORMATS[dtype]
+        good = (index >= 0 and k.is_contiguous()
+                and v.get_device() == index and v.shape == shape and v.dtype is dtype and v.is_contiguous()
+                and ks.get_device() == index and ks.shape == pair and ks.dtype is torch.float32
+                and ks.is_contiguous()
+                and vs.get_device() == index and vs.shape == pair and vs.dtype is torch.float32
+                and vs.is_contiguous())
+        mp = sp = 0
+        if good and (mean is not None or ms is not None):
+            good = (mean.get_device() == index and mean.shape == (num_pages, heads, d)
+                    and mean.dtype is torch.int8 and mean.is_contiguous()
+                    and ms.get_device() == index and ms.shape == pair and ms.dtype is torch.float32
+                    and ms.is_contiguous())
+            mp, sp = mean.data_ptr(), ms.data_ptr()
+    except (AttributeError, KeyError, TypeError, ValueError):
+        good = False
+    if not good:
+        raise FAError(1, "an FACache holds contiguous CUDA tensors of one device: k, v [num_pages, heads, page, d] "
+                      "of float8_e4m3fn or int8, k_scale, v_scale [num_pages, heads] of float32 and, both or "
+                      "neither, k_mean [num_pages, heads, d] of int8, k_mean_scale like k_scale")
+    return (_DESC(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), mp, sp, num_pages, heads, page, d, fmt),
+            heads, d, index)
 
 
-def _check_batch(device, page_table, seq_lens):
-    for t, name, dim in ((page_table, "page_table", 2), (seq_lens, "seq_lens", 1)):
-        if (not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.int32
-                or t.dim() != dim or (t.numel() and t.stride(-1) != 1)):
-            raise FAError(1, "%s must be a %d-dimensional int32 tensor on %s, its last dimension "
-                          "contiguous" % (name, dim, device))
-    B = seq_lens.shape[0]
-    if page_table.shape[0] != B:
-        raise FAError(1, "page_table and seq_lens must have one row for each sequence")
-    P = page_table.shape[1]
+def _check_batch(index, page_table, seq_lens):
+    """Sequences, distance of the page table's rows, its columns."""
+    try:
+        B, P = page_table.shape
+        good = (seq_lens.shape == (B,) and page_table.get_device() == index and seq_lens.get_device() == index
+                and page_table.dtype is torch.int32 and seq_lens.dtype is torch.int32
+                and (P <= 1 or page_table.stride(1) == 1) and seq_lens.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        raise FAError(1, "page_table [B, max_pages] and seq_lens [B] must be int32 tensors on the cache's device, "
+                      "their last dimension contiguous")
     return B, page_table.stride(0) if B > 1 else P, P
 
 
-def _code(t, name):
-    code = _CODES.get(t.dtype)
+def _rows(t, name, dim, index, d):
+    """Checks an input whose rows of d values are contiguous; returns its type's code, and the strides of its other
+    dimensions (those of a dimension of one do not matter)."""
+    try:
+        shape, strides = t.shape, t.stride()
+        if len(shape) != dim or shape[-1] != d or strides[-1] != 1 or t.get_device() != index:
+            if t.numel() or len(shape) != dim or t.get_device() != index:
+                raise TypeError
+        code = _CODES.get(t.dtype)
+    except (AttributeError, TypeError):
+        raise FAError(1, "%s must be a %d-dimensional tensor of rows of %d contiguous values on the cache's device"
+                      % (name, dim, d)) from None
     if code is None:
         raise FAError(2, "%s must be float16 or bfloat16, got %s" % (name, t.dtype))
-    return code
+    return code, [s if n > 1 else 0 for s, n in zip(strides, shape)][:-1]
 
 
-def _strides(t):
-    """Element strides of all dimensions but the last; those of a dimension of one do not matter."""
-    return [s if n > 1 else 0 for s, n in zip(t.stride()[:-1], t.shape[:-1])]
-
-
-def _rows(t, name, dim, device, heads, d):
-    """Checks an input whose rows of d values are contiguous; returns its type's code."""
-    if (not isinstance(t, torch.Tensor) or t.device != device or t.dim() != dim or t.shape[-1] != d
-            or (t.numel() and t.stride(-1) != 1) or (heads is not None and t.shape[1] != heads)):
-        raise FAError(1, "%s must be a %d-dimensional CUDA tensor of rows of %d contiguous values on "
-                      "%s%s" % (name, dim, d, device, " with %d heads" % heads if heads else ""))
-    return _code(t, name)
-
-
-def _output(t, name, shape, dtype, device):
-    if (not isinstance(t, torch.Tensor) or t.device != device or t.shape != shape or t.dtype != dtype
+def _output(t, name, shape, dtype, index):
+    if (not isinstance(t, torch.Tensor) or t.get_device() != index or t.shape != shape or t.dtype != dtype
             or not t.is_contiguous()):
-        raise FAError(1, "%s must be a contiguous CUDA tensor %s of %s on %s" % (name, shape, dtype, device))
+        raise FAError(1, "%s must be a contiguous tensor %s of %s on the cache's device" % (name, shape, dtype))
     return t
 
 
 class _On:
-    """The device and stream of a call; memory that is allocated inside belongs to that stream."""
+    """A call on a device that is not the current one, or on a given stream: what it allocates inside belongs to
+    that stream."""
 
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
-            raise FAError(1, "the stream must be one of %s" % device)
-        self.stream = stream
-        self.within = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
-        self.device = device
+    def __init__(self, index, stream):
+        if stream is not None and stream.device.index != index:
+            raise FAError(1, "the stream must be one of the cache's device")
+        self.within = torch.cuda.device(index) if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        self.within.__enter__()
-        if self.stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
-        return self.stream.cuda_stream
+        return self.within.__enter__()
 
     def __exit__(self, *exc):
         return self.within.__exit__(*exc)
 
 
-def _workspace(workspace, need, device):
+_HERE = nullcontext()
+
+
+def _on(index, stream):
+    """The context of a call: none where the current device and stream are meant (the usual call, and a cheap one)."""
+    return _HERE if stream is None and torch.cuda.current_device() == index else _On(index, stream)
+
+
+def _stream(index):
+    """The current stream's handle."""
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same without a Stream object, where this torch has it: 0.1 us instead of 2
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
+
+
+def _workspace(workspace, need, index):
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
-        raise FAError(1, "workspace must be a contiguous CUDA tensor on %s" % device)
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=_device(index))
+    if (not isinstance(workspace, torch.Tensor) or workspace.get_device() != index
+            or not workspace.is_contiguous()):
+        raise FAError(1, "workspace must be a contiguous tensor on the cache's device")
     return workspace
+
+
+def _device(index):
+    return torch.device("cuda", index)
 
 
 def fa_cache_write(cache, k, v, page_table, seq_lens, cu_seqlens=None, stream=None):
@@ -154,21 +183,21 @@ def fa_cache_write(cache, k, v, page_table, seq_lens, cu_seqlens=None, stream=No
     rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 go to sequence b from position seq_lens[b] on; without
     cu_seqlens every sequence gets T / B.  The caller then adds the counts to seq_lens.  A partly filled
     page keeps its scale or takes the larger one of its new tokens; see include/fa.h."""
-    desc = _describe(cache)
-    device = cache.k.device
-    B, stride, P = _check_batch(device, page_table, seq_lens)
-    code = _rows(k, "k", 3, device, desc.heads, desc.d)
-    if _rows(v, "v", 3, device, desc.heads, desc.d) != code or v.shape != k.shape:
-        raise FAError(1, "k and v must share shape and dtype")
-    if cu_seqlens is not None and (not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.device != device
-                                   or cu_seqlens.dtype != torch.int32 or cu_seqlens.shape != (B + 1,)
-                                   or not cu_seqlens.is_contiguous()):
-        raise FAError(1, "cu_seqlens must be a contiguous int32 tensor of B + 1 on %s" % device)
-    with _On(device, stream) as on:
-        st = fa_cache_write_raw(byref(desc), k.data_ptr(), v.data_ptr(), *_strides(k), *_strides(v),
-                                cu_seqlens.data_ptr() if cu_seqlens is not None else None,
-                                seq_lens.data_ptr(), page_table.data_ptr(), stride, P, B, k.shape[0],
-                                code, on)
+    desc, heads, d, index = _describe(cache)
+    B, stride, P = _check_batch(index, page_table, seq_lens)
+    code, k_strides = _rows(k, "k", 3, index, d)
+    v_code, v_strides = _rows(v, "v", 3, index, d)
+    shape = k.shape
+    if v_code != code or v.shape != shape or shape[1] != heads:
+        raise FAError(1, "k and v must be [T, heads, d] of one dtype")
+    cu = None
+    if cu_seqlens is not None:
+        _output(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, index)
+        cu = cu_seqlens.data_ptr()
+    with _on(index, stream):
+        st = fa_cache_write_raw(desc, k.data_ptr(), v.data_ptr(), *k_strides, *v_strides, cu,
+                                seq_lens.data_ptr(), page_table.data_ptr(), stride, P, B, shape[0], code,
+                                _stream(index))
     if st != 0:
         raise FAError(st, "fa_cache_write")
 
@@ -176,23 +205,23 @@ def fa_cache_write(cache, k, v, page_table, seq_lens, cu_seqlens=None, stream=No
 def fa_cache_read(cache, page_table, seq_lens, N, dtype=torch.bfloat16, k=None, v=None, stream=None):
     """The first N positions of every sequence as 16-bit k, v [B, heads, N, d], zeros behind seq_lens[b].
     k, v: optional preallocated outputs (their dtype counts then).  Returns (k, v)."""
-    desc = _describe(cache)
-    device = cache.k.device
-    B, stride, P = _check_batch(device, page_table, seq_lens)
-    if isinstance(k, torch.Tensor):
-        dtype = k.dtype
-    elif isinstance(v, torch.Tensor):
-        dtype = v.dtype
+    desc, heads, d, index = _describe(cache)
+    B, stride, P = _check_batch(index, page_table, seq_lens)
+    given = k if k is not None else v
+    if isinstance(given, torch.Tensor):
+        dtype = given.dtype
     if dtype not in _CODES:
         raise FAError(2, "dtype must be float16 or bfloat16, got %s" % dtype)
     if N < 0:
         raise FAError(1, "N must not be negative")
-    shape = (B, desc.heads, N, desc.d)
-    with _On(device, stream) as on:
-        k, v = (torch.empty(shape, dtype=dtype, device=device) if t is None
-                else _output(t, name, shape, dtype, device) for t, name in ((k, "k"), (v, "v")))
-        st = fa_cache_read_raw(byref(desc), k.data_ptr(), v.data_ptr(), seq_lens.data_ptr(),
-                               page_table.data_ptr(), stride, P, B, N, _CODES[dtype], on)
+    shape = (B, heads, N, d)
+    with _on(index, stream):
+        k = (torch.empty(shape, dtype=dtype, device=_device(index)) if k is None
+             else _output(k, "k", shape, dtype, index))
+        v = (torch.empty(shape, dtype=dtype, device=_device(index)) if v is None
+             else _output(v, "v", shape, dtype, index))
+        st = fa_cache_read_raw(desc, k.data_ptr(), v.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), stride,
+                               P, B, N, _CODES[dtype], _stream(index))
     if st != 0:
         raise FAError(st, "fa_cache_read")
     return k, v
@@ -205,37 +234,34 @@ def fa_decode_cache(q, cache, page_table, seq_lens, pages=None, o=None, lse=None
     puts the queries at the end of the sequence.  pages: int32 [B, heads, Nq, slots], the pages that each
     query and KV head reads (``fa_cache_select``), or None for all.  scale defaults to 1/sqrt(d).
     Returns (o, lse); a row without keys has o = 0, lse = -inf."""
-    desc = _describe(cache)
-    device = cache.k.device
-    B, stride, P = _check_batch(device, page_table, seq_lens)
-    d = desc.d
-    code = _rows(q, "q", 4, device, None, d)
-    Hq, Nq = q.shape[1], q.shape[2]
-    if q.shape[0] != B or Hq % desc.heads:
+    desc, heads, d, index = _describe(cache)
+    B, stride, P = _check_batch(index, page_table, seq_lens)
+    code, strides = _rows(q, "q", 4, index, d)
+    shape = q.shape
+    _, Hq, Nq, _ = shape
+    if shape[0] != B or Hq % heads:
         raise FAError(1, "q must be [B, Hq, Nq, d] with Hq a multiple of the cache's heads")
-    slots = 0
+    slots, listed = 0, None
     if pages is not None:
         slots = pages.shape[-1] if isinstance(pages, torch.Tensor) and pages.dim() else 0
-        _output(pages, "pages", (B, desc.heads, Nq, slots), torch.int32, device)
+        listed = _output(pages, "pages", (B, heads, Nq, slots), torch.int32, index).data_ptr()
     if scale is None:
         scale = float(d) ** -0.5
-    need = fa_decode_cache_workspace_size(B, Hq, desc.heads, Nq, d)
-    with _On(device, stream) as on:
+    need = fa_decode_cache_workspace_size(B, Hq, heads, Nq, d)
+    with _on(index, stream):
         if o is None:
-            o = torch.empty((B, Hq, Nq, d), dtype=q.dtype, device=device)
+            o = torch.empty(shape, dtype=q.dtype, device=_device(index))
         else:
-            _output(o, "o", (B, Hq, Nq, d), q.dtype, device)
+            _output(o, "o", shape, q.dtype, index)
         if lse is not None:
-            _output(lse, "lse", (B, Hq, Nq), torch.float32, device)
+            _output(lse, "lse", shape[:3], torch.float32, index)
         elif return_lse:
-            lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device)
-        workspace = _workspace(workspace, need, device)
-        st = fa_decode_cache_raw(byref(desc), q.data_ptr(), *_strides(q), o.data_ptr(),
+            lse = torch.empty(shape[:3], dtype=torch.float32, device=_device(index))
+        workspace = _workspace(workspace, need, index)
+        st = fa_decode_cache_raw(desc, q.data_ptr(), *strides, o.data_ptr(),
                                  lse.data_ptr() if lse is not None else None, seq_lens.data_ptr(),
-                                 page_table.data_ptr(), stride, P,
-                                 pages.data_ptr() if pages is not None else None, slots,
-                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                 B, Hq, Nq, float(scale), int(bool(causal)), code, on)
+                                 page_table.data_ptr(), stride, P, listed, slots, workspace.data_ptr(),
+                                 workspace.nbytes, B, Hq, Nq, scale, 1 if causal else 0, code, _stream(index))
     if st != 0:
         raise FAError(st, "fa_decode_cache")
     return o, lse
@@ -246,28 +272,25 @@ def fa_cache_select(q, cache, page_table, seq_lens, slots, keep_first=1, keep_la
     """The pages [B, heads, Nq, slots] (int32, ascending, then -1) that q's rows read: the first
     keep_first, the last keep_last and, by the mean keys' scores, the best of the others; all of them
     where there are no more than slots.  Arguments as for fa_decode_cache."""
-    desc = _describe(cache)
-    device = cache.k.device
-    B, stride, P = _check_batch(device, page_table, seq_lens)
-    code = _rows(q, "q", 4, device, None, desc.d)
-    Hq, Nq = q.shape[1], q.shape[2]
-    if q.shape[0] != B or Hq % desc.heads:
+    desc, heads, d, index = _describe(cache)
+    B, stride, P = _check_batch(index, page_table, seq_lens)
+    code, strides = _rows(q, "q", 4, index, d)
+    _, Hq, Nq, _ = q.shape
+    if q.shape[0] != B or Hq % heads:
         raise FAError(1, "q must be [B, Hq, Nq, d] with Hq a multiple of the cache's heads")
     if slots < 1:
         raise FAError(1, "slots must be at least 1")
-    need = fa_cache_select_workspace_size(B, desc.heads, Nq, P)
-    shape = (B, desc.heads, Nq, slots)
-    with _On(device, stream) as on:
+    need = fa_cache_select_workspace_size(B, heads, Nq, P)
+    shape = (B, heads, Nq, slots)
+    with _on(index, stream):
         if pages is None:
-            pages = torch.empty(shape, dtype=torch.int32, device=device)
+            pages = torch.empty(shape, dtype=torch.int32, device=_device(index))
         else:
-            _output(pages, "pages", shape, torch.int32, device)
-        workspace = _workspace(workspace, need, device)
-        st = fa_cache_select_raw(byref(desc), q.data_ptr(), *_strides(q), seq_lens.data_ptr(),
-                                 page_table.data_ptr(), stride, P, pages.data_ptr(), slots, keep_first,
-                                 keep_last, workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), B, Hq, Nq,
-                                 int(bool(causal)), code, on)
+            _output(pages, "pages", shape, torch.int32, index)
+        workspace = _workspace(workspace, need, index)
+        st = fa_cache_select_raw(desc, q.data_ptr(), *strides, seq_lens.data_ptr(), page_table.data_ptr(), stride, P,
+                                 pages.data_ptr(), slots, keep_first, keep_last, workspace.data_ptr(),
+                                 workspace.nbytes, B, Hq, Nq, 1 if causal else 0, code, _stream(index))
     if st != 0:
         raise FAError(st, "fa_cache_select")
     return pages

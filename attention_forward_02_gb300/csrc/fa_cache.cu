@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+
 #include <cstdint>
 #include <functional>
 #include <mutex>
@@ -72,6 +73,7 @@ struct Shape {
 };
 Shape shape_of(int R)
 {
+    
     if (R <= 8)
         return {1, 1, 8};
     const int row_warps = R <= 16 ? 1 : R <= 32 ? 2 : 4;

@@ -70,8 +70,8 @@ struct DecCfg {
     static constexpr int MERGE_OFF = META_OFF + STAGES * 80;
     static constexpr int ML_OFF = MERGE_OFF + kDecWarps * ROWS * OROW * 4;
     static constexpr int BAR_OFF = ML_OFF + kDecWarps * ROWS * 8;
-    static constexpr int FLAG_OFF = BAR_OFF + 16 * STAGES + 8;  // full, empty, merge
-    static constexpr int SMEM = FLAG_OFF + 16 + 1024;  // and room to align the ring
+    static constexpr int FLAG_OFF = BAR_OFF + 16 * STAGES + 16;  // full, empty, merge
+    static constexpr int SMEM = FLAG_OFF + 16 + 16 * kDecWarps + 1024;  // and room to align the ring
     static_assert(STAGES * STAGE % 16 == 0 && STAGE % 1024 == 0, "alignment of the ring");
 };
 
@@ -170,7 +170,7 @@ __device__ __forceinline__ float ex2(float x)
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                  "{%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -428,10 +428,11 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
     const int wk = warp % key_warps, wr = warp / key_warps;
     uint32_t qb[NT][KW][2];  // Q^T operand: query g of each 8, its d in the order of the thread's K words
     float qf[NT][2];         // per query 2 c, 2 c + 1: scale to log2 units
-    int lim[NT][2];          // ... keys that it sees
+    uint32_t behind[NT] = {};  // ... keys that it sees beyond `least`, a byte each
     float m[NT][2], l[NT][2], acc[D / 16][NT][4];
-    int least = 0, most = 0;  // keys that all rows see, that any row sees
-    int b_seg = 0, i_seg = 0, head = 0, group = 0;  // the segment's
+    int least = 0, most = 0;  // keys that all rows see (negative: the first ones see none), that any row sees
+    auto limit = [&](int nt, int u) -> int { return least + static_cast<int>((behind[nt] >> (8 * u)) & 255u); };
+    int4 *segment = reinterpret_cast<int4 *>(smem + F::FLAG_OFF + 16) + warp;  // b, i, head, group
     uint32_t merges = 0;
     // a barrier of the computing warps whose wait is bounded
     auto meet = [&]() -> bool {
@@ -448,13 +449,12 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
         const int flags = info->flags;
 
         if (flags & kFirst) {
-            b_seg = info->b;
-            i_seg = info->i;
-            head = info->head;
-            group = info->group;
+            const int b_seg = info->b, i_seg = info->i, head = info->head, group = info->group;
+            if (lane == 0)
+                *segment = make_int4(b_seg, i_seg, head, group);
             const int n = w.batch.length(b_seg, w.cache.log2_page);
-            least = w.pages ? context(w.q, n, i_seg) : context(w.q, n, 0);
-            most = w.pages ? least : n;
+            most = w.pages ? context(w.q, n, i_seg) : n;
+            least = w.pages || !w.q.causal ? most : n - w.q.Nq + 1;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int row = group * rows_block + wr * F::ROWS + nt * 8 + g;
@@ -488,11 +488,12 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
                         const float2 y = DTypeTraits<T>::unpack(qb[nt][s][u]);
                         qb[nt][s][u] = DTypeTraits<__half>::pack(y.x * by, y.y * by);
                     }
-                const int limit = context(w.q, n, qi);
+                behind[nt] = 0;
+                const int extra = w.pages || !w.q.causal ? 0 : qi;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     qf[nt][u] = pow2f(__shfl_sync(0xffffffffu, e, 8 * c + 4 * u)) * w.scale_log2;
-                    lim[nt][u] = __shfl_sync(0xffffffffu, limit, 8 * c + 4 * u);
+                    behind[nt] |= __shfl_sync(0xffffffffu, extra, 8 * c + 4 * u) << (8 * u);
                     m[nt][u] = -INFINITY;
                     l[nt][u] = 0.f;
                 }
@@ -516,43 +517,21 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
                 continue;
             }
             const float k_scale = info->k_scale[sub], v_scale = info->v_scale[sub];
-            uint32_t kw[2][KW], vw[4][VW];
-            {
-                const uint32_t k0 = sbase + F::RING_OFF + slot * F::STAGE + sub * kTile * F::W0, v0 = k0 + F::HALF;
+            const uint32_t k0 = sbase + F::RING_OFF + slot * F::STAGE + sub * kTile * F::W0, v0 = k0 + F::HALF;
+            const uint32_t k1 = sbase + F::RING_OFF + slot * F::STAGE + kStep * F::W0 + sub * kTile * F::W1;  // d = 96
+            uint32_t kw[2][KW];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    if constexpr (D == 128) {
-                        load_words<4>(&kw[r][0], k0 + k_offset<128>(g, c, 0) + r * 1024);
-                        load_words<4>(&kw[r][4], k0 + k_offset<128>(g, c, 1) + r * 1024);
-                    } else if constexpr (D == 32) {
-                        load_words<2>(&kw[r][0], k0 + k_offset<32>(g, c, 0) + r * 256);
-                    } else {
-                        load_words<4>(&kw[r][0], k0 + k_offset<64>(g, c, 0) + r * 512);
-                    }
+            for (int r = 0; r < 2; ++r) {
+                if constexpr (D == 128) {
+                    load_words<4>(&kw[r][0], k0 + k_offset<128>(g, c, 0) + r * 1024);
+                    load_words<4>(&kw[r][4], k0 + k_offset<128>(g, c, 1) + r * 1024);
+                } else if constexpr (D == 32) {
+                    load_words<2>(&kw[r][0], k0 + k_offset<32>(g, c, 0) + r * 256);
+                } else {
+                    load_words<4>(&kw[r][0], k0 + k_offset<64>(g, c, 0) + r * 512);
                 }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    if constexpr (D == 128)
-                        load_words<4>(&vw[r][0], v0 + v_offset<128>(g, c, r & 1) + (r >> 1) * 1024);
-                    else if constexpr (D == 32)
-                        load_words<1>(&vw[r][0], v0 + v_offset<32>(g, c, r & 1) + (r >> 1) * 256);
-                    else
-                        load_words<2>(&vw[r][0], v0 + v_offset<64>(g, c, r & 1) + (r >> 1) * 512);
-                }
-                if constexpr (D == 96) {
-                    const uint32_t k1 = sbase + F::RING_OFF + slot * F::STAGE + kStep * F::W0 + sub * kTile * 32;
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        load_words<2>(&kw[r][4], k1 + k_offset<32>(g, c, 0) + r * 256);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        load_words<1>(&vw[r][2], k1 + F::HALF + v_offset<32>(g, c, r & 1) + (r >> 1) * 256);
-                }
-            }
-            if (last_sub) {  // the stage's codes are in registers
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(empty(slot));
+                if constexpr (D == 96)
+                    load_words<2>(&kw[r][4], k1 + k_offset<32>(g, c, 0) + r * 256);
             }
             // ---- S^T = K Q^T ----
             float s[NT][4];
@@ -570,25 +549,97 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
                 for (int nt = 0; nt < NT; ++nt)
                     mma_f16(s[nt], a0, a1, a2, a3, qb[nt][x][0], qb[nt][x][1]);
             }
-            // ---- log2 units, masks; does any score outgrow its reference? ----
-            const float ev = static_cast<float>(static_cast<int>(__float_as_uint(v_scale) >> 23) - 127);
-            bool grown = false;
+            // ---- exponents of P v_scale, masks; does any outgrow its reference? ----
+            const int v_exp = static_cast<int>(__float_as_uint(v_scale) >> 23) - 127;
+            const float ev = static_cast<float>(v_exp);
+            float f[NT][2], e[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float f0 = k_scale * qf[nt][0], f1 = k_scale * qf[nt][1];
-                s[nt][0] *= f0;
-                s[nt][1] *= f1;
-                s[nt][2] *= f0;
-                s[nt][3] *= f1;
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    f[nt][u & 1] = k_scale * qf[nt][u & 1];
+                    e[nt][u] = fmaf(s[nt][u], f[nt][u & 1], ev - m[nt][u & 1]);  // +inf at first
+                }
             const bool masked = key0 + kTile > least;
             if (masked) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        if (key0 + g + 8 * (u >> 1) >= lim[nt][u & 1])
-                            s[nt][u] = -INFINITY;
+                        if (key0 + g + 8 * (u >> 1) >= limit(nt, u & 1))
+                            e[nt][u] = -INFINITY;
+            }
+            bool grown = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    grown |= !(e[nt][u] <= 8.f);
+            if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float y[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            y[h] = fmaf(s[nt][u + 2 * h], f[nt][u], ev);
+                            if (masked && key0 + g + 8 * h >= limit(nt, u))
+                                y[h] = -INFINITY;
+                        }
+                        float top = fmaxf(y[0], y[1]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        const float next = fmaxf(m[nt][u], top);
+                        const float alpha = next == m[nt][u] ? 1.f : ex2(m[nt][u] - next);
+                        const float ref = next == -INFINITY ? 0.f : next;
+                        m[nt][u] = next;
+                        l[nt][u] *= alpha;
+                        e[nt][u] = y[0] - ref;
+                        e[nt][u + 2] = y[1] - ref;
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            acc[j][nt][u] *= alpha;
+                            acc[j][nt][u + 2] *= alpha;
+                        }
+                    }
+            }
+            // ---- P, and O^T += V^T P^T ----
+            uint32_t pb[NT][2];
+            const float inv = pow2f(-v_exp), mantissa = v_scale * inv;  // 1 for a power of two
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    e[nt][u] = ex2(e[nt][u]);
+                    l[nt][u & 1] = fmaf(e[nt][u], inv, l[nt][u & 1]);
+                }
+                if (mantissa != 1.f)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        e[nt][u] *= mantissa;
+                pb[nt][0] = transpose8(DTypeTraits<__half>::pack(e[nt][0], e[nt][1]));
+                pb[nt][1] = transpose8(DTypeTraits<__half>::pack(e[nt][2], e[nt][3]));
+            }
+            uint32_t vw[4][VW];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if constexpr (D == 128)
+                    load_words<4>(&vw[r][0], v0 + v_offset<128>(g, c, r & 1) + (r >> 1) * 1024);
+                else if constexpr (D == 32)
+                    load_words<1>(&vw[r][0], v0 + v_offset<32>(g, c, r & 1) + (r >> 1) * 256);
+                else
+                    load_words<2>(&vw[r][0], v0 + v_offset<64>(g, c, r & 1) + (r >> 1) * 512);
+                if constexpr (D == 96)
+                    load_words<1>(&vw[r][2], k1 + F::HALF + v_offset<32>(g, c, r & 1) + (r >> 1) * 256);
+            }
+            if (last_sub) {  // the stage's codes are in registers
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(empty(slot));
+            }
+            if (masked) {
                 // codes behind the last key are whatever the page held
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
@@ -620,7 +671,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
                                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                         for (int u = 0; u < 2; ++u)
-                                            if ((bits >> (8 * e + 7) & 1u) && key0 + key < lim[nt][u])
+                                            if ((bits >> (8 * e + 7) & 1u) && key0 + key < limit(nt, u))
                                                 acc[2 * x + (e >> 1)][nt][(e & 1) * 2 + u] = __int_as_float(0x7FC00000);
                             }
                         }
@@ -633,43 +684,6 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
                             }
                     }
                 }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    grown = grown || s[nt][u] + ev > m[nt][u & 1] + 8.f;
-            if (__any_sync(0xffffffffu, grown)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        float top = fmaxf(s[nt][u], s[nt][u + 2]) + ev;
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        const float next = fmaxf(m[nt][u], top);
-                        const float alpha = next == m[nt][u] ? 1.f : ex2(m[nt][u] - next);
-                        m[nt][u] = next;
-                        l[nt][u] *= alpha;
-#pragma unroll
-                        for (int j = 0; j < D / 16; ++j) {
-                            acc[j][nt][u] *= alpha;
-                            acc[j][nt][u + 2] *= alpha;
-                        }
-                    }
-            }
-            // ---- P, and O^T += V^T P^T ----
-            uint32_t pb[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float r0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], r1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-                const float p0 = ex2(s[nt][0] - r0), p1 = ex2(s[nt][1] - r1);
-                const float p2 = ex2(s[nt][2] - r0), p3 = ex2(s[nt][3] - r1);
-                l[nt][0] += p0 + p2;
-                l[nt][1] += p1 + p3;
-                pb[nt][0] = transpose8(DTypeTraits<__half>::pack(p0 * v_scale, p1 * v_scale));
-                pb[nt][1] = transpose8(DTypeTraits<__half>::pack(p2 * v_scale, p3 * v_scale));
             }
 #pragma unroll
             for (int x = 0; x < VW; ++x) {
@@ -716,6 +730,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
                 }
             if (!meet())
                 return;
+            const int b_seg = segment->x, i_seg = segment->y, head = segment->z, group = segment->w;
             const bool part = flags & (kHeadPart | kTailPart);
             const long long seg_row =
                 w.pages ? 0 : (static_cast<long long>(b_seg) * w.cache.heads + head) * w.R;
