@@ -5,7 +5,6 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-
 #include <cstdint>
 #include <functional>
 #include <mutex>
@@ -33,26 +32,19 @@ struct CacheState {
 };
 CacheState g_cache[kMaxDevices];
 
-template <int D, int NT>
-cudaError_t set_smem_attr()
-{
-    using namespace fa::cache;
-    const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, NT, __half, E4M3>, a, DecCfg<D, NT>::SMEM);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, NT, __half, I8>, a, DecCfg<D, NT>::SMEM);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, NT, __nv_bfloat16, E4M3>, a, DecCfg<D, NT>::SMEM);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, NT, __nv_bfloat16, I8>, a, DecCfg<D, NT>::SMEM);
-    return e;
-}
-
 template <int D>
 cudaError_t set_smem_attrs()
 {
-    const cudaError_t e = set_smem_attr<D, 1>();
-    return e == cudaSuccess ? set_smem_attr<D, 2>() : e;
+    using namespace fa::cache;
+    const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, __half, E4M3>, a, DecCfg<D>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, __half, I8>, a, DecCfg<D>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, __nv_bfloat16, E4M3>, a, DecCfg<D>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, __nv_bfloat16, I8>, a, DecCfg<D>::SMEM);
+    return e;
 }
 
 void init_cache(CacheState &st)
@@ -66,19 +58,13 @@ void init_cache(CacheState &st)
     if (st.err == cudaSuccess) st.err = set_smem_attrs<128>();
 }
 
-// How query rows of one KV head (R of them) are laid out: 8-row tiles a warp,
-// warps along the rows (the others take keys), rows a block.
-struct Shape {
-    int tiles, row_warps, rows_block;
-};
-Shape shape_of(int R)
-{
-    
-    if (R <= 8)
-        return {1, 1, 8};
-    const int row_warps = R <= 16 ? 1 : R <= 32 ? 2 : 4;
-    return {2, row_warps, 16 * row_warps};
-}
+// Warps of a block along the R query rows of a KV head (8 rows each; the others
+// take keys).  More rows than 32 go to further row groups, which read the codes
+// again.  Two or four warps that convert the same codes are faster than one that
+// multiplies them with 16 or 32 rows: 16 rows, d = 128, int8: 93 against 101 us
+// (attend_spec's sizes: 16 x 16,384 keys, 8 heads), as 12 warps an SM hide latency
+// where the registers of 16 rows leave 8.
+int row_warps_of(int R) { return R <= 8 ? 1 : R <= 16 ? 2 : 4; }
 
 // A code buffer as [num_pages * heads, page, d] bytes: boxes of `box` rows of
 // `width` columns, each row swizzled by its width.
@@ -207,6 +193,24 @@ fa_status_t check_queries(const fa_cache_t *cache, const void *q, long long sb, 
         return FA_ERR_MISALIGNED;
     *r = {u(q), static_cast<size_t>((B - 1) * sb + (Hq - 1) * sh + (Nq - 1) * sr + cache->d) * 2};
     return FA_OK;
+}
+
+// Launch of a kernel that may begin before the one ahead of it has ended (it
+// waits for that one itself).
+template <typename... P, typename... A>
+bool launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A &...args)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess;
 }
 
 fa_status_t launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
@@ -356,8 +360,8 @@ size_t fa_decode_cache_workspace_size(int B, int Hq, int Hkv, int Nq, int d)
     if (B < 0 || Hq < 0 || Hkv < 1 || Hq % Hkv != 0 || Nq < 1 || Nq > kMaxNq ||
         (d != 32 && d != 64 && d != 96 && d != 128))
         return 0;
-    const Shape shape = shape_of(Hq / Hkv * Nq);
-    return plan_bytes(B) + static_cast<size_t>(2 * fa::cache::kMaxBlocks) * shape.rows_block * (d + 2) * 4;
+    const int rows_block = fa::cache::kRows * row_warps_of(Hq / Hkv * Nq);
+    return plan_bytes(B) + static_cast<size_t>(2 * fa::cache::kMaxBlocks) * rows_block * (d + 2) * 4;
 }
 
 fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_batch_stride, long long q_head_stride,
@@ -415,12 +419,12 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
     w.slots = slots;
     w.B = B;
     w.R = qs.G * (pages ? 1 : Nq);
-    const Shape shape = shape_of(w.R);
-    w.groups = (w.R + shape.rows_block - 1) / shape.rows_block;
-    w.row_warps = shape.row_warps;
+    w.row_warps = row_warps_of(w.R);
+    const int rows_block = fa::cache::kRows * w.row_warps;
+    w.groups = (w.R + rows_block - 1) / rows_block;
     w.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     w.plan = static_cast<long long *>(workspace);
-    const size_t part_rows = static_cast<size_t>(2 * fa::cache::kMaxBlocks) * shape.rows_block;
+    const size_t part_rows = static_cast<size_t>(2 * fa::cache::kMaxBlocks) * rows_block;
     w.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan_bytes(B));
     w.part_m = w.part_o + part_rows * cache->d;
     w.part_l = w.part_m + part_rows;
@@ -436,7 +440,7 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
     const long long keys = static_cast<long long>(pages && slots < max_pages ? slots : max_pages) * cache->page;
     const long long most = static_cast<long long>(B) * (pages ? Nq : 1) * cache->heads * w.groups *
                            ((keys - 1) / fa::cache::kStep + 1);
-    const long long resident = static_cast<long long>(sms) * (shape.tiles == 1 ? 3 : 2);
+    const long long resident = static_cast<long long>(sms) * fa::cache::kBlocksPerSm;
     long long blocks = resident < fa::cache::kMaxBlocks ? resident : fa::cache::kMaxBlocks;
     if (most < blocks)
         blocks = most;
@@ -445,18 +449,24 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
             constexpr int D = decltype(dim)::value;
             using T = decltype(t);
             using C = decltype(code);
-            if (shape.tiles == 1)
-                fa::cache::fa_cache_decode_kernel<D, 1, T, C>
-                    <<<static_cast<unsigned>(blocks), fa::cache::kDecThreads, fa::cache::DecCfg<D, 1>::SMEM, cs>>>(
-                        maps, w, static_cast<T *>(o), lse);
-            else
-                fa::cache::fa_cache_decode_kernel<D, 2, T, C>
-                    <<<static_cast<unsigned>(blocks), fa::cache::kDecThreads, fa::cache::DecCfg<D, 2>::SMEM, cs>>>(
-                        maps, w, static_cast<T *>(o), lse);
-            if (cudaGetLastError() != cudaSuccess)
+            const bool first = launch_dependent(fa::cache::fa_cache_decode_kernel<D, T, C>, static_cast<unsigned>(blocks),
+                                                fa::cache::kDecThreads, fa::cache::DecCfg<D>::SMEM, cs, maps, w,
+                                                static_cast<T *>(o), lse);
+            if (!first)
                 return FA_ERR_CUDA;
-            fa::cache::fa_cache_combine_kernel<D, T><<<static_cast<unsigned>(rows), fa::cache::kCombineThreads, 0, cs>>>(
-                w, static_cast<T *>(o), lse, shape.rows_block);
+            // parts of a segment, on average: a warp takes a few of them alone
+            constexpr int kWarps = fa::cache::kCombineThreads / 32;
+            const long long segments = static_cast<long long>(B) * (pages ? Nq : 1) * cache->heads * w.groups;
+            const bool second =
+                blocks <= segments * fa::cache::kCombineEach
+                    ? launch_dependent(fa::cache::fa_cache_combine_kernel<D, T, 1>,
+                                       static_cast<unsigned>((rows + kWarps - 1) / kWarps), fa::cache::kCombineThreads, 0,
+                                       cs, w, static_cast<T *>(o), lse, rows_block, rows)
+                    : launch_dependent(fa::cache::fa_cache_combine_kernel<D, T, kWarps>, static_cast<unsigned>(rows),
+                                       fa::cache::kCombineThreads, 0, cs, w, static_cast<T *>(o), lse,
+                                       rows_block, rows);
+            if (!second)
+                return FA_ERR_CUDA;
             return launched();
         });
     });
@@ -513,18 +523,18 @@ fa_status_t fa_cache_select(const fa_cache_t *cache, const void *q, long long q_
     const dim3 grid((max_pages + fa::cache::kScorePages - 1) / fa::cache::kScorePages, cache->heads, B);
     s = by_dim(cache->d, [&](auto dim) {
         constexpr int D = decltype(dim)::value;
-        if (dtype == FA_FP16)
-            fa::cache::fa_cache_score_kernel<D, __half>
-                <<<grid, fa::cache::kScoreThreads, 0, cs>>>(c, batch, qs, scores, slots);
-        else
-            fa::cache::fa_cache_score_kernel<D, __nv_bfloat16>
-                <<<grid, fa::cache::kScoreThreads, 0, cs>>>(c, batch, qs, scores, slots);
-        return launched();
+        const bool ok = dtype == FA_FP16
+                            ? launch_dependent(fa::cache::fa_cache_score_kernel<D, __half>, grid,
+                                               fa::cache::kScoreThreads, 0, cs, c, batch, qs, scores, slots)
+                            : launch_dependent(fa::cache::fa_cache_score_kernel<D, __nv_bfloat16>, grid,
+                                               fa::cache::kScoreThreads, 0, cs, c, batch, qs, scores, slots);
+        return ok ? FA_OK : FA_ERR_CUDA;
     });
     if (s != FA_OK)
         return s;
-    fa::cache::fa_cache_pick_kernel<<<static_cast<unsigned>(segments), fa::cache::kPickThreads, 0, cs>>>(
-        c, batch, qs, scores, pages, slots, keep_first, keep_last);
+    if (!launch_dependent(fa::cache::fa_cache_pick_kernel, static_cast<unsigned>(segments), fa::cache::kPickThreads, 0, cs,
+                          c, batch, qs, scores, pages, slots, keep_first, keep_last))
+        return FA_ERR_CUDA;
     return launched();
 }
 

@@ -50,20 +50,22 @@ constexpr int kTile = 16;         // keys of one product
 constexpr int kStep = 64;         // keys of a stage: a unit of work
 constexpr int kLog2Step = 6;
 constexpr int kSubs = kStep / kTile;
+constexpr int kRows = 8;          // query rows a warp
+constexpr int kBlocksPerSm = 3;
 constexpr int kMaxBlocks = 640;   // of the persistent grid
 constexpr int kCombineThreads = 128;
+constexpr int kCombineEach = 8;   // parts of a warp under way at once
 
 // A code row of d bytes is held in one or two column parts, each with the TMA
 // swizzle of its width: 32, 64, 128, or 64 + 32.
-template <int D, int NT>
+template <int D>
 struct DecCfg {
     static constexpr int PARTS = D == 96 ? 2 : 1;
     static constexpr int W0 = D == 96 ? 64 : D, W1 = D - W0;  // widths
     static constexpr int HALF = kStep * D;                    // K or V of a stage, bytes
     static constexpr int STAGE = 2 * HALF;
-    static constexpr int RING = NT == 1 ? 49152 : 65536;      // bytes; 3 blocks an SM, or 2
-    static constexpr int STAGES = RING / STAGE < 8 ? RING / STAGE : 8;  // 3 or 4 at d = 128
-    static constexpr int ROWS = 8 * NT;                       // query rows a warp
+    static constexpr int STAGES = 49152 / STAGE < 8 ? 49152 / STAGE : 8;  // 3 at d = 128; 3 blocks an SM
+    static constexpr int ROWS = kRows;                        // query rows a warp
     static constexpr int OROW = D + 4;                        // floats of a row of the merge
     static constexpr int RING_OFF = 0;
     static constexpr int META_OFF = STAGES * STAGE;
@@ -207,12 +209,12 @@ struct Maps {
     CUtensorMap k[2], v[2];  // of the column parts
 };
 
-template <int D, int NT, typename T, typename C>
-__global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
+template <int D, typename T, typename C>
+__global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
     fa_cache_decode_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Work w, T *__restrict__ out,
                            float *__restrict__ lse)
 {
-    using F = DecCfg<D, NT>;
+    using F = DecCfg<D>;
     constexpr int S = F::STAGES;
     constexpr int KW = D / 16;  // words of a key's codes a thread holds = steps of the first product
     constexpr int VW = D / 32;  // words of a key's V a thread holds
@@ -239,6 +241,8 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
         *abort_flag = 0;
         fence_mbar_init();
     }
+    wait_ahead();
+    let_next();
 
     // ---- this block's run of units ----
     int all;      // units of this block
@@ -426,12 +430,12 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
     const int g = lane >> 2, c = lane & 3;
     const int key_warps = kDecWarps / w.row_warps;
     const int wk = warp % key_warps, wr = warp / key_warps;
-    uint32_t qb[NT][KW][2];  // Q^T operand: query g of each 8, its d in the order of the thread's K words
-    float qf[NT][2];         // per query 2 c, 2 c + 1: scale to log2 units
-    uint32_t behind[NT] = {};  // ... keys that it sees beyond `least`, a byte each
-    float m[NT][2], l[NT][2], acc[D / 16][NT][4];
+    uint32_t qb[KW][2];   // Q^T operand: query row g, its d in the order of the thread's K words
+    float qf[2];          // per query row 2 c, 2 c + 1: scale to log2 units
+    uint32_t behind = 0;  // ... keys that it sees beyond `least`, a byte each
+    float m[2], l[2], acc[D / 16][4];
     int least = 0, most = 0;  // keys that all rows see (negative: the first ones see none), that any row sees
-    auto limit = [&](int nt, int u) -> int { return least + static_cast<int>((behind[nt] >> (8 * u)) & 255u); };
+    auto limit = [&](int u) -> int { return least + static_cast<int>((behind >> (8 * u)) & 255u); };
     int4 *segment = reinterpret_cast<int4 *>(smem + F::FLAG_OFF + 16) + warp;  // b, i, head, group
     uint32_t merges = 0;
     // a barrier of the computing warps whose wait is bounded
@@ -455,54 +459,51 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
             const int n = w.batch.length(b_seg, w.cache.log2_page);
             most = w.pages ? context(w.q, n, i_seg) : n;
             least = w.pages || !w.q.causal ? most : n - w.q.Nq + 1;
+            const int row = group * rows_block + wr * F::ROWS + g;
+            const int hq = w.pages ? row : row / w.q.Nq, qi = w.pages ? i_seg : row % w.q.Nq;
+            const T *src = static_cast<const T *>(w.q.q) + b_seg * w.q.batch_stride +
+                           static_cast<long long>(head * w.q.G + hq) * w.q.head_stride + qi * w.q.row_stride;
+            float top = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int row = group * rows_block + wr * F::ROWS + nt * 8 + g;
-                const int hq = w.pages ? row : row / w.q.Nq, qi = w.pages ? i_seg : row % w.q.Nq;
-                const T *src = static_cast<const T *>(w.q.q) + b_seg * w.q.batch_stride +
-                               static_cast<long long>(head * w.q.G + hq) * w.q.head_stride + qi * w.q.row_stride;
-                float top = 0.f;
+            for (int s = 0; s < KW; ++s) {
+                const int d = k_column<D>(c, s);
+                uint2 x = make_uint2(0, 0);
+                if (row < w.R)
+                    x = *reinterpret_cast<const uint2 *>(src + d);
+                qb[s][0] = x.x;
+                qb[s][1] = x.y;
+                const float2 y = DTypeTraits<T>::unpack(x.x), z = DTypeTraits<T>::unpack(x.y);
+                const float f[4] = {fabsf(y.x), fabsf(y.y), fabsf(z.x), fabsf(z.y)};
 #pragma unroll
-                for (int s = 0; s < KW; ++s) {
-                    const int d = k_column<D>(c, s);
-                    uint2 x = make_uint2(0, 0);
-                    if (row < w.R)
-                        x = *reinterpret_cast<const uint2 *>(src + d);
-                    qb[nt][s][0] = x.x;
-                    qb[nt][s][1] = x.y;
-                    const float2 y = DTypeTraits<T>::unpack(x.x), z = DTypeTraits<T>::unpack(x.y);
-                    const float f[4] = {fabsf(y.x), fabsf(y.y), fabsf(z.x), fabsf(z.y)};
+                for (int u = 0; u < 4; ++u)
+                    if (f[u] <= 3.402823466e38f)
+                        top = fmaxf(top, f[u]);
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = top > 0.f ? max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -100) : 0;
+            const float by = pow2f(-e);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (f[u] <= 3.402823466e38f)
-                            top = fmaxf(top, f[u]);
-                }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int e = top > 0.f ? max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -100) : 0;
-                const float by = pow2f(-e);
-#pragma unroll
-                for (int s = 0; s < KW; ++s)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float2 y = DTypeTraits<T>::unpack(qb[nt][s][u]);
-                        qb[nt][s][u] = DTypeTraits<__half>::pack(y.x * by, y.y * by);
-                    }
-                behind[nt] = 0;
-                const int extra = w.pages || !w.q.causal ? 0 : qi;
+            for (int s = 0; s < KW; ++s)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    qf[nt][u] = pow2f(__shfl_sync(0xffffffffu, e, 8 * c + 4 * u)) * w.scale_log2;
-                    behind[nt] |= __shfl_sync(0xffffffffu, extra, 8 * c + 4 * u) << (8 * u);
-                    m[nt][u] = -INFINITY;
-                    l[nt][u] = 0.f;
+                    const float2 y = DTypeTraits<T>::unpack(qb[s][u]);
+                    qb[s][u] = DTypeTraits<__half>::pack(y.x * by, y.y * by);
                 }
+            behind = 0;
+            const int extra = w.pages || !w.q.causal ? 0 : qi;
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        acc[j][nt][u] = 0.f;
+            for (int u = 0; u < 2; ++u) {
+                qf[u] = pow2f(__shfl_sync(0xffffffffu, e, 8 * c + 4 * u)) * w.scale_log2;
+                behind |= __shfl_sync(0xffffffffu, extra, 8 * c + 4 * u) << (8 * u);
+                m[u] = -INFINITY;
+                l[u] = 0.f;
             }
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    acc[j][u] = 0.f;
         }
 
         for (int sub = wk; sub < kSubs; sub += key_warps) {
@@ -534,94 +535,79 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
                     load_words<2>(&kw[r][4], k1 + k_offset<32>(g, c, 0) + r * 256);
             }
             // ---- S^T = K Q^T ----
-            float s[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            float s[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                    s[nt][u] = 0.f;
+                    s[u] = 0.f;
 #pragma unroll
             for (int x = 0; x < KW; ++x) {
                 uint32_t a0, a1, a2, a3;
                 C::halves(kw[0][x], a0, a2);
                 C::halves(kw[1][x], a1, a3);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_f16(s[nt], a0, a1, a2, a3, qb[nt][x][0], qb[nt][x][1]);
+                    mma_f16(s, a0, a1, a2, a3, qb[x][0], qb[x][1]);
             }
             // ---- exponents of P v_scale, masks; does any outgrow its reference? ----
             const int v_exp = static_cast<int>(__float_as_uint(v_scale) >> 23) - 127;
             const float ev = static_cast<float>(v_exp);
-            float f[NT][2], e[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            float f[2], e[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    f[nt][u & 1] = k_scale * qf[nt][u & 1];
-                    e[nt][u] = fmaf(s[nt][u], f[nt][u & 1], ev - m[nt][u & 1]);  // +inf at first
+                    f[u & 1] = k_scale * qf[u & 1];
+                    e[u] = fmaf(s[u], f[u & 1], ev - m[u & 1]);  // +inf at first
                 }
             const bool masked = key0 + kTile > least;
             if (masked) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        if (key0 + g + 8 * (u >> 1) >= limit(nt, u & 1))
-                            e[nt][u] = -INFINITY;
+                        if (key0 + g + 8 * (u >> 1) >= limit(u & 1))
+                            e[u] = -INFINITY;
             }
             bool grown = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
                 for (int u = 0; u < 4; ++u)
-                    grown |= !(e[nt][u] <= 8.f);
+                    grown |= !(e[u] <= 8.f);
             if (__any_sync(0xffffffffu, grown)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         float y[2];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            y[h] = fmaf(s[nt][u + 2 * h], f[nt][u], ev);
-                            if (masked && key0 + g + 8 * h >= limit(nt, u))
+                            y[h] = fmaf(s[u + 2 * h], f[u], ev);
+                            if (masked && key0 + g + 8 * h >= limit(u))
                                 y[h] = -INFINITY;
                         }
                         float top = fmaxf(y[0], y[1]);
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        const float next = fmaxf(m[nt][u], top);
-                        const float alpha = next == m[nt][u] ? 1.f : ex2(m[nt][u] - next);
+                        const float next = fmaxf(m[u], top);
+                        const float alpha = next == m[u] ? 1.f : ex2(m[u] - next);
                         const float ref = next == -INFINITY ? 0.f : next;
-                        m[nt][u] = next;
-                        l[nt][u] *= alpha;
-                        e[nt][u] = y[0] - ref;
-                        e[nt][u + 2] = y[1] - ref;
+                        m[u] = next;
+                        l[u] *= alpha;
+                        e[u] = y[0] - ref;
+                        e[u + 2] = y[1] - ref;
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j) {
-                            acc[j][nt][u] *= alpha;
-                            acc[j][nt][u + 2] *= alpha;
+                            acc[j][u] *= alpha;
+                            acc[j][u + 2] *= alpha;
                         }
                     }
             }
             // ---- P, and O^T += V^T P^T ----
-            uint32_t pb[NT][2];
+            uint32_t pb[2];
             const float inv = pow2f(-v_exp), mantissa = v_scale * inv;  // 1 for a power of two
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    e[nt][u] = ex2(e[nt][u]);
-                    l[nt][u & 1] = fmaf(e[nt][u], inv, l[nt][u & 1]);
-                }
-                if (mantissa != 1.f)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        e[nt][u] *= mantissa;
-                pb[nt][0] = transpose8(DTypeTraits<__half>::pack(e[nt][0], e[nt][1]));
-                pb[nt][1] = transpose8(DTypeTraits<__half>::pack(e[nt][2], e[nt][3]));
+            for (int u = 0; u < 4; ++u) {
+                e[u] = ex2(e[u]);
+                l[u & 1] = fmaf(e[u], inv, l[u & 1]);
             }
+            if (mantissa != 1.f)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    e[u] *= mantissa;
+            pb[0] = transpose8(DTypeTraits<__half>::pack(e[0], e[1]));
+            pb[1] = transpose8(DTypeTraits<__half>::pack(e[2], e[3]));
             uint32_t vw[4][VW];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -668,11 +654,9 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
 #pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
                                         for (int u = 0; u < 2; ++u)
-                                            if ((bits >> (8 * e + 7) & 1u) && key0 + key < limit(nt, u))
-                                                acc[2 * x + (e >> 1)][nt][(e & 1) * 2 + u] = __int_as_float(0x7FC00000);
+                                            if ((bits >> (8 * e + 7) & 1u) && key0 + key < limit(u))
+                                                acc[2 * x + (e >> 1)][(e & 1) * 2 + u] = __int_as_float(0x7FC00000);
                             }
                         }
 #pragma unroll
@@ -693,11 +677,8 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
                 C::halves(__byte_perm(vw[0][x], vw[1][x], 0x7362), a[2][0], a[3][0]);
                 C::halves(__byte_perm(vw[2][x], vw[3][x], 0x5140), a[0][1], a[1][1]);
                 C::halves(__byte_perm(vw[2][x], vw[3][x], 0x7362), a[2][1], a[3][1]);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16(acc[2 * x][nt], a[0][0], a[1][0], a[0][1], a[1][1], pb[nt][0], pb[nt][1]);
-                    mma_f16(acc[2 * x + 1][nt], a[2][0], a[3][0], a[2][1], a[3][1], pb[nt][0], pb[nt][1]);
-                }
+                mma_f16(acc[2 * x], a[0][0], a[1][0], a[0][1], a[1][1], pb[0], pb[1]);
+                mma_f16(acc[2 * x + 1], a[2][0], a[3][0], a[2][1], a[3][1], pb[0], pb[1]);
             }
         }
 
@@ -708,24 +689,22 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
             if (!meet())  // the segment before has been read
                 return;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    float sum = l[nt][u];
+                    float sum = l[u];
                     sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-                    const int row = warp * F::ROWS + nt * 8 + 2 * c + u;
+                    const int row = warp * F::ROWS + 2 * c + u;
                     if (g == 0) {
-                        mm[row] = m[nt][u];
+                        mm[row] = m[u];
                         ml[row] = sum;
                     }
 #pragma unroll
                     for (int x = 0; x < VW; ++x) {
                         const int d = v_column<D>(g, x);
                         *reinterpret_cast<float4 *>(mo + row * F::OROW + d) =
-                            make_float4(acc[2 * x][nt][u], acc[2 * x][nt][u + 2], acc[2 * x + 1][nt][u],
-                                        acc[2 * x + 1][nt][u + 2]);
+                            make_float4(acc[2 * x][u], acc[2 * x][u + 2], acc[2 * x + 1][u],
+                                        acc[2 * x + 1][u + 2]);
                     }
                 }
             if (!meet())
@@ -776,19 +755,22 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
     }
 }
 
-// Merges the parts of every segment that more than one block has, a block a
+// Merges the parts of every segment that more than one block has, SPLIT warps a
 // query row; writes the rows of segments without keys.
-template <int D, typename T>
+template <int D, typename T, int SPLIT>
 __global__ void __launch_bounds__(kCombineThreads)
-    fa_cache_combine_kernel(const __grid_constant__ Work w, T *__restrict__ out, float *__restrict__ lse, int rows_block)
+    fa_cache_combine_kernel(const __grid_constant__ Work w, T *__restrict__ out, float *__restrict__ lse, int rows_block,
+                            long long rows)
 {
     constexpr int WARPS = kCombineThreads / 32;
-    __shared__ float red_o[WARPS][D];
+    __shared__ __align__(16) float red_o[SPLIT > 1 ? WARPS : 1][D];
     __shared__ float red_m[WARPS], red_l[WARPS];
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    // block = ((b * queries + i) * heads + head) * R + row
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % SPLIT;
+    // row = ((b * queries + i) * heads + head) * R + row of the segment
     const int queries = w.pages ? w.q.Nq : 1;
-    long long x = blockIdx.x;
+    long long x = static_cast<long long>(blockIdx.x) * (WARPS / SPLIT) + (threadIdx.x >> 5) / SPLIT;
+    if (x >= rows)
+        return;
     const int row = static_cast<int>(x % w.R);
     x /= w.R;
     const int head = static_cast<int>(x % w.cache.heads);
@@ -801,12 +783,14 @@ __global__ void __launch_bounds__(kCombineThreads)
         w.pages ? ((static_cast<long long>(b) * w.cache.heads + head) * w.q.G + row) * w.q.Nq + i
                 : (static_cast<long long>(b) * w.cache.heads + head) * w.R + row;
     if (units == 0) {
-        for (int d = 2 * t; d < D; d += 2 * kCombineThreads)
+        wait_ahead();
+        for (int d = 2 * (32 * warp + lane); d < D; d += 64 * SPLIT)
             *reinterpret_cast<uint32_t *>(out + orow * D + d) = 0;
-        if (t == 0 && lse != nullptr)
+        if (lane == 0 && warp == 0 && lse != nullptr)
             lse[orow] = -INFINITY;
         return;
     }
+    wait_ahead();
     const long long share = w.plan[0];
     long long first = w.plan[1 + b];
     for (int y = 0; y < i; ++y)
@@ -816,58 +800,82 @@ __global__ void __launch_bounds__(kCombineThreads)
     if (x0 == x1)
         return;  // one block had it all, and has written it
     const int in_block = row % rows_block;
-    // a block's place: its head part if the segment began before its run
-    auto place = [&](int y) -> long long {
-        return (2ll * y + (y * share > first ? 0 : 1)) * rows_block + in_block;
-    };
-    float top = -INFINITY;
-    for (int y = x0 + t; y <= x1; y += kCombineThreads)
-        top = fmaxf(top, w.part_m[place(y)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0)
-        red_m[warp] = top;
-    __syncthreads();
-    top = red_m[0];
-    for (int y = 1; y < WARPS; ++y)
-        top = fmaxf(top, red_m[y]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    // warp v: blocks x0 + v, + WARPS, ...; lane: columns 4 lane .. 4 lane + 3
+    // warp v: the parts of blocks x0 + v, + SPLIT, ..., several at once; lane: columns 4 lane .. 4 lane + 3
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-#pragma unroll 4
-    for (int y = x0 + warp; y <= x1; y += WARPS) {
-        const long long p = place(y);
-        const float f = ex2(w.part_m[p] - ref);
-        sum = fmaf(w.part_l[p], f, sum);
-        if (4 * lane < D) {
-            const float4 z = *reinterpret_cast<const float4 *>(w.part_o + p * D + 4 * lane);
-            o.x = fmaf(z.x, f, o.x);
-            o.y = fmaf(z.y, f, o.y);
-            o.z = fmaf(z.z, f, o.z);
-            o.w = fmaf(z.w, f, o.w);
+    float top = -INFINITY, sum = 0.f;
+    for (int y0 = x0 + warp; y0 <= x1; y0 += SPLIT * kCombineEach) {
+        float m[kCombineEach], l[kCombineEach];
+        float4 z[kCombineEach];
+#pragma unroll
+        for (int u = 0; u < kCombineEach; ++u) {
+            const int y = y0 + u * SPLIT;
+            m[u] = -INFINITY;
+            l[u] = 0.f;
+            z[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (y <= x1) {
+                // a block's place: its head part if the segment began before its run
+                const long long p = (2ll * y + (y * share > first ? 0 : 1)) * rows_block + in_block;
+                m[u] = w.part_m[p];
+                l[u] = w.part_l[p];
+                if (4 * lane < D)
+                    z[u] = *reinterpret_cast<const float4 *>(w.part_o + p * D + 4 * lane);
+            }
+        }
+        float next = top;
+#pragma unroll
+        for (int u = 0; u < kCombineEach; ++u)
+            next = fmaxf(next, m[u]);
+        if (next == -INFINITY)
+            continue;  // no key so far
+        const float alpha = ex2(top - next);
+        top = next;
+        sum *= alpha;
+        o = make_float4(o.x * alpha, o.y * alpha, o.z * alpha, o.w * alpha);
+#pragma unroll
+        for (int u = 0; u < kCombineEach; ++u) {
+            const float f = ex2(m[u] - next);
+            sum = fmaf(l[u], f, sum);
+            o.x = fmaf(z[u].x, f, o.x);
+            o.y = fmaf(z[u].y, f, o.y);
+            o.z = fmaf(z[u].z, f, o.z);
+            o.w = fmaf(z[u].w, f, o.w);
         }
     }
-    if (4 * lane < D)
-        *reinterpret_cast<float4 *>(&red_o[warp][4 * lane]) = o;
-    if (lane == 0)
-        red_l[warp] = sum;
-    __syncthreads();
-    sum = 0.f;
-    for (int y = 0; y < WARPS; ++y)
-        sum += red_l[y];
+    if (SPLIT > 1) {  // a block has one row: join its warps
+        if (4 * lane < D)
+            *reinterpret_cast<float4 *>(&red_o[warp][4 * lane]) = o;
+        if (lane == 0) {
+            red_m[warp] = top;
+            red_l[warp] = sum;
+        }
+        __syncthreads();
+        if (warp != 0)
+            return;
+        top = red_m[0];
+#pragma unroll
+        for (int y = 1; y < SPLIT; ++y)
+            top = fmaxf(top, red_m[y]);
+        sum = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int y = 0; y < SPLIT; ++y) {
+            const float f = red_m[y] == -INFINITY ? 0.f : ex2(red_m[y] - top);
+            sum = fmaf(red_l[y], f, sum);
+            if (4 * lane < D) {
+                const float4 z = *reinterpret_cast<const float4 *>(&red_o[y][4 * lane]);
+                o.x = fmaf(z.x, f, o.x);
+                o.y = fmaf(z.y, f, o.y);
+                o.z = fmaf(z.z, f, o.z);
+                o.w = fmaf(z.w, f, o.w);
+            }
+        }
+    }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    for (int d = 2 * t; d < D; d += 2 * kCombineThreads) {
-        float2 z = make_float2(0.f, 0.f);
-        for (int y = 0; y < WARPS; ++y) {
-            z.x += red_o[y][d];
-            z.y += red_o[y][d + 1];
-        }
-        *reinterpret_cast<uint32_t *>(out + orow * D + d) = DTypeTraits<T>::pack(z.x * inv, z.y * inv);
-    }
-    if (t == 0 && lse != nullptr)
-        lse[orow] = sum == 0.f ? -INFINITY : (ref + __log2f(sum)) * 0.6931471805599453f;
+    if (4 * lane < D)
+        *reinterpret_cast<uint2 *>(out + orow * D + 4 * lane) =
+            make_uint2(DTypeTraits<T>::pack(o.x * inv, o.y * inv), DTypeTraits<T>::pack(o.z * inv, o.w * inv));
+    if (lane == 0 && lse != nullptr)
+        lse[orow] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.6931471805599453f;
 }
 
 }  // namespace cache

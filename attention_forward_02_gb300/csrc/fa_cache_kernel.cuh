@@ -74,6 +74,14 @@ __device__ __forceinline__ int round_int8(float x)
     return x == x ? __float2int_rn(fminf(fmaxf(x, -127.f), 127.f)) : 0;
 }
 
+// Dependent launches.  A kernel launched so may begin before the one ahead of it
+// in the stream has ended: it calls wait_ahead() before it touches memory, which
+// returns when that one has completed and its writes are visible.  let_next() lets
+// the next such launch begin; it is called after wait_ahead(), so whatever a later
+// kernel reads before its own wait was complete before this one's work began.
+__device__ __forceinline__ void wait_ahead() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 struct E4M3 {
     static constexpr int kUnit = 512;  // codes are whole multiples of 1 / kUnit
     static __device__ __forceinline__ int exp_of(float a) { return scale_exp<0x600000u, 8>(a); }  // 448 = 1.75 2^8
@@ -83,6 +91,10 @@ struct E4M3 {
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
         return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+    }
+    static __device__ __forceinline__ uint32_t encode4_finite(float a, float b, float c, float d)
+    {
+        return encode4(a, b, c, d);
     }
     // Two codes to fp16, exactly.
     static __device__ __forceinline__ uint32_t half2_of(uint16_t w)
@@ -106,6 +118,15 @@ struct I8 {
     {
         return (round_int8(a) & 0xFF) | (round_int8(b) & 0xFF) << 8 | (round_int8(c) & 0xFF) << 16 |
                static_cast<uint32_t>(round_int8(d)) << 24;
+    }
+    // Values of at most 127: 1.5 2^23 + x has x rounded to the nearest whole
+    // number (ties to even) in its low bits, two's complement.
+    static __device__ __forceinline__ uint32_t encode4_finite(float a, float b, float c, float d)
+    {
+        const float k = 12582912.f;
+        const uint32_t x = __byte_perm(__float_as_uint(a + k), __float_as_uint(b + k), 0x0040);
+        const uint32_t y = __byte_perm(__float_as_uint(c + k), __float_as_uint(d + k), 0x0040);
+        return __byte_perm(x, y, 0x5410);
     }
     // With its sign bit flipped a code is c + 128, which as the low byte of
     // 0x64.. is the fp16 1024 + c + 128; taking 1152 off leaves c, exactly.
@@ -165,8 +186,11 @@ __device__ __forceinline__ float finite_max(float a, const float (&f)[8])
 // new rows of a page (at most 128 x 128 16-bit values) are held in registers
 // between the pass that finds amax and the one that encodes: one read, one
 // write.  Thread t holds 8 columns (t % (d / 8)) of the rows t / (d / 8),
-// + page / 8, ...; eight 16-byte loads in flight a thread.
-constexpr int kWriteRows = 8;     // rows a thread
+// + page / 8, ...; eight 16-byte loads in flight a thread.  For long prompts the
+// instructions bound it, so amax is taken on the 16-bit patterns, two at a time
+// (magnitudes order as their bits do), and infinities and NaN, which those
+// show, go another way.
+constexpr int kWriteRows = 8;       // rows a thread
 constexpr int kWriteThreads = 256;  // most threads: page = d = 128
 
 struct NewRows {
@@ -176,27 +200,77 @@ struct NewRows {
     int each, total;
 };
 
-__device__ __forceinline__ float block_max(float a, float *smem)
+// The block's largest x (of unsigned numbers).
+__device__ __forceinline__ uint32_t block_max(uint32_t x, uint32_t *smem)
 {
     const int warps = (blockDim.x + 31) >> 5;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+        x = max(x, __shfl_xor_sync(0xffffffffu, x, off));
     __syncthreads();  // earlier reads of smem are done
     if ((threadIdx.x & 31) == 0)
-        smem[threadIdx.x >> 5] = a;
+        smem[threadIdx.x >> 5] = x;
     __syncthreads();
-    a = smem[0];
+    x = smem[0];
     for (int w = 1; w < warps; ++w)
-        a = fmaxf(a, smem[w]);
-    return a;
+        x = max(x, smem[w]);
+    return x;
 }
 
+// Sums of a thread's codes down its rows, for its eight columns, in units of
+// 1 / kUnit; exact (int8: two biased 16-bit sums a word; e4m3: 21 bits in fp32).
+template <typename C>
+struct ColumnSums;
+template <>
+struct ColumnSums<I8> {
+    uint32_t even[2] = {0, 0}, odd[2] = {0, 0};
+    int rows = 0;
+    __device__ __forceinline__ void add(const uint2 &c)
+    {
+        const uint32_t w[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            even[i] += w[i] & 0x00FF00FFu;
+            odd[i] += (w[i] >> 8) & 0x00FF00FFu;
+        }
+        ++rows;
+    }
+    __device__ __forceinline__ int sum(int j) const
+    {
+        const uint32_t x = j & 1 ? odd[j >> 2] : even[j >> 2];
+        return static_cast<int>(j & 2 ? x >> 16 : x & 0xFFFFu) - 128 * rows;
+    }
+};
+template <>
+struct ColumnSums<E4M3> {
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    __device__ __forceinline__ void add(uint2 c)
+    {
+        // NaN codes (all but the sign set) count as 0
+        const uint32_t x = ((c.x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+        const uint32_t y = ((c.y & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+        if (x | y) {
+            c.x &= ~((x >> 7) * 0xFFu);
+            c.y &= ~((y >> 7) * 0xFFu);
+        }
+        float f[4], g[4];
+        decode4<E4M3>(c.x, f);
+        decode4<E4M3>(c.y, g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            s[j] += f[j];
+            s[4 + j] += g[j];
+        }
+    }
+    __device__ __forceinline__ int sum(int j) const { return __float2int_rn(s[j] * E4M3::kUnit); }
+};
+
 template <typename T, typename C>
-__global__ void __launch_bounds__(kWriteThreads) fa_cache_write_kernel(Cache cache, Batch batch, NewRows in, int d)
+__global__ void __launch_bounds__(kWriteThreads, 3) fa_cache_write_kernel(Cache cache, Batch batch, NewRows in, int d)
 {
-    __shared__ float red[kWriteThreads / 32];
+    __shared__ uint32_t red[kWriteThreads / 32];
     __shared__ int sums[128];
+    const uint32_t infinity = DTypeTraits<T>::kBF16 ? 0x7F80u : 0x7C00u;
     const int b = blockIdx.z, h = blockIdx.y >> 1, which = blockIdx.y & 1;
     const int page = cache.page;
     const int groups = d / 8;              // threads a row
@@ -221,7 +295,9 @@ __global__ void __launch_bounds__(kWriteThreads) fa_cache_write_kernel(Cache cac
     const long long had = max(batch.seq_lens[b], 0);  // tokens before
     const long long end = had + n;
     const long long last = (end - 1) >> cache.log2_page;
-    const T *x = static_cast<const T *>(in.x[which]) + h * in.head_stride[which] + col;
+    const long long token_stride = which ? in.token_stride[1] : in.token_stride[0];
+    const T *x = static_cast<const T *>(which ? in.x[1] : in.x[0]) +
+                 h * (which ? in.head_stride[1] : in.head_stride[0]) + col;
     uint8_t *codes = which ? cache.v : cache.k;
     float *scales = which ? cache.v_scale : cache.k_scale;
     for (long long at = (had >> cache.log2_page) + blockIdx.x; at <= last; at += gridDim.x) {
@@ -233,42 +309,64 @@ __global__ void __launch_bounds__(kWriteThreads) fa_cache_write_kernel(Cache cac
         }
         const long long base = at << cache.log2_page;  // position of the page's slot 0
         const int lo = static_cast<int>(max(had - base, 0ll));
-        const int hi = static_cast<int>(min(end - base, static_cast<long long>(page)));
+        const int hi = live ? static_cast<int>(min(end - base, static_cast<long long>(page))) : 0;
+        const T *src = x + (t0 + (base - had) + row0) * token_stride;  // of slot row0, if that is new
+        const long long step = stride * token_stride;
         uint4 raw[kWriteRows];
-        float a = 0.f;
+        uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < kWriteRows; ++i) {
             const int row = row0 + i * stride;
             raw[i] = make_uint4(0, 0, 0, 0);
-            if (live && row >= lo && row < hi)
-                raw[i] = __ldcs(reinterpret_cast<const uint4 *>(x + (t0 + (base - had) + row) * in.token_stride[which]));
+            if (row >= lo && row < hi)
+                raw[i] = __ldcs(reinterpret_cast<const uint4 *>(src + i * step));
         }
 #pragma unroll
         for (int i = 0; i < kWriteRows; ++i) {
-            float f[8];
-            unpack8<T>(raw[i], f);
-            a = finite_max(a, f);
+            m = __vmaxu2(m, __vmaxu2(raw[i].x & 0x7FFF7FFFu, raw[i].y & 0x7FFF7FFFu));
+            m = __vmaxu2(m, __vmaxu2(raw[i].z & 0x7FFF7FFFu, raw[i].w & 0x7FFF7FFFu));
         }
         const size_t ph = static_cast<size_t>(p) * cache.heads + h;
         const float old = lo > 0 ? scales[ph] : 0.f;
-        a = block_max(a, red);  // every thread has read the old scale when it returns
+        m = block_max(max(m & 0xFFFFu, m >> 16), red);  // every thread has read the old scale when it returns
+        const bool finite = m < infinity;
+        float a = DTypeTraits<T>::unpack(m).x;
+        if (!finite) {
+            a = 0.f;
+#pragma unroll
+            for (int i = 0; i < kWriteRows; ++i) {
+                float f[8];
+                unpack8<T>(raw[i], f);
+                a = finite_max(a, f);
+            }
+            a = __uint_as_float(block_max(__float_as_uint(a), red));
+        }
         const float scale = fmaxf(old, pow2f(C::exp_of(a)));
         const float inv = 1.f / scale;
-        uint8_t *dst = codes + ph * page * d + col;
-        const bool mean = which == 0 && hi == page && cache.k_mean != nullptr;
-        int sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        uint8_t *dst = codes + ph * page * d + row0 * d + col;
+        const bool mean = which == 0 && end - base >= page && cache.k_mean != nullptr;
+        ColumnSums<C> sum;
 #pragma unroll
         for (int i = 0; i < kWriteRows; ++i) {
             const int row = row0 + i * stride;
+            uint2 *to = reinterpret_cast<uint2 *>(dst + i * stride * d);
             uint2 c = make_uint2(0, 0);
-            if (live && row >= lo && row < hi) {
+            if (row >= lo && row < hi) {
                 float f[8];
                 unpack8<T>(raw[i], f);
-                c.x = C::encode4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-                c.y = C::encode4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
-                *reinterpret_cast<uint2 *>(dst + row * d) = c;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    f[j] *= inv;
+                if (finite) {
+                    c.x = C::encode4_finite(f[0], f[1], f[2], f[3]);
+                    c.y = C::encode4_finite(f[4], f[5], f[6], f[7]);
+                } else {
+                    c.x = C::encode4(f[0], f[1], f[2], f[3]);
+                    c.y = C::encode4(f[4], f[5], f[6], f[7]);
+                }
+                *to = c;
             } else if (live && row < lo && (scale > old || mean)) {
-                c = *reinterpret_cast<const uint2 *>(dst + row * d);
+                c = *to;
                 if (scale > old) {  // old codes at the new scale
                     const float r = old * inv;
                     float f[4], g[4];
@@ -276,19 +374,11 @@ __global__ void __launch_bounds__(kWriteThreads) fa_cache_write_kernel(Cache cac
                     decode4<C>(c.y, g);
                     c.x = C::encode4(f[0] * r, f[1] * r, f[2] * r, f[3] * r);
                     c.y = C::encode4(g[0] * r, g[1] * r, g[2] * r, g[3] * r);
-                    *reinterpret_cast<uint2 *>(dst + row * d) = c;
+                    *to = c;
                 }
             }
-            if (mean) {
-                float f[4], g[4];
-                decode4<C>(c.x, f);
-                decode4<C>(c.y, g);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {  // NaN converts to 0
-                    sum[j] += __float2int_rn(f[j] * C::kUnit);
-                    sum[4 + j] += __float2int_rn(g[j] * C::kUnit);
-                }
-            }
+            if (mean)
+                sum.add(c);
         }
         if (threadIdx.x == 0)
             scales[ph] = scale;
@@ -301,14 +391,14 @@ __global__ void __launch_bounds__(kWriteThreads) fa_cache_write_kernel(Cache cac
             if (live)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    atomicAdd(&sums[col + j], sum[j]);
+                    atomicAdd(&sums[col + j], sum.sum(j));
             __syncthreads();
             const float unit = 1.f / (static_cast<float>(C::kUnit) * page);  // a power of two
-            float m = 0.f;
+            float top = 0.f;
             for (int c = threadIdx.x; c < d; c += blockDim.x)
-                m = fmaxf(m, fabsf(static_cast<float>(sums[c]) * unit));
-            m = block_max(m, red);
-            const int e = int8_exp(m);
+                top = fmaxf(top, fabsf(static_cast<float>(sums[c]) * unit));
+            top = __uint_as_float(block_max(__float_as_uint(top), red));
+            const int e = int8_exp(top);
             const double by = static_cast<double>(unit) * pow2f(-e);
             for (int c = threadIdx.x; c < d; c += blockDim.x)
                 cache.k_mean[ph * d + c] = static_cast<int8_t>(max(-127, min(127, __double2int_rn(sums[c] * by))));
@@ -409,105 +499,137 @@ __device__ __forceinline__ uint32_t ordered(float f)
     return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-// Scores of 64 pages of one (sequence, KV head) a block, for every query.  Four
-// lanes share a page: each holds a quarter of its int8 mean and multiplies it
-// with the same quarter of the int8 query rows (dp4a, int32), which lie in
-// shared memory, `kScoreRows` at a time.
+// Scores of 128 pages of one (sequence, KV head) a block, for every query: int8
+// products on the tensor cores (m16n8k32, int32 sums), 16 pages a warp as the
+// rows, eight query heads as the columns.  The order of d in the product is
+// free: a lane holds D / 4 consecutive bytes of two pages' means, loaded
+// straight into the operand, and the same bytes of a query row from shared
+// memory.  Query heads are padded to eights, query by query; a padded row's
+// scale is NaN, which fmaxf passes over.  d + 4 bytes a page are read once; what
+// the kernel costs is the latency of length, page number, mean and query row,
+// so the first three are under way while the rows are rounded to int8.
 constexpr int kScoreThreads = 256;
-constexpr int kScorePages = kScoreThreads / 4;
-constexpr int kScoreRows = 64;
+constexpr int kScorePages = kScoreThreads / 32 * 16;
+constexpr int kScoreRows = 64;  // of shared memory at a time
+
+__device__ __forceinline__ void mma_s8(int (&d)[4], int a0, int a1, int a2, int a3, int b0, int b1)
+{
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kScoreThreads)
     fa_cache_score_kernel(Cache cache, Batch batch, Queries q, uint32_t *__restrict__ scores, int slots)
 {
-    constexpr int QUARTER = D / 16;  // 32-bit words a lane
-    __shared__ __align__(16) int q8[kScoreRows][D / 4];
+    constexpr int QUARTER = D / 16;  // 32-bit words a lane, page and row
+    constexpr int STRIDE = D / 4 + 4;  // words of a row in shared memory
+    __shared__ __align__(16) int q8[kScoreRows][STRIDE];
     __shared__ float q8_scale[kScoreRows];
+    wait_ahead();
+    let_next();
     const int b = blockIdx.z, h = blockIdx.y;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = threadIdx.x & 3;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const int first = (blockIdx.x * (kScoreThreads / 32) + warp) * 16;
+    int page[2];  // of pages first + g, + 8; read before the length is known
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+        page[x] = batch.page(b, first + g + 8 * x);
     const int len = batch.length(b, cache.log2_page);
     const int n = (context(q, len, q.Nq - 1) + cache.page - 1) >> cache.log2_page;  // of the longest context
-    const int at = blockIdx.x * kScorePages + (threadIdx.x >> 2);
     if (static_cast<int>(blockIdx.x) * kScorePages >= n || n <= slots)
         return;  // no page here, or every page is chosen anyway
-    int mean[QUARTER];
-    float mean_scale = 0.f;
+    int mean[2][QUARTER];
+    float mean_scale[2];
 #pragma unroll
-    for (int i = 0; i < QUARTER; ++i)
-        mean[i] = 0;
-    // a page that is not complete has no summary yet; it is the last of every
-    // context that reaches it
-    const bool whole = at < (len >> cache.log2_page);
-    bool ok = false;
-    if (whole) {
-        const int p = batch.page(b, at);
-        ok = p >= 0;
-        if (ok) {
-            const size_t ph = static_cast<size_t>(p) * cache.heads + h;
-            mean_scale = cache.k_mean_scale[ph];
-            const int2 *src = reinterpret_cast<const int2 *>(cache.k_mean + ph * D) + quarter * (QUARTER / 2);
+    for (int x = 0; x < 2; ++x) {
+        // a page that is not complete has no summary yet; it is the last of
+        // every context that reaches it
+        const bool whole = first + g + 8 * x < (len >> cache.log2_page);
+        if (whole && page[x] < 0)
+            batch.bad();
+        if (!whole)
+            page[x] = -1;
+        mean_scale[x] = 0.f;
+#pragma unroll
+        for (int i = 0; i < QUARTER; ++i)
+            mean[x][i] = 0;
+        if (page[x] >= 0) {
+            const size_t ph = static_cast<size_t>(page[x]) * cache.heads + h;
+            mean_scale[x] = cache.k_mean_scale[ph];
+            const int2 *src = reinterpret_cast<const int2 *>(cache.k_mean + ph * D) + c * (QUARTER / 2);
 #pragma unroll
             for (int i = 0; i < QUARTER / 2; ++i) {
                 const int2 w = src[i];
-                mean[2 * i] = w.x;
-                mean[2 * i + 1] = w.y;
+                mean[x][2 * i] = w.x;
+                mean[x][2 * i + 1] = w.y;
             }
-        } else {
-            batch.bad();
         }
     }
-    for (int i = 0; i < q.Nq; ++i) {
-        float best = -INFINITY;
-        for (int g0 = 0; g0 < q.G; g0 += kScoreRows) {
-            const int rows = min(kScoreRows, q.G - g0);
-            __syncthreads();  // the rows before are read
-            for (int g = warp; g < rows; g += kScoreThreads / 32) {
+    const int tiles = (q.G + 7) / 8;  // of one query's heads
+    const int all_rows = q.Nq * tiles * 8;
+    float best[2] = {0.f, 0.f};
+    for (int r0 = 0; r0 < all_rows; r0 += kScoreRows) {
+        const int rows = min(kScoreRows, all_rows - r0);
+        __syncthreads();  // the rows before are read
+        for (int r = warp; r < rows; r += kScoreThreads / 32) {
+            const int i = (r0 + r) / (tiles * 8), head = (r0 + r) % (tiles * 8);
+            // lane l holds columns 4 l .. 4 l + 3
+            float f[4] = {0.f, 0.f, 0.f, 0.f};
+            if (head < q.G && lane < D / 4) {
                 const T *src = static_cast<const T *>(q.q) + b * q.batch_stride +
-                               static_cast<long long>(h * q.G + g0 + g) * q.head_stride + i * q.row_stride;
-                // lane l holds columns 4 l .. 4 l + 3
-                float f[4] = {0.f, 0.f, 0.f, 0.f};
-                if (lane < D / 4) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(src + 4 * lane);
-                    const float2 x = DTypeTraits<T>::unpack(w.x), y = DTypeTraits<T>::unpack(w.y);
-                    f[0] = x.x;
-                    f[1] = x.y;
-                    f[2] = y.x;
-                    f[3] = y.y;
-                }
-                float a = 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (fabsf(f[j]) <= 3.402823466e38f)
-                        a = fmaxf(a, fabsf(f[j]));
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1)
-                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-                const int e = int8_exp(a);
-                const float inv = pow2f(-e);
-                if (lane < D / 4)
-                    q8[g][lane] = static_cast<int>(I8::encode4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv));
-                if (lane == 0)
-                    q8_scale[g] = pow2f(e);
+                               static_cast<long long>(h * q.G + head) * q.head_stride + i * q.row_stride;
+                const uint2 w = *reinterpret_cast<const uint2 *>(src + 4 * lane);
+                const float2 x = DTypeTraits<T>::unpack(w.x), y = DTypeTraits<T>::unpack(w.y);
+                f[0] = x.x;
+                f[1] = x.y;
+                f[2] = y.x;
+                f[3] = y.y;
             }
-            __syncthreads();
-            for (int g = 0; g < rows; ++g) {
-                int dot = 0;
+            float a = 0.f;
 #pragma unroll
-                for (int w = 0; w < QUARTER; w += 2) {
-                    const int2 x = *reinterpret_cast<const int2 *>(&q8[g][quarter * QUARTER + w]);
-                    dot = __dp4a(mean[w], x.x, dot);
-                    dot = __dp4a(mean[w + 1], x.y, dot);
-                }
-                dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-                dot += __shfl_xor_sync(0xffffffffu, dot, 2);
-                // a whole number below 2^21, and powers of two: exact
-                best = fmaxf(best, (static_cast<float>(dot) * q8_scale[g]) * mean_scale);
-            }
+            for (int j = 0; j < 4; ++j)
+                if (fabsf(f[j]) <= 3.402823466e38f)
+                    a = fmaxf(a, fabsf(f[j]));
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+            const int e = int8_exp(a);
+            const float inv = pow2f(-e);
+            if (lane < D / 4)
+                q8[r][lane] = static_cast<int>(I8::encode4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv));
+            if (lane == 0)
+                q8_scale[r] = head < q.G ? pow2f(e) : __int_as_float(0x7FC00000);
         }
-        if (quarter == 0 && at < n) {
-            const long long seg = (static_cast<long long>(b) * cache.heads + h) * q.Nq + i;
-            scores[seg * batch.max_pages + at] = ok ? ordered(best) : 0u;
+        __syncthreads();
+        for (int r = 0; r < rows; r += 8) {
+            int dot[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < QUARTER; s += 2) {
+                const int2 y = *reinterpret_cast<const int2 *>(&q8[r + g][c * QUARTER + s]);
+                mma_s8(dot, mean[0][s], mean[1][s], mean[0][s + 1], mean[1][s + 1], y.x, y.y);
+            }
+            const int tile = (r0 + r) / 8 % tiles;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                // whole numbers below 2^21, and powers of two: exact
+                const float s0 = (static_cast<float>(dot[2 * x]) * q8_scale[r + 2 * c]) * mean_scale[x];
+                const float s1 = (static_cast<float>(dot[2 * x + 1]) * q8_scale[r + 2 * c + 1]) * mean_scale[x];
+                const float top = fmaxf(s0, s1);
+                best[x] = tile == 0 ? top : fmaxf(best[x], top);
+            }
+            if (tile == tiles - 1) {  // the query's last heads
+                const long long seg = (static_cast<long long>(b) * cache.heads + h) * q.Nq + (r0 + r) / (tiles * 8);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float top = fmaxf(best[x], __shfl_xor_sync(0xffffffffu, best[x], 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const int at = first + g + 8 * x;
+                    if (c == 0 && at < n)
+                        scores[seg * batch.max_pages + at] = page[x] >= 0 ? ordered(top) : 0u;
+                }
+            }
         }
     }
 }
@@ -515,16 +637,46 @@ __global__ void __launch_bounds__(kScoreThreads)
 // The `want` largest of the candidates' scores, ties to the lower page, with
 // the kept pages, in ascending order.  One block a (sequence, KV head, query):
 // the smallest chosen score by four 8-bit digits (a histogram of the scores
-// that share the digits found so far), then one ordered pass that writes.
-constexpr int kPickThreads = 256;
+// that share the digits found so far), then one ordered pass that writes, each
+// thread a run of pages.  Up to kPickHeld scores are held in shared memory.
+constexpr int kPickThreads = 512;
+constexpr int kPickHeld = 8192;
+
+// Sum over the block's earlier threads of x (and, in `total`, over all).
+__device__ __forceinline__ int block_before(int x, int *smem, int &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off)
+            incl += y;
+    }
+    __syncthreads();  // earlier reads of smem are done
+    if (lane == 31)
+        smem[warp] = incl;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < kPickThreads / 32; ++w) {
+        const int y = smem[w];
+        if (w < warp)
+            incl += y;
+        total += y;
+    }
+    return incl - x;
+}
 
 __global__ void __launch_bounds__(kPickThreads)
     fa_cache_pick_kernel(Cache cache, Batch batch, Queries q, const uint32_t *__restrict__ scores,
                          int *__restrict__ pages, int slots, int keep_first, int keep_last)
 {
+    __shared__ uint32_t held[kPickHeld];
     __shared__ int hist[256];
-    __shared__ int above[kPickThreads / 32], equal[kPickThreads / 32];
+    __shared__ int sums[kPickThreads / 32];
     __shared__ int found[2];
+    wait_ahead();
+    let_next();
     const long long seg = blockIdx.x;
     const int i = static_cast<int>(seg % q.Nq);
     const int b = static_cast<int>(seg / q.Nq / cache.heads);
@@ -538,15 +690,30 @@ __global__ void __launch_bounds__(kPickThreads)
     }
     const uint32_t *key = scores + seg * batch.max_pages;
     const int lo = keep_first, hi = n - keep_last;  // candidates
+    const bool any = slots > keep_first + keep_last;
     int want = slots - keep_first - keep_last;      // < hi - lo
+    if (n <= kPickHeld && any) {
+        for (int j = lo + t; j < hi; j += kPickThreads)
+            held[j] = key[j];
+        key = held;
+    }
     uint32_t prefix = 0;
     for (int shift = 24; want > 0 && shift >= 0; shift -= 8) {
-        hist[t] = 0;
+        if (t < 256)
+            hist[t] = 0;
         __syncthreads();
-        for (int j = lo + t; j < hi; j += kPickThreads) {
-            const uint32_t x = key[j];
-            if (shift == 24 || (x >> (shift + 8)) == prefix)
-                atomicAdd(&hist[(x >> shift) & 255u], 1);
+        for (int j0 = lo; j0 < hi; j0 += kPickThreads) {
+            const int j = j0 + t;
+            const uint32_t x = j < hi ? key[j] : 0u;
+            const bool in = j < hi && (shift == 24 || (x >> (shift + 8)) == prefix);
+            const unsigned digit = in ? (x >> shift) & 255u : 256u;
+            if (shift == 24) {  // few different ones: one addition for the lanes of a digit
+                const unsigned same = __match_any_sync(0xffffffffu, digit);
+                if (in && lane == __ffs(same) - 1)
+                    atomicAdd(&hist[digit], __popc(same));
+            } else if (in) {
+                atomicAdd(&hist[digit], 1);
+            }
         }
         __syncthreads();
         if (warp == 0) {
@@ -566,59 +733,44 @@ __global__ void __launch_bounds__(kPickThreads)
             }
             before -= sum;
             if (before < want && before + sum >= want) {
-                int u = 0;
-                while (before + c[u] < want)
-                    before += c[u++];
-                found[0] = 255 - 8 * lane - u;
-                found[1] = want - before;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    if (before < want && before + c[u] >= want) {
+                        found[0] = 255 - 8 * lane - u;
+                        found[1] = want - before;
+                    }
+                    before += c[u];
+                }
             }
         }
         __syncthreads();
         prefix = (prefix << 8) | static_cast<uint32_t>(found[0]);
         want = found[1];  // still to take among the scores that begin with `prefix`
     }
-    // ordered pass over all pages: kept, above the smallest chosen score, or
-    // one of the first `want` that equal it
-    const bool any = slots > keep_first + keep_last;
-    int written = 0, taken = 0;
-    for (int j0 = 0; j0 < n; j0 += kPickThreads) {
-        const int j = j0 + t;
-        bool in = false, eq = false;
-        if (j < n) {
-            if (j < lo || j >= hi) {
-                in = true;
-            } else if (any) {
-                const uint32_t x = key[j];
-                in = x > prefix;
-                eq = x == prefix;
-            }
+    // a page is written if it is kept, above the smallest chosen score, or one of
+    // the first `want` that equal it
+    const int each = (n + kPickThreads - 1) / kPickThreads;
+    const int j0 = t * each, j1 = min(n, j0 + each);
+    int above = 0, equal = 0, total;
+    for (int j = j0; j < j1; ++j) {
+        const bool kept = j < lo || j >= hi;
+        const uint32_t x = !kept && any ? key[j] : 0u;
+        above += kept || (any && x > prefix);
+        equal += !kept && any && x == prefix;
+    }
+    const int equal_before = block_before(equal, sums, total);
+    const int take = max(0, min(equal, want - equal_before));  // of its equal ones
+    int pos = block_before(above + take, sums, total), left = take;
+    for (int j = j0; j < j1; ++j) {
+        const bool kept = j < lo || j >= hi;
+        const uint32_t x = !kept && any ? key[j] : 0u;
+        bool in = kept || (any && x > prefix);
+        if (!in && any && x == prefix && left > 0) {
+            --left;
+            in = true;
         }
-        const unsigned eqs = __ballot_sync(0xffffffffu, eq);
-        if (lane == 0)
-            equal[warp] = __popc(eqs);
-        __syncthreads();
-        int rank = taken + __popc(eqs & ((1u << lane) - 1u)), total = 0;
-        for (int w = 0; w < kPickThreads / 32; ++w) {
-            if (w < warp)
-                rank += equal[w];
-            total += equal[w];
-        }
-        taken += total;
-        in = in || (eq && rank < want);
-        const unsigned ins = __ballot_sync(0xffffffffu, in);
-        if (lane == 0)
-            above[warp] = __popc(ins);
-        __syncthreads();
-        int pos = written + __popc(ins & ((1u << lane) - 1u));
-        total = 0;
-        for (int w = 0; w < kPickThreads / 32; ++w) {
-            if (w < warp)
-                pos += above[w];
-            total += above[w];
-        }
-        written += total;
         if (in)
-            out[pos] = j;
+            out[pos++] = j;
     }
 }
 
