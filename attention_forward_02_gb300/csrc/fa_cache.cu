@@ -32,19 +32,26 @@ struct CacheState {
 };
 CacheState g_cache[kMaxDevices];
 
-template <int D>
-cudaError_t set_smem_attrs()
+template <int D, int J>
+cudaError_t set_smem_attr()
 {
     using namespace fa::cache;
     const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, __half, E4M3>, a, DecCfg<D>::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, J, __half, E4M3>, a, DecCfg<D>::SMEM);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, __half, I8>, a, DecCfg<D>::SMEM);
+        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, J, __half, I8>, a, DecCfg<D>::SMEM);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, __nv_bfloat16, E4M3>, a, DecCfg<D>::SMEM);
+        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, J, __nv_bfloat16, E4M3>, a, DecCfg<D>::SMEM);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, __nv_bfloat16, I8>, a, DecCfg<D>::SMEM);
+        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, J, __nv_bfloat16, I8>, a, DecCfg<D>::SMEM);
     return e;
+}
+
+template <int D>
+cudaError_t set_smem_attrs()
+{
+    const cudaError_t e = set_smem_attr<D, 1>();
+    return e == cudaSuccess ? set_smem_attr<D, 2>() : e;
 }
 
 void init_cache(CacheState &st)
@@ -449,9 +456,11 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
             constexpr int D = decltype(dim)::value;
             using T = decltype(t);
             using C = decltype(code);
-            const bool first = launch_dependent(fa::cache::fa_cache_decode_kernel<D, T, C>, static_cast<unsigned>(blocks),
-                                                fa::cache::kDecThreads, fa::cache::DecCfg<D>::SMEM, cs, maps, w,
-                                                static_cast<T *>(o), lse);
+            const bool first = launch_dependent(
+                w.row_warps == 1 ? fa::cache::fa_cache_decode_kernel<D, 1, T, C>
+                                 : fa::cache::fa_cache_decode_kernel<D, 2, T, C>,
+                static_cast<unsigned>(blocks), fa::cache::kDecThreads, fa::cache::DecCfg<D>::SMEM, cs, maps, w,
+                static_cast<T *>(o), lse);
             if (!first)
                 return FA_ERR_CUDA;
             // parts of a segment, on average: a warp takes a few of them alone

@@ -80,11 +80,12 @@ struct DecCfg {
 // What the computing warps know of a stage.
 struct __align__(16) StageMeta {
     float k_scale[kSubs], v_scale[kSubs];
-    int key0[kSubs];  // position of the 16-key tile's first key; -1: nothing to see
+    int key0[kSubs];  // position of the 16-key tile's first key, or kNoKey
     int flags, b, i, head, group, pad[3];
 };
 static_assert(sizeof(StageMeta) == 80, "stage record");
 constexpr int kFirst = 1, kLast = 2, kHeadPart = 4, kTailPart = 8;
+constexpr int kNoKey = 0x7FFFFF00;  // behind every context
 
 // Where a thread (g = lane / 4, c = lane % 4) finds its bytes of a 16-key tile in
 // a part W bytes wide: of K, 4 words (2 if W = 32) ... of rows g and g + 8; of V,
@@ -209,7 +210,7 @@ struct Maps {
     CUtensorMap k[2], v[2];  // of the column parts
 };
 
-template <int D, typename T, typename C>
+template <int D, int J, typename T, typename C>
 __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
     fa_cache_decode_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Work w, T *__restrict__ out,
                            float *__restrict__ lse)
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                 if (mine)
                     for (int y = 0; y < box / kTile; ++y) {
                         const int k0 = key0 + y * kTile, sub = row0 / kTile + y;
-                        m->key0[sub] = p >= 0 && k0 < ctx ? k0 : -1;
+                        m->key0[sub] = p >= 0 && k0 < ctx ? k0 : kNoKey;
                         m->k_scale[sub] = ks;
                         m->v_scale[sub] = vs;
                     }
@@ -506,179 +507,209 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                     acc[j][u] = 0.f;
         }
 
-        for (int sub = wk; sub < kSubs; sub += key_warps) {
-            const int key0 = info->key0[sub];
-            const bool last_sub = sub + key_warps >= kSubs;
-            if (key0 < 0) {
-                if (last_sub) {
+        for (int set = wk; set < kSubs / J; set += key_warps) {
+            // J tiles at once: one look at the reference, and twice the independent work
+            const int sub0 = set * J;
+            const bool last_set = set + key_warps >= kSubs / J;
+            int key0[J];
+            int nearest = kNoKey, farthest = 0;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                key0[j] = info->key0[sub0 + j];
+                nearest = min(nearest, key0[j]);
+                farthest = max(farthest, key0[j]);
+            }
+            if (nearest == kNoKey) {
+                if (last_set) {
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(empty(slot));
                 }
                 continue;
             }
-            const float k_scale = info->k_scale[sub], v_scale = info->v_scale[sub];
-            const uint32_t k0 = sbase + F::RING_OFF + slot * F::STAGE + sub * kTile * F::W0, v0 = k0 + F::HALF;
-            const uint32_t k1 = sbase + F::RING_OFF + slot * F::STAGE + kStep * F::W0 + sub * kTile * F::W1;  // d = 96
-            uint32_t kw[2][KW];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                if constexpr (D == 128) {
-                    load_words<4>(&kw[r][0], k0 + k_offset<128>(g, c, 0) + r * 1024);
-                    load_words<4>(&kw[r][4], k0 + k_offset<128>(g, c, 1) + r * 1024);
-                } else if constexpr (D == 32) {
-                    load_words<2>(&kw[r][0], k0 + k_offset<32>(g, c, 0) + r * 256);
-                } else {
-                    load_words<4>(&kw[r][0], k0 + k_offset<64>(g, c, 0) + r * 512);
-                }
-                if constexpr (D == 96)
-                    load_words<2>(&kw[r][4], k1 + k_offset<32>(g, c, 0) + r * 256);
-            }
+            const uint32_t k0 = sbase + F::RING_OFF + slot * F::STAGE + sub0 * kTile * F::W0, v0 = k0 + F::HALF;
+            const uint32_t k1 = sbase + F::RING_OFF + slot * F::STAGE + kStep * F::W0 + sub0 * kTile * F::W1;  // d = 96
             // ---- S^T = K Q^T ----
-            float s[4];
+            float e[J][4];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                uint32_t kw[2][KW];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t kj = k0 + j * kTile * F::W0;
+                    if constexpr (D == 128) {
+                        load_words<4>(&kw[r][0], kj + k_offset<128>(g, c, 0) + r * 1024);
+                        load_words<4>(&kw[r][4], kj + k_offset<128>(g, c, 1) + r * 1024);
+                    } else if constexpr (D == 32) {
+                        load_words<2>(&kw[r][0], kj + k_offset<32>(g, c, 0) + r * 256);
+                    } else {
+                        load_words<4>(&kw[r][0], kj + k_offset<64>(g, c, 0) + r * 512);
+                    }
+                    if constexpr (D == 96)
+                        load_words<2>(&kw[r][4], k1 + j * kTile * F::W1 + k_offset<32>(g, c, 0) + r * 256);
+                }
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                    s[u] = 0.f;
+                    e[j][u] = 0.f;
 #pragma unroll
-            for (int x = 0; x < KW; ++x) {
-                uint32_t a0, a1, a2, a3;
-                C::halves(kw[0][x], a0, a2);
-                C::halves(kw[1][x], a1, a3);
-                    mma_f16(s, a0, a1, a2, a3, qb[x][0], qb[x][1]);
+                for (int x = 0; x < KW; ++x) {
+                    uint32_t a0, a1, a2, a3;
+                    C::halves(kw[0][x], a0, a2);
+                    C::halves(kw[1][x], a1, a3);
+                    mma_f16(e[j], a0, a1, a2, a3, qb[x][0], qb[x][1]);
+                }
             }
             // ---- exponents of P v_scale, masks; does any outgrow its reference? ----
-            const int v_exp = static_cast<int>(__float_as_uint(v_scale) >> 23) - 127;
-            const float ev = static_cast<float>(v_exp);
-            float f[2], e[4];
+            const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+            float v_scale[J];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    f[u & 1] = k_scale * qf[u & 1];
-                    e[u] = fmaf(s[u], f[u & 1], ev - m[u & 1]);  // +inf at first
-                }
-            const bool masked = key0 + kTile > least;
+            for (int j = 0; j < J; ++j) {
+                const float k_scale = info->k_scale[sub0 + j];
+                v_scale[j] = info->v_scale[sub0 + j];
+                const float ev = static_cast<float>(static_cast<int>(__float_as_uint(v_scale[j]) >> 23) - 127);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    e[j][u] = fmaf(e[j][u], k_scale * qf[u & 1], ev - ref[u & 1]);
+            }
+            const bool masked = farthest + kTile > least;
             if (masked) {
+#pragma unroll
+                for (int j = 0; j < J; ++j)
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        if (key0 + g + 8 * (u >> 1) >= limit(u & 1))
-                            e[u] = -INFINITY;
+                        if (key0[j] + g + 8 * (u >> 1) >= limit(u & 1))
+                            e[j][u] = -INFINITY;
             }
+            // with no reference yet, any score that is seen outgrows it
+            const float most_e[2] = {m[0] == -INFINITY ? -INFINITY : 8.f, m[1] == -INFINITY ? -INFINITY : 8.f};
             bool grown = false;
 #pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
                 for (int u = 0; u < 4; ++u)
-                    grown |= !(e[u] <= 8.f);
+                    grown |= !(e[j][u] <= most_e[u & 1]);
             if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        float y[2];
+                for (int u = 0; u < 2; ++u) {
+                    float top = -INFINITY;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            y[h] = fmaf(s[u + 2 * h], f[u], ev);
-                            if (masked && key0 + g + 8 * h >= limit(u))
-                                y[h] = -INFINITY;
-                        }
-                        float top = fmaxf(y[0], y[1]);
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        const float next = fmaxf(m[u], top);
-                        const float alpha = next == m[u] ? 1.f : ex2(m[u] - next);
-                        const float ref = next == -INFINITY ? 0.f : next;
-                        m[u] = next;
-                        l[u] *= alpha;
-                        e[u] = y[0] - ref;
-                        e[u + 2] = y[1] - ref;
+                    for (int j = 0; j < J; ++j)
+                        top = fmaxf(top, fmaxf(e[j][u], e[j][u + 2]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    const float next = fmaxf(m[u], top + ref[u]);
+                    const float alpha = next == m[u] ? 1.f : ex2(m[u] - next);
+                    const float down = next == -INFINITY ? 0.f : ref[u] - next;
+                    m[u] = next;
+                    l[u] *= alpha;
 #pragma unroll
-                        for (int j = 0; j < D / 16; ++j) {
-                            acc[j][u] *= alpha;
-                            acc[j][u + 2] *= alpha;
-                        }
+                    for (int j = 0; j < J; ++j) {
+                        e[j][u] += down;
+                        e[j][u + 2] += down;
                     }
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        acc[j][u] *= alpha;
+                        acc[j][u + 2] *= alpha;
+                    }
+                }
             }
             // ---- P, and O^T += V^T P^T ----
-            uint32_t pb[2];
-            const float inv = pow2f(-v_exp), mantissa = v_scale * inv;  // 1 for a power of two
+            uint32_t pb[J][2];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                e[u] = ex2(e[u]);
-                l[u & 1] = fmaf(e[u], inv, l[u & 1]);
+            for (int j = 0; j < J; ++j) {
+                const float inv = pow2f(127 - static_cast<int>(__float_as_uint(v_scale[j]) >> 23));
+                const float mantissa = v_scale[j] * inv;  // 1 for a power of two
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    e[j][u] = ex2(e[j][u]);
+                    l[u & 1] = fmaf(e[j][u], inv, l[u & 1]);
+                }
+                if (mantissa != 1.f)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        e[j][u] *= mantissa;
+                pb[j][0] = transpose8(DTypeTraits<__half>::pack(e[j][0], e[j][1]));
+                pb[j][1] = transpose8(DTypeTraits<__half>::pack(e[j][2], e[j][3]));
             }
-            if (mantissa != 1.f)
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    e[u] *= mantissa;
-            pb[0] = transpose8(DTypeTraits<__half>::pack(e[0], e[1]));
-            pb[1] = transpose8(DTypeTraits<__half>::pack(e[2], e[3]));
-            uint32_t vw[4][VW];
+            for (int j = 0; j < J; ++j) {
+                const uint32_t vj = v0 + j * kTile * F::W0;
+                uint32_t vw[4][VW];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                if constexpr (D == 128)
-                    load_words<4>(&vw[r][0], v0 + v_offset<128>(g, c, r & 1) + (r >> 1) * 1024);
-                else if constexpr (D == 32)
-                    load_words<1>(&vw[r][0], v0 + v_offset<32>(g, c, r & 1) + (r >> 1) * 256);
-                else
-                    load_words<2>(&vw[r][0], v0 + v_offset<64>(g, c, r & 1) + (r >> 1) * 512);
-                if constexpr (D == 96)
-                    load_words<1>(&vw[r][2], k1 + F::HALF + v_offset<32>(g, c, r & 1) + (r >> 1) * 256);
-            }
-            if (last_sub) {  // the stage's codes are in registers
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(empty(slot));
-            }
-            if (masked) {
-                // codes behind the last key are whatever the page held
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (key0 + 2 * c + (r & 1) + 8 * (r >> 1) >= most)
-#pragma unroll
-                        for (int x = 0; x < VW; ++x)
-                            vw[r][x] = 0;
-                if (C::kUnit != 1) {
-                    // NaN codes of V at keys that some rows do not see: 0 * NaN
-                    // must not reach those rows, so the rows that do see such a
-                    // key get their NaN here and the code becomes 0
-                    uint32_t any = 0;
+                for (int r = 0; r < 4; ++r) {
+                    if constexpr (D == 128)
+                        load_words<4>(&vw[r][0], vj + v_offset<128>(g, c, r & 1) + (r >> 1) * 1024);
+                    else if constexpr (D == 32)
+                        load_words<1>(&vw[r][0], vj + v_offset<32>(g, c, r & 1) + (r >> 1) * 256);
+                    else
+                        load_words<2>(&vw[r][0], vj + v_offset<64>(g, c, r & 1) + (r >> 1) * 512);
+                    if constexpr (D == 96)
+                        load_words<1>(&vw[r][2],
+                                      k1 + j * kTile * F::W1 + F::HALF + v_offset<32>(g, c, r & 1) + (r >> 1) * 256);
+                }
+                if (j == J - 1 && last_set) {  // the stage's codes are in registers
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(empty(slot));
+                }
+                if (masked) {
+                    // codes behind the last key are whatever the page held
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
+                        if (key0[j] + 2 * c + (r & 1) + 8 * (r >> 1) >= most)
 #pragma unroll
-                        for (int x = 0; x < VW; ++x)
-                            any |= nan_bytes(vw[r][x]);
-                    if (__any_sync(0xffffffffu, any != 0)) {
-#pragma unroll 1
-                        for (int key = 0; key < kTile; ++key) {
-                            const int r = (key & 1) + 2 * (key >> 3), from = (lane & ~3) | ((key & 7) >> 1);
-#pragma unroll
-                            for (int x = 0; x < VW; ++x) {
-                                const uint32_t own = r == 0 ? vw[0][x] : r == 1 ? vw[1][x] : r == 2 ? vw[2][x] : vw[3][x];
-                                const uint32_t bits = nan_bytes(__shfl_sync(0xffffffffu, own, from));
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                                        for (int u = 0; u < 2; ++u)
-                                            if ((bits >> (8 * e + 7) & 1u) && key0 + key < limit(u))
-                                                acc[2 * x + (e >> 1)][(e & 1) * 2 + u] = __int_as_float(0x7FC00000);
-                            }
-                        }
+                            for (int x = 0; x < VW; ++x)
+                                vw[r][x] = 0;
+                    if (C::kUnit != 1) {
+                        // NaN codes of V at keys that some rows do not see: 0 * NaN
+                        // must not reach those rows, so the rows that do see such a
+                        // key get their NaN here and the code becomes 0
+                        uint32_t any = 0;
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
 #pragma unroll
-                            for (int x = 0; x < VW; ++x) {
-                                const uint32_t bits = nan_bytes(vw[r][x]);
-                                vw[r][x] &= ~((bits >> 7) * 0xFFu);
+                            for (int x = 0; x < VW; ++x)
+                                any |= nan_bytes(vw[r][x]);
+                        if (__any_sync(0xffffffffu, any != 0)) {
+#pragma unroll 1
+                            for (int key = 0; key < kTile; ++key) {
+                                const int r = (key & 1) + 2 * (key >> 3), from = (lane & ~3) | ((key & 7) >> 1);
+#pragma unroll
+                                for (int x = 0; x < VW; ++x) {
+                                    const uint32_t own =
+                                        r == 0 ? vw[0][x] : r == 1 ? vw[1][x] : r == 2 ? vw[2][x] : vw[3][x];
+                                    const uint32_t bits = nan_bytes(__shfl_sync(0xffffffffu, own, from));
+#pragma unroll
+                                    for (int y = 0; y < 4; ++y)
+#pragma unroll
+                                        for (int u = 0; u < 2; ++u)
+                                            if ((bits >> (8 * y + 7) & 1u) && key0[j] + key < limit(u))
+                                                acc[2 * x + (y >> 1)][(y & 1) * 2 + u] = __int_as_float(0x7FC00000);
+                                }
                             }
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                                for (int x = 0; x < VW; ++x) {
+                                    const uint32_t bits = nan_bytes(vw[r][x]);
+                                    vw[r][x] &= ~((bits >> 7) * 0xFFu);
+                                }
+                        }
                     }
                 }
-            }
 #pragma unroll
-            for (int x = 0; x < VW; ++x) {
-                // four columns of V: bytes of keys 2 c, 2 c + 1 and 2 c + 8, 2 c + 9 side by side
-                uint32_t a[4][2];  // column, key pair
-                C::halves(__byte_perm(vw[0][x], vw[1][x], 0x5140), a[0][0], a[1][0]);
-                C::halves(__byte_perm(vw[0][x], vw[1][x], 0x7362), a[2][0], a[3][0]);
-                C::halves(__byte_perm(vw[2][x], vw[3][x], 0x5140), a[0][1], a[1][1]);
-                C::halves(__byte_perm(vw[2][x], vw[3][x], 0x7362), a[2][1], a[3][1]);
-                mma_f16(acc[2 * x], a[0][0], a[1][0], a[0][1], a[1][1], pb[0], pb[1]);
-                mma_f16(acc[2 * x + 1], a[2][0], a[3][0], a[2][1], a[3][1], pb[0], pb[1]);
+                for (int x = 0; x < VW; ++x) {
+                    // four columns of V: bytes of keys 2 c, 2 c + 1 and 2 c + 8, 2 c + 9 side by side
+                    uint32_t a[4][2];  // column, key pair
+                    C::halves(__byte_perm(vw[0][x], vw[1][x], 0x5140), a[0][0], a[1][0]);
+                    C::halves(__byte_perm(vw[0][x], vw[1][x], 0x7362), a[2][0], a[3][0]);
+                    C::halves(__byte_perm(vw[2][x], vw[3][x], 0x5140), a[0][1], a[1][1]);
+                    C::halves(__byte_perm(vw[2][x], vw[3][x], 0x7362), a[2][1], a[3][1]);
+                    mma_f16(acc[2 * x], a[0][0], a[1][0], a[0][1], a[1][1], pb[j][0], pb[j][1]);
+                    mma_f16(acc[2 * x + 1], a[2][0], a[3][0], a[2][1], a[3][1], pb[j][0], pb[j][1]);
+                }
             }
         }
 
@@ -825,15 +856,15 @@ __global__ void __launch_bounds__(kCombineThreads)
 #pragma unroll
         for (int u = 0; u < kCombineEach; ++u)
             next = fmaxf(next, m[u]);
-        if (next == -INFINITY)
-            continue;  // no key so far
-        const float alpha = ex2(top - next);
+        // no key so far, or only NaN scores, whose sum is NaN: factors of 0
+        const float ref = next == -INFINITY ? 0.f : next;
+        const float alpha = ex2(top - ref);
         top = next;
         sum *= alpha;
         o = make_float4(o.x * alpha, o.y * alpha, o.z * alpha, o.w * alpha);
 #pragma unroll
         for (int u = 0; u < kCombineEach; ++u) {
-            const float f = ex2(m[u] - next);
+            const float f = ex2(m[u] - ref);
             sum = fmaf(l[u], f, sum);
             o.x = fmaf(z[u].x, f, o.x);
             o.y = fmaf(z[u].y, f, o.y);
