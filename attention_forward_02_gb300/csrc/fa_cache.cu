@@ -302,12 +302,16 @@ fa_status_t fa_cache_write(const fa_cache_t *cache, const void *k, const void *v
                                      {k_head_stride, v_head_stride},
                                      cu_seqlens,
                                      cu_seqlens ? 0 : T / B,
-                                     T};
-    // pages that a sequence of the mean length touches; the blocks of a longer
-    // one go on to its later pages
-    const int each = (T + B - 1) / B;
-    const unsigned pages = static_cast<unsigned>((each + cache->page - 1) / cache->page + (each > 1 ? 1 : 0));
-    const dim3 grid(pages, 2 * cache->heads, B);
+                                     T,
+                                     B,
+                                     T > B};
+    // More rows than sequences: a block a touched page, of which there are at most
+    // T / page + 2 B however the rows are spread over the sequences.  Else a block
+    // a sequence, which goes on to its later pages if there are any.
+    const long long pages = rows.spread ? T / cache->page + 2ll * B : 1;
+    if (pages > 0x7fffffffLL)
+        return FA_ERR_UNSUPPORTED;
+    const dim3 grid(static_cast<unsigned>(pages), 2 * cache->heads, rows.spread ? 1 : B);
     const int threads = (cache->page / fa::cache::kWriteRows * (cache->d / 8) + 31) / 32 * 32;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     return by_types(dtype, cache->format, [&](auto t, auto code) {

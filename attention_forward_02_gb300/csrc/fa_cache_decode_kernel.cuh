@@ -317,8 +317,10 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
             ++i;
             open_query();
         }
-        int head = static_cast<int>(off / units) / w.groups, group = static_cast<int>(off / units) % w.groups;
-        int unit = static_cast<int>(off % units);
+        // off < units * heads * groups here: 32 bits hold it unless a sequence's work is vast
+        const int seg = off >> 31 ? static_cast<int>(off / units) : static_cast<int>(off) / units;
+        int head = seg / w.groups, group = seg % w.groups;
+        int unit = static_cast<int>(off - static_cast<long long>(seg) * units);
         const int log2_boxes = kLog2Step - w.log2_box;  // copies of a stage: 1, 2 or 4
         const int box = 1 << w.log2_box, batch_units = 32 >> log2_boxes;
         const uint64_t policy = l2_policy_evict_first();
@@ -361,6 +363,20 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                 const bool ended = unit + 1 == units || done + 1 == all;
                 const int row0 = (lane & ((1 << log2_boxes) - 1)) << w.log2_box;  // of the stage
                 StageMeta *m = meta + s;
+                // the copies first (their bytes may arrive before they are
+                // expected: the phase waits for the arrival below), then the
+                // record, whose scales may still be under way
+                if (mine && p >= 0) {
+                    const uint32_t dst = sbase + F::RING_OFF + s * F::STAGE + row0 * F::W0;
+                    const int y = key0 & (w.cache.page - 1);
+                    tma_load_3d(dst, &maps.k[0], full(s), 0, y, ph, policy);
+                    tma_load_3d(dst + F::HALF, &maps.v[0], full(s), 0, y, ph, policy);
+                    if (F::PARTS == 2) {
+                        const uint32_t dst1 = sbase + F::RING_OFF + s * F::STAGE + kStep * F::W0 + row0 * F::W1;
+                        tma_load_3d(dst1, &maps.k[1], full(s), F::W0, y, ph, policy);
+                        tma_load_3d(dst1 + F::HALF, &maps.v[1], full(s), F::W0, y, ph, policy);
+                    }
+                }
                 if (mine)
                     for (int y = 0; y < box / kTile; ++y) {
                         const int k0 = key0 + y * kTile, sub = row0 / kTile + y;
@@ -387,18 +403,6 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive_expect_tx(full(s), __popc(live) * 2 * box * D);
-                __syncwarp();
-                if (mine && p >= 0) {
-                    const uint32_t dst = sbase + F::RING_OFF + s * F::STAGE + row0 * F::W0;
-                    const int y = key0 & (w.cache.page - 1);
-                    tma_load_3d(dst, &maps.k[0], full(s), 0, y, ph, policy);
-                    tma_load_3d(dst + F::HALF, &maps.v[0], full(s), 0, y, ph, policy);
-                    if (F::PARTS == 2) {
-                        const uint32_t dst1 = sbase + F::RING_OFF + s * F::STAGE + kStep * F::W0 + row0 * F::W1;
-                        tma_load_3d(dst1, &maps.k[1], full(s), F::W0, y, ph, policy);
-                        tma_load_3d(dst1 + F::HALF, &maps.v[1], full(s), F::W0, y, ph, policy);
-                    }
-                }
                 opened = ended;
                 ++unit;
             }

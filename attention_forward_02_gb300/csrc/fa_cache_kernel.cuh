@@ -197,7 +197,16 @@ struct NewRows {
     const void *x[2];  // K, V
     long long token_stride[2], head_stride[2];
     const int *cu;  // or NULL: `each` tokens a sequence
-    int each, total;
+    int each, total, batch;
+    bool spread;  // blocks stand for touched pages
+
+    // First row and rows of sequence b; false if its offsets are none.
+    __device__ bool tokens(int b, int &first, int &count) const
+    {
+        first = cu ? cu[b] : b * each;
+        count = cu ? cu[b + 1] - first : each;
+        return first >= 0 && first <= total && count >= 0 && count <= total - first;
+    }
 };
 
 // The block's largest x (of unsigned numbers).
@@ -271,28 +280,57 @@ __global__ void __launch_bounds__(kWriteThreads, 3) fa_cache_write_kernel(Cache 
     __shared__ uint32_t red[kWriteThreads / 32];
     __shared__ int sums[128];
     const uint32_t infinity = DTypeTraits<T>::kBF16 ? 0x7F80u : 0x7C00u;
-    const int b = blockIdx.z, h = blockIdx.y >> 1, which = blockIdx.y & 1;
+    const int h = blockIdx.y >> 1, which = blockIdx.y & 1;
     const int page = cache.page;
     const int groups = d / 8;              // threads a row
     const int stride = page / kWriteRows;  // rows between a thread's rows
     const bool live = threadIdx.x < static_cast<unsigned>(groups * stride);
     const int col = (threadIdx.x % groups) * 8, row0 = threadIdx.x / groups;
-    int t0, n;
-    if (in.cu != nullptr) {
-        t0 = in.cu[b];
-        n = in.cu[b + 1] - t0;
-        if (t0 < 0 || t0 > in.total || n < 0 || n > in.total - t0) {
-            if (threadIdx.x == 0)
-                batch.bad();
-            return;
+    // the block's sequence and page: with `spread` the blockIdx.x-th touched page
+    // of the batch (a warp counts the pages of 32 sequences at a time), else
+    // page blockIdx.x of sequence blockIdx.z, and every gridDim.x-th after it
+    int b = blockIdx.z, t0, n;
+    long long skip = blockIdx.x, had = 0;
+    if (in.spread) {
+        const int lane = threadIdx.x & 31;
+        long long before = 0;
+        b = -1;
+        for (int b0 = 0; b < 0 && b0 < in.batch; b0 += 32) {
+            const int x = b0 + lane;
+            int count = 0;
+            if (x < in.batch) {
+                had = max(batch.seq_lens[x], 0);
+                if (!in.tokens(x, t0, n))
+                    batch.bad();
+                else if (n > 0)
+                    count = static_cast<int>(((had + n - 1) >> cache.log2_page) - (had >> cache.log2_page)) + 1;
+            }
+            int incl = count;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off)
+                    incl += y;
+            }
+            const unsigned here = __ballot_sync(0xffffffffu, skip < before + incl);
+            if (here) {
+                const int from = __ffs(here) - 1;
+                b = b0 + from;
+                skip -= before + __shfl_sync(0xffffffffu, incl - count, from);
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
         }
-    } else {
-        t0 = b * in.each;
-        n = in.each;
+        if (b < 0)
+            return;  // fewer pages than blocks
+    }
+    if (!in.tokens(b, t0, n)) {
+        if (threadIdx.x == 0)
+            batch.bad();
+        return;
     }
     if (n == 0)
         return;
-    const long long had = max(batch.seq_lens[b], 0);  // tokens before
+    had = max(batch.seq_lens[b], 0);  // tokens before
     const long long end = had + n;
     const long long last = (end - 1) >> cache.log2_page;
     const long long token_stride = which ? in.token_stride[1] : in.token_stride[0];
@@ -300,11 +338,13 @@ __global__ void __launch_bounds__(kWriteThreads, 3) fa_cache_write_kernel(Cache 
                  h * (which ? in.head_stride[1] : in.head_stride[0]) + col;
     uint8_t *codes = which ? cache.v : cache.k;
     float *scales = which ? cache.v_scale : cache.k_scale;
-    for (long long at = (had >> cache.log2_page) + blockIdx.x; at <= last; at += gridDim.x) {
+    for (long long at = (had >> cache.log2_page) + skip; at <= last; at += gridDim.x) {
         const int p = at < batch.max_pages ? batch.page(b, static_cast<int>(at)) : -1;
         if (p < 0) {
             if (threadIdx.x == 0)
                 batch.bad();
+            if (in.spread)
+                return;
             continue;
         }
         const long long base = at << cache.log2_page;  // position of the page's slot 0
@@ -404,8 +444,10 @@ __global__ void __launch_bounds__(kWriteThreads, 3) fa_cache_write_kernel(Cache 
                 cache.k_mean[ph * d + c] = static_cast<int8_t>(max(-127, min(127, __double2int_rn(sums[c] * by))));
             if (threadIdx.x == 0)
                 cache.k_mean_scale[ph] = pow2f(e) * scale;
-            __syncthreads();  // sums are free for the next page
         }
+        if (in.spread)
+            return;
+        __syncthreads();  // the shared sums are free for the next page
     }
 }
 
