@@ -92,9 +92,21 @@ struct E4M3 {
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
         return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
     }
-    static __device__ __forceinline__ uint32_t encode4_finite(float a, float b, float c, float d)
+    // Finite values, scaled on the way.
+    static __device__ __forceinline__ uint32_t encode4_finite(float a, float b, float c, float d, float inv)
     {
-        return encode4(a, b, c, d);
+        return encode4(a * inv, b * inv, c * inv, d * inv);
+    }
+    // The same on two pairs of fp16: the scaled value has fp16's 11 bits, or is
+    // below the smallest code (2^-9) by far, so it is exact where it matters.
+    static __device__ __forceinline__ uint32_t encode4_half(uint32_t ab, uint32_t cd, __half2 inv)
+    {
+        const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&ab), inv);
+        const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&cd), inv);
+        uint16_t lo, hi;
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(*reinterpret_cast<const uint32_t *>(&y)));
+        return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
     }
     // Two codes to fp16, exactly.
     static __device__ __forceinline__ uint32_t half2_of(uint16_t w)
@@ -119,14 +131,22 @@ struct I8 {
         return (round_int8(a) & 0xFF) | (round_int8(b) & 0xFF) << 8 | (round_int8(c) & 0xFF) << 16 |
                static_cast<uint32_t>(round_int8(d)) << 24;
     }
-    // Values of at most 127: 1.5 2^23 + x has x rounded to the nearest whole
-    // number (ties to even) in its low bits, two's complement.
-    static __device__ __forceinline__ uint32_t encode4_finite(float a, float b, float c, float d)
+    // Finite values of at most 127 once scaled: 1.5 2^23 + x has x rounded to the
+    // nearest whole number (ties to even) in its low bits, two's complement.
+    static __device__ __forceinline__ uint32_t encode4_finite(float a, float b, float c, float d, float inv)
     {
         const float k = 12582912.f;
-        const uint32_t x = __byte_perm(__float_as_uint(a + k), __float_as_uint(b + k), 0x0040);
-        const uint32_t y = __byte_perm(__float_as_uint(c + k), __float_as_uint(d + k), 0x0040);
+        const uint32_t x = __byte_perm(__float_as_uint(fmaf(a, inv, k)), __float_as_uint(fmaf(b, inv, k)), 0x0040);
+        const uint32_t y = __byte_perm(__float_as_uint(fmaf(c, inv, k)), __float_as_uint(fmaf(d, inv, k)), 0x0040);
         return __byte_perm(x, y, 0x5410);
+    }
+    // The same on two pairs of fp16, with 1.5 2^10: one rounding, in the fused addition.
+    static __device__ __forceinline__ uint32_t encode4_half(uint32_t ab, uint32_t cd, __half2 inv)
+    {
+        const __half2 k = __halves2half2(__ushort_as_half(0x6600), __ushort_as_half(0x6600));
+        const __half2 x = __hfma2(*reinterpret_cast<const __half2 *>(&ab), inv, k);
+        const __half2 y = __hfma2(*reinterpret_cast<const __half2 *>(&cd), inv, k);
+        return __byte_perm(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y), 0x6420);
     }
     // With its sign bit flipped a code is c + 128, which as the low byte of
     // 0x64.. is the fp16 1024 + c + 128; taking 1152 off leaves c, exactly.
@@ -187,9 +207,9 @@ __device__ __forceinline__ float finite_max(float a, const float (&f)[8])
 // between the pass that finds amax and the one that encodes: one read, one
 // write.  Thread t holds 8 columns (t % (d / 8)) of the rows t / (d / 8),
 // + page / 8, ...; eight 16-byte loads in flight a thread.  For long prompts the
-// instructions bound it, so amax is taken on the 16-bit patterns, two at a time
-// (magnitudes order as their bits do), and infinities and NaN, which those
-// show, go another way.
+// instructions bound it, so amax is taken on pairs of 16-bit values and fp16 is
+// encoded in pairs; pages with infinities or NaN, which the maximum shows, and
+// scales beyond fp16's range go another way.
 constexpr int kWriteRows = 8;       // rows a thread
 constexpr int kWriteThreads = 256;  // most threads: page = d = 128
 
@@ -208,6 +228,18 @@ struct NewRows {
         return first >= 0 && first <= total && count >= 0 && count <= total - first;
     }
 };
+
+// Larger magnitudes of two pairs (NaN if one is; the sign means nothing).
+template <typename T>
+__device__ __forceinline__ uint32_t max_magnitude2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    if (DTypeTraits<T>::kBF16)
+        asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
 
 // The block's largest x (of unsigned numbers).
 __device__ __forceinline__ uint32_t block_max(uint32_t x, uint32_t *smem)
@@ -234,7 +266,7 @@ template <>
 struct ColumnSums<I8> {
     uint32_t even[2] = {0, 0}, odd[2] = {0, 0};
     int rows = 0;
-    __device__ __forceinline__ void add(const uint2 &c)
+    __device__ __forceinline__ void add(const uint2 &c, bool)
     {
         const uint32_t w[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
 #pragma unroll
@@ -253,12 +285,11 @@ struct ColumnSums<I8> {
 template <>
 struct ColumnSums<E4M3> {
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    __device__ __forceinline__ void add(uint2 c)
+    __device__ __forceinline__ void add(uint2 c, bool finite)
     {
-        // NaN codes (all but the sign set) count as 0
-        const uint32_t x = ((c.x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-        const uint32_t y = ((c.y & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-        if (x | y) {
+        if (!finite) {  // NaN codes (all but the sign set) count as 0
+            const uint32_t x = ((c.x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+            const uint32_t y = ((c.y & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
             c.x &= ~((x >> 7) * 0xFFu);
             c.y &= ~((y >> 7) * 0xFFu);
         }
@@ -275,7 +306,7 @@ struct ColumnSums<E4M3> {
 };
 
 template <typename T, typename C>
-__global__ void __launch_bounds__(kWriteThreads, 3) fa_cache_write_kernel(Cache cache, Batch batch, NewRows in, int d)
+__global__ void __launch_bounds__(kWriteThreads, 4) fa_cache_write_kernel(Cache cache, Batch batch, NewRows in, int d)
 {
     __shared__ uint32_t red[kWriteThreads / 32];
     __shared__ int sums[128];
@@ -352,20 +383,29 @@ __global__ void __launch_bounds__(kWriteThreads, 3) fa_cache_write_kernel(Cache 
         const int hi = live ? static_cast<int>(min(end - base, static_cast<long long>(page))) : 0;
         const T *src = x + (t0 + (base - had) + row0) * token_stride;  // of slot row0, if that is new
         const long long step = stride * token_stride;
+        const bool whole = lo == 0 && end - base >= page;  // every slot is new: no row of it needs a look
         uint4 raw[kWriteRows];
         uint32_t m = 0;
+        if (whole && live) {
+            const T *from = src;
 #pragma unroll
-        for (int i = 0; i < kWriteRows; ++i) {
-            const int row = row0 + i * stride;
-            raw[i] = make_uint4(0, 0, 0, 0);
-            if (row >= lo && row < hi)
-                raw[i] = __ldcs(reinterpret_cast<const uint4 *>(src + i * step));
+            for (int i = 0; i < kWriteRows; ++i, from += step)
+                raw[i] = __ldcs(reinterpret_cast<const uint4 *>(from));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWriteRows; ++i) {
+                const int row = row0 + i * stride;
+                raw[i] = make_uint4(0, 0, 0, 0);
+                if (row >= lo && row < hi)
+                    raw[i] = __ldcs(reinterpret_cast<const uint4 *>(src + i * step));
+            }
         }
 #pragma unroll
         for (int i = 0; i < kWriteRows; ++i) {
-            m = __vmaxu2(m, __vmaxu2(raw[i].x & 0x7FFF7FFFu, raw[i].y & 0x7FFF7FFFu));
-            m = __vmaxu2(m, __vmaxu2(raw[i].z & 0x7FFF7FFFu, raw[i].w & 0x7FFF7FFFu));
+            m = max_magnitude2<T>(m, max_magnitude2<T>(raw[i].x, raw[i].y));
+            m = max_magnitude2<T>(m, max_magnitude2<T>(raw[i].z, raw[i].w));
         }
+        m &= 0x7FFF7FFFu;
         const size_t ph = static_cast<size_t>(p) * cache.heads + h;
         const float old = lo > 0 ? scales[ph] : 0.f;
         m = block_max(max(m & 0xFFFFu, m >> 16), red);  // every thread has read the old scale when it returns
@@ -383,42 +423,58 @@ __global__ void __launch_bounds__(kWriteThreads, 3) fa_cache_write_kernel(Cache 
         }
         const float scale = fmaxf(old, pow2f(C::exp_of(a)));
         const float inv = 1.f / scale;
+        const bool pairs = finite && inv >= 6.103515625e-5f && inv <= 32768.f;  // a normal fp16 number
+        const __half2 inv2 = __float2half2_rn(inv);
         uint8_t *dst = codes + ph * page * d + row0 * d + col;
         const bool mean = which == 0 && end - base >= page && cache.k_mean != nullptr;
         ColumnSums<C> sum;
+        if (whole && finite && (DTypeTraits<T>::kBF16 || pairs)) {
+            if (live) {
+                uint8_t *to = dst;
 #pragma unroll
-        for (int i = 0; i < kWriteRows; ++i) {
-            const int row = row0 + i * stride;
-            uint2 *to = reinterpret_cast<uint2 *>(dst + i * stride * d);
-            uint2 c = make_uint2(0, 0);
-            if (row >= lo && row < hi) {
-                float f[8];
-                unpack8<T>(raw[i], f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    f[j] *= inv;
-                if (finite) {
-                    c.x = C::encode4_finite(f[0], f[1], f[2], f[3]);
-                    c.y = C::encode4_finite(f[4], f[5], f[6], f[7]);
-                } else {
-                    c.x = C::encode4(f[0], f[1], f[2], f[3]);
-                    c.y = C::encode4(f[4], f[5], f[6], f[7]);
-                }
-                *to = c;
-            } else if (live && row < lo && (scale > old || mean)) {
-                c = *to;
-                if (scale > old) {  // old codes at the new scale
-                    const float r = old * inv;
-                    float f[4], g[4];
-                    decode4<C>(c.x, f);
-                    decode4<C>(c.y, g);
-                    c.x = C::encode4(f[0] * r, f[1] * r, f[2] * r, f[3] * r);
-                    c.y = C::encode4(g[0] * r, g[1] * r, g[2] * r, g[3] * r);
-                    *to = c;
+                for (int i = 0; i < kWriteRows; ++i, to += stride * d) {
+                    uint2 c;
+                    if (DTypeTraits<T>::kBF16) {
+                        float f[8];
+                        unpack8<T>(raw[i], f);
+                        c.x = C::encode4_finite(f[0], f[1], f[2], f[3], inv);
+                        c.y = C::encode4_finite(f[4], f[5], f[6], f[7], inv);
+                    } else {
+                        c.x = C::encode4_half(raw[i].x, raw[i].y, inv2);
+                        c.y = C::encode4_half(raw[i].z, raw[i].w, inv2);
+                    }
+                    *reinterpret_cast<uint2 *>(to) = c;
+                    if (mean)
+                        sum.add(c, true);
                 }
             }
-            if (mean)
-                sum.add(c);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWriteRows; ++i) {
+                const int row = row0 + i * stride;
+                uint2 *to = reinterpret_cast<uint2 *>(dst + i * stride * d);
+                uint2 c = make_uint2(0, 0);
+                if (row >= lo && row < hi) {
+                    float f[8];
+                    unpack8<T>(raw[i], f);
+                    c.x = C::encode4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+                    c.y = C::encode4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+                    *to = c;
+                } else if (live && row < lo && (scale > old || mean)) {
+                    c = *to;
+                    if (scale > old) {  // old codes at the new scale
+                        const float r = old * inv;
+                        float f[4], g[4];
+                        decode4<C>(c.x, f);
+                        decode4<C>(c.y, g);
+                        c.x = C::encode4(f[0] * r, f[1] * r, f[2] * r, f[3] * r);
+                        c.y = C::encode4(g[0] * r, g[1] * r, g[2] * r, g[3] * r);
+                        *to = c;
+                    }
+                }
+                if (mean)
+                    sum.add(c, finite && lo == 0);
+            }
         }
         if (threadIdx.x == 0)
             scales[ph] = scale;
