@@ -50,7 +50,7 @@ cudaError_t set_smem_attr()
 template <int D>
 cudaError_t set_smem_attrs()
 {
-    const cudaError_t e = set_smem_attr<D, 1>();
+    const cudaError_t e = set_smem_attr<D, D <= 64 ? 2 : 1>();
     return e == cudaSuccess ? set_smem_attr<D, 2>() : e;
 }
 
@@ -439,8 +439,9 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
     w.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan_bytes(B));
     w.part_m = w.part_o + part_rows * cache->d;
     w.part_l = w.part_m + part_rows;
-    const int box = cache->page < fa::cache::kStep ? cache->page : fa::cache::kStep;
-    w.log2_box = box == 64 ? 6 : box == 32 ? 5 : 4;
+    const int step = cache->d <= 64 ? fa::cache::DecCfg<64>::STEP : fa::cache::DecCfg<128>::STEP;
+    const int box = cache->page < step ? cache->page : step;
+    w.log2_box = box == 128 ? 7 : box == 64 ? 6 : box == 32 ? 5 : 4;
     fa::cache::Maps maps = {};
     const int width[2] = {cache->d == 96 ? 64 : cache->d, 32};
     for (int i = 0; i < (cache->d == 96 ? 2 : 1); ++i)
@@ -450,7 +451,7 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
     // no more blocks than units there can be
     const long long keys = static_cast<long long>(pages && slots < max_pages ? slots : max_pages) * cache->page;
     const long long most = static_cast<long long>(B) * (pages ? Nq : 1) * cache->heads * w.groups *
-                           ((keys - 1) / fa::cache::kStep + 1);
+                           ((keys - 1) / step + 1);
     const long long resident = static_cast<long long>(sms) * fa::cache::kBlocksPerSm;
     long long blocks = resident < fa::cache::kMaxBlocks ? resident : fa::cache::kMaxBlocks;
     if (most < blocks)
@@ -461,7 +462,7 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
             using T = decltype(t);
             using C = decltype(code);
             const bool first = launch_dependent(
-                w.row_warps == 1 ? fa::cache::fa_cache_decode_kernel<D, 1, T, C>
+                w.row_warps == 1 ? fa::cache::fa_cache_decode_kernel<D, D <= 64 ? 2 : 1, T, C>
                                  : fa::cache::fa_cache_decode_kernel<D, 2, T, C>,
                 static_cast<unsigned>(blocks), fa::cache::kDecThreads, fa::cache::DecCfg<D>::SMEM, cs, maps, w,
                 static_cast<T *>(o), lse);

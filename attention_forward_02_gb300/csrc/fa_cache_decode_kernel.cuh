@@ -21,8 +21,9 @@
 // conflicts under the swizzle that TMA writes (d = 128; a few two-way ones below).
 //
 // One warp loads: it looks up page numbers and scales, 32 pages at a time, and
-// copies 64 keys of K and V a stage into a ring.  Four warps compute, 16 keys
-// each, or, with more than 16 query rows a head, fewer keys and more rows.
+// copies 64 keys of K and V a stage (128 at d <= 64) into a ring.  Four warps
+// compute, 16 or 32 keys each, or, with more than 8 query rows a head, more keys
+// and fewer warps on the same rows.
 //
 // Query rows are scaled by a power of two to a row maximum in [2^14, 2^15)
 // before they become fp16: a bf16 row keeps every bit that fp32 sums would see.
@@ -31,7 +32,7 @@
 // so that no product with a V scale overflows and V scales of any size mix.
 // m moves (and O, l are rescaled) only when a score outgrows it by 2^8.
 //
-// Work is dealt in units of 64 keys (16 a warp) of one (sequence, KV head, row
+// Work is dealt in units of a stage's 64 keys (128 at d <= 64) of one (sequence, KV head, row
 // group): the blocks of a persistent grid take equal runs of the concatenated
 // units of all sequences, whatever their lengths, which are read from device
 // memory.  A run may begin and end inside a segment; those parts (at most two a
@@ -47,9 +48,7 @@ namespace cache {
 constexpr int kDecWarps = 4;      // that compute
 constexpr int kDecThreads = 32 * (kDecWarps + 1);
 constexpr int kTile = 16;         // keys of one product
-constexpr int kStep = 64;         // keys of a stage: a unit of work
-constexpr int kLog2Step = 6;
-constexpr int kSubs = kStep / kTile;
+constexpr int kMaxSubs = 8;       // tiles of a stage
 constexpr int kRows = 8;          // query rows a warp
 constexpr int kBlocksPerSm = 3;
 constexpr int kMaxBlocks = 640;   // of the persistent grid
@@ -60,16 +59,19 @@ constexpr int kCombineEach = 8;   // parts of a warp under way at once
 // swizzle of its width: 32, 64, 128, or 64 + 32.
 template <int D>
 struct DecCfg {
+    static constexpr int LOG2_STEP = D <= 64 ? 7 : 6;
+    static constexpr int STEP = 1 << LOG2_STEP;               // keys of a stage: a unit of work
+    static constexpr int SUBS = STEP / kTile;
     static constexpr int PARTS = D == 96 ? 2 : 1;
     static constexpr int W0 = D == 96 ? 64 : D, W1 = D - W0;  // widths
-    static constexpr int HALF = kStep * D;                    // K or V of a stage, bytes
+    static constexpr int HALF = STEP * D;                     // K or V of a stage, bytes
     static constexpr int STAGE = 2 * HALF;
     static constexpr int STAGES = 49152 / STAGE < 8 ? 49152 / STAGE : 8;  // 3 at d = 128; 3 blocks an SM
     static constexpr int ROWS = kRows;                        // query rows a warp
     static constexpr int OROW = D + 4;                        // floats of a row of the merge
     static constexpr int RING_OFF = 0;
     static constexpr int META_OFF = STAGES * STAGE;
-    static constexpr int MERGE_OFF = META_OFF + STAGES * 80;
+    static constexpr int MERGE_OFF = META_OFF + STAGES * 128;
     static constexpr int ML_OFF = MERGE_OFF + kDecWarps * ROWS * OROW * 4;
     static constexpr int BAR_OFF = ML_OFF + kDecWarps * ROWS * 8;
     static constexpr int FLAG_OFF = BAR_OFF + 16 * STAGES + 16;  // full, empty, merge
@@ -79,11 +81,11 @@ struct DecCfg {
 
 // What the computing warps know of a stage.
 struct __align__(16) StageMeta {
-    float k_scale[kSubs], v_scale[kSubs];
-    int key0[kSubs];  // position of the 16-key tile's first key, or kNoKey
+    float k_scale[kMaxSubs], v_scale[kMaxSubs];
+    int key0[kMaxSubs];  // position of the 16-key tile's first key, or kNoKey
     int flags, b, i, head, group, pad[3];
 };
-static_assert(sizeof(StageMeta) == 80, "stage record");
+static_assert(sizeof(StageMeta) == 128, "stage record");
 constexpr int kFirst = 1, kLast = 2, kHeadPart = 4, kTailPart = 8;
 constexpr int kNoKey = 0x7FFFFF00;  // behind every context
 
@@ -138,7 +140,7 @@ struct Work {
     int slots;
     int B, R, groups;  // rows of a segment (G Nq, or G with listed pages), row groups
     int row_warps;     // warps along the rows (1, 2, 4), the others along the keys
-    int log2_box;      // keys of one copy: 64, or a page if that is smaller
+    int log2_box;      // keys of one copy: a page, or a stage if that is smaller
     float scale_log2;
     // workspace: [0] blocks' share, [1 + b] first unit of sequence b; then the parts
     long long *plan;
@@ -146,6 +148,7 @@ struct Work {
 };
 
 // Units of query i's segment of a sequence of `len` keys (all queries' with no list).
+template <int LOG2_STEP>
 __device__ __forceinline__ int units_of(const Work &w, int len, int i)
 {
     int keys = len;
@@ -153,14 +156,15 @@ __device__ __forceinline__ int units_of(const Work &w, int len, int i)
         const int n = (context(w.q, len, i) + w.cache.page - 1) >> w.cache.log2_page;
         keys = min(n, w.slots) << w.cache.log2_page;
     }
-    return keys > 0 ? ((keys - 1) >> kLog2Step) + 1 : 0;
+    return keys > 0 ? ((keys - 1) >> LOG2_STEP) + 1 : 0;
 }
+template <int LOG2_STEP>
 __device__ __forceinline__ long long units_of_sequence(const Work &w, int b)
 {
     const int len = w.batch.length(b, w.cache.log2_page);
     long long n = 0;
     for (int i = 0; i < (w.pages ? w.q.Nq : 1); ++i)
-        n += units_of(w, len, i);
+        n += units_of<LOG2_STEP>(w, len, i);
     return n * w.cache.heads * w.groups;
 }
 
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
         const int b0 = min(w.B, t * each), b1 = min(w.B, b0 + each);
         long long sum = 0;
         for (int x = b0; x < b1; ++x)
-            sum += units_of_sequence(w, x);
+            sum += units_of_sequence<F::LOG2_STEP>(w, x);
         long long incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -280,13 +284,13 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
             long long y = at;
             for (int x = b0; x < b1; ++x) {
                 w.plan[1 + x] = y;
-                y += units_of_sequence(w, x);
+                y += units_of_sequence<F::LOG2_STEP>(w, x);
             }
         }
         if (first_unit >= at && first_unit < incl) {
             int x = b0;
             for (; x + 1 < b1; ++x) {
-                const long long n = units_of_sequence(w, x);
+                const long long n = units_of_sequence<F::LOG2_STEP>(w, x);
                 if (first_unit < at + n)
                     break;
                 at += n;
@@ -308,7 +312,7 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
         auto open_query = [&]() {
             len = b < w.B ? w.batch.length(b, w.cache.log2_page) : 0;
             ctx = w.pages ? context(w.q, len, i) : len;
-            units = units_of(w, len, i);
+            units = units_of<F::LOG2_STEP>(w, len, i);
         };
         const int per_unit = w.cache.heads * w.groups;
         open_query();
@@ -321,7 +325,7 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
         const int seg = off >> 31 ? static_cast<int>(off / units) : static_cast<int>(off) / units;
         int head = seg / w.groups, group = seg % w.groups;
         int unit = static_cast<int>(off - static_cast<long long>(seg) * units);
-        const int log2_boxes = kLog2Step - w.log2_box;  // copies of a stage: 1, 2 or 4
+        const int log2_boxes = F::LOG2_STEP - w.log2_box;  // copies of a stage: 1 to 8
         const int box = 1 << w.log2_box, batch_units = 32 >> log2_boxes;
         const uint64_t policy = l2_policy_evict_first();
         bool opened = true, ok = true;  // opened: the next unit is this block's first of its segment
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
         while (done < all && ok) {
             // lane l: page and scales of the l-th of the next 32 copies of this segment
             const int here = min(min(batch_units, units - unit), all - done);
-            const int key = (unit << kLog2Step) + lane * box;
+            const int key = (unit << F::LOG2_STEP) + lane * box;
             int at = key >> w.cache.log2_page, key0 = key, p = -1;
             float ks = 1.f, vs = 1.f;
             if ((lane >> log2_boxes) < here) {
@@ -372,7 +376,7 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                     tma_load_3d(dst, &maps.k[0], full(s), 0, y, ph, policy);
                     tma_load_3d(dst + F::HALF, &maps.v[0], full(s), 0, y, ph, policy);
                     if (F::PARTS == 2) {
-                        const uint32_t dst1 = sbase + F::RING_OFF + s * F::STAGE + kStep * F::W0 + row0 * F::W1;
+                        const uint32_t dst1 = sbase + F::RING_OFF + s * F::STAGE + F::STEP * F::W0 + row0 * F::W1;
                         tma_load_3d(dst1, &maps.k[1], full(s), F::W0, y, ph, policy);
                         tma_load_3d(dst1 + F::HALF, &maps.v[1], full(s), F::W0, y, ph, policy);
                     }
@@ -511,10 +515,10 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                     acc[j][u] = 0.f;
         }
 
-        for (int set = wk; set < kSubs / J; set += key_warps) {
+        for (int set = wk; set < F::SUBS / J; set += key_warps) {
             // J tiles at once: one look at the reference, and twice the independent work
             const int sub0 = set * J;
-            const bool last_set = set + key_warps >= kSubs / J;
+            const bool last_set = set + key_warps >= F::SUBS / J;
             int key0[J];
             int nearest = kNoKey, farthest = 0;
 #pragma unroll
@@ -532,7 +536,7 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                 continue;
             }
             const uint32_t k0 = sbase + F::RING_OFF + slot * F::STAGE + sub0 * kTile * F::W0, v0 = k0 + F::HALF;
-            const uint32_t k1 = sbase + F::RING_OFF + slot * F::STAGE + kStep * F::W0 + sub0 * kTile * F::W1;  // d = 96
+            const uint32_t k1 = sbase + F::RING_OFF + slot * F::STAGE + F::STEP * F::W0 + sub0 * kTile * F::W1;  // d = 96
             // ---- S^T = K Q^T ----
             float e[J][4];
 #pragma unroll
@@ -813,7 +817,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     const int i = static_cast<int>(x % queries), b = static_cast<int>(x / queries);
     const int group = row / rows_block;
     const int len = w.batch.length(b, w.cache.log2_page);
-    const int units = units_of(w, len, i);
+    const int units = units_of<DecCfg<D>::LOG2_STEP>(w, len, i);
     const long long orow =
         w.pages ? ((static_cast<long long>(b) * w.cache.heads + head) * w.q.G + row) * w.q.Nq + i
                 : (static_cast<long long>(b) * w.cache.heads + head) * w.R + row;
@@ -829,7 +833,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     const long long share = w.plan[0];
     long long first = w.plan[1 + b];
     for (int y = 0; y < i; ++y)
-        first += static_cast<long long>(units_of(w, len, y)) * w.cache.heads * w.groups;
+        first += static_cast<long long>(units_of<DecCfg<D>::LOG2_STEP>(w, len, y)) * w.cache.heads * w.groups;
     first += (static_cast<long long>(head) * w.groups + group) * units;
     const int x0 = static_cast<int>(first / share), x1 = static_cast<int>((first + units - 1) / share);
     if (x0 == x1)

@@ -108,18 +108,15 @@ struct E4M3 {
         asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(*reinterpret_cast<const uint32_t *>(&y)));
         return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
     }
-    // Two codes to fp16, exactly.
-    static __device__ __forceinline__ uint32_t half2_of(uint16_t w)
-    {
-        uint32_t r;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(w));
-        return r;
-    }
-    // Four codes to four fp16.
+    // Four codes to four fp16, exactly.
     static __device__ __forceinline__ void halves(uint32_t w, uint32_t &lo, uint32_t &hi)
     {
-        lo = half2_of(static_cast<uint16_t>(w & 0xFFFFu));
-        hi = half2_of(static_cast<uint16_t>(w >> 16));
+        asm("{\n\t.reg .b16 l, h;\n\t"
+            "mov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=&r"(lo), "=r"(hi)
+            : "r"(w));
     }
 };
 
