@@ -17,7 +17,6 @@ whatever they hold then.  What they hold cannot be checked by the call: a page
 number or length outside the cache is left out, and
 ``fa_last_device_status`` reports it.
 """
-from contextlib import nullcontext
 from struct import Struct
 from typing import NamedTuple, Optional
 
@@ -108,21 +107,21 @@ def _check_batch(index, page_table, seq_lens):
     return B, page_table.stride(0) if B > 1 else P, P
 
 
-def _rows(t, name, dim, index, d):
-    """Checks an input whose rows of d values are contiguous; returns its type's code, and the strides of its other
-    dimensions (those of a dimension of one do not matter)."""
+def _code(t, name, dim, index, d):
+    """Checks an input whose rows of d values are contiguous; returns its type's code."""
     try:
-        shape, strides = t.shape, t.stride()
-        if len(shape) != dim or shape[-1] != d or strides[-1] != 1 or t.get_device() != index:
-            if t.numel() or len(shape) != dim or t.get_device() != index:
-                raise TypeError
-        code = _CODES.get(t.dtype)
-    except (AttributeError, TypeError):
+        shape = t.shape
+        good = (len(shape) == dim and shape[-1] == d and t.get_device() == index
+                and (t.stride(-1) == 1 or t.numel() == 0))
+    except (AttributeError, TypeError, IndexError):
+        good = False
+    if not good:
         raise FAError(1, "%s must be a %d-dimensional tensor of rows of %d contiguous values on the cache's device"
-                      % (name, dim, d)) from None
+                      % (name, dim, d))
+    code = _CODES.get(t.dtype)
     if code is None:
         raise FAError(2, "%s must be float16 or bfloat16, got %s" % (name, t.dtype))
-    return code, [s if n > 1 else 0 for s, n in zip(strides, shape)][:-1]
+    return code
 
 
 def _output(t, name, shape, dtype, index):
@@ -132,28 +131,18 @@ def _output(t, name, shape, dtype, index):
     return t
 
 
-class _On:
-    """A call on a device that is not the current one, or on a given stream: what it allocates inside belongs to
-    that stream."""
-
-    def __init__(self, index, stream):
-        if stream is not None and stream.device.index != index:
-            raise FAError(1, "the stream must be one of the cache's device")
-        self.within = torch.cuda.device(index) if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        return self.within.__enter__()
-
-    def __exit__(self, *exc):
-        return self.within.__exit__(*exc)
+def _elsewhere(index, stream):
+    """Whether a call has to go to a device or stream that is not the current one."""
+    return stream is not None or torch.cuda.current_device() != index
 
 
-_HERE = nullcontext()
-
-
-def _on(index, stream):
-    """The context of a call: none where the current device and stream are meant (the usual call, and a cheap one)."""
-    return _HERE if stream is None and torch.cuda.current_device() == index else _On(index, stream)
+def _there(index, stream):
+    """The context for it.  What a call allocates inside belongs to that stream."""
+    if stream is None:
+        return torch.cuda.device(index)
+    if stream.device.index != index:
+        raise FAError(1, "the stream must be one of the cache's device")
+    return torch.cuda.stream(stream)
 
 
 def _stream(index):
@@ -165,17 +154,11 @@ def _stream(index):
 _stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
 
 
-def _workspace(workspace, need, index):
-    if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=_device(index))
+def _workspace(workspace, index):
     if (not isinstance(workspace, torch.Tensor) or workspace.get_device() != index
             or not workspace.is_contiguous()):
         raise FAError(1, "workspace must be a contiguous tensor on the cache's device")
     return workspace
-
-
-def _device(index):
-    return torch.device("cuda", index)
 
 
 def fa_cache_write(cache, k, v, page_table, seq_lens, cu_seqlens=None, stream=None):
@@ -184,20 +167,22 @@ def fa_cache_write(cache, k, v, page_table, seq_lens, cu_seqlens=None, stream=No
     cu_seqlens every sequence gets T / B.  The caller then adds the counts to seq_lens.  A partly filled
     page keeps its scale or takes the larger one of its new tokens; see include/fa.h."""
     desc, heads, d, index = _describe(cache)
+    if _elsewhere(index, stream):
+        with _there(index, stream):
+            return fa_cache_write(cache, k, v, page_table, seq_lens, cu_seqlens)
     B, stride, P = _check_batch(index, page_table, seq_lens)
-    code, k_strides = _rows(k, "k", 3, index, d)
-    v_code, v_strides = _rows(v, "v", 3, index, d)
+    code = _code(k, "k", 3, index, d)
     shape = k.shape
-    if v_code != code or v.shape != shape or shape[1] != heads:
+    if _code(v, "v", 3, index, d) != code or v.shape != shape or shape[1] != heads:
         raise FAError(1, "k and v must be [T, heads, d] of one dtype")
     cu = None
     if cu_seqlens is not None:
         _output(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, index)
         cu = cu_seqlens.data_ptr()
-    with _on(index, stream):
-        st = fa_cache_write_raw(desc, k.data_ptr(), v.data_ptr(), *k_strides, *v_strides, cu,
-                                seq_lens.data_ptr(), page_table.data_ptr(), stride, P, B, shape[0], code,
-                                _stream(index))
+    kt, kh, _ = k.stride()
+    vt, vh, _ = v.stride()
+    st = fa_cache_write_raw(desc, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, cu, seq_lens.data_ptr(),
+                            page_table.data_ptr(), stride, P, B, shape[0], code, _stream(index))
     if st != 0:
         raise FAError(st, "fa_cache_write")
 
@@ -206,22 +191,24 @@ def fa_cache_read(cache, page_table, seq_lens, N, dtype=torch.bfloat16, k=None, 
     """The first N positions of every sequence as 16-bit k, v [B, heads, N, d], zeros behind seq_lens[b].
     k, v: optional preallocated outputs (their dtype counts then).  Returns (k, v)."""
     desc, heads, d, index = _describe(cache)
+    if _elsewhere(index, stream):
+        with _there(index, stream):
+            return fa_cache_read(cache, page_table, seq_lens, N, dtype, k, v)
     B, stride, P = _check_batch(index, page_table, seq_lens)
     given = k if k is not None else v
     if isinstance(given, torch.Tensor):
         dtype = given.dtype
-    if dtype not in _CODES:
+    code = _CODES.get(dtype)
+    if code is None:
         raise FAError(2, "dtype must be float16 or bfloat16, got %s" % dtype)
     if N < 0:
         raise FAError(1, "N must not be negative")
     shape = (B, heads, N, d)
-    with _on(index, stream):
-        k = (torch.empty(shape, dtype=dtype, device=_device(index)) if k is None
-             else _output(k, "k", shape, dtype, index))
-        v = (torch.empty(shape, dtype=dtype, device=_device(index)) if v is None
-             else _output(v, "v", shape, dtype, index))
-        st = fa_cache_read_raw(desc, k.data_ptr(), v.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), stride,
-                               P, B, N, _CODES[dtype], _stream(index))
+    device = cache.k.device
+    k = torch.empty(shape, dtype=dtype, device=device) if k is None else _output(k, "k", shape, dtype, index)
+    v = torch.empty(shape, dtype=dtype, device=device) if v is None else _output(v, "v", shape, dtype, index)
+    st = fa_cache_read_raw(desc, k.data_ptr(), v.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), stride, P, B,
+                           N, code, _stream(index))
     if st != 0:
         raise FAError(st, "fa_cache_read")
     return k, v
@@ -235,11 +222,14 @@ def fa_decode_cache(q, cache, page_table, seq_lens, pages=None, o=None, lse=None
     query and KV head reads (``fa_cache_select``), or None for all.  scale defaults to 1/sqrt(d).
     Returns (o, lse); a row without keys has o = 0, lse = -inf."""
     desc, heads, d, index = _describe(cache)
+    if _elsewhere(index, stream):
+        with _there(index, stream):
+            return fa_decode_cache(q, cache, page_table, seq_lens, pages, o, lse, scale, causal, return_lse, workspace)
     B, stride, P = _check_batch(index, page_table, seq_lens)
-    code, strides = _rows(q, "q", 4, index, d)
+    code = _code(q, "q", 4, index, d)
     shape = q.shape
-    _, Hq, Nq, _ = shape
-    if shape[0] != B or Hq % heads:
+    Bq, Hq, Nq, _ = shape
+    if Bq != B or Hq % heads:
         raise FAError(1, "q must be [B, Hq, Nq, d] with Hq a multiple of the cache's heads")
     slots, listed = 0, None
     if pages is not None:
@@ -247,21 +237,25 @@ def fa_decode_cache(q, cache, page_table, seq_lens, pages=None, o=None, lse=None
         listed = _output(pages, "pages", (B, heads, Nq, slots), torch.int32, index).data_ptr()
     if scale is None:
         scale = float(d) ** -0.5
-    need = fa_decode_cache_workspace_size(B, Hq, heads, Nq, d)
-    with _on(index, stream):
-        if o is None:
-            o = torch.empty(shape, dtype=q.dtype, device=_device(index))
-        else:
-            _output(o, "o", shape, q.dtype, index)
-        if lse is not None:
-            _output(lse, "lse", shape[:3], torch.float32, index)
-        elif return_lse:
-            lse = torch.empty(shape[:3], dtype=torch.float32, device=_device(index))
-        workspace = _workspace(workspace, need, index)
-        st = fa_decode_cache_raw(desc, q.data_ptr(), *strides, o.data_ptr(),
-                                 lse.data_ptr() if lse is not None else None, seq_lens.data_ptr(),
-                                 page_table.data_ptr(), stride, P, listed, slots, workspace.data_ptr(),
-                                 workspace.nbytes, B, Hq, Nq, scale, 1 if causal else 0, code, _stream(index))
+    device = cache.k.device
+    if o is None:
+        o = torch.empty(shape, dtype=q.dtype, device=device)
+    else:
+        _output(o, "o", shape, q.dtype, index)
+    if lse is not None:
+        _output(lse, "lse", (B, Hq, Nq), torch.float32, index)
+    elif return_lse:
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device)
+    if workspace is None:
+        need = fa_decode_cache_workspace_size(B, Hq, heads, Nq, d)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    else:
+        _workspace(workspace, index)
+    sb, sh, sn, _ = q.stride()
+    st = fa_decode_cache_raw(desc, q.data_ptr(), sb, sh, sn, o.data_ptr(), lse.data_ptr() if lse is not None else None,
+                             seq_lens.data_ptr(), page_table.data_ptr(), stride, P, listed, slots,
+                             workspace.data_ptr(), workspace.nbytes, B, Hq, Nq, scale, 1 if causal else 0, code,
+                             _stream(index))
     if st != 0:
         raise FAError(st, "fa_decode_cache")
     return o, lse
@@ -273,24 +267,31 @@ def fa_cache_select(q, cache, page_table, seq_lens, slots, keep_first=1, keep_la
     keep_first, the last keep_last and, by the mean keys' scores, the best of the others; all of them
     where there are no more than slots.  Arguments as for fa_decode_cache."""
     desc, heads, d, index = _describe(cache)
+    if _elsewhere(index, stream):
+        with _there(index, stream):
+            return fa_cache_select(q, cache, page_table, seq_lens, slots, keep_first, keep_last, causal, pages, workspace)
     B, stride, P = _check_batch(index, page_table, seq_lens)
-    code, strides = _rows(q, "q", 4, index, d)
-    _, Hq, Nq, _ = q.shape
-    if q.shape[0] != B or Hq % heads:
+    code = _code(q, "q", 4, index, d)
+    Bq, Hq, Nq, _ = q.shape
+    if Bq != B or Hq % heads:
         raise FAError(1, "q must be [B, Hq, Nq, d] with Hq a multiple of the cache's heads")
     if slots < 1:
         raise FAError(1, "slots must be at least 1")
-    need = fa_cache_select_workspace_size(B, heads, Nq, P)
     shape = (B, heads, Nq, slots)
-    with _on(index, stream):
-        if pages is None:
-            pages = torch.empty(shape, dtype=torch.int32, device=_device(index))
-        else:
-            _output(pages, "pages", shape, torch.int32, index)
-        workspace = _workspace(workspace, need, index)
-        st = fa_cache_select_raw(desc, q.data_ptr(), *strides, seq_lens.data_ptr(), page_table.data_ptr(), stride, P,
-                                 pages.data_ptr(), slots, keep_first, keep_last, workspace.data_ptr(),
-                                 workspace.nbytes, B, Hq, Nq, 1 if causal else 0, code, _stream(index))
+    device = cache.k.device
+    if pages is None:
+        pages = torch.empty(shape, dtype=torch.int32, device=device)
+    else:
+        _output(pages, "pages", shape, torch.int32, index)
+    if workspace is None:
+        need = fa_cache_select_workspace_size(B, heads, Nq, P)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    else:
+        _workspace(workspace, index)
+    sb, sh, sn, _ = q.stride()
+    st = fa_cache_select_raw(desc, q.data_ptr(), sb, sh, sn, seq_lens.data_ptr(), page_table.data_ptr(), stride, P,
+                             pages.data_ptr(), slots, keep_first, keep_last, workspace.data_ptr(), workspace.nbytes, B,
+                             Hq, Nq, 1 if causal else 0, code, _stream(index))
     if st != 0:
         raise FAError(st, "fa_cache_select")
     return pages

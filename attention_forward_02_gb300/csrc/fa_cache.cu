@@ -185,9 +185,12 @@ bool strides_ok(long long a, long long b, long long c = 0) { return a >= 0 && b 
 bool strides_aligned(long long a, long long b, long long c = 0) { return ((a | b | c) & 7) == 0; }
 
 // Checks of the queries of fa_decode_cache and fa_cache_select.
-fa_status_t check_queries(const fa_cache_t *cache, const void *q, long long sb, long long sh, long long sr, int B,
+fa_status_t check_queries(const fa_cache_t *cache, const void *q, long long &sb, long long &sh, long long &sr, int B,
                           int Hq, int Nq, int causal, fa_dtype_t dtype, Range *r)
 {
+    sb = B == 1 ? 0 : sb;  // the stride of a dimension of one means nothing
+    sh = Hq == 1 ? 0 : sh;
+    sr = Nq == 1 ? 0 : sr;
     if (causal != 0 && causal != 1)
         return FA_ERR_INVALID_ARG;
     if (dtype != FA_FP16 && dtype != FA_BF16)
@@ -277,6 +280,10 @@ fa_status_t fa_cache_write(const fa_cache_t *cache, const void *k, const void *v
         return FA_OK;  // empty problem
     if ((s = check_batch(seq_lens, page_table, table_stride, max_pages, B, cache->page)) != FA_OK)
         return s;
+    if (T == 1)  // the stride of a dimension of one means nothing
+        k_token_stride = v_token_stride = 0;
+    if (cache->heads == 1)
+        k_head_stride = v_head_stride = 0;
     if (!k || !v || !strides_ok(k_token_stride, k_head_stride) || !strides_ok(v_token_stride, v_head_stride) ||
         (!cu_seqlens && T % B != 0))
         return FA_ERR_INVALID_ARG;

@@ -286,8 +286,9 @@ typedef struct {
  *
  *  cache   : the cache (host struct; its buffers on the device).
  *  k, v    : new rows, element (t, h, c) at t * token_stride + h * head_stride
- *            + c (strides in elements, multiples of 8); 16-byte aligned; must
- *            not overlap the cache.  Read only.
+ *            + c (strides in elements, multiples of 8, not negative; that of a
+ *            dimension of one is ignored); 16-byte aligned; must not overlap
+ *            the cache.  Read only.
  *  cu_seqlens : [B + 1] int32 on the device, ascending, 0 .. T, or NULL: T / B
  *            tokens for every sequence (T a multiple of B).  Rows from
  *            cu_seqlens[B] on are ignored.
@@ -336,7 +337,7 @@ FA_API size_t fa_decode_cache_workspace_size(int B, int Hq, int Hkv, int Nq, int
  * A row that sees no key gets O = 0 and LSE = -infinity.
  *
  *  q       : element (b, h, i, c) at b * q_batch_stride + h * q_head_stride +
- *            i * q_row_stride + c (elements, multiples of 8); 16-byte aligned.
+ *            i * q_row_stride + c (strides as in fa_cache_write); 16-byte aligned.
  *  o       : contiguous [B, Hq, Nq, d] of `dtype`, 16-byte aligned.
  *  lse     : [B, Hq, Nq] fp32, or NULL.
  *  seq_lens: [B] int32 on the device: keys, the queries' own among them.  A
