@@ -32,25 +32,32 @@ struct CacheState {
 };
 CacheState g_cache[kMaxDevices];
 
-template <int D, int J>
+// The decoding kernel: warps of 8 or 16 query rows, one or two 16-key tiles at once.
+template <int D, int NT, typename T, typename C>
+constexpr auto decode_kernel()
+{
+    return fa::cache::fa_cache_decode_kernel<D, NT, D <= 64 ? 2 : 1, T, C>;
+}
+
+template <int D, int NT>
 cudaError_t set_smem_attr()
 {
     using namespace fa::cache;
     const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, J, __half, E4M3>, a, DecCfg<D>::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, NT, __half, E4M3>(), a, DecCfg<D>::SMEM);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, J, __half, I8>, a, DecCfg<D>::SMEM);
+        e = cudaFuncSetAttribute(decode_kernel<D, NT, __half, I8>(), a, DecCfg<D>::SMEM);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, J, __nv_bfloat16, E4M3>, a, DecCfg<D>::SMEM);
+        e = cudaFuncSetAttribute(decode_kernel<D, NT, __nv_bfloat16, E4M3>(), a, DecCfg<D>::SMEM);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(fa_cache_decode_kernel<D, J, __nv_bfloat16, I8>, a, DecCfg<D>::SMEM);
+        e = cudaFuncSetAttribute(decode_kernel<D, NT, __nv_bfloat16, I8>(), a, DecCfg<D>::SMEM);
     return e;
 }
 
 template <int D>
 cudaError_t set_smem_attrs()
 {
-    const cudaError_t e = set_smem_attr<D, D <= 64 ? 2 : 1>();
+    const cudaError_t e = set_smem_attr<D, 1>();
     return e == cudaSuccess ? set_smem_attr<D, 2>() : e;
 }
 
@@ -65,13 +72,19 @@ void init_cache(CacheState &st)
     if (st.err == cudaSuccess) st.err = set_smem_attrs<128>();
 }
 
-// Warps of a block along the R query rows of a KV head (8 rows each; the others
-// take keys).  More rows than 32 go to further row groups, which read the codes
-// again.  Two or four warps that convert the same codes are faster than one that
-// multiplies them with 16 or 32 rows: 16 rows, d = 128, int8: 93 against 101 us
-// (attend_spec's sizes: 16 x 16,384 keys, 8 heads), as 12 warps an SM hide latency
-// where the registers of 16 rows leave 8.
-int row_warps_of(int R) { return R <= 8 ? 1 : R <= 16 ? 2 : 4; }
+// How the R query rows of a KV head are laid out: tiles of 8 rows a warp, warps of
+// a block along the rows (the others take keys), rows a block.  Rows beyond 64 go
+// to further row groups, which read the codes again.
+struct Shape {
+    int tiles, row_warps, rows_block;
+};
+Shape shape_of(int R)
+{
+    if (R <= 8)
+        return {1, 1, 8};
+    const int row_warps = R <= 16 ? 1 : R <= 32 ? 2 : 4;
+    return {2, row_warps, 16 * row_warps};
+}
 
 // A code buffer as [num_pages * heads, page, d] bytes: boxes of `box` rows of
 // `width` columns, each row swizzled by its width.
@@ -378,7 +391,7 @@ size_t fa_decode_cache_workspace_size(int B, int Hq, int Hkv, int Nq, int d)
     if (B < 0 || Hq < 0 || Hkv < 1 || Hq % Hkv != 0 || Nq < 1 || Nq > kMaxNq ||
         (d != 32 && d != 64 && d != 96 && d != 128))
         return 0;
-    const int rows_block = fa::cache::kRows * row_warps_of(Hq / Hkv * Nq);
+    const int rows_block = shape_of(Hq / Hkv * Nq).rows_block;
     return plan_bytes(B) + static_cast<size_t>(2 * fa::cache::kMaxBlocks) * rows_block * (d + 2) * 4;
 }
 
@@ -437,8 +450,9 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
     w.slots = slots;
     w.B = B;
     w.R = qs.G * (pages ? 1 : Nq);
-    w.row_warps = row_warps_of(w.R);
-    const int rows_block = fa::cache::kRows * w.row_warps;
+    const Shape shape = shape_of(w.R);
+    w.row_warps = shape.row_warps;
+    const int rows_block = shape.rows_block;
     w.groups = (w.R + rows_block - 1) / rows_block;
     w.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     w.plan = static_cast<long long *>(workspace);
@@ -469,8 +483,7 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
             using T = decltype(t);
             using C = decltype(code);
             const bool first = launch_dependent(
-                w.row_warps == 1 ? fa::cache::fa_cache_decode_kernel<D, D <= 64 ? 2 : 1, T, C>
-                                 : fa::cache::fa_cache_decode_kernel<D, 2, T, C>,
+                shape.tiles == 1 ? decode_kernel<D, 1, T, C>() : decode_kernel<D, 2, T, C>(),
                 static_cast<unsigned>(blocks), fa::cache::kDecThreads, fa::cache::DecCfg<D>::SMEM, cs, maps, w,
                 static_cast<T *>(o), lse);
             if (!first)

@@ -49,7 +49,6 @@ constexpr int kDecWarps = 4;      // that compute
 constexpr int kDecThreads = 32 * (kDecWarps + 1);
 constexpr int kTile = 16;         // keys of one product
 constexpr int kMaxSubs = 8;       // tiles of a stage
-constexpr int kRows = 8;          // query rows a warp
 constexpr int kBlocksPerSm = 3;
 constexpr int kMaxBlocks = 640;   // of the persistent grid
 constexpr int kCombineThreads = 128;
@@ -67,13 +66,12 @@ struct DecCfg {
     static constexpr int HALF = STEP * D;                     // K or V of a stage, bytes
     static constexpr int STAGE = 2 * HALF;
     static constexpr int STAGES = 49152 / STAGE < 8 ? 49152 / STAGE : 8;  // 3 at d = 128; 3 blocks an SM
-    static constexpr int ROWS = kRows;                        // query rows a warp
     static constexpr int OROW = D + 4;                        // floats of a row of the merge
     static constexpr int RING_OFF = 0;
     static constexpr int META_OFF = STAGES * STAGE;
     static constexpr int MERGE_OFF = META_OFF + STAGES * 128;
-    static constexpr int ML_OFF = MERGE_OFF + kDecWarps * ROWS * OROW * 4;
-    static constexpr int BAR_OFF = ML_OFF + kDecWarps * ROWS * 8;
+    static constexpr int ML_OFF = MERGE_OFF + kDecWarps * 8 * OROW * 4;  // eight rows a warp at a time
+    static constexpr int BAR_OFF = ML_OFF + kDecWarps * 8 * 8;
     static constexpr int FLAG_OFF = BAR_OFF + 16 * STAGES + 16;  // full, empty, merge
     static constexpr int SMEM = FLAG_OFF + 16 + 16 * kDecWarps + 1024;  // and room to align the ring
     static_assert(STAGES * STAGE % 16 == 0 && STAGE % 1024 == 0, "alignment of the ring");
@@ -207,6 +205,12 @@ __device__ __forceinline__ void load_words(uint32_t *w, uint32_t addr)
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
 }
 
+__device__ __forceinline__ void store_pair(uint32_t addr, uint32_t a, uint32_t b)
+{
+    if (smem_ok(addr, 8, 8))
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
 // Bytes of a word that are e4m3 NaN codes, as their top bits.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
@@ -214,7 +218,7 @@ struct Maps {
     CUtensorMap k[2], v[2];  // of the column parts
 };
 
-template <int D, int J, typename T, typename C>
+template <int D, int NT, int J, typename T, typename C>
 __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
     fa_cache_decode_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Work w, T *__restrict__ out,
                            float *__restrict__ lse)
@@ -235,7 +239,8 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + F::FLAG_OFF);
     StageMeta *meta = reinterpret_cast<StageMeta *>(smem + F::META_OFF);
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int rows_block = F::ROWS * w.row_warps;
+    constexpr int ROWS = 8 * NT;  // query rows a warp
+    const int rows_block = ROWS * w.row_warps;
 
     if (t == 0) {
         for (int s = 0; s < S; ++s) {
@@ -439,12 +444,17 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
     const int g = lane >> 2, c = lane & 3;
     const int key_warps = kDecWarps / w.row_warps;
     const int wk = warp % key_warps, wr = warp / key_warps;
-    uint32_t qb[KW][2];   // Q^T operand: query row g, its d in the order of the thread's K words
-    float qf[2];          // per query row 2 c, 2 c + 1: scale to log2 units
-    uint32_t behind = 0;  // ... keys that it sees beyond `least`, a byte each
-    float m[2], l[2], acc[D / 16][4];
+    // Q^T operand: of query rows g (+ 8), their d in the order of the thread's K
+    // words; in registers for eight rows, for sixteen in the warp's merge area
+    // (each lane its own), where registers would cost a third of the warps
+    uint32_t qb[NT == 1 ? KW : 1][2];
+    const uint32_t q_own = sbase + F::MERGE_OFF + warp * (8 * F::OROW * 4) + lane * 16;
+    static_assert(KW * 512 <= 8 * F::OROW * 4, "sixteen rows of Q fit the merge area");
+    float qf[NT][2];          // per query row 2 c, 2 c + 1 (+ 8): scale to log2 units
+    uint32_t behind = 0;      // ... keys that it sees beyond `least`, a byte each
+    float m[NT][2], l[NT][2], acc[D / 16][NT][4];
     int least = 0, most = 0;  // keys that all rows see (negative: the first ones see none), that any row sees
-    auto limit = [&](int u) -> int { return least + static_cast<int>((behind >> (8 * u)) & 255u); };
+    auto limit = [&](int nt, int u) -> int { return least + static_cast<int>((behind >> (8 * (2 * nt + u))) & 255u); };
     int4 *segment = reinterpret_cast<int4 *>(smem + F::FLAG_OFF + 16) + warp;  // b, i, head, group
     uint32_t merges = 0;
     // a barrier of the computing warps whose wait is bounded
@@ -468,51 +478,60 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
             const int n = w.batch.length(b_seg, w.cache.log2_page);
             most = w.pages ? context(w.q, n, i_seg) : n;
             least = w.pages || !w.q.causal ? most : n - w.q.Nq + 1;
-            const int row = group * rows_block + wr * F::ROWS + g;
-            const int hq = w.pages ? row : row / w.q.Nq, qi = w.pages ? i_seg : row % w.q.Nq;
-            const T *src = static_cast<const T *>(w.q.q) + b_seg * w.q.batch_stride +
-                           static_cast<long long>(head * w.q.G + hq) * w.q.head_stride + qi * w.q.row_stride;
-            float top = 0.f;
+            behind = 0;
 #pragma unroll
-            for (int s = 0; s < KW; ++s) {
-                const int d = k_column<D>(c, s);
-                uint2 x = make_uint2(0, 0);
-                if (row < w.R)
-                    x = *reinterpret_cast<const uint2 *>(src + d);
-                qb[s][0] = x.x;
-                qb[s][1] = x.y;
-                const float2 y = DTypeTraits<T>::unpack(x.x), z = DTypeTraits<T>::unpack(x.y);
-                const float f[4] = {fabsf(y.x), fabsf(y.y), fabsf(z.x), fabsf(z.y)};
+            for (int nt = 0; nt < NT; ++nt) {
+                const int row = group * rows_block + wr * ROWS + nt * 8 + g;
+                const int hq = w.pages ? row : row / w.q.Nq, qi = w.pages ? i_seg : row % w.q.Nq;
+                const T *src = static_cast<const T *>(w.q.q) + b_seg * w.q.batch_stride +
+                               static_cast<long long>(head * w.q.G + hq) * w.q.head_stride + qi * w.q.row_stride;
+                uint2 x[KW];
+                float top = 0.f;
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (f[u] <= 3.402823466e38f)
-                        top = fmaxf(top, f[u]);
-            }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = top > 0.f ? max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -100) : 0;
-            const float by = pow2f(-e);
+                for (int s = 0; s < KW; ++s) {
+                    x[s] = make_uint2(0, 0);
+                    if (row < w.R)
+                        x[s] = *reinterpret_cast<const uint2 *>(src + k_column<D>(c, s));
+                }
 #pragma unroll
-            for (int s = 0; s < KW; ++s)
+                for (int s = 0; s < KW; ++s) {
+                    const float2 y = DTypeTraits<T>::unpack(x[s].x), z = DTypeTraits<T>::unpack(x[s].y);
+                    const float f[4] = {fabsf(y.x), fabsf(y.y), fabsf(z.x), fabsf(z.y)};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (f[u] <= 3.402823466e38f)
+                            top = fmaxf(top, f[u]);
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int e = top > 0.f ? max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -100) : 0;
+                const float by = pow2f(-e);
+#pragma unroll
+                for (int s = 0; s < KW; ++s) {
+                    const float2 y = DTypeTraits<T>::unpack(x[s].x), z = DTypeTraits<T>::unpack(x[s].y);
+                    const uint32_t b0 = DTypeTraits<__half>::pack(y.x * by, y.y * by);
+                    const uint32_t b1 = DTypeTraits<__half>::pack(z.x * by, z.y * by);
+                    if constexpr (NT == 1) {
+                        qb[s][0] = b0;
+                        qb[s][1] = b1;
+                    } else {
+                        store_pair(q_own + s * 512 + nt * 8, b0, b1);
+                    }
+                }
+                const int extra = w.pages || !w.q.causal ? 0 : qi;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const float2 y = DTypeTraits<T>::unpack(qb[s][u]);
-                    qb[s][u] = DTypeTraits<__half>::pack(y.x * by, y.y * by);
+                    qf[nt][u] = pow2f(__shfl_sync(0xffffffffu, e, 8 * c + 4 * u)) * w.scale_log2;
+                    behind |= __shfl_sync(0xffffffffu, extra, 8 * c + 4 * u) << (8 * (2 * nt + u));
+                    m[nt][u] = -INFINITY;
+                    l[nt][u] = 0.f;
                 }
-            behind = 0;
-            const int extra = w.pages || !w.q.causal ? 0 : qi;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                qf[u] = pow2f(__shfl_sync(0xffffffffu, e, 8 * c + 4 * u)) * w.scale_log2;
-                behind |= __shfl_sync(0xffffffffu, extra, 8 * c + 4 * u) << (8 * u);
-                m[u] = -INFINITY;
-                l[u] = 0.f;
+                for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        acc[j][nt][u] = 0.f;
             }
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    acc[j][u] = 0.f;
         }
 
         for (int set = wk; set < F::SUBS / J; set += key_warps) {
@@ -538,7 +557,7 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
             const uint32_t k0 = sbase + F::RING_OFF + slot * F::STAGE + sub0 * kTile * F::W0, v0 = k0 + F::HALF;
             const uint32_t k1 = sbase + F::RING_OFF + slot * F::STAGE + F::STEP * F::W0 + sub0 * kTile * F::W1;  // d = 96
             // ---- S^T = K Q^T ----
-            float e[J][4];
+            float e[J][NT][4];
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 uint32_t kw[2][KW];
@@ -557,18 +576,32 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                         load_words<2>(&kw[r][4], k1 + j * kTile * F::W1 + k_offset<32>(g, c, 0) + r * 256);
                 }
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    e[j][u] = 0.f;
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        e[j][nt][u] = 0.f;
 #pragma unroll
                 for (int x = 0; x < KW; ++x) {
                     uint32_t a0, a1, a2, a3;
                     C::halves(kw[0][x], a0, a2);
                     C::halves(kw[1][x], a1, a3);
-                    mma_f16(e[j], a0, a1, a2, a3, qb[x][0], qb[x][1]);
+                    if constexpr (NT == 1) {
+                        mma_f16(e[j][0], a0, a1, a2, a3, qb[x][0], qb[x][1]);
+                    } else {
+                        uint32_t y[4];
+                        load_words<4>(y, q_own + x * 512);
+                        mma_f16(e[j][0], a0, a1, a2, a3, y[0], y[1]);
+                        mma_f16(e[j][1], a0, a1, a2, a3, y[2], y[3]);
+                    }
                 }
             }
             // ---- exponents of P v_scale, masks; does any outgrow its reference? ----
-            const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+            float ref[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    ref[nt][u] = m[nt][u] == -INFINITY ? 0.f : m[nt][u];
             float v_scale[J];
 #pragma unroll
             for (int j = 0; j < J; ++j) {
@@ -576,70 +609,83 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                 v_scale[j] = info->v_scale[sub0 + j];
                 const float ev = static_cast<float>(static_cast<int>(__float_as_uint(v_scale[j]) >> 23) - 127);
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    e[j][u] = fmaf(e[j][u], k_scale * qf[u & 1], ev - ref[u & 1]);
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        e[j][nt][u] = fmaf(e[j][nt][u], k_scale * qf[nt][u & 1], ev - ref[nt][u & 1]);
             }
             const bool masked = farthest + kTile > least;
             if (masked) {
 #pragma unroll
                 for (int j = 0; j < J; ++j)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (key0[j] + g + 8 * (u >> 1) >= limit(u & 1))
-                            e[j][u] = -INFINITY;
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (key0[j] + g + 8 * (u >> 1) >= limit(nt, u & 1))
+                                e[j][nt][u] = -INFINITY;
             }
             // with no reference yet, any score that is seen outgrows it
-            const float most_e[2] = {m[0] == -INFINITY ? -INFINITY : 8.f, m[1] == -INFINITY ? -INFINITY : 8.f};
             bool grown = false;
 #pragma unroll
-            for (int j = 0; j < J; ++j)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    grown |= !(e[j][u] <= most_e[u & 1]);
-            if (__any_sync(0xffffffffu, grown)) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float top = -INFINITY;
+                for (int u = 0; u < 4; ++u) {
+                    const float most_e = m[nt][u & 1] == -INFINITY ? -INFINITY : 8.f;
 #pragma unroll
                     for (int j = 0; j < J; ++j)
-                        top = fmaxf(top, fmaxf(e[j][u], e[j][u + 2]));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    const float next = fmaxf(m[u], top + ref[u]);
-                    const float alpha = next == m[u] ? 1.f : ex2(m[u] - next);
-                    const float down = next == -INFINITY ? 0.f : ref[u] - next;
-                    m[u] = next;
-                    l[u] *= alpha;
-#pragma unroll
-                    for (int j = 0; j < J; ++j) {
-                        e[j][u] += down;
-                        e[j][u + 2] += down;
-                    }
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        acc[j][u] *= alpha;
-                        acc[j][u + 2] *= alpha;
-                    }
+                        grown |= !(e[j][nt][u] <= most_e);
                 }
+            if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < J; ++j)
+                            top = fmaxf(top, fmaxf(e[j][nt][u], e[j][nt][u + 2]));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        const float next = fmaxf(m[nt][u], top + ref[nt][u]);
+                        const float alpha = next == m[nt][u] ? 1.f : ex2(m[nt][u] - next);
+                        const float down = next == -INFINITY ? 0.f : ref[nt][u] - next;
+                        m[nt][u] = next;
+                        l[nt][u] *= alpha;
+#pragma unroll
+                        for (int j = 0; j < J; ++j) {
+                            e[j][nt][u] += down;
+                            e[j][nt][u + 2] += down;
+                        }
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            acc[j][nt][u] *= alpha;
+                            acc[j][nt][u + 2] *= alpha;
+                        }
+                    }
             }
             // ---- P, and O^T += V^T P^T ----
-            uint32_t pb[J][2];
+            uint32_t pb[J][NT][2];
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const float inv = pow2f(127 - static_cast<int>(__float_as_uint(v_scale[j]) >> 23));
                 const float mantissa = v_scale[j] * inv;  // 1 for a power of two
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    e[j][u] = ex2(e[j][u]);
-                    l[u & 1] = fmaf(e[j][u], inv, l[u & 1]);
-                }
-                if (mantissa != 1.f)
+                for (int nt = 0; nt < NT; ++nt) {
+                    float(&p)[4] = e[j][nt];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        e[j][u] *= mantissa;
-                pb[j][0] = transpose8(DTypeTraits<__half>::pack(e[j][0], e[j][1]));
-                pb[j][1] = transpose8(DTypeTraits<__half>::pack(e[j][2], e[j][3]));
+                    for (int u = 0; u < 4; ++u) {
+                        p[u] = ex2(p[u]);
+                        l[nt][u & 1] = fmaf(p[u], inv, l[nt][u & 1]);
+                    }
+                    if (mantissa != 1.f)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            p[u] *= mantissa;
+                    pb[j][nt][0] = transpose8(DTypeTraits<__half>::pack(p[0], p[1]));
+                    pb[j][nt][1] = transpose8(DTypeTraits<__half>::pack(p[2], p[3]));
+                }
             }
 #pragma unroll
             for (int j = 0; j < J; ++j) {
@@ -692,9 +738,11 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
 #pragma unroll
                                     for (int y = 0; y < 4; ++y)
 #pragma unroll
-                                        for (int u = 0; u < 2; ++u)
-                                            if ((bits >> (8 * y + 7) & 1u) && key0[j] + key < limit(u))
-                                                acc[2 * x + (y >> 1)][(y & 1) * 2 + u] = __int_as_float(0x7FC00000);
+                                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                            for (int u = 0; u < 2; ++u)
+                                                if ((bits >> (8 * y + 7) & 1u) && key0[j] + key < limit(nt, u))
+                                                    acc[2 * x + (y >> 1)][nt][(y & 1) * 2 + u] = __int_as_float(0x7FC00000);
                                 }
                             }
 #pragma unroll
@@ -715,80 +763,82 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                     C::halves(__byte_perm(vw[0][x], vw[1][x], 0x7362), a[2][0], a[3][0]);
                     C::halves(__byte_perm(vw[2][x], vw[3][x], 0x5140), a[0][1], a[1][1]);
                     C::halves(__byte_perm(vw[2][x], vw[3][x], 0x7362), a[2][1], a[3][1]);
-                    mma_f16(acc[2 * x], a[0][0], a[1][0], a[0][1], a[1][1], pb[j][0], pb[j][1]);
-                    mma_f16(acc[2 * x + 1], a[2][0], a[3][0], a[2][1], a[3][1], pb[j][0], pb[j][1]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(acc[2 * x][nt], a[0][0], a[1][0], a[0][1], a[1][1], pb[j][nt][0], pb[j][nt][1]);
+                        mma_f16(acc[2 * x + 1][nt], a[2][0], a[3][0], a[2][1], a[3][1], pb[j][nt][0], pb[j][nt][1]);
+                    }
                 }
             }
         }
 
         if (flags & kLast) {
-            // ---- merge the warps of each row group; write the rows, or the block's part ----
+            // ---- merge the warps of each row group, eight rows a warp at a time;
+            // write the rows, or the block's part ----
             float *mo = reinterpret_cast<float *>(smem + F::MERGE_OFF);
-            float *mm = reinterpret_cast<float *>(smem + F::ML_OFF), *ml = mm + kDecWarps * F::ROWS;
-            if (!meet())  // the segment before has been read
-                return;
+            float *mm = reinterpret_cast<float *>(smem + F::ML_OFF), *ml = mm + kDecWarps * 8;
+            const int b_seg = segment->x, i_seg = segment->y, head = segment->z, group = segment->w;
+            const bool part = flags & (kHeadPart | kTailPart);
+            const long long place = 2ll * blockIdx.x + (flags & kTailPart ? 1 : 0);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    float sum = l[u];
+                    float sum = l[nt][u];
                     sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-                    const int row = warp * F::ROWS + 2 * c + u;
+                    const int row = warp * 8 + 2 * c + u;
                     if (g == 0) {
-                        mm[row] = m[u];
+                        mm[row] = m[nt][u];
                         ml[row] = sum;
                     }
 #pragma unroll
-                    for (int x = 0; x < VW; ++x) {
-                        const int d = v_column<D>(g, x);
-                        *reinterpret_cast<float4 *>(mo + row * F::OROW + d) =
-                            make_float4(acc[2 * x][u], acc[2 * x][u + 2], acc[2 * x + 1][u],
-                                        acc[2 * x + 1][u + 2]);
+                    for (int x = 0; x < VW; ++x)
+                        *reinterpret_cast<float4 *>(mo + row * F::OROW + v_column<D>(g, x)) =
+                            make_float4(acc[2 * x][nt][u], acc[2 * x][nt][u + 2], acc[2 * x + 1][nt][u],
+                                        acc[2 * x + 1][nt][u + 2]);
+                }
+                if (!meet())
+                    return;
+                for (int x = t; x < 8 * w.row_warps * (D / 2); x += 32 * kDecWarps) {
+                    const int r8 = x / (D / 2), d = 2 * (x % (D / 2));
+                    const int row = r8 / 8 * ROWS + nt * 8 + r8 % 8;  // of the block
+                    const int abs_row = group * rows_block + row;
+                    if (abs_row >= w.R)
+                        continue;
+                    const int from = (r8 / 8) * key_warps * 8 + r8 % 8;  // of its first warp
+                    float top = -INFINITY;
+                    for (int y = 0; y < key_warps; ++y)
+                        top = fmaxf(top, mm[from + y * 8]);
+                    float2 o = make_float2(0.f, 0.f);
+                    float sum = 0.f;
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    for (int y = 0; y < key_warps; ++y) {
+                        const float f = ex2(mm[from + y * 8] - ref);
+                        const float2 z = *reinterpret_cast<const float2 *>(mo + (from + y * 8) * F::OROW + d);
+                        o.x = fmaf(z.x, f, o.x);
+                        o.y = fmaf(z.y, f, o.y);
+                        sum = fmaf(ml[from + y * 8], f, sum);
+                    }
+                    if (part) {
+                        const long long pr = place * rows_block + row;
+                        *reinterpret_cast<float2 *>(w.part_o + pr * D + d) = o;
+                        if (d == 0) {
+                            w.part_m[pr] = top;
+                            w.part_l[pr] = sum;
+                        }
+                    } else {
+                        const long long bh = static_cast<long long>(b_seg) * w.cache.heads + head;
+                        const long long orow = w.pages ? (bh * w.q.G + abs_row) * w.q.Nq + i_seg : bh * w.R + abs_row;
+                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                        *reinterpret_cast<uint32_t *>(out + orow * D + d) = DTypeTraits<T>::pack(o.x * inv, o.y * inv);
+                        if (d == 0 && lse != nullptr)
+                            lse[orow] = sum == 0.f ? -INFINITY : (ref + __log2f(sum)) * 0.6931471805599453f;
                     }
                 }
-            if (!meet())
-                return;
-            const int b_seg = segment->x, i_seg = segment->y, head = segment->z, group = segment->w;
-            const bool part = flags & (kHeadPart | kTailPart);
-            const long long seg_row =
-                w.pages ? 0 : (static_cast<long long>(b_seg) * w.cache.heads + head) * w.R;
-            const long long place = 2ll * blockIdx.x + (flags & kTailPart ? 1 : 0);
-            for (int x = t; x < rows_block * (D / 2); x += 32 * kDecWarps) {
-                const int row = x / (D / 2), d = 2 * (x % (D / 2));
-                const int abs_row = group * rows_block + row;
-                if (abs_row >= w.R)
-                    break;
-                const int from = (row / F::ROWS) * key_warps * F::ROWS + row % F::ROWS;  // of its first warp
-                float top = -INFINITY;
-                for (int y = 0; y < key_warps; ++y)
-                    top = fmaxf(top, mm[from + y * F::ROWS]);
-                float2 o = make_float2(0.f, 0.f);
-                float sum = 0.f;
-                const float ref = top == -INFINITY ? 0.f : top;
-                for (int y = 0; y < key_warps; ++y) {
-                    const float f = ex2(mm[from + y * F::ROWS] - ref);
-                    const float2 z = *reinterpret_cast<const float2 *>(mo + (from + y * F::ROWS) * F::OROW + d);
-                    o.x = fmaf(z.x, f, o.x);
-                    o.y = fmaf(z.y, f, o.y);
-                    sum = fmaf(ml[from + y * F::ROWS], f, sum);
-                }
-                if (part) {
-                    const long long pr = place * rows_block + row;
-                    *reinterpret_cast<float2 *>(w.part_o + pr * D + d) = o;
-                    if (d == 0) {
-                        w.part_m[pr] = top;
-                        w.part_l[pr] = sum;
-                    }
-                } else {
-                    const long long orow =
-                        w.pages ? ((static_cast<long long>(b_seg) * w.cache.heads + head) * w.q.G + abs_row) * w.q.Nq +
-                                      i_seg
-                                : seg_row + abs_row;
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    *reinterpret_cast<uint32_t *>(out + orow * D + d) = DTypeTraits<T>::pack(o.x * inv, o.y * inv);
-                    if (d == 0 && lse != nullptr)
-                        lse[orow] = sum == 0.f ? -INFINITY : (ref + __log2f(sum)) * 0.6931471805599453f;
-                }
+                if (!meet())  // the area is free: for the next rows, for the next segment's Q
+                    return;
             }
         }
     }
