@@ -69,7 +69,7 @@ struct DecCfg {
     static constexpr int OROW = D + 4;                        // floats of a row of the merge
     static constexpr int RING_OFF = 0;
     static constexpr int META_OFF = STAGES * STAGE;
-    static constexpr int MERGE_OFF = META_OFF + STAGES * 128;
+    static constexpr int MERGE_OFF = META_OFF + STAGES * 192;
     static constexpr int ML_OFF = MERGE_OFF + kDecWarps * 8 * OROW * 4;  // eight rows a warp at a time
     static constexpr int BAR_OFF = ML_OFF + kDecWarps * 8 * 8;
     static constexpr int FLAG_OFF = BAR_OFF + 16 * STAGES + 16;  // full, empty, merge
@@ -78,13 +78,18 @@ struct DecCfg {
 };
 
 // What the computing warps know of a stage.
-struct __align__(16) StageMeta {
-    float k_scale[kMaxSubs], v_scale[kMaxSubs];
-    int key0[kMaxSubs];  // position of the 16-key tile's first key, or kNoKey
-    int flags, b, i, head, group, pad[3];
+struct __align__(16) TileMeta {
+    float k_scale;
+    float v_log2, v_inv;  // the V scale's power of two, its exponent and reciprocal
+    int key0;             // position of the 16-key tile's first key, or kNoKey
 };
-static_assert(sizeof(StageMeta) == 128, "stage record");
-constexpr int kFirst = 1, kLast = 2, kHeadPart = 4, kTailPart = 8;
+struct __align__(16) StageMeta {
+    TileMeta tile[kMaxSubs];
+    float v_rest[kMaxSubs];  // V scale over its power of two; written with kOddScale
+    int flags, b, i, head, group, pad[3];  // b .. group with kFirst
+};
+static_assert(sizeof(StageMeta) == 192, "stage record");
+constexpr int kFirst = 1, kLast = 2, kHeadPart = 4, kTailPart = 8, kOddScale = 16;
 constexpr int kNoKey = 0x7FFFFF00;  // behind every context
 
 // Where a thread (g = lane / 4, c = lane % 4) finds its bytes of a 16-key tile in
@@ -334,7 +339,9 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
         const int box = 1 << w.log2_box, batch_units = 32 >> log2_boxes;
         const uint64_t policy = l2_policy_evict_first();
         bool opened = true, ok = true;  // opened: the next unit is this block's first of its segment
-        int done = 0;
+        const unsigned stage_lanes = (1u << (1 << log2_boxes)) - 1u;
+        int done = 0, s = 0;
+        uint32_t phase = 0;  // of the ring's round
         while (done < all && ok) {
             // lane l: page and scales of the l-th of the next 32 copies of this segment
             const int here = min(min(batch_units, units - unit), all - done);
@@ -364,18 +371,20 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                 ks = w.cache.k_scale[ph];
                 vs = w.cache.v_scale[ph];
             }
+            const unsigned alive = __ballot_sync(0xffffffffu, p >= 0);
+            // lane l < SUBS writes the record of a stage's tile l: the lane that has its copy
+            const int tile_lane = (lane * kTile) >> w.log2_box, tile_key = (lane * kTile) & (box - 1);
             for (int u = 0; u < here; ++u, ++done) {
-                const int s = done % S;
-                if (done >= S && !(ok = wait_warp(empty(s), ((done / S) - 1) & 1, abort_flag)))
+                if (done >= S && !(ok = wait_warp(empty(s), phase ^ 1u, abort_flag)))
                     break;
+                const int first_lane = u << log2_boxes;
                 const bool mine = (lane >> log2_boxes) == u;
                 const bool ended = unit + 1 == units || done + 1 == all;
-                const int row0 = (lane & ((1 << log2_boxes) - 1)) << w.log2_box;  // of the stage
-                StageMeta *m = meta + s;
                 // the copies first (their bytes may arrive before they are
                 // expected: the phase waits for the arrival below), then the
                 // record, whose scales may still be under way
                 if (mine && p >= 0) {
+                    const int row0 = (lane - first_lane) << w.log2_box;  // of the stage
                     const uint32_t dst = sbase + F::RING_OFF + s * F::STAGE + row0 * F::W0;
                     const int y = key0 & (w.cache.page - 1);
                     tma_load_3d(dst, &maps.k[0], full(s), 0, y, ph, policy);
@@ -386,34 +395,45 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                         tma_load_3d(dst1 + F::HALF, &maps.v[1], full(s), F::W0, y, ph, policy);
                     }
                 }
-                if (mine)
-                    for (int y = 0; y < box / kTile; ++y) {
-                        const int k0 = key0 + y * kTile, sub = row0 / kTile + y;
-                        m->key0[sub] = p >= 0 && k0 < ctx ? k0 : kNoKey;
-                        m->k_scale[sub] = ks;
-                        m->v_scale[sub] = vs;
-                    }
-                const unsigned live = __ballot_sync(0xffffffffu, mine && p >= 0);
+                StageMeta *m = meta + s;
+                const int from = (first_lane + tile_lane) & 31;
+                const float tk = __shfl_sync(0xffffffffu, ks, from), tv = __shfl_sync(0xffffffffu, vs, from);
+                const int t0 = __shfl_sync(0xffffffffu, key0, from) + tile_key;
+                const int v_exp = static_cast<int>(__float_as_uint(tv) >> 23);
+                const float v_inv = __int_as_float((254 - v_exp) << 23);
+                const bool odd = lane < F::SUBS && tv * v_inv != 1.f;
+                if (lane < F::SUBS) {
+                    const bool seen = (alive >> from & 1u) && t0 < ctx;
+                    m->tile[lane] = {tk, static_cast<float>(v_exp - 127), v_inv, seen ? t0 : kNoKey};
+                }
+                int flags = (opened ? kFirst : 0) | (ended ? kLast : 0) | (__any_sync(0xffffffffu, odd) ? kOddScale : 0);
+                if (ended) {
+                    // did this block have the segment from its first to its last unit?
+                    if (unit > done)
+                        flags |= kHeadPart;  // it began before this block's run
+                    else if (unit + 1 < units)
+                        flags |= kTailPart;
+                }
+                if ((flags & kOddScale) && lane < F::SUBS)
+                    m->v_rest[lane] = tv * v_inv;
                 if (lane == 0) {
-                    int flags = (opened ? kFirst : 0) | (ended ? kLast : 0);
-                    if (ended) {
-                        // did this block have the segment from its first to its last unit?
-                        if (unit > done)
-                            flags |= kHeadPart;  // it began before this block's run
-                        else if (unit + 1 < units)
-                            flags |= kTailPart;
-                    }
                     m->flags = flags;
-                    m->b = b;
-                    m->i = i;
-                    m->head = head;
-                    m->group = group;
+                    if (opened) {
+                        m->b = b;
+                        m->i = i;
+                        m->head = head;
+                        m->group = group;
+                    }
                 }
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_expect_tx(full(s), __popc(live) * 2 * box * D);
+                    mbar_arrive_expect_tx(full(s), __popc(alive >> first_lane & stage_lanes) * 2 * box * D);
                 opened = ended;
                 ++unit;
+                if (++s == S) {
+                    s = 0;
+                    phase ^= 1u;
+                }
             }
             if (unit == units && done < all) {  // on to the next segment
                 unit = 0;
@@ -434,9 +454,9 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
         }
         // the computing warps wait for every copy; after a failed wait this one does
         if (!ok)
-            for (int s = 0; s < S; ++s)
-                if (done > s)
-                    drain_bounded(full(s), ((done - 1 - s) / S) & 1);
+            for (int x = 0; x < S; ++x)
+                if (done > x)
+                    drain_bounded(full(x), ((done - 1 - x) / S) & 1);
         return;
     }
 
@@ -464,12 +484,20 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
             mbar_arrive(merged);
         return wait_warp(merged, merges++ & 1u, abort_flag);
     };
+    bool fresh = true;   // some row may have no reference yet
+    uint32_t unset = 0;  // ... a bit each of the thread's
+    int slot = S - 1;
+    uint32_t phase = 1;
     for (int done = 0; done < all; ++done) {
-        const int slot = done % S;
-        if (!wait_warp(full(slot), (done / S) & 1, abort_flag))
+        if (++slot == S)
+            slot = 0;
+        if (slot == 0)
+            phase ^= 1u;
+        if (!wait_warp(full(slot), phase, abort_flag))
             return;
         const StageMeta *info = meta + slot;
         const int flags = info->flags;
+        const bool odd_scale = flags & kOddScale;  // a V scale that is no power of two
 
         if (flags & kFirst) {
             const int b_seg = info->b, i_seg = info->i, head = info->head, group = info->group;
@@ -479,6 +507,8 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
             most = w.pages ? context(w.q, n, i_seg) : n;
             least = w.pages || !w.q.causal ? most : n - w.q.Nq + 1;
             behind = 0;
+            fresh = true;
+            unset = (1u << (2 * NT)) - 1u;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int row = group * rows_block + wr * ROWS + nt * 8 + g;
@@ -523,7 +553,7 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                 for (int u = 0; u < 2; ++u) {
                     qf[nt][u] = pow2f(__shfl_sync(0xffffffffu, e, 8 * c + 4 * u)) * w.scale_log2;
                     behind |= __shfl_sync(0xffffffffu, extra, 8 * c + 4 * u) << (8 * (2 * nt + u));
-                    m[nt][u] = -INFINITY;
+                    m[nt][u] = 0.f;
                     l[nt][u] = 0.f;
                 }
 #pragma unroll
@@ -538,11 +568,13 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
             // J tiles at once: one look at the reference, and twice the independent work
             const int sub0 = set * J;
             const bool last_set = set + key_warps >= F::SUBS / J;
+            TileMeta tile[J];
             int key0[J];
             int nearest = kNoKey, farthest = 0;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                key0[j] = info->key0[sub0 + j];
+                tile[j] = info->tile[sub0 + j];
+                key0[j] = tile[j].key0;
                 nearest = min(nearest, key0[j]);
                 farthest = max(farthest, key0[j]);
             }
@@ -596,24 +628,13 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                 }
             }
             // ---- exponents of P v_scale, masks; does any outgrow its reference? ----
-            float ref[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    ref[nt][u] = m[nt][u] == -INFINITY ? 0.f : m[nt][u];
-            float v_scale[J];
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const float k_scale = info->k_scale[sub0 + j];
-                v_scale[j] = info->v_scale[sub0 + j];
-                const float ev = static_cast<float>(static_cast<int>(__float_as_uint(v_scale[j]) >> 23) - 127);
+            for (int j = 0; j < J; ++j)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        e[j][nt][u] = fmaf(e[j][nt][u], k_scale * qf[nt][u & 1], ev - ref[nt][u & 1]);
-            }
+                        e[j][nt][u] = fmaf(e[j][nt][u], tile[j].k_scale * qf[nt][u & 1], tile[j].v_log2 - m[nt][u & 1]);
             const bool masked = farthest + kTile > least;
             if (masked) {
 #pragma unroll
@@ -625,38 +646,37 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                             if (key0[j] + g + 8 * (u >> 1) >= limit(nt, u & 1))
                                 e[j][nt][u] = -INFINITY;
             }
-            // with no reference yet, any score that is seen outgrows it
-            bool grown = false;
+            bool grown = fresh;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int j = 0; j < J; ++j)
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float most_e = m[nt][u & 1] == -INFINITY ? -INFINITY : 8.f;
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < J; ++j)
-                        grown |= !(e[j][nt][u] <= most_e);
-                }
+                    for (int u = 0; u < 4; ++u)
+                        grown |= !(e[j][nt][u] <= 8.f);
             if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        float top = -INFINITY;
+                        const uint32_t bit = 1u << (2 * nt + u);
+                        float top = -INFINITY;  // over the reference, which is 0 as long as it is not set
 #pragma unroll
                         for (int j = 0; j < J; ++j)
                             top = fmaxf(top, fmaxf(e[j][nt][u], e[j][nt][u + 2]));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        const float next = fmaxf(m[nt][u], top + ref[nt][u]);
-                        const float alpha = next == m[nt][u] ? 1.f : ex2(m[nt][u] - next);
-                        const float down = next == -INFINITY ? 0.f : ref[nt][u] - next;
-                        m[nt][u] = next;
+                        const float up = unset & bit ? (top == -INFINITY ? 0.f : top) : fmaxf(top, 0.f);
+                        const float alpha = unset & bit ? 1.f : ex2(-up);
+                        if (top > -INFINITY)
+                            unset &= ~bit;
+                        m[nt][u] += up;
                         l[nt][u] *= alpha;
 #pragma unroll
                         for (int j = 0; j < J; ++j) {
-                            e[j][nt][u] += down;
-                            e[j][nt][u + 2] += down;
+                            e[j][nt][u] -= up;
+                            e[j][nt][u + 2] -= up;
                         }
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j) {
@@ -664,25 +684,26 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                             acc[j][nt][u + 2] *= alpha;
                         }
                     }
+                fresh = __any_sync(0xffffffffu, unset != 0);
             }
             // ---- P, and O^T += V^T P^T ----
             uint32_t pb[J][NT][2];
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const float inv = pow2f(127 - static_cast<int>(__float_as_uint(v_scale[j]) >> 23));
-                const float mantissa = v_scale[j] * inv;  // 1 for a power of two
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float(&p)[4] = e[j][nt];
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         p[u] = ex2(p[u]);
-                        l[nt][u & 1] = fmaf(p[u], inv, l[nt][u & 1]);
+                        l[nt][u & 1] = fmaf(p[u], tile[j].v_inv, l[nt][u & 1]);
                     }
-                    if (mantissa != 1.f)
+                    if (odd_scale) {
+                        const float rest = info->v_rest[sub0 + j];
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            p[u] *= mantissa;
+                            p[u] *= rest;
+                    }
                     pb[j][nt][0] = transpose8(DTypeTraits<__half>::pack(p[0], p[1]));
                     pb[j][nt][1] = transpose8(DTypeTraits<__half>::pack(p[2], p[3]));
                 }
@@ -790,7 +811,7 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
                     sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                     const int row = warp * 8 + 2 * c + u;
                     if (g == 0) {
-                        mm[row] = m[nt][u];
+                        mm[row] = unset >> (2 * nt + u) & 1u ? -INFINITY : m[nt][u];
                         ml[row] = sum;
                     }
 #pragma unroll

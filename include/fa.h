@@ -334,7 +334,9 @@ FA_API size_t fa_decode_cache_workspace_size(int B, int Hq, int Hkv, int Nq, int
  * fa_decode, with Nq (1 .. 16) query rows a head, seq_lens[b] keys, and Hq =
  * G * heads query heads, head hq reading KV head hq / G.  causal = 1 puts the
  * queries at the end of the sequence: query i sees keys 0 .. seq_lens[b] - Nq + i.
- * A row that sees no key gets O = 0 and LSE = -infinity.
+ * A row that sees no key gets O = 0 and LSE = -infinity.  Scales other than
+ * powers of two (of a cache that something else has filled) are read as well, if
+ * they are normal positive numbers.
  *
  *  q       : element (b, h, i, c) at b * q_batch_stride + h * q_head_stride +
  *            i * q_row_stride + c (strides as in fa_cache_write); 16-byte aligned.

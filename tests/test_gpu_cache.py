@@ -279,6 +279,19 @@ def test_attention_uneven_scales(fa, fmt):
     check_attention(fa, ref, q, table, lens, False)
 
 
+@pytest.mark.parametrize("page", [16, 64])
+def test_attention_scales_that_are_no_powers_of_two(fa, page):
+    """A cache that something else has filled, with scales of any size (calibrated ones, say)."""
+    lens = [333, 64]
+    table, pool = pages_for(lens, page, 1)
+    ref = Ref(pool, 2, page, 128, "int8", 2)
+    g = torch.Generator().manual_seed(9)
+    ref.k_scale, ref.v_scale = (torch.rand(ref.k_scale.shape, generator=g).float().double() * 0.03 + 0.01 for _ in range(2))
+    for G in (4, 12):
+        q = randn((2, 2 * G, 1, 128), torch.float16, 3)
+        check_attention(fa, ref, q, table, lens, False)
+
+
 def test_attention_peaked_and_rising(fa):
     """Scores with a wide spread, and scores that rise along the keys, so that the running reference moves."""
     lens = [900, 900]
