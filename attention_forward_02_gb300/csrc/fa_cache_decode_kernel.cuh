@@ -503,6 +503,7 @@ __global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
             const int b_seg = info->b, i_seg = info->i, head = info->head, group = info->group;
             if (lane == 0)
                 *segment = make_int4(b_seg, i_seg, head, group);
+            __syncwarp();
             const int n = w.batch.length(b_seg, w.cache.log2_page);
             most = w.pages ? context(w.q, n, i_seg) : n;
             least = w.pages || !w.q.causal ? most : n - w.q.Nq + 1;
