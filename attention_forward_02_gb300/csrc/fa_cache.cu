@@ -473,7 +473,8 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
     const long long keys = static_cast<long long>(pages && slots < max_pages ? slots : max_pages) * cache->page;
     const long long most = static_cast<long long>(B) * (pages ? Nq : 1) * cache->heads * w.groups *
                            ((keys - 1) / step + 1);
-    const long long resident = static_cast<long long>(sms) * fa::cache::kBlocksPerSm;
+    const long long resident =
+        static_cast<long long>(sms) * (cache->d == 32 ? fa::cache::DecCfg<32>::BLOCKS : fa::cache::DecCfg<128>::BLOCKS);
     long long blocks = resident < fa::cache::kMaxBlocks ? resident : fa::cache::kMaxBlocks;
     if (most < blocks)
         blocks = most;

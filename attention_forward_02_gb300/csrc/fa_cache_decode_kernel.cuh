@@ -49,7 +49,6 @@ constexpr int kDecWarps = 4;      // that compute
 constexpr int kDecThreads = 32 * (kDecWarps + 1);
 constexpr int kTile = 16;         // keys of one product
 constexpr int kMaxSubs = 8;       // tiles of a stage
-constexpr int kBlocksPerSm = 3;
 constexpr int kMaxBlocks = 640;   // of the persistent grid
 constexpr int kCombineThreads = 128;
 constexpr int kCombineEach = 8;   // parts of a warp under way at once
@@ -65,7 +64,9 @@ struct DecCfg {
     static constexpr int W0 = D == 96 ? 64 : D, W1 = D - W0;  // widths
     static constexpr int HALF = STEP * D;                     // K or V of a stage, bytes
     static constexpr int STAGE = 2 * HALF;
-    static constexpr int STAGES = 49152 / STAGE < 8 ? 49152 / STAGE : 8;  // 3 at d = 128; 3 blocks an SM
+    static constexpr int BLOCKS = D == 32 ? 4 : 3;            // an SM
+    static constexpr int RING = D == 32 ? 32768 : 49152;      // bytes
+    static constexpr int STAGES = RING / STAGE < 8 ? RING / STAGE : 8;  // 3 at d = 128
     static constexpr int OROW = D + 4;                        // floats of a row of the merge
     static constexpr int RING_OFF = 0;
     static constexpr int META_OFF = STAGES * STAGE;
@@ -224,7 +225,7 @@ struct Maps {
 };
 
 template <int D, int NT, int J, typename T, typename C>
-__global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
+__global__ void __launch_bounds__(kDecThreads, DecCfg<D>::BLOCKS)
     fa_cache_decode_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Work w, T *__restrict__ out,
                            float *__restrict__ lse)
 {

@@ -383,6 +383,84 @@ def test_attention_listed_pages(fa, fmt, G, Nq, page):
                     pages[b, h, i, 2] = -5
     q = randn((len(lens), 2 * G, Nq, 64), torch.bfloat16, 3)
     check_attention(fa, ref, q, table, lens, True, pages=pages)
+    check_attention(fa, ref, q, table, lens, False, pages=pages)
+
+
+@pytest.mark.parametrize("d", [32, 128])
+def test_attention_many_listed_pages(fa, d):
+    """Lists long enough that one query's pages go to many blocks, beside a sequence that has fewer pages than slots."""
+    page, lens = 32, [6000, 500]
+    table, pool = pages_for(lens, page, 1)
+    ref = Ref(pool, 2, page, d, "e4m3", 2)
+    g = torch.Generator().manual_seed(5)
+    pages = torch.full((2, 2, 2, 120), -1, dtype=torch.int32)
+    for h in range(2):
+        for i in range(2):
+            pages[0, h, i] = torch.randperm(6000 // page, generator=g)[:120].int()
+            pages[1, h, i, :16] = torch.arange(16)
+    q = randn((2, 12, 2, d), torch.float16, 3)
+    check_attention(fa, ref, q, table, lens, False, pages=pages)
+
+
+def test_calls_repeat_bit_for_bit_and_on_two_streams(fa):
+    """The same call gives the same bits, alone and beside others on another stream with workspaces of their own."""
+    lens = [3000, 17, 900]
+    table, pool = pages_for(lens, 16, 1)
+    ref = Ref(pool, 2, 16, 64, "e4m3", 2)
+    cache, table, lens = ref.to("cuda"), dev(table), dev(lens)
+    qs = [randn((3, 8, 2, 64), torch.bfloat16, s).cuda() for s in (3, 4)]
+
+    def call(q):
+        pages = fa.fa_cache_select(q, cache, table, lens, 20)
+        return (pages, *fa.fa_decode_cache(q, cache, table, lens), *fa.fa_decode_cache(q, cache, table, lens, pages=pages))
+
+    first = [call(q) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    got = [[], []]
+    for _ in range(20):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(call(qs[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for again in got[k]:
+            assert all(torch.equal(x, y) for x, y in zip(again, first[k]))
+    assert status(fa) == 0
+
+
+def test_first_call_may_be_captured(fa):
+    """A process whose first calls are inside a capture."""
+    import subprocess
+    import sys
+    code = """
+import sys, torch
+sys.path[:0] = %r
+import attention_forward_02_gb300 as fa
+from cache_util import Ref, pages_for
+table, pool = pages_for([70], 16, 1)
+cache = Ref(pool, 1, 16, 32, "int8", 2).to("cuda")
+table, lens = table.cuda(), torch.tensor([70], dtype=torch.int32, device="cuda")
+q = torch.randn(1, 4, 1, 32, device="cuda").half()
+x = torch.randn(1, 1, 32, device="cuda").half()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    fa.fa_cache_write(cache, x, x, table, lens)
+    pages = fa.fa_cache_select(q, cache, table, lens, 3)
+    o, lse = fa.fa_decode_cache(q, cache, table, lens, pages=pages)
+    k, v = fa.fa_cache_read(cache, table, lens, 70)
+g.replay()
+torch.cuda.synchronize()
+want = [t.clone() for t in (pages, o, lse, k, v)]
+pages = fa.fa_cache_select(q, cache, table, lens, 3)
+o, lse = fa.fa_decode_cache(q, cache, table, lens, pages=pages)
+k, v = fa.fa_cache_read(cache, table, lens, 70)
+assert all(torch.equal(a, b) for a, b in zip(want, (pages, o, lse, k, v)))
+print("captured")
+""" % ([p for p in sys.path if p][:8],)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
 
 
 def test_attention_strides_streams_and_outputs(fa):
@@ -398,7 +476,11 @@ def test_attention_strides_streams_and_outputs(fa):
     lse = torch.empty((2, 8, 3), device="cuda")
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
-    got = fa.fa_decode_cache(qd, cache, table_d, lens_d, causal=True, o=o, lse=lse, stream=s)
+    # page numbers out of a wider table
+    wide = torch.full((2, table.shape[1] + 5), -9, dtype=torch.int32, device="cuda")
+    wide[:, 2:2 + table.shape[1]] = table_d
+    s.wait_stream(torch.cuda.current_stream())
+    got = fa.fa_decode_cache(qd, cache, wide[:, 2:2 + table.shape[1]], lens_d, causal=True, o=o, lse=lse, stream=s)
     s.synchronize()
     assert got[0] is o and got[1] is lse
     check_attention(fa, ref, q, table, lens, True, got=got)
