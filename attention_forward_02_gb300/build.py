@@ -5,11 +5,14 @@ Four translation units (forward, backward, decoding, the paged cache), one -genc
 encoder is fetched through the runtime's driver entry-point query).  The same
 units are compiled a second time with FA_BOUNDS_CHECK into the checked
 build (libfa_gb300_checked.so, device-side address checks; a test build).  All
-of them compile in parallel.
+of them compile in parallel, and beside them, with g++, the small CPython module
+that shortens the host's way to the cache's entry points (fa_cache_py.cpp).
 """
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -29,6 +32,9 @@ DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_fwd_kernel.cuh", "fa1_fwd_
                                                   "fa_common.cuh",
                                                   "fa_host.h", "sm100_ptx.cuh")] + [
     os.path.join(INCLUDE, "fa.h")]
+BINDING_NAME = "_fa_cache_py"
+BINDING_SOURCE = os.path.join(CSRC, "fa_cache_py.cpp")
+BINDING = os.path.join(OUT_DIR, BINDING_NAME + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -65,6 +71,37 @@ def _stale(lib):
     return any(os.path.getmtime(p) > t for p in DEPS)
 
 
+def binding_command(out):
+    """g++ against the installed torch's headers and libraries."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+            "-isystem" + include, "-isystem" + os.path.join(include, "torch", "csrc", "api", "include"),
+            "-isystem" + cuda, "-I" + sysconfig.get_paths()["include"], "-I" + INCLUDE, BINDING_SOURCE,
+            "-o", out, "-L" + lib, "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_cuda", "-Wl,-rpath," + lib]
+
+
+def build_binding(force=False):
+    """Compile the CPython module if its source is newer; returns its path, or None where it cannot be
+    built (the cache's functions then take their longer way through ctypes)."""
+    os.makedirs(OUT_DIR, exist_ok=True)
+    sources = [BINDING_SOURCE, os.path.join(INCLUDE, "fa.h")]
+    if not force and os.path.exists(BINDING) and all(
+            os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in sources):
+        return BINDING
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    try:
+        subprocess.run(binding_command(tmp), check=True)
+    except (ImportError, AttributeError, OSError, subprocess.CalledProcessError) as e:
+        print("the cache's CPython module was not built: %s" % e, file=sys.stderr)
+        return None
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build_library(force=False, verbose_ptxas=False, checked=True):
     """Compile the library (and, with checked=True, its checked build) if a
     source is newer than it; return the product library's path.  All
@@ -73,15 +110,18 @@ def build_library(force=False, verbose_ptxas=False, checked=True):
     jobs = [(LIB, False)] + ([(LIB_CHECKED, True)] if checked else [])
     jobs = [(lib, chk) for lib, chk in jobs if force or _stale(lib)]
     if not jobs:
+        build_binding(force)
         return LIB
     plans = []
     for lib, chk in jobs:
         tmp = lib + ".tmp%d" % os.getpid()
         plans.append((lib, tmp) + compile_commands(tmp, verbose_ptxas and not chk, chk))
     compiles = [c for _, _, cs, _, _ in plans for c in cs]
-    with ThreadPoolExecutor(len(compiles)) as ex:
+    with ThreadPoolExecutor(len(compiles) + 1) as ex:
+        binding = ex.submit(build_binding, force)
         for f in [ex.submit(subprocess.run, c, check=True) for c in compiles]:
             f.result()
+        binding.result()
     for lib, tmp, _, link, objs in plans:
         subprocess.run(link, check=True)
         for o in objs:

@@ -17,6 +17,10 @@ whatever they hold then.  What they hold cannot be checked by the call: a page
 number or length outside the cache is left out, and
 ``fa_last_device_status`` reports it.
 """
+import importlib.machinery
+import importlib.util
+import os
+from ctypes import c_void_p, cast
 from struct import Struct
 from typing import NamedTuple, Optional
 
@@ -24,7 +28,8 @@ import torch
 
 from ._lib import (FA_BF16, FA_E4M3, FA_FP16, FA_INT8, FAError, fa_cache_read_raw,
                    fa_cache_select_raw, fa_cache_select_workspace_size, fa_cache_write_raw,
-                   fa_decode_cache_raw, fa_decode_cache_workspace_size)
+                   fa_decode_cache_raw, fa_decode_cache_workspace_size, load)
+from .build import BINDING, BINDING_NAME
 
 _CODES = {torch.float16: FA_FP16, torch.bfloat16: FA_BF16}
 _FORMATS = {torch.float8_e4m3fn: FA_E4M3, torch.int8: FA_INT8}
@@ -53,6 +58,31 @@ class FACache(NamedTuple):
             return cls(k, v, ks, vs)
         mean = torch.empty((num_pages, heads, d), dtype=torch.int8, device=device)
         return cls(k, v, ks, vs, mean, ms)
+
+
+# The CPython module of csrc/fa_cache_py.cpp goes through a usual call's checks and allocations in less
+# time than Python does; it hands back (None) what is not usual, and the functions below see to that.
+_module = None   # the module; False where it was not built
+_bound = None    # the library whose addresses it holds
+
+
+def _quick():
+    global _module, _bound
+    lib = load()
+    if lib is not _bound:
+        if _module is None:
+            if os.path.exists(BINDING):
+                loader = importlib.machinery.ExtensionFileLoader(BINDING_NAME, BINDING)
+                _module = importlib.util.module_from_spec(importlib.util.spec_from_loader(BINDING_NAME, loader))
+                loader.exec_module(_module)
+            else:
+                _module = False
+        if _module:
+            _module.bind(*(cast(f, c_void_p).value for f in (
+                lib.fa_cache_write, lib.fa_cache_read, lib.fa_decode_cache, lib.fa_decode_cache_workspace_size,
+                lib.fa_cache_select, lib.fa_cache_select_workspace_size)))
+        _bound = lib
+    return _module
 
 
 # fa_cache_t of include/fa.h: six pointers, five ints
@@ -166,6 +196,12 @@ def fa_cache_write(cache, k, v, page_table, seq_lens, cu_seqlens=None, stream=No
     rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 go to sequence b from position seq_lens[b] on; without
     cu_seqlens every sequence gets T / B.  The caller then adds the counts to seq_lens.  A partly filled
     page keeps its scale or takes the larger one of its new tokens; see include/fa.h."""
+    if stream is None and type(cache) is FACache and (quick := _quick()):
+        done = quick.write(cache, k, v, page_table, seq_lens, cu_seqlens)
+        if done is not None:
+            if done:
+                raise FAError(done, "fa_cache_write")
+            return
     desc, heads, d, index = _describe(cache)
     if _elsewhere(index, stream):
         with _there(index, stream):
@@ -190,6 +226,14 @@ def fa_cache_write(cache, k, v, page_table, seq_lens, cu_seqlens=None, stream=No
 def fa_cache_read(cache, page_table, seq_lens, N, dtype=torch.bfloat16, k=None, v=None, stream=None):
     """The first N positions of every sequence as 16-bit k, v [B, heads, N, d], zeros behind seq_lens[b].
     k, v: optional preallocated outputs (their dtype counts then).  Returns (k, v)."""
+    if stream is None and type(cache) is FACache and dtype in _CODES and (quick := _quick()):
+        given = k if k is not None else v
+        done = quick.read(cache, page_table, seq_lens, N,
+                          (dtype if given is None else getattr(given, "dtype", None)) is torch.float16, k, v)
+        if type(done) is tuple:
+            return done
+        if done is not None:
+            raise FAError(done, "fa_cache_read")
     desc, heads, d, index = _describe(cache)
     if _elsewhere(index, stream):
         with _there(index, stream):
@@ -221,6 +265,13 @@ def fa_decode_cache(q, cache, page_table, seq_lens, pages=None, o=None, lse=None
     puts the queries at the end of the sequence.  pages: int32 [B, heads, Nq, slots], the pages that each
     query and KV head reads (``fa_cache_select``), or None for all.  scale defaults to 1/sqrt(d).
     Returns (o, lse); a row without keys has o = 0, lse = -inf."""
+    if stream is None and type(cache) is FACache and (quick := _quick()):
+        done = quick.decode(q, cache, page_table, seq_lens, pages, o, lse, scale if scale is None else float(scale),
+                            True if causal else False, True if return_lse else False, workspace)
+        if type(done) is tuple:
+            return done
+        if done is not None:
+            raise FAError(done, "fa_decode_cache")
     desc, heads, d, index = _describe(cache)
     if _elsewhere(index, stream):
         with _there(index, stream):
@@ -266,6 +317,13 @@ def fa_cache_select(q, cache, page_table, seq_lens, slots, keep_first=1, keep_la
     """The pages [B, heads, Nq, slots] (int32, ascending, then -1) that q's rows read: the first
     keep_first, the last keep_last and, by the mean keys' scores, the best of the others; all of them
     where there are no more than slots.  Arguments as for fa_decode_cache."""
+    if stream is None and type(cache) is FACache and (quick := _quick()):
+        done = quick.select(q, cache, page_table, seq_lens, slots, keep_first, keep_last,
+                            True if causal else False, pages, workspace)
+        if type(done) is int:
+            raise FAError(done, "fa_cache_select")
+        if done is not None:
+            return done
     desc, heads, d, index = _describe(cache)
     if _elsewhere(index, stream):
         with _there(index, stream):

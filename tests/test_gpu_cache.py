@@ -429,6 +429,64 @@ def test_calls_repeat_bit_for_bit_and_on_two_streams(fa):
     assert status(fa) == 0
 
 
+def test_both_ways_through_python(fa, monkeypatch):
+    """The CPython module's way and the longer one give the same results, in new memory and in given one, and refuse
+    the same calls."""
+    from attention_forward_02_gb300 import cache as module
+    from attention_forward_02_gb300._lib import load
+    assert module._quick(), "the CPython module is not built"
+    lens = [300, 1, 0, 77]
+    table, pool = pages_for([n + 1 for n in lens], 16, 1)
+    ref = Ref(pool, 2, 16, 64, "e4m3", 2)
+    table, new = dev(table), randn((4, 2, 64), torch.float16, 3).cuda()
+    q = randn((4, 6, 2, 64), torch.float16, 4).cuda()
+
+    def everything():
+        cache, n = ref.to("cuda"), dev(lens)
+        fa.fa_cache_write(cache, new, new, table, n)
+        fa.fa_cache_write(cache, new, new, table, n, cu_seqlens=dev([0, 0, 1, 3, 4]))
+        n += 1
+        pages = fa.fa_cache_select(q, cache, table, n, 5, 2, 1, True)
+        given = (torch.empty_like(q), torch.empty(4, 6, 2, device="cuda"), torch.empty_like(pages),
+                 *(torch.empty(4, 2, 90, 64, dtype=torch.float16, device="cuda") for _ in range(2)))
+        ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+        out = [*cache, pages, *fa.fa_decode_cache(q, cache, table, n), *fa.fa_cache_read(cache, table, n, 90)]
+        a = fa.fa_decode_cache(q, cache, table, n, pages, given[0], given[1], 0.5, True, True, ws)
+        b = fa.fa_cache_select(q, cache, table, n, 5, 2, 1, True, given[2], ws)
+        c = fa.fa_cache_read(cache, table, n, 90, k=given[3], v=given[4])
+        assert a[0] is given[0] and a[1] is given[1] and b is given[2] and c[0] is given[3] and c[1] is given[4]
+        assert fa.fa_decode_cache(q, cache, table, n, return_lse=False)[1] is None
+        bad = (lambda: fa.fa_decode_cache(q[:3], cache, table, n), lambda: fa.fa_decode_cache(q.float(), cache, table, n),
+               lambda: fa.fa_decode_cache(q, cache, table.long(), n), lambda: fa.fa_decode_cache(q, cache, table, n.cpu()),
+               lambda: fa.fa_decode_cache(q, cache._replace(v=cache.v[1:]), table, n),
+               lambda: fa.fa_decode_cache(q, cache, table, n, o=given[0].transpose(1, 2)),
+               lambda: fa.fa_decode_cache(q, cache, table, n, scale=-1.0),
+               lambda: fa.fa_decode_cache(q, cache, table, n, workspace=ws[:100]),
+               lambda: fa.fa_decode_cache(q, cache, table, n, pages=pages.long()),
+               lambda: fa.fa_cache_select(q, cache, table, n, 2, 2, 1), lambda: fa.fa_cache_select(q, cache, table, n, 0),
+               lambda: fa.fa_cache_select(q, cache._replace(k_mean=None, k_mean_scale=None), table, n, 5),
+               lambda: fa.fa_cache_read(cache, table, n, -1), lambda: fa.fa_cache_read(cache, table, n, 5, torch.float32),
+               lambda: fa.fa_cache_read(cache, table, n, 90, k=given[3][:3]),
+               lambda: fa.fa_cache_write(cache, new, new[:3], table, n), lambda: fa.fa_cache_write(cache, new[:3], new[:3], table, n),
+               lambda: fa.fa_cache_write(cache, new, new, table, n, cu_seqlens=n))
+        said = []
+        for call in bad:
+            with pytest.raises(fa.FAError) as e:
+                call()
+            said.append(e.value.status)
+        return out + list(given), said
+
+    quick, quick_said = everything()
+    monkeypatch.setattr(module, "_module", False)
+    monkeypatch.setattr(module, "_bound", load())
+    longer, longer_said = everything()
+    assert not module._quick()
+    assert quick_said == longer_said
+    for x, y in zip(quick, longer):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    assert status(fa) == 0
+
+
 def test_first_call_may_be_captured(fa):
     """A process whose first calls are inside a capture."""
     import subprocess
