@@ -32,7 +32,9 @@ struct CacheState {
 };
 CacheState g_cache[kMaxDevices];
 
-// The decoding kernel: warps of 8 or 16 query rows, one or two 16-key tiles at once.
+// The decoding kernel: warps of 8 or 16 query rows, one 16-key tile at a time or,
+// where stages hold 128 keys (d <= 64), two (8 x 8,000 keys of 32 heads of 64: 32 us
+// against 37).
 template <int D, int NT, typename T, typename C>
 constexpr auto decode_kernel()
 {
@@ -75,6 +77,11 @@ void init_cache(CacheState &st)
 // How the R query rows of a KV head are laid out: tiles of 8 rows a warp, warps of
 // a block along the rows (the others take keys), rows a block.  Rows beyond 64 go
 // to further row groups, which read the codes again.
+// Sixteen rows a warp share one conversion of the codes, where two warps of eight
+// convert them twice; they need Q in shared memory.  16 x 16,384 keys (mean 8,700)
+// of 8 heads, sixteen a warp against eight: 16 rows, d = 128, int8 83 / 89 us, e4m3
+// 82 / 75; d = 64 47 / 55 and 44 / 47; 64 rows, d = 128 233 / 285 and 216 / 229,
+// d = 64 126 / 177 and 113 / 142.  Up to 8 rows the second eight would be padding.
 struct Shape {
     int tiles, row_warps, rows_block;
 };
@@ -489,7 +496,9 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
                 static_cast<T *>(o), lse);
             if (!first)
                 return FA_ERR_CUDA;
-            // parts of a segment, on average: a warp takes a few of them alone
+            // parts of a segment, on average: a warp takes a few of them alone (32 x 2
+            // queries of 4 heads: 5.5 us against 8.0 with four warps a row), four share
+            // many (57 a segment at one sequence of 131,072 keys: 6.1 us against 9)
             constexpr int kWarps = fa::cache::kCombineThreads / 32;
             const long long segments = static_cast<long long>(B) * (pages ? Nq : 1) * cache->heads * w.groups;
             const bool second =

