@@ -24,6 +24,12 @@ using fa_host::overlaps;
 
 constexpr int kMaxNq = 16;
 constexpr int kMaxBatch = 65535;  // a grid's y and z extent
+// Units of a segment that one block may take whole: one launch in place of two,
+// but the units one after the other.  One sequence, 8 heads of 128, whole against
+// shared out, on the GPU and as called: 64 keys 4.7 / 6.6 and 8.0 / 11.0 us, 256
+// keys 6.2 / 7.4 and 8.1 / 11.0, 512 keys (8 units) 8.5 / 7.7 and 8.9 / 11.1, 1,024
+// keys 13.0 / 8.0 and 13.5 / 10.8.
+constexpr long long kWholeUnits = 8;
 
 struct CacheState {
     std::once_flag once;
@@ -476,15 +482,17 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
         if ((s = encode_codes(encode, &maps.k[i], cache->k, cache, width[i], box)) != FA_OK ||
             (s = encode_codes(encode, &maps.v[i], cache->v, cache, width[i], box)) != FA_OK)
             return s;
-    // no more blocks than units there can be
+    const long long segments = static_cast<long long>(B) * (pages ? Nq : 1) * cache->heads * w.groups;
     const long long keys = static_cast<long long>(pages && slots < max_pages ? slots : max_pages) * cache->page;
-    const long long most = static_cast<long long>(B) * (pages ? Nq : 1) * cache->heads * w.groups *
-                           ((keys - 1) / step + 1);
+    const long long units = (keys - 1) / step + 1;  // of a segment, at most
     const long long resident =
         static_cast<long long>(sms) * (cache->d == 32 ? fa::cache::DecCfg<32>::BLOCKS : fa::cache::DecCfg<128>::BLOCKS);
     long long blocks = resident < fa::cache::kMaxBlocks ? resident : fa::cache::kMaxBlocks;
-    if (most < blocks)
-        blocks = most;
+    w.whole = units <= kWholeUnits && segments <= blocks;
+    if (w.whole)
+        blocks = segments;
+    else if (segments * units < blocks)
+        blocks = segments * units;
     return by_dim(cache->d, [&](auto dim) {
         return by_types(dtype, cache->format, [&](auto t, auto code) {
             constexpr int D = decltype(dim)::value;
@@ -496,11 +504,12 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
                 static_cast<T *>(o), lse);
             if (!first)
                 return FA_ERR_CUDA;
+            if (w.whole)
+                return launched();
             // parts of a segment, on average: a warp takes a few of them alone (32 x 2
             // queries of 4 heads: 5.5 us against 8.0 with four warps a row), four share
             // many (57 a segment at one sequence of 131,072 keys: 6.1 us against 9)
             constexpr int kWarps = fa::cache::kCombineThreads / 32;
-            const long long segments = static_cast<long long>(B) * (pages ? Nq : 1) * cache->heads * w.groups;
             const bool second =
                 blocks <= segments * fa::cache::kCombineEach
                     ? launch_dependent(fa::cache::fa_cache_combine_kernel<D, T, 1>,

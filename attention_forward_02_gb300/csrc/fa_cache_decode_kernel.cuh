@@ -37,7 +37,9 @@
 // concatenated units of all sequences, whatever their lengths, which are read
 // from device memory.  A run may begin and end inside a segment; those parts (at
 // most two a block) go to the workspace as (m, l, O) and fa_cache_combine_kernel
-// merges them, in a fixed order.
+// merges them, in a fixed order.  Where the page table bounds the contexts to a
+// few units and there are no more segments than resident blocks, a block takes a
+// whole segment instead, and that launch is all.
 //
 // Measured, whole calls back to back (e4m3, d = 128, 8 KV heads): 64 sequences of
 // up to 16,384 keys, 4 rows a head, 1.20 GB: 181 us, 6.6 TB/s, 98 % of the
@@ -153,6 +155,7 @@ struct Work {
     int slots;
     int B, R, groups;  // rows of a segment (G Nq, or G with listed pages), row groups
     int row_warps;     // warps along the rows (1, 2, 4), the others along the keys
+    bool whole;        // a block a segment, from its first key to its last: nothing to merge
     int log2_box;      // keys of one copy: a page, or a stage if that is smaller
     float scale_log2;
     // workspace: [0] blocks' share, [1 + b] first unit of sequence b; then the parts
@@ -272,8 +275,20 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::BLOCKS)
     // ---- this block's run of units ----
     int all;      // units of this block
     int b;        // its first sequence
-    long long off;  // ... and the unit of that sequence it begins with
-    {
+    long long off = 0;  // ... and the unit of that sequence it begins with
+    int i = 0, head = 0, group = 0;  // with `whole`, its segment
+    if (w.whole) {
+        int x = blockIdx.x;
+        group = x % w.groups;
+        x /= w.groups;
+        head = x % w.cache.heads;
+        x /= w.cache.heads;
+        i = w.pages ? x % w.q.Nq : 0;
+        b = w.pages ? x / w.q.Nq : x;
+        // a segment without keys has a unit all the same, and writes its rows in it
+        all = max(1, units_of<F::LOG2_STEP>(w, w.batch.length(b, w.cache.log2_page), i));
+        __syncthreads();  // the barriers are set
+    } else {
         const int each = (w.B + kDecThreads - 1) / kDecThreads;
         const int b0 = min(w.B, t * each), b1 = min(w.B, b0 + each);
         long long sum = 0;
@@ -328,23 +343,28 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::BLOCKS)
 
     if (warp == kDecWarps) {
         // ---------------- the warp that loads ----------------
-        int i = 0, len = 0, ctx = 0, units = 0;
+        int len = 0, ctx = 0, units = 0, unit = 0;
         auto open_query = [&]() {
             len = b < w.B ? w.batch.length(b, w.cache.log2_page) : 0;
             ctx = w.pages ? context(w.q, len, i) : len;
             units = units_of<F::LOG2_STEP>(w, len, i);
         };
-        const int per_unit = w.cache.heads * w.groups;
         open_query();
-        while (i + 1 < w.q.Nq && off >= static_cast<long long>(units) * per_unit) {
-            off -= static_cast<long long>(units) * per_unit;
-            ++i;
-            open_query();
+        if (w.whole) {
+            units = all;
+        } else {
+            const int per_unit = w.cache.heads * w.groups;
+            while (i + 1 < w.q.Nq && off >= static_cast<long long>(units) * per_unit) {
+                off -= static_cast<long long>(units) * per_unit;
+                ++i;
+                open_query();
+            }
+            // off < units * heads * groups here: 32 bits hold it unless a sequence's work is vast
+            const int seg = off >> 31 ? static_cast<int>(off / units) : static_cast<int>(off) / units;
+            head = seg / w.groups;
+            group = seg % w.groups;
+            unit = static_cast<int>(off - static_cast<long long>(seg) * units);
         }
-        // off < units * heads * groups here: 32 bits hold it unless a sequence's work is vast
-        const int seg = off >> 31 ? static_cast<int>(off / units) : static_cast<int>(off) / units;
-        int head = seg / w.groups, group = seg % w.groups;
-        int unit = static_cast<int>(off - static_cast<long long>(seg) * units);
         const int log2_boxes = F::LOG2_STEP - w.log2_box;  // copies of a stage: 1 to 8
         const int box = 1 << w.log2_box, batch_units = 32 >> log2_boxes;
         const uint64_t policy = l2_policy_evict_first();
@@ -510,7 +530,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::BLOCKS)
         const bool odd_scale = flags & kOddScale;  // a V scale that is no power of two
 
         if (flags & kFirst) {
-            const int b_seg = info->b, i_seg = info->i, head = info->head, group = info->group;
+            const int b_seg = info->b, i_seg = info->i;
+            head = info->head;
+            group = info->group;
             if (lane == 0)
                 *segment = make_int4(b_seg, i_seg, head, group);
             __syncwarp();
@@ -809,7 +831,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::BLOCKS)
             // write the rows, or the block's part ----
             float *mo = reinterpret_cast<float *>(smem + F::MERGE_OFF);
             float *mm = reinterpret_cast<float *>(smem + F::ML_OFF), *ml = mm + kDecWarps * 8;
-            const int b_seg = segment->x, i_seg = segment->y, head = segment->z, group = segment->w;
+            const int b_seg = segment->x, i_seg = segment->y;
+            head = segment->z;
+            group = segment->w;
             const bool part = flags & (kHeadPart | kTailPart);
             const long long place = 2ll * blockIdx.x + (flags & kTailPart ? 1 : 0);
 #pragma unroll
