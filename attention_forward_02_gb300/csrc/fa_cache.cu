@@ -336,17 +336,26 @@ fa_status_t fa_cache_write(const fa_cache_t *cache, const void *k, const void *v
                                      cu_seqlens,
                                      cu_seqlens ? 0 : T / B,
                                      T,
-                                     B,
-                                     T > B};
-    // More rows than sequences: a block a touched page, of which there are at most
-    // T / page + 2 B however the rows are spread over the sequences.  Else a block
-    // a sequence, which goes on to its later pages if there are any.
-    const long long pages = rows.spread ? T / cache->page + 2ll * B : 1;
+                                     B};
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (T <= B) {  // a warp a sequence, head, and of K and V
+        const long long units = 2ll * B * cache->heads;
+        if (units > 0x7fffffffLL)
+            return FA_ERR_UNSUPPORTED;
+        const unsigned blocks = static_cast<unsigned>((units + fa::cache::kStepWarps - 1) / fa::cache::kStepWarps);
+        return by_types(dtype, cache->format, [&](auto t, auto code) {
+            fa::cache::fa_cache_step_kernel<decltype(t), decltype(code)>
+                <<<blocks, 32 * fa::cache::kStepWarps, 0, cs>>>(c, batch, rows, cache->d);
+            return launched();
+        });
+    }
+    // a block a touched page, of which there are at most T / page + 2 B however the
+    // rows are spread over the sequences
+    const long long pages = T / cache->page + 2ll * B;
     if (pages > 0x7fffffffLL)
         return FA_ERR_UNSUPPORTED;
-    const dim3 grid(static_cast<unsigned>(pages), 2 * cache->heads, rows.spread ? 1 : B);
+    const dim3 grid(static_cast<unsigned>(pages), 2 * cache->heads);
     const int threads = (cache->page / fa::cache::kWriteRows * (cache->d / 8) + 31) / 32 * 32;
-    cudaStream_t cs = static_cast<cudaStream_t>(stream);
     return by_types(dtype, cache->format, [&](auto t, auto code) {
         fa::cache::fa_cache_write_kernel<decltype(t), decltype(code)><<<grid, threads, 0, cs>>>(c, batch, rows, cache->d);
         return launched();

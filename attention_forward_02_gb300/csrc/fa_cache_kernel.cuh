@@ -82,8 +82,20 @@ __device__ __forceinline__ int round_int8(float x)
 __device__ __forceinline__ void wait_ahead() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// x 2^-s rounded to the nearest whole number (ties to even), for |x| < 2^25 and a
+// result of at most 127.
+__device__ __forceinline__ int scale_round(int x, int s)
+{
+    if (s <= 0)
+        return x * (1 << min(-s, 30));  // exact; x = 0 where s is far below
+    if (s > 26)
+        return 0;
+    const int q = x >> s, rest = x - q * (1 << s), half = 1 << (s - 1);
+    return q + (rest > half || (rest == half && (q & 1)) ? 1 : 0);
+}
+
 struct E4M3 {
-    static constexpr int kUnit = 512;  // codes are whole multiples of 1 / kUnit
+    static constexpr int kUnit = 512, kLog2Unit = 9;  // codes are whole multiples of 1 / kUnit
     static __device__ __forceinline__ int exp_of(float a) { return scale_exp<0x600000u, 8>(a); }  // 448 = 1.75 2^8
     static __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d)
     {
@@ -121,7 +133,7 @@ struct E4M3 {
 };
 
 struct I8 {
-    static constexpr int kUnit = 1;
+    static constexpr int kUnit = 1, kLog2Unit = 0;
     static __device__ __forceinline__ int exp_of(float a) { return int8_exp(a); }
     static __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d)
     {
@@ -198,8 +210,9 @@ __device__ __forceinline__ float finite_max(float a, const float (&f)[8])
 // ---------------------------------------------------------------------------
 // Writing
 //
-// One block per (sequence, touched page, head, K or V): it owns the page's
-// codes and scale, so nothing is shared and nothing is atomic in memory.  The
+// More new rows than sequences, as in prompts: one block per (touched page, head, K
+// or V).  It owns the page's codes and scale, so nothing is shared and nothing is
+// atomic in memory.  The
 // new rows of a page (at most 128 x 128 16-bit values) are held in registers
 // between the pass that finds amax and the one that encodes: one read, one
 // write.  Thread t holds 8 columns (t % (d / 8)) of the rows t / (d / 8),
@@ -207,9 +220,7 @@ __device__ __forceinline__ float finite_max(float a, const float (&f)[8])
 // instructions bound it, so amax is taken on pairs of 16-bit values and fp16 is
 // encoded in pairs; pages with infinities or NaN, which the maximum shows, and
 // scales beyond fp16's range go another way.  58,800 tokens of 8 heads of 128 (fp16
-// to int8, 361 MB): 66 us, 5.5 TB/s, 81 % of the measured copy rate; 256 single
-// tokens 7 us, of which 2 are the launch and the rest the chain length - page number
-// - scale - row.
+// to int8, 361 MB): 62 us, 5.9 TB/s, 86 % of the measured copy rate.
 constexpr int kWriteRows = 8;       // rows a thread
 constexpr int kWriteThreads = 256;  // most threads: page = d = 128
 
@@ -218,7 +229,6 @@ struct NewRows {
     long long token_stride[2], head_stride[2];
     const int *cu;  // or NULL: `each` tokens a sequence
     int each, total, batch;
-    bool spread;  // blocks stand for touched pages
 
     // First row and rows of sequence b; false if its offsets are none.
     __device__ bool tokens(int b, int &first, int &count) const
@@ -317,15 +327,13 @@ __global__ void __launch_bounds__(kWriteThreads, 4) fa_cache_write_kernel(Cache 
     const int stride = page / kWriteRows;  // rows between a thread's rows
     const bool live = threadIdx.x < static_cast<unsigned>(groups * stride);
     const int col = (threadIdx.x % groups) * 8, row0 = threadIdx.x / groups;
-    // the block's sequence and page: with `spread` the blockIdx.x-th touched page
-    // of the batch (a warp counts the pages of 32 sequences at a time), else
-    // page blockIdx.x of sequence blockIdx.z, and every gridDim.x-th after it
-    int b = blockIdx.z, t0, n;
+    // the block's page is the blockIdx.x-th touched one of the batch: a warp counts
+    // the pages of 32 sequences at a time
+    int b = -1, t0, n;
     long long skip = blockIdx.x, had = 0;
-    if (in.spread) {
+    {
         const int lane = threadIdx.x & 31;
         long long before = 0;
-        b = -1;
         for (int b0 = 0; b < 0 && b0 < in.batch; b0 += 32) {
             const int x = b0 + lane;
             int count = 0;
@@ -354,156 +362,273 @@ __global__ void __launch_bounds__(kWriteThreads, 4) fa_cache_write_kernel(Cache 
         if (b < 0)
             return;  // fewer pages than blocks
     }
-    if (!in.tokens(b, t0, n)) {
-        if (threadIdx.x == 0)
-            batch.bad();
-        return;
-    }
-    if (n == 0)
-        return;
+    in.tokens(b, t0, n);
     had = max(batch.seq_lens[b], 0);  // tokens before
     const long long end = had + n;
-    const long long last = (end - 1) >> cache.log2_page;
     const long long token_stride = which ? in.token_stride[1] : in.token_stride[0];
     const T *x = static_cast<const T *>(which ? in.x[1] : in.x[0]) +
                  h * (which ? in.head_stride[1] : in.head_stride[0]) + col;
     uint8_t *codes = which ? cache.v : cache.k;
     float *scales = which ? cache.v_scale : cache.k_scale;
-    for (long long at = (had >> cache.log2_page) + skip; at <= last; at += gridDim.x) {
-        const int p = at < batch.max_pages ? batch.page(b, static_cast<int>(at)) : -1;
-        if (p < 0) {
-            if (threadIdx.x == 0)
-                batch.bad();
-            if (in.spread)
-                return;
-            continue;
-        }
-        const long long base = at << cache.log2_page;  // position of the page's slot 0
-        const int lo = static_cast<int>(max(had - base, 0ll));
-        const int hi = live ? static_cast<int>(min(end - base, static_cast<long long>(page))) : 0;
-        const T *src = x + (t0 + (base - had) + row0) * token_stride;  // of slot row0, if that is new
-        const long long step = stride * token_stride;
-        const bool whole = lo == 0 && end - base >= page;  // every slot is new: no row of it needs a look
-        uint4 raw[kWriteRows];
-        uint32_t m = 0;
-        if (whole && live) {
-            const T *from = src;
+    const long long at = (had >> cache.log2_page) + skip;
+    const int p = at < batch.max_pages ? batch.page(b, static_cast<int>(at)) : -1;
+    if (p < 0) {
+        if (threadIdx.x == 0)
+            batch.bad();
+        return;
+    }
+    const long long base = at << cache.log2_page;  // position of the page's slot 0
+    const int lo = static_cast<int>(max(had - base, 0ll));
+    const int hi = live ? static_cast<int>(min(end - base, static_cast<long long>(page))) : 0;
+    const T *src = x + (t0 + (base - had) + row0) * token_stride;  // of slot row0, if that is new
+    const long long step = stride * token_stride;
+    const bool whole = lo == 0 && end - base >= page;  // every slot is new: no row of it needs a look
+    uint4 raw[kWriteRows];
+    uint32_t m = 0;
+    if (whole && live) {
+        const T *from = src;
 #pragma unroll
-            for (int i = 0; i < kWriteRows; ++i, from += step)
-                raw[i] = __ldcs(reinterpret_cast<const uint4 *>(from));
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWriteRows; ++i) {
-                const int row = row0 + i * stride;
-                raw[i] = make_uint4(0, 0, 0, 0);
-                if (row >= lo && row < hi)
-                    raw[i] = __ldcs(reinterpret_cast<const uint4 *>(src + i * step));
-            }
-        }
+        for (int i = 0; i < kWriteRows; ++i, from += step)
+            raw[i] = __ldcs(reinterpret_cast<const uint4 *>(from));
+    } else {
 #pragma unroll
         for (int i = 0; i < kWriteRows; ++i) {
-            m = max_magnitude2<T>(m, max_magnitude2<T>(raw[i].x, raw[i].y));
-            m = max_magnitude2<T>(m, max_magnitude2<T>(raw[i].z, raw[i].w));
+            const int row = row0 + i * stride;
+            raw[i] = make_uint4(0, 0, 0, 0);
+            if (row >= lo && row < hi)
+                raw[i] = __ldcs(reinterpret_cast<const uint4 *>(src + i * step));
         }
-        m &= 0x7FFF7FFFu;
-        const size_t ph = static_cast<size_t>(p) * cache.heads + h;
-        const float old = lo > 0 ? scales[ph] : 0.f;
-        m = block_max(max(m & 0xFFFFu, m >> 16), red);  // every thread has read the old scale when it returns
-        const bool finite = m < infinity;
-        float a = DTypeTraits<T>::unpack(m).x;
-        if (!finite) {
-            a = 0.f;
+    }
 #pragma unroll
-            for (int i = 0; i < kWriteRows; ++i) {
+    for (int i = 0; i < kWriteRows; ++i) {
+        m = max_magnitude2<T>(m, max_magnitude2<T>(raw[i].x, raw[i].y));
+        m = max_magnitude2<T>(m, max_magnitude2<T>(raw[i].z, raw[i].w));
+    }
+    m &= 0x7FFF7FFFu;
+    const size_t ph = static_cast<size_t>(p) * cache.heads + h;
+    const float old = lo > 0 ? scales[ph] : 0.f;
+    m = block_max(max(m & 0xFFFFu, m >> 16), red);  // every thread has read the old scale when it returns
+    const bool finite = m < infinity;
+    float a = DTypeTraits<T>::unpack(m).x;
+    if (!finite) {
+        a = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWriteRows; ++i) {
+            float f[8];
+            unpack8<T>(raw[i], f);
+            a = finite_max(a, f);
+        }
+        a = __uint_as_float(block_max(__float_as_uint(a), red));
+    }
+    const float scale = fmaxf(old, pow2f(C::exp_of(a)));
+    const float inv = 1.f / scale;
+    const bool pairs = finite && inv >= 6.103515625e-5f && inv <= 32768.f;  // a normal fp16 number
+    const __half2 inv2 = __float2half2_rn(inv);
+    uint8_t *dst = codes + ph * page * d + row0 * d + col;
+    const bool mean = which == 0 && end - base >= page && cache.k_mean != nullptr;
+    ColumnSums<C> sum;
+    if (whole && finite && (DTypeTraits<T>::kBF16 || pairs)) {
+        if (live) {
+            uint8_t *to = dst;
+#pragma unroll
+            for (int i = 0; i < kWriteRows; ++i, to += stride * d) {
+                uint2 c;
+                if (DTypeTraits<T>::kBF16) {
+                    float f[8];
+                    unpack8<T>(raw[i], f);
+                    c.x = C::encode4_finite(f[0], f[1], f[2], f[3], inv);
+                    c.y = C::encode4_finite(f[4], f[5], f[6], f[7], inv);
+                } else {
+                    c.x = C::encode4_half(raw[i].x, raw[i].y, inv2);
+                    c.y = C::encode4_half(raw[i].z, raw[i].w, inv2);
+                }
+                *reinterpret_cast<uint2 *>(to) = c;
+                if (mean)
+                    sum.add(c, true);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kWriteRows; ++i) {
+            const int row = row0 + i * stride;
+            uint2 *to = reinterpret_cast<uint2 *>(dst + i * stride * d);
+            uint2 c = make_uint2(0, 0);
+            if (row >= lo && row < hi) {
                 float f[8];
                 unpack8<T>(raw[i], f);
+                c.x = C::encode4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+                c.y = C::encode4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+                *to = c;
+            } else if (live && row < lo && (scale > old || mean)) {
+                c = *to;
+                if (scale > old) {  // old codes at the new scale
+                    const float r = old * inv;
+                    float f[4], g[4];
+                    decode4<C>(c.x, f);
+                    decode4<C>(c.y, g);
+                    c.x = C::encode4(f[0] * r, f[1] * r, f[2] * r, f[3] * r);
+                    c.y = C::encode4(g[0] * r, g[1] * r, g[2] * r, g[3] * r);
+                    *to = c;
+                }
+            }
+            if (mean)
+                sum.add(c, finite && lo == 0);
+        }
+    }
+    if (threadIdx.x == 0)
+        scales[ph] = scale;
+    if (mean) {
+        // channel sums in units of 1 / kUnit: whole numbers below 2^25, so
+        // their order does not matter
+        for (int c = threadIdx.x; c < d; c += blockDim.x)
+            sums[c] = 0;
+        __syncthreads();
+        if (live)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                atomicAdd(&sums[col + j], sum.sum(j));
+        __syncthreads();
+        const float unit = 1.f / (static_cast<float>(C::kUnit) * page);  // a power of two
+        float top = 0.f;
+        for (int c = threadIdx.x; c < d; c += blockDim.x)
+            top = fmaxf(top, fabsf(static_cast<float>(sums[c]) * unit));
+        top = __uint_as_float(block_max(__float_as_uint(top), red));
+        const int e = int8_exp(top);
+        for (int c = threadIdx.x; c < d; c += blockDim.x)
+            cache.k_mean[ph * d + c] = static_cast<int8_t>(scale_round(sums[c], C::kLog2Unit + cache.log2_page + e));
+        if (threadIdx.x == 0)
+            cache.k_mean_scale[ph] = pow2f(e) * scale;
+    }
+}
+
+// No more new rows than sequences, as in a decoding step: one warp per (sequence,
+// head, K or V), page by page; lane l holds columns 4 l .. 4 l + 3.  The same
+// arithmetic; with a row or two a page nothing is worth holding, so a page's new
+// rows are read once for amax and again to be encoded.  What it costs is the chain
+// length - page number - scale and row, so the warps of a block share nothing and
+// meet nowhere: one token of 8 heads takes 2.3 us against 3.3 with a block a page,
+// 256 tokens (pages of 16) 6.7 against 7.2.
+constexpr int kStepWarps = 8;
+
+template <typename T, typename C>
+__global__ void __launch_bounds__(32 * kStepWarps) fa_cache_step_kernel(Cache cache, Batch batch, NewRows in, int d)
+{
+    const int lane = threadIdx.x & 31;
+    const unsigned unit = blockIdx.x * kStepWarps + (threadIdx.x >> 5);
+    const int which = unit & 1, h = static_cast<int>(unit / 2 % cache.heads), b = static_cast<int>(unit / 2 / cache.heads);
+    if (b >= in.batch)
+        return;
+    const bool live = 4 * lane < d;
+    const uint32_t infinity = DTypeTraits<T>::kBF16 ? 0x7F80u : 0x7C00u;
+    const long long had = max(batch.seq_lens[b], 0);  // tokens before
+    int t0, n;
+    if (!in.tokens(b, t0, n)) {
+        if (lane == 0)
+            batch.bad();
+        return;
+    }
+    if (n == 0)
+        return;
+    const long long end = had + n, last = (end - 1) >> cache.log2_page;
+    const int page = cache.page;
+    const long long token_stride = which ? in.token_stride[1] : in.token_stride[0];
+    const T *x = static_cast<const T *>(which ? in.x[1] : in.x[0]) +
+                 h * (which ? in.head_stride[1] : in.head_stride[0]) + 4 * lane;
+    uint8_t *codes = which ? cache.v : cache.k;
+    float *scales = which ? cache.v_scale : cache.k_scale;
+    for (long long at = had >> cache.log2_page; at <= last; ++at) {
+        const int p = at < batch.max_pages ? batch.page(b, static_cast<int>(at)) : -1;
+        const long long base = at << cache.log2_page;  // position of the page's slot 0
+        const int lo = static_cast<int>(max(had - base, 0ll));
+        const int hi = static_cast<int>(min(end - base, static_cast<long long>(page)));
+        const T *src = x + (t0 + (base - had)) * token_stride;  // of slot 0, if that is new
+        auto row_of = [&](int row) -> uint2 {
+            return live ? *reinterpret_cast<const uint2 *>(src + row * token_stride) : make_uint2(0, 0);
+        };
+        uint32_t m = 0;  // the rows are on their way while the page number is
+#pragma unroll 4
+        for (int row = lo; row < hi; ++row) {
+            const uint2 r = row_of(row);
+            m = max_magnitude2<T>(m, max_magnitude2<T>(r.x, r.y));
+        }
+        if (p < 0) {
+            if (lane == 0)
+                batch.bad();
+            continue;
+        }
+        const size_t ph = static_cast<size_t>(p) * cache.heads + h;
+        const float old = lo > 0 ? scales[ph] : 0.f;
+        m &= 0x7FFF7FFFu;
+        m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+        float a = DTypeTraits<T>::unpack(m).x;
+        if (m >= infinity) {  // the largest of the finite ones
+            a = 0.f;
+            for (int row = lo; row < hi; ++row) {
+                const uint2 r = row_of(row);
+                const float2 y = DTypeTraits<T>::unpack(r.x), z = DTypeTraits<T>::unpack(r.y);
+                const float f[8] = {y.x, y.y, z.x, z.y, 0.f, 0.f, 0.f, 0.f};
                 a = finite_max(a, f);
             }
-            a = __uint_as_float(block_max(__float_as_uint(a), red));
+            a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
         }
         const float scale = fmaxf(old, pow2f(C::exp_of(a)));
         const float inv = 1.f / scale;
-        const bool pairs = finite && inv >= 6.103515625e-5f && inv <= 32768.f;  // a normal fp16 number
-        const __half2 inv2 = __float2half2_rn(inv);
-        uint8_t *dst = codes + ph * page * d + row0 * d + col;
-        const bool mean = which == 0 && end - base >= page && cache.k_mean != nullptr;
-        ColumnSums<C> sum;
-        if (whole && finite && (DTypeTraits<T>::kBF16 || pairs)) {
-            if (live) {
-                uint8_t *to = dst;
+        uint8_t *dst = codes + ph * page * d + 4 * lane;
+        const bool mean = which == 0 && hi == page && cache.k_mean != nullptr;
+        int sum[4] = {0, 0, 0, 0};
+        auto add = [&](uint32_t c) {
+            float f[4];
+            decode4<C>(c, f);
 #pragma unroll
-                for (int i = 0; i < kWriteRows; ++i, to += stride * d) {
-                    uint2 c;
-                    if (DTypeTraits<T>::kBF16) {
-                        float f[8];
-                        unpack8<T>(raw[i], f);
-                        c.x = C::encode4_finite(f[0], f[1], f[2], f[3], inv);
-                        c.y = C::encode4_finite(f[4], f[5], f[6], f[7], inv);
-                    } else {
-                        c.x = C::encode4_half(raw[i].x, raw[i].y, inv2);
-                        c.y = C::encode4_half(raw[i].z, raw[i].w, inv2);
-                    }
-                    *reinterpret_cast<uint2 *>(to) = c;
-                    if (mean)
-                        sum.add(c, true);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWriteRows; ++i) {
-                const int row = row0 + i * stride;
-                uint2 *to = reinterpret_cast<uint2 *>(dst + i * stride * d);
-                uint2 c = make_uint2(0, 0);
-                if (row >= lo && row < hi) {
-                    float f[8];
-                    unpack8<T>(raw[i], f);
-                    c.x = C::encode4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-                    c.y = C::encode4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+            for (int j = 0; j < 4; ++j)
+                sum[j] += __float2int_rn(f[j] * C::kUnit);  // NaN converts to 0
+        };
+        if (live && (scale > old || mean)) {
+#pragma unroll 16
+            for (int row = 0; row < lo; ++row) {
+                uint32_t *to = reinterpret_cast<uint32_t *>(dst + row * d);
+                uint32_t c = *to;
+                if (scale > old) {  // old codes at the new scale
+                    const float r = old * inv;
+                    float f[4];
+                    decode4<C>(c, f);
+                    c = C::encode4(f[0] * r, f[1] * r, f[2] * r, f[3] * r);
                     *to = c;
-                } else if (live && row < lo && (scale > old || mean)) {
-                    c = *to;
-                    if (scale > old) {  // old codes at the new scale
-                        const float r = old * inv;
-                        float f[4], g[4];
-                        decode4<C>(c.x, f);
-                        decode4<C>(c.y, g);
-                        c.x = C::encode4(f[0] * r, f[1] * r, f[2] * r, f[3] * r);
-                        c.y = C::encode4(g[0] * r, g[1] * r, g[2] * r, g[3] * r);
-                        *to = c;
-                    }
                 }
                 if (mean)
-                    sum.add(c, finite && lo == 0);
+                    add(c);
             }
         }
-        if (threadIdx.x == 0)
+        if (live) {
+#pragma unroll 4
+            for (int row = lo; row < hi; ++row) {
+                const uint2 r = row_of(row);
+                const float2 y = DTypeTraits<T>::unpack(r.x), z = DTypeTraits<T>::unpack(r.y);
+                const uint32_t c = C::encode4(y.x * inv, y.y * inv, z.x * inv, z.y * inv);
+                *reinterpret_cast<uint32_t *>(dst + row * d) = c;
+                if (mean)
+                    add(c);
+            }
+        }
+        if (lane == 0)
             scales[ph] = scale;
         if (mean) {
-            // channel sums in units of 1 / kUnit: whole numbers below 2^25, so
-            // their order does not matter
-            for (int c = threadIdx.x; c < d; c += blockDim.x)
-                sums[c] = 0;
-            __syncthreads();
-            if (live)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    atomicAdd(&sums[col + j], sum.sum(j));
-            __syncthreads();
-            const float unit = 1.f / (static_cast<float>(C::kUnit) * page);  // a power of two
+            const float per = 1.f / (static_cast<float>(C::kUnit) * page);  // a power of two
             float top = 0.f;
-            for (int c = threadIdx.x; c < d; c += blockDim.x)
-                top = fmaxf(top, fabsf(static_cast<float>(sums[c]) * unit));
-            top = __uint_as_float(block_max(__float_as_uint(top), red));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                top = fmaxf(top, fabsf(static_cast<float>(sum[j]) * per));
+            top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
             const int e = int8_exp(top);
-            const double by = static_cast<double>(unit) * pow2f(-e);
-            for (int c = threadIdx.x; c < d; c += blockDim.x)
-                cache.k_mean[ph * d + c] = static_cast<int8_t>(max(-127, min(127, __double2int_rn(sums[c] * by))));
-            if (threadIdx.x == 0)
+            uint32_t r = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                r |= static_cast<uint32_t>(scale_round(sum[j], C::kLog2Unit + cache.log2_page + e) & 0xFF) << (8 * j);
+            if (live)
+                *reinterpret_cast<uint32_t *>(cache.k_mean + ph * d + 4 * lane) = r;
+            if (lane == 0)
                 cache.k_mean_scale[ph] = pow2f(e) * scale;
         }
-        if (in.spread)
-            return;
-        __syncthreads();  // the shared sums are free for the next page
     }
 }
 

@@ -142,6 +142,55 @@ def test_write_uneven_batch(fa):
     check_cache(cache, ref)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("page,d,heads", [(16, 96, 2), (32, 32, 1), (128, 128, 1)])
+def test_write_few_rows(fa, fmt, dtype, page, d, heads):
+    """No more rows than sequences: single tokens, none, and the rows of others on one sequence; steps that complete
+    pages, move codes to larger scales, and bring infinities and NaN."""
+    new = [0] * 10 + [30] + [1] * 10 + [0] * 19
+    before = [(7 * i) % (2 * page) for i in range(40)]
+    before[10], before[11], before[12], before[13] = page - 7, page - 1, 2 * page - 1, page
+    table, pool = pages_for([a + n + 8 for a, n in zip(before, new)], page, 5)
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    ref = Ref(pool, heads, page, d, fmt, 6)
+    cache = ref.to("cuda")
+    k, v = (randn((cu[-1], heads, d), DTYPES[dtype], s, 4.0) for s in (7, 8))
+    k[3, 0, 1], k[33, 0, 2], v[31, 0, 3], v[34, 0, 0] = math.inf, math.nan, -math.inf, math.nan
+    k[36] = math.nan
+    fa.fa_cache_write(cache, k.cuda(), v.cuda(), dev(table), dev(before), cu_seqlens=dev(cu))
+    assert status(fa) == 0
+    ref.write(k, v, table, before, cu)
+    check_cache(cache, ref)
+    lens = [a + n for a, n in zip(before, new)]
+    for step in range(6):  # a token each: pages end, scales grow
+        k, v = (randn((40, heads, d), DTYPES[dtype], 20 + 2 * step + s, 2.0 ** (step - 2)) for s in (0, 1))
+        fa.fa_cache_write(cache, k.cuda(), v.cuda(), dev(table), dev(lens))
+        ref.write(k, v, table, lens, list(range(41)))
+        lens = [n + 1 for n in lens]
+    assert status(fa) == 0
+    check_cache(cache, ref)
+
+
+def test_write_few_rows_bad_pages(fa):
+    """The same refusals on that way: bad page numbers, places behind the table, offsets that are none."""
+    page, d = 16, 32
+    table = torch.tensor([[0, 99], [-1, 1], [2, 3], [4, 5], [6, 7]], dtype=torch.int32)
+    before = [16, 3, 40, 5, 31]
+    ref = Ref(8, 1, page, d, "e4m3", 6)
+    cache = ref.to("cuda")
+    k, v = (randn((5, 1, d), torch.bfloat16, s) for s in (7, 8))
+    fa.fa_cache_write(cache, k.cuda(), v.cuda(), dev(table), dev(before))
+    assert status(fa) == FA_ERR_BOUNDS
+    ref.write(k, v, table, before, list(range(6)))
+    check_cache(cache, ref)
+    fa.fa_cache_write(cache, k.cuda(), v.cuda(), dev(table), dev(before), cu_seqlens=dev([5, 4, 9, -3, 77, 6]))
+    assert status(fa) == FA_ERR_BOUNDS
+    check_cache(cache, ref)
+
+
 def test_write_bad_pages(fa):
     """Tokens whose page number is bad, or whose place lies behind the table, are skipped and reported."""
     page, d, heads = 16, 32, 1
