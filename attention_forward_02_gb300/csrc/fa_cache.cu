@@ -594,8 +594,13 @@ fa_status_t fa_cache_select(const fa_cache_t *cache, const void *q, long long q_
     });
     if (s != FA_OK)
         return s;
-    if (!launch_dependent(fa::cache::fa_cache_pick_kernel, static_cast<unsigned>(segments), fa::cache::kPickThreads, 0, cs,
-                          c, batch, qs, scores, pages, slots, keep_first, keep_last))
+    using namespace fa::cache;
+    const auto pick = [&](auto kernel, int threads) {
+        return launch_dependent(kernel, static_cast<unsigned>(segments), threads, 0, cs, c, batch, qs, scores, pages, slots,
+                                keep_first, keep_last);
+    };
+    if (!(max_pages <= kPickFew ? pick(fa_cache_pick_kernel<kPickFewThreads, kPickFew>, kPickFewThreads)
+                                : pick(fa_cache_pick_kernel<kPickThreads, kPickHeld>, kPickThreads)))
         return FA_ERR_CUDA;
     return launched();
 }

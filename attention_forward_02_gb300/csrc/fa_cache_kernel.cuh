@@ -866,10 +866,20 @@ __global__ void __launch_bounds__(kScoreThreads)
 // the smallest chosen score by four 8-bit digits (a histogram of the scores
 // that share the digits found so far), then one ordered pass that writes, each
 // thread a run of pages.  Up to kPickHeld scores are held in shared memory.
-constexpr int kPickThreads = 512;
-constexpr int kPickHeld = 8192;
+//
+// A table of at most kPickFew pages gives a block no more than two scores a
+// thread with 128 threads, and 16 such blocks share an SM instead of four: the
+// selection takes 18.5 us instead of 35.5 for 77 sequences x 8 heads x 4 queries
+// of 26 pages, 9.9 instead of 12.5 for 39 x 32 of 133, 8.4 instead of 9.0 for
+// 7 x 8 x 2 of 214, and 7.8 instead of 7.7 for 6 x 8 of 177.  A warp a segment,
+// with its scores in registers and ballots for counts, took twice as long (19.5
+// at 7 x 8 x 2 of 214).  Over 256 pages 512 threads stay: 256 threads took 10.5
+// instead of 9.8 at 8 segments of 2,048 pages.
+constexpr int kPickThreads = 512, kPickHeld = 8192;
+constexpr int kPickFewThreads = 128, kPickFew = 256;
 
 // Sum over the block's earlier threads of x (and, in `total`, over all).
+template <int THREADS>
 __device__ __forceinline__ int block_before(int x, int *smem, int &total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -885,7 +895,7 @@ __device__ __forceinline__ int block_before(int x, int *smem, int &total)
         smem[warp] = incl;
     __syncthreads();
     total = 0;
-    for (int w = 0; w < kPickThreads / 32; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
         const int y = smem[w];
         if (w < warp)
             incl += y;
@@ -894,13 +904,14 @@ __device__ __forceinline__ int block_before(int x, int *smem, int &total)
     return incl - x;
 }
 
-__global__ void __launch_bounds__(kPickThreads)
+template <int THREADS, int HELD>
+__global__ void __launch_bounds__(THREADS)
     fa_cache_pick_kernel(Cache cache, Batch batch, Queries q, const uint32_t *__restrict__ scores,
                          int *__restrict__ pages, int slots, int keep_first, int keep_last)
 {
-    __shared__ uint32_t held[kPickHeld];
+    __shared__ uint32_t held[HELD];
     __shared__ int hist[256];
-    __shared__ int sums[kPickThreads / 32];
+    __shared__ int sums[THREADS / 32];
     __shared__ int found[2];
     wait_ahead();
     let_next();
@@ -911,7 +922,7 @@ __global__ void __launch_bounds__(kPickThreads)
     int *out = pages + seg * slots;
     const int n = (context(q, batch.length(b, cache.log2_page), i) + cache.page - 1) >> cache.log2_page;
     if (n <= slots) {
-        for (int j = t; j < slots; j += kPickThreads)
+        for (int j = t; j < slots; j += THREADS)
             out[j] = j < n ? j : -1;
         return;
     }
@@ -919,17 +930,17 @@ __global__ void __launch_bounds__(kPickThreads)
     const int lo = keep_first, hi = n - keep_last;  // candidates
     const bool any = slots > keep_first + keep_last;
     int want = slots - keep_first - keep_last;      // < hi - lo
-    if (n <= kPickHeld && any) {
-        for (int j = lo + t; j < hi; j += kPickThreads)
+    if (n <= HELD && any) {
+        for (int j = lo + t; j < hi; j += THREADS)
             held[j] = key[j];
         key = held;
     }
     uint32_t prefix = 0;
     for (int shift = 24; want > 0 && shift >= 0; shift -= 8) {
-        if (t < 256)
-            hist[t] = 0;
+        for (int digit = t; digit < 256; digit += THREADS)
+            hist[digit] = 0;
         __syncthreads();
-        for (int j0 = lo; j0 < hi; j0 += kPickThreads) {
+        for (int j0 = lo; j0 < hi; j0 += THREADS) {
             const int j = j0 + t;
             const uint32_t x = j < hi ? key[j] : 0u;
             const bool in = j < hi && (shift == 24 || (x >> (shift + 8)) == prefix);
@@ -976,7 +987,7 @@ __global__ void __launch_bounds__(kPickThreads)
     }
     // a page is written if it is kept, above the smallest chosen score, or one of
     // the first `want` that equal it
-    const int each = (n + kPickThreads - 1) / kPickThreads;
+    const int each = (n + THREADS - 1) / THREADS;
     const int j0 = t * each, j1 = min(n, j0 + each);
     int above = 0, equal = 0, total;
     for (int j = j0; j < j1; ++j) {
@@ -985,9 +996,9 @@ __global__ void __launch_bounds__(kPickThreads)
         above += kept || (any && x > prefix);
         equal += !kept && any && x == prefix;
     }
-    const int equal_before = block_before(equal, sums, total);
+    const int equal_before = block_before<THREADS>(equal, sums, total);
     const int take = max(0, min(equal, want - equal_before));  // of its equal ones
-    int pos = block_before(above + take, sums, total), left = take;
+    int pos = block_before<THREADS>(above + take, sums, total), left = take;
     for (int j = j0; j < j1; ++j) {
         const bool kept = j < lo || j >= hi;
         const uint32_t x = !kept && any ? key[j] : 0u;

@@ -667,6 +667,22 @@ def test_select_many_pages(fa, n, B, heads):
     assert (got[..., 1:] > got[..., :-1]).all() and (got[..., 0] == 0).all()
 
 
+@pytest.mark.parametrize("n", [255, 256, 257])
+@pytest.mark.parametrize("slots,first,last", [(8, 1, 1), (254, 0, 0), (5, 3, 2)])
+def test_select_table_widths(fa, n, slots, first, last):
+    """Tables about the width where the number of threads changes, with ties and short sequences among them."""
+    page, d, heads = 16, 64, 2
+    lens = [page * n, page * n - 7, page * slots + 1, 0]
+    ref = Ref(300, heads, page, d, "int8", 2)
+    ref.k_mean[:] = (ref.k_mean / 32).round()
+    table = torch.randint(0, 300, (len(lens), n), generator=torch.Generator().manual_seed(4)).int()
+    q = randn((len(lens), heads, 2, d), torch.bfloat16, 3)
+    got = fa.fa_cache_select(q.cuda(), ref.to("cuda"), dev(table), dev(lens), slots, keep_first=first, keep_last=last,
+                             causal=True)
+    assert status(fa) == 0
+    assert torch.equal(got.cpu(), ref.select(q, table, lens, slots, first, last, True))
+
+
 def _scores(ref, q, row, h):
     from cache_util import encode, finite_max, scale_of
     s = scale_of(finite_max(q.double()), 127.0)
