@@ -142,6 +142,27 @@ def test_write_uneven_batch(fa):
     check_cache(cache, ref)
 
 
+@pytest.mark.parametrize("B", [32, 33, 128, 129, 300])
+def test_write_many_sequences(fa, B):
+    """Short sequences, runs of empty ones and a long one, in batches about the numbers that are counted at a time."""
+    page, d, heads = 16, 32, 1
+    new = [0 if i % 50 > 40 else (3 * i) % 7 for i in range(B)]
+    new[B - 2], new[B - 1] = 90, 2
+    before = [(5 * i) % 40 for i in range(B)]
+    table, pool = pages_for([a + n for a, n in zip(before, new)], page, 5)
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    assert cu[-1] > B
+    ref = Ref(pool, heads, page, d, "int8", 6)
+    cache = ref.to("cuda")
+    k, v = (randn((cu[-1], heads, d), torch.float16, s) for s in (7, 8))
+    fa.fa_cache_write(cache, k.cuda(), v.cuda(), dev(table), dev(before), cu_seqlens=dev(cu))
+    assert status(fa) == 0
+    ref.write(k, v, table, before, cu)
+    check_cache(cache, ref)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("page,d,heads", [(16, 96, 2), (32, 32, 1), (128, 128, 1)])
@@ -668,7 +689,7 @@ def test_select_many_pages(fa, n, B, heads):
 
 
 @pytest.mark.parametrize("n", [255, 256, 257])
-@pytest.mark.parametrize("slots,first,last", [(8, 1, 1), (254, 0, 0), (5, 3, 2)])
+@pytest.mark.parametrize("slots,first,last", [(8, 1, 1), (254, 0, 1), (5, 3, 2)])
 def test_select_table_widths(fa, n, slots, first, last):
     """Tables about the width where the number of threads changes, with ties and short sequences among them."""
     page, d, heads = 16, 64, 2
