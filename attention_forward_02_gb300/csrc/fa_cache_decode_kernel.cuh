@@ -42,8 +42,8 @@
 // whole segment instead, and that launch is all.
 //
 // Measured, whole calls back to back (e4m3, d = 128, 8 KV heads): 64 sequences of
-// up to 16,384 keys, 4 rows a head, 1.20 GB: 181 us, 6.6 TB/s, 98 % of the
-// measured copy rate, and DRAM reads 1.2036 GB; one of 131,072 keys, 8 rows,
+// up to 16,384 keys, 4 rows a head, 1.20 GB: 181 to 184 us, 6.5 TB/s, 96 to 98 % of
+// the measured copy rate, DRAM reads 1.2036 GB; one of 131,072 keys, 8 rows,
 // 269 MB: 51 us, 77 %, where some 10 us of a call are no streaming (lengths, page
 // numbers and scales one after the other, the first copies, the merges).  With 16
 // rows a head the instructions bound it: 16 sequences, 340 MB of int8 codes,
