@@ -28,9 +28,9 @@
 // Query rows are scaled by a power of two to a row maximum in [2^14, 2^15)
 // before they become fp16: a bf16 row keeps every bit that fp32 sums would see.
 // P is rounded to fp16 (2^-12) as P * v_scale against a reference m that
-// includes v_scale's exponent, m >= s_j + log2 v_scale_j - 8 for every key j,
-// so that no product with a V scale overflows and V scales of any size mix.
-// m moves (and O, l are rescaled) only when a score outgrows it by 2^8.
+// includes v_scale's exponent, so that V scales of any size mix, and lies 2^10 under
+// the largest one seen (kAim below).  m moves (and O, l are rescaled) only when
+// one outgrows it by 2^14.9.
 //
 // Work is dealt in units of a stage's 64 keys (128 at d <= 64) of one (sequence,
 // KV head, row group): the blocks of a persistent grid take equal runs of the
@@ -103,6 +103,20 @@ struct __align__(16) StageMeta {
 static_assert(sizeof(StageMeta) == 192, "stage record");
 constexpr int kFirst = 1, kLast = 2, kHeadPart = 4, kTailPart = 8, kOddScale = 16;
 constexpr int kNoKey = 0x7FFFFF00;  // behind every context
+
+// P is rounded to fp16, whose 2^-14 .. 65,504 has to hold the largest weight of a row and
+// the small ones beside it: an attention sink, a key with nearly all the weight and a
+// value near zero, leaves the output to weights of 2^-20 of its own and less.  So the
+// reference is put 2^kAim under the largest P * v_scale (its power of two), and moves when
+// one has grown to 2^kMost (the V scale's factor over its power of two, below 2, is still
+// to come: 2^15.9 < 65,504).  Weights down to 2^-24 of the largest keep all eleven bits,
+// those down to 2^-34 some.  A sink of 0.9999 over 4,096 keys, bf16: o off by 1.86e-3 of
+// itself (rms), of which its own rounding is 1.84e-3; with the reference at the largest
+// one 9.0e-3, and 1.8e-2 where a warp has all keys of a row.  The room left for growth
+// decides how often the reference moves: at 16 rows a head (16 x 16,384 keys, int8,
+// d = 128) 6 and 8 octaves take 84.0 us, 4.9 take 84.4, 4 85.0, 2 87.0 and 1 88.9; up to
+// 8 rows it does not show.
+constexpr float kAim = 10.f, kMost = 14.9f;
 
 // Where a thread (g = lane / 4, c = lane % 4) finds its bytes of a 16-key tile in
 // a part W bytes wide: of K, 4 words (2 if W = 32) ... of rows g and g + 8; of V,
@@ -686,7 +700,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::BLOCKS)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        grown |= !(e[j][nt][u] <= 8.f);
+                        grown |= !(e[j][nt][u] <= kMost);
             if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -700,7 +714,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::BLOCKS)
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        const float up = unset & bit ? (top == -INFINITY ? 0.f : top) : fmaxf(top, 0.f);
+                        const float over = top - kAim;
+                        const float up = unset & bit ? (top == -INFINITY ? 0.f : over) : fmaxf(over, 0.f);
                         const float alpha = unset & bit ? 1.f : ex2(-up);
                         if (top > -INFINITY)
                             unset &= ~bit;
