@@ -14,8 +14,9 @@ and ``k, v = fa_cache_read(cache, page_table, seq_lens, N)`` for ``fa_fwd`` or
 ``fa_decode``.  ``page_table`` [B, max_pages] and ``seq_lens`` [B] are int32 CUDA
 tensors; the calls read them on the device, so a captured graph replays with
 whatever they hold then.  What they hold cannot be checked by the call: a page
-number or length outside the cache is left out, and
-``fa_last_device_status`` reports it.
+number outside the cache is left out, a length outside the page table is cut to it
+(and nothing is written for a negative one), and ``fa_last_device_status`` reports
+either.
 """
 import importlib.machinery
 import importlib.util

@@ -299,6 +299,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::BLOCKS)
         x /= w.cache.heads;
         i = w.pages ? x % w.q.Nq : 0;
         b = w.pages ? x / w.q.Nq : x;
+        if (t == 0 && group == 0 && head == 0 && i == 0)
+            w.batch.check_length(b, w.cache.log2_page);
         // a segment without keys has a unit all the same, and writes its rows in it
         all = max(1, units_of<F::LOG2_STEP>(w, w.batch.length(b, w.cache.log2_page), i));
         __syncthreads();  // the barriers are set
@@ -333,6 +335,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::BLOCKS)
             long long y = at;
             for (int x = b0; x < b1; ++x) {
                 w.plan[1 + x] = y;
+                w.batch.check_length(x, w.cache.log2_page);
                 y += units_of_sequence<F::LOG2_STEP>(w, x);
             }
         }

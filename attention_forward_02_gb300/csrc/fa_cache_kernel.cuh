@@ -50,6 +50,13 @@ struct Batch {
         const int n = seq_lens[b];
         return n <= 0 ? 0 : static_cast<int>(n < cap ? n : cap);
     }
+    // Reports a length that length() cuts; one thread of a call does it for a sequence.
+    __device__ void check_length(int b, int log2_page) const
+    {
+        const int n = seq_lens[b];
+        if (n < 0 || n > static_cast<long long>(max_pages) << log2_page)
+            bad();
+    }
 };
 
 __device__ __forceinline__ float pow2f(int e)  // 2^e, -126 <= e <= 127
@@ -332,9 +339,9 @@ __device__ __forceinline__ int touched_page(const Cache &cache, const Batch &bat
             const int x = b0 + 32 * u + lane;
             count[u] = 0;
             if (x < in.batch) {
-                const long long had = max(batch.seq_lens[x], 0);
+                const long long had = batch.seq_lens[x];
                 int t0, n;
-                if (!in.tokens(x, t0, n))
+                if (!in.tokens(x, t0, n) || (n > 0 && had < 0))
                     batch.bad();
                 else if (n > 0)
                     count[u] = static_cast<int>(((had + n - 1) >> cache.log2_page) - (had >> cache.log2_page)) + 1;
@@ -386,7 +393,7 @@ __global__ void __launch_bounds__(kWriteThreads, 4) fa_cache_write_kernel(Cache 
         return;  // fewer pages than blocks
     int t0, n;
     in.tokens(b, t0, n);
-    const long long had = max(batch.seq_lens[b], 0);  // tokens before
+    const long long had = batch.seq_lens[b];  // tokens before
     const long long end = had + n;
     const long long token_stride = which ? in.token_stride[1] : in.token_stride[0];
     const T *x = static_cast<const T *>(which ? in.x[1] : in.x[0]) +
@@ -543,9 +550,9 @@ __global__ void __launch_bounds__(32 * kStepWarps) fa_cache_step_kernel(Cache ca
         return;
     const bool live = 4 * lane < d;
     const uint32_t infinity = DTypeTraits<T>::kBF16 ? 0x7F80u : 0x7C00u;
-    const long long had = max(batch.seq_lens[b], 0);  // tokens before
+    const long long had = batch.seq_lens[b];  // tokens before
     int t0, n;
-    if (!in.tokens(b, t0, n)) {
+    if (!in.tokens(b, t0, n) || (n > 0 && had < 0)) {
         if (lane == 0)
             batch.bad();
         return;
@@ -677,6 +684,8 @@ __global__ void __launch_bounds__(kReadThreads)
     const int groups = d / 16;
     const long long vectors = static_cast<long long>(N) * groups;
     const int len = batch.length(b, cache.log2_page);
+    if (chunk == 0 && h == 0 && which == 0 && threadIdx.x == 0)
+        batch.check_length(b, cache.log2_page);
     const uint8_t *codes = which ? cache.v : cache.k;
     const float *scales = which ? cache.v_scale : cache.k_scale;
     T *out = (which ? v : k) + bh * N * d;
@@ -787,6 +796,8 @@ __global__ void __launch_bounds__(kScoreThreads)
     for (int x = 0; x < 2; ++x)
         page[x] = batch.page(b, first + g + 8 * x);
     const int len = batch.length(b, cache.log2_page);
+    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0)
+        batch.check_length(b, cache.log2_page);
     const int n = (context(q, len, q.Nq - 1) + cache.page - 1) >> cache.log2_page;  // of the longest context
     if (static_cast<int>(blockIdx.x) * kScorePages >= n || n <= slots)
         return;  // no page here, or every page is chosen anyway

@@ -299,7 +299,8 @@ typedef struct {
  *  dtype   : type of k and v.
  * A token whose position lies behind the page table, or whose page number is
  * not in 0 .. num_pages - 1, is skipped and reported as FA_ERR_BOUNDS by
- * fa_last_device_status.
+ * fa_last_device_status; so are all of a sequence whose length is negative or
+ * whose offsets are none.
  */
 FA_API fa_status_t fa_cache_write(const fa_cache_t *cache, const void *k, const void *v,
                                   long long k_token_stride, long long k_head_stride,
@@ -316,7 +317,9 @@ FA_API fa_status_t fa_cache_write(const fa_cache_t *cache, const void *k, const 
  *
  *  k, v    : contiguous [B, heads, N, d] of `dtype`, 16-byte aligned; must not
  *            overlap each other or the cache.  Written.
- *  Other arguments as for fa_cache_write (seq_lens: tokens in the cache).
+ *  Other arguments as for fa_cache_write (seq_lens: tokens in the cache; one
+ *            behind the page table is cut to it, a negative one is 0, and both
+ *            are reported as FA_ERR_BOUNDS, as bad pages are).
  */
 FA_API fa_status_t fa_cache_read(const fa_cache_t *cache, void *k, void *v, const int *seq_lens,
                                  const int *page_table, long long table_stride, int max_pages,
@@ -343,7 +346,8 @@ FA_API size_t fa_decode_cache_workspace_size(int B, int Hq, int Hkv, int Nq, int
  *  o       : contiguous [B, Hq, Nq, d] of `dtype`, 16-byte aligned.
  *  lse     : [B, Hq, Nq] fp32, or NULL.
  *  seq_lens: [B] int32 on the device: keys, the queries' own among them.  A
- *            length behind the page table is cut to it, a negative one is 0.
+ *            length behind the page table is cut to it, a negative one is 0;
+ *            both are reported as FA_ERR_BOUNDS.
  *  pages   : NULL, or [B, heads, Nq, slots] int32: query i of KV head h sees
  *            only keys of the pages (numbers within the sequence) listed there.
  *            The first min(slots, pages of its context) entries count; negative
