@@ -79,27 +79,49 @@ def binding_command(out):
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
             "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+            '-DFA_TORCH_VERSION="%s"' % torch.__version__,
             "-isystem" + include, "-isystem" + os.path.join(include, "torch", "csrc", "api", "include"),
             "-isystem" + cuda, "-I" + sysconfig.get_paths()["include"], "-I" + INCLUDE, BINDING_SOURCE,
             "-o", out, "-L" + lib, "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_cuda", "-Wl,-rpath," + lib]
 
 
 def build_binding(force=False):
-    """Compile the CPython module if its source is newer; returns its path, or None where it cannot be
-    built (the cache's functions then take their longer way through ctypes)."""
+    """Compile the CPython module if its source is newer or torch another one; returns its path, or None
+    where it cannot be built (the cache's functions then take their longer way through ctypes).  An older
+    module does not outlive a failed compilation: it may speak to another ABI."""
     os.makedirs(OUT_DIR, exist_ok=True)
     sources = [BINDING_SOURCE, os.path.join(INCLUDE, "fa.h")]
-    if not force and os.path.exists(BINDING) and all(
-            os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in sources):
-        return BINDING
+    note = BINDING + ".torch"  # the torch it was built against
+    try:
+        import torch
+        version = str(torch.__version__)
+        if not force and os.path.exists(BINDING) and all(
+                os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in sources):
+            with open(note) as f:
+                if f.read() == version:
+                    return BINDING
+    except FileNotFoundError:  # a module that does not say
+        pass
+    except ImportError as e:
+        return _no_binding(note, e)
     tmp = BINDING + ".tmp%d" % os.getpid()
     try:
         subprocess.run(binding_command(tmp), check=True)
     except (ImportError, AttributeError, OSError, subprocess.CalledProcessError) as e:
-        print("the cache's CPython module was not built: %s" % e, file=sys.stderr)
-        return None
+        return _no_binding(note, e)
     os.replace(tmp, BINDING)
+    with open(tmp, "w") as f:
+        f.write(version)
+    os.replace(tmp, note)
     return BINDING
+
+
+def _no_binding(note, why):
+    print("the cache's CPython module was not built: %s" % why, file=sys.stderr)
+    for path in (note, BINDING):
+        if os.path.exists(path):
+            os.remove(path)
+    return None
 
 
 def build_library(force=False, verbose_ptxas=False, checked=True):

@@ -63,8 +63,21 @@ class FACache(NamedTuple):
 
 # The CPython module of csrc/fa_cache_py.cpp goes through a usual call's checks and allocations in less
 # time than Python does; it hands back (None) what is not usual, and the functions below see to that.
-_module = None   # the module; False where it was not built
+_module = None   # the module; False where there is none that can be used
 _bound = None    # the library whose addresses it holds
+
+
+def _load_module():
+    """The module, if it was built, loads, and was built for this torch; else False."""
+    if not os.path.exists(BINDING):
+        return False
+    try:
+        loader = importlib.machinery.ExtensionFileLoader(BINDING_NAME, BINDING)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader(BINDING_NAME, loader))
+        loader.exec_module(module)
+    except (ImportError, OSError):
+        return False
+    return module if getattr(module, "torch", None) == str(torch.__version__) else False
 
 
 def _quick():
@@ -72,12 +85,9 @@ def _quick():
     lib = load()
     if lib is not _bound:
         if _module is None:
-            if os.path.exists(BINDING):
-                loader = importlib.machinery.ExtensionFileLoader(BINDING_NAME, BINDING)
-                _module = importlib.util.module_from_spec(importlib.util.spec_from_loader(BINDING_NAME, loader))
-                loader.exec_module(_module)
-            else:
-                _module = False
+            _module = _load_module()
+        if _module and _module.abi != lib.fa_abi_version():
+            _module = False
         if _module:
             _module.bind(*(cast(f, c_void_p).value for f in (
                 lib.fa_cache_write, lib.fa_cache_read, lib.fa_decode_cache, lib.fa_decode_cache_workspace_size,

@@ -9,6 +9,8 @@
 //
 // A CPython module without state but the addresses of the library's functions,
 // which cache.py sets (bind), so that either build of the library can be used.
+// It says which ABI and which torch it was compiled for; cache.py binds it only
+// where both are those it runs with.
 #include <Python.h>
 
 #include <cmath>
@@ -353,4 +355,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fa_cache_py", nullptr, -1, method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fa_cache_py() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__fa_cache_py()
+{
+    PyObject *m = PyModule_Create(&module);
+    if (m && (PyModule_AddIntConstant(m, "abi", FA_ABI_VERSION) < 0 ||
+              PyModule_AddStringConstant(m, "torch", FA_TORCH_VERSION) < 0)) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
