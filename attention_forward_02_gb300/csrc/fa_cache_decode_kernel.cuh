@@ -434,12 +434,12 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::BLOCKS)
                     const int row0 = (lane - first_lane) << w.log2_box;  // of the stage
                     const uint32_t dst = sbase + F::RING_OFF + s * F::STAGE + row0 * F::W0;
                     const int y = key0 & (w.cache.page - 1);
-                    tma_load_3d(dst, &maps.k[0], full(s), 0, y, ph, policy);
-                    tma_load_3d(dst + F::HALF, &maps.v[0], full(s), 0, y, ph, policy);
+                    tma_load_3d(dst, &maps.k[0], full(s), 0, y, ph, policy, box * F::W0);
+                    tma_load_3d(dst + F::HALF, &maps.v[0], full(s), 0, y, ph, policy, box * F::W0);
                     if (F::PARTS == 2) {
                         const uint32_t dst1 = sbase + F::RING_OFF + s * F::STAGE + F::STEP * F::W0 + row0 * F::W1;
-                        tma_load_3d(dst1, &maps.k[1], full(s), F::W0, y, ph, policy);
-                        tma_load_3d(dst1 + F::HALF, &maps.v[1], full(s), F::W0, y, ph, policy);
+                        tma_load_3d(dst1, &maps.k[1], full(s), F::W0, y, ph, policy, box * F::W1);
+                        tma_load_3d(dst1 + F::HALF, &maps.v[1], full(s), F::W0, y, ph, policy, box * F::W1);
                     }
                 }
                 StageMeta *m = meta + s;

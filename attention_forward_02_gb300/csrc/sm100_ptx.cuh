@@ -174,11 +174,12 @@ __device__ __forceinline__ void tma_prefetch_desc(const void *tmap)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
 }
 
+// bytes: of the map's box, for the check (the attention kernels' boxes are at least
+// 1 KB, the paged cache's 512 bytes to 8 KB).  dst is 128-byte aligned.
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, uint32_t bar, int x,
-                                            int y, int z, uint64_t policy)
+                                            int y, int z, uint64_t policy, uint32_t bytes = 1024)
 {
-    // every box here is at least 1 KB and 128-byte aligned
-    if (!smem_ok(dst, 1024, 128) || !smem_ok(bar, 8, 8))
+    if (!smem_ok(dst, bytes, 128) || !smem_ok(bar, 8, 8))
         return;
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
