@@ -133,6 +133,13 @@ def _describe(cache):
             heads, d, index)
 
 
+def _int(x, name):
+    """A whole number as the C ABI takes it: ctypes would cut it to its low 32 bits."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise FAError(1, "%s must fit 32 bits, got %s" % (name, x))
+    return x
+
+
 def _check_batch(index, page_table, seq_lens):
     """Sequences, distance of the page table's rows, its columns."""
     try:
@@ -145,7 +152,7 @@ def _check_batch(index, page_table, seq_lens):
     if not good:
         raise FAError(1, "page_table [B, max_pages] and seq_lens [B] must be int32 tensors on the cache's device, "
                       "their last dimension contiguous")
-    return B, page_table.stride(0) if B > 1 else P, P
+    return _int(B, "B"), page_table.stride(0) if B > 1 else P, _int(P, "max_pages")
 
 
 def _code(t, name, dim, index, d):
@@ -229,7 +236,7 @@ def fa_cache_write(cache, k, v, page_table, seq_lens, cu_seqlens=None, stream=No
     kt, kh, _ = k.stride()
     vt, vh, _ = v.stride()
     st = fa_cache_write_raw(desc, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, cu, seq_lens.data_ptr(),
-                            page_table.data_ptr(), stride, P, B, shape[0], code, _stream(index))
+                            page_table.data_ptr(), stride, P, B, _int(shape[0], "T"), code, _stream(index))
     if st != 0:
         raise FAError(st, "fa_cache_write")
 
@@ -256,7 +263,7 @@ def fa_cache_read(cache, page_table, seq_lens, N, dtype=torch.bfloat16, k=None, 
     code = _CODES.get(dtype)
     if code is None:
         raise FAError(2, "dtype must be float16 or bfloat16, got %s" % dtype)
-    if N < 0:
+    if _int(N, "N") < 0:
         raise FAError(1, "N must not be negative")
     shape = (B, heads, N, d)
     device = cache.k.device
@@ -291,11 +298,12 @@ def fa_decode_cache(q, cache, page_table, seq_lens, pages=None, o=None, lse=None
     code = _code(q, "q", 4, index, d)
     shape = q.shape
     Bq, Hq, Nq, _ = shape
-    if Bq != B or Hq % heads:
+    if Bq != B or _int(Hq, "Hq") % heads:
         raise FAError(1, "q must be [B, Hq, Nq, d] with Hq a multiple of the cache's heads")
+    _int(Nq, "Nq")
     slots, listed = 0, None
     if pages is not None:
-        slots = pages.shape[-1] if isinstance(pages, torch.Tensor) and pages.dim() else 0
+        slots = _int(pages.shape[-1], "slots") if isinstance(pages, torch.Tensor) and pages.dim() else 0
         listed = _output(pages, "pages", (B, heads, Nq, slots), torch.int32, index).data_ptr()
     if scale is None:
         scale = float(d) ** -0.5
@@ -342,10 +350,12 @@ def fa_cache_select(q, cache, page_table, seq_lens, slots, keep_first=1, keep_la
     B, stride, P = _check_batch(index, page_table, seq_lens)
     code = _code(q, "q", 4, index, d)
     Bq, Hq, Nq, _ = q.shape
-    if Bq != B or Hq % heads:
+    if Bq != B or _int(Hq, "Hq") % heads:
         raise FAError(1, "q must be [B, Hq, Nq, d] with Hq a multiple of the cache's heads")
-    if slots < 1:
+    _int(Nq, "Nq")
+    if _int(slots, "slots") < 1:
         raise FAError(1, "slots must be at least 1")
+    _int(keep_first, "keep_first"), _int(keep_last, "keep_last")
     shape = (B, heads, Nq, slots)
     device = cache.k.device
     if pages is None:
