@@ -353,6 +353,8 @@ def fa_cache_select(q, cache, page_table, seq_lens, slots, keep_first=1, keep_la
     if Bq != B or _int(Hq, "Hq") % heads:
         raise FAError(1, "q must be [B, Hq, Nq, d] with Hq a multiple of the cache's heads")
     _int(Nq, "Nq")
+    if Hq == 0 and B > 0:
+        raise FAError(1, "pages are chosen by their scores with query heads, and q has none")
     if _int(slots, "slots") < 1:
         raise FAError(1, "slots must be at least 1")
     _int(keep_first, "keep_first"), _int(keep_last, "keep_last")

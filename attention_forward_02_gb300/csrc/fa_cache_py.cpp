@@ -307,7 +307,8 @@ PyObject *py_select(PyObject *, PyObject *const *a, Py_ssize_t n)
             return handed_back();
         }
         const Tensor *q = rows(a[0], device, 4, c.d, type);
-        if (!q || q->size(0) != b.B || !to_int(q->size(1), Hq) || !to_int(q->size(2), Nq) || c.heads < 1 || Hq % c.heads)
+        if (!q || q->size(0) != b.B || !to_int(q->size(1), Hq) || !to_int(q->size(2), Nq) || c.heads < 1 || Hq % c.heads ||
+            (Hq == 0 && b.B > 0))
             return handed_back();
         const int64_t shape[4] = {b.B, c.heads, Nq, slots};
         Tensor pages, ws;

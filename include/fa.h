@@ -390,7 +390,8 @@ FA_API size_t fa_cache_select_workspace_size(int B, int Hkv, int Nq, int max_pag
  *  slots   : >= keep_first + keep_last; keep_first >= 0, keep_last >= 1.
  *  workspace: device, 16-byte aligned, >= fa_cache_select_workspace_size bytes.
  *  Other arguments as for fa_decode_cache.  A page with a bad number scores
- *  lowest and is reported as FA_ERR_BOUNDS.
+ *  lowest and is reported as FA_ERR_BOUNDS.  Hq = 0 is an empty problem, as
+ *  there: no query reads a list, and `pages` stays as it was.
  */
 FA_API fa_status_t fa_cache_select(const fa_cache_t *cache, const void *q, long long q_batch_stride,
                                    long long q_head_stride, long long q_row_stride,

@@ -1,5 +1,5 @@
-"""Arguments of the 8-bit cache's Python functions that the C ABI cannot see: whole numbers that 32 bits do not hold.
-Through the CPython module and through ctypes."""
+"""Arguments of the 8-bit cache's Python functions that the C ABI cannot see: whole numbers that 32 bits do not hold,
+and a selection without query heads.  Through the CPython module and through ctypes."""
 import pytest
 import torch
 
@@ -74,3 +74,18 @@ def test_select_refuses_heads_beyond_32_bits(fa):
     with pytest.raises(fa.FAError) as e:
         fa.fa_cache_select(q[:, :1].expand(1, HUGE + 4, 1, 32), cache, table, lens, 4)
     assert e.value.status == 1
+
+
+def test_select_without_query_heads(fa):
+    """Its output would not be empty, and nothing says what it holds."""
+    cache, table, lens, q = case()
+    for pages in (None, torch.full((1, 2, 1, 4), -9, dtype=torch.int32, device="cuda")):
+        with pytest.raises(fa.FAError) as e:
+            fa.fa_cache_select(q[:, :0], cache, table, lens, 4, pages=pages)
+        assert e.value.status == 1
+    assert (pages == -9).all()
+    # attention without query heads has an empty result
+    o, lse = fa.fa_decode_cache(q[:, :0], cache, table, lens)
+    assert o.shape == (1, 0, 1, 32) and lse.shape == (1, 0, 1)
+    # and so has a selection for no sequences
+    assert fa.fa_cache_select(q[:0], cache, table[:0], lens[:0], 4).shape == (0, 2, 1, 4)
