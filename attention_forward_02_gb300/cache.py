@@ -10,13 +10,13 @@ or, over the best pages of a long cache,
     pages = fa_cache_select(q, cache, page_table, seq_lens, slots)
     o, lse = fa_decode_cache(q, cache, page_table, seq_lens, pages=pages)
 
-and ``k, v = fa_cache_read(cache, page_table, seq_lens, N)`` for ``fa_fwd`` or
-``fa_decode``.  ``page_table`` [B, max_pages] and ``seq_lens`` [B] are int32 CUDA
-tensors; the calls read them on the device, so a captured graph replays with
-whatever they hold then.  What they hold cannot be checked by the call: a page
-number outside the cache is left out, a length outside the page table is cut to it
-(and nothing is written for a negative one), and ``fa_last_device_status`` reports
-either.
+and ``k, v = fa_cache_read(cache, page_table, seq_lens, N)`` in 16 bits, for
+``fa_fwd`` with ``causal`` or, each sequence cut to its length, ``fa_decode``.
+``page_table`` [B, max_pages] and ``seq_lens`` [B] are int32 CUDA tensors; the calls
+read them on the device, so a captured graph replays with whatever they hold then.
+What they hold cannot be checked by the call: a page number outside the cache is
+left out, a length outside the page table is cut to it (and nothing is written for a
+negative one), and ``fa_last_device_status`` reports either.
 """
 import importlib.machinery
 import importlib.util
@@ -242,7 +242,8 @@ def fa_cache_write(cache, k, v, page_table, seq_lens, cu_seqlens=None, stream=No
 
 
 def fa_cache_read(cache, page_table, seq_lens, N, dtype=torch.bfloat16, k=None, v=None, stream=None):
-    """The first N positions of every sequence as 16-bit k, v [B, heads, N, d], zeros behind seq_lens[b].
+    """The first N positions of every sequence as 16-bit k, v [B, heads, N, d], zeros behind seq_lens[b]
+    (which are no mask: attention that sees them counts them as keys of score 0).
     k, v: optional preallocated outputs (their dtype counts then).  Returns (k, v)."""
     if stream is None and type(cache) is FACache and dtype in _CODES and (quick := _quick()):
         given = k if k is not None else v

@@ -312,8 +312,14 @@ FA_API fa_status_t fa_cache_write(const fa_cache_t *cache, const void *k, const 
 /*
  * fa_cache_read -- read the first N positions of every sequence back into
  * 16-bit tensors (asynchronous): code * scale rounded to nearest.  Positions
- * from seq_lens[b] on, and those of a bad page, become zeros, so that the
- * result can serve as K and V of fa_fwd or fa_decode.
+ * from seq_lens[b] on, and those of a bad page, become zeros.
+ *
+ * Zeros are finite, which is what causal attention needs of rows that it does
+ * not see: fa_fwd with causal = 1 may run over the padded batch, and its rows
+ * before a sequence's end are right.  They are no mask: to a call that sees them
+ * they are keys of score 0, which take weight.  fa_fwd without causal and
+ * fa_decode need each sequence cut to its length (or N no larger than the
+ * shortest), and K and V of `heads` heads repeated where the queries have more.
  *
  *  k, v    : contiguous [B, heads, N, d] of `dtype`, 16-byte aligned; must not
  *            overlap each other or the cache.  Written.
