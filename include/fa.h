@@ -345,7 +345,9 @@ FA_API size_t fa_decode_cache_workspace_size(int B, int Hq, int Hkv, int Nq, int
  * queries at the end of the sequence: query i sees keys 0 .. seq_lens[b] - Nq + i.
  * A row that sees no key gets O = 0 and LSE = -infinity.  Scales other than
  * powers of two (of a cache that something else has filled) are read as well, if
- * they are normal positive numbers.
+ * they lie in 2^-80 .. 2^120.  The V scales of one sequence may differ by up to
+ * 2^100 (a page of zeros has 2^-60, so: up to values of 1e14 beside it); the
+ * weight of a key whose page is further below the largest can be lost.
  *
  *  q       : element (b, h, i, c) at b * q_batch_stride + h * q_head_stride +
  *            i * q_row_stride + c (strides as in fa_cache_write); 16-byte aligned.

@@ -125,3 +125,17 @@ def test_peaked_and_rising_scores(fa, fmt):
         ref.k[p] = ref.k[p].abs()
         ref.k_scale[p] = 2.0 ** -9 * (1 if at < 5 else 2 if at < 10 else 4)
     check(fa, ref, q.abs() * 4, table, lens)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("G", [4, 20])
+@pytest.mark.parametrize("low,high", [(-80, -80), (100, 100), (-60, 40), (-80, 20)])
+def test_scales_at_the_ends_of_their_range(fa, fmt, G, low, high):
+    """V scales as small and as large as they may be, and as far apart within one sequence; small and large ones take
+    turns, so that half of the weight is at pages of the lowest."""
+    page, n = 16, 700
+    table, pool = pages_for([n], page, 1)
+    ref = tiles_apart(Ref(pool, 1, page, 64, fmt, 2))
+    for at in range(-(-n // page)):
+        ref.v_scale[int(table[0, at])] = 2.0 ** (low if at % 2 else high)
+    check(fa, ref, randn((1, G, 1, 64), torch.bfloat16, 3), table, [n])
