@@ -25,10 +25,17 @@ using fa_host::overlaps;
 constexpr int kMaxNq = 16;
 constexpr int kMaxBatch = 65535;  // a grid's y and z extent
 // Units of a segment that one block may take whole: one launch in place of two,
-// but the units one after the other.  One sequence, 8 heads of 128, whole against
-// shared out, on the GPU and as called: 64 keys 4.7 / 6.6 and 8.0 / 11.0 us, 256
-// keys 6.2 / 7.4 and 8.1 / 11.0, 512 keys (8 units) 8.5 / 7.7 and 8.9 / 11.1, 1,024
-// keys 13.0 / 8.0 and 13.5 / 10.8.
+// but the units one after the other.  8 KV heads, e4m3, whole / shared out, us on the
+// GPU (in a graph):
+//                      1 unit     4 units     8 units     16 units
+//   d = 128, 1 seq.    4.6 / 6.6  6.2 / 7.4   8.4 / 7.7   13.0 / 8.0
+//            16                   6.6 / 8.7   8.8 / 10.9
+//            56                   8.5 / 15.8  13.0 / 21.7
+//   d = 64,  1         4.1 / 6.0  5.7 / 6.9   8.0 / 7.2
+//            16                   6.3 / 8.0   8.5 / 9.9
+//            56                   7.9 / 13.2  11.4 / 18.3
+// As called from Python one sequence takes 8.9 / 11 us at 1 to 8 units.  So eight units
+// of few segments are where a captured call loses (0.7 us); all else gains.
 constexpr long long kWholeUnits = 8;
 
 struct CacheState {
@@ -338,7 +345,11 @@ fa_status_t fa_cache_write(const fa_cache_t *cache, const void *k, const void *v
                                      T,
                                      B};
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (T <= B) {  // a warp a sequence, head, and of K and V
+    // A warp a sequence, head, and of K and V.  The totals decide, so that a batch whose
+    // rows are nearly all one sequence's is slow on either side: a prompt of 512 rows
+    // takes 114 us in 512 slots (one warp a head walks it), 48 in 511 (every block of the
+    // other kernel counts over the slots), and 4.4 alone (8 heads of 128, e4m3).
+    if (T <= B) {
         const long long units = 2ll * B * cache->heads;
         if (units > 0x7fffffffLL)
             return FA_ERR_UNSUPPORTED;

@@ -45,10 +45,11 @@
 // up to 16,384 keys, 4 rows a head, 1.20 GB: 181 to 184 us, 6.5 TB/s, 96 to 98 % of
 // the measured copy rate, DRAM reads 1.2036 GB; one of 131,072 keys, 8 rows,
 // 269 MB: 51 us, 77 %, where some 10 us of a call are no streaming (lengths, page
-// numbers and scales one after the other, the first copies, the merges).  With 16
+// numbers and scales one after the other, the first copies, the merges): twice the
+// keys take 37 us more.  The same at d = 64 with one row a head: 8 x up to 8,000 keys,
+// 32 heads, 138 MB take 32 us, 63 %, and as many again 22 more, 93 %.  With 16
 // rows a head the instructions bound it: 16 sequences, 340 MB of int8 codes,
-// 84 us, 60 %; conversions are over a third of them.  At d = 64 with one row a
-// head (8 x 8,000 keys, 32 heads, 138 MB) 32 us, 63 %, likewise.
+// 84 us, 59 %; conversions are over a third of them.
 #pragma once
 
 #include "fa_cache_kernel.cuh"

@@ -226,8 +226,9 @@ __device__ __forceinline__ float finite_max(float a, const float (&f)[8])
 // + page / 8, ...; eight 16-byte loads in flight a thread.  For long prompts the
 // instructions bound it, so amax is taken on pairs of 16-bit values and fp16 is
 // encoded in pairs; pages with infinities or NaN, which the maximum shows, and
-// scales beyond fp16's range go another way.  58,800 tokens of 8 heads of 128 (fp16
-// to int8, 361 MB): 62 us, 5.9 TB/s, 86 % of the measured copy rate.
+// scales beyond fp16's range go another way.  58,800 tokens of 8 heads of 128 (361 MB):
+// from fp16 to int8 62 us on the GPU, 5.8 TB/s, 86 % of the measured copy rate, to e4m3
+// 64; from bf16, which is encoded one by one in fp32, 66 and 67.
 constexpr int kWriteRows = 8;       // rows a thread
 constexpr int kWriteThreads = 256;  // most threads: page = d = 128
 
@@ -537,7 +538,10 @@ __global__ void __launch_bounds__(kWriteThreads, 4) fa_cache_write_kernel(Cache 
 // rows are read once for amax and again to be encoded.  What it costs is the chain
 // length - page number - scale and row, so the warps of a block share nothing and
 // meet nowhere: one token of 8 heads takes 2.3 us against 3.3 with a block a page,
-// 256 tokens (pages of 16) 6.7 against 7.2.
+// 256 tokens (pages of 16) 6.7 against 7.2.  Where a token is larger than its page
+// holds, the page's codes are read, moved to the new scale and written: 256 tokens of
+// 8 heads into pages of 64 with 40 tokens in them take 3.2 us where the scales stay,
+// 11 (e4m3) or 16 us (int8) where all of them grow.
 constexpr int kStepWarps = 8;
 
 template <typename T, typename C>
@@ -667,7 +671,7 @@ __global__ void __launch_bounds__(32 * kStepWarps) fa_cache_step_kernel(Cache ca
 //
 // 16 codes (16 bytes) in, 16 values (32 bytes) out a thread and step; bound by
 // the bytes it writes.  Two steps a thread: 8 x 16,384 tokens of 8 heads of 128
-// (749 MB) take 116 us, 95 % of the measured copy rate; one step 137, four 127,
+// (749 MB) take 116 us on the GPU, 95 % of the measured copy rate; one step 137, four 127,
 // eight 151, and 8 codes a step 153 us.
 constexpr int kReadThreads = 256;
 constexpr int kReadSteps = 2;
@@ -766,7 +770,9 @@ __device__ __forceinline__ uint32_t ordered(float f)
 // the kernel costs is the latency of length, page number, mean and query row,
 // so the first three are under way while the rows are rounded to int8.  With the
 // choice below: 9.8 us for one sequence of 2,048 pages and 8 heads, 24 us for 32 of
-// up to 2,048 pages, 4 heads and 2 queries (17 MB of means).
+// up to 2,048 pages, 4 heads and 2 queries (17 MB of means), of which the scores are the
+// larger part (cold and alone 17 us against 12 for the choice): each of its 2,048 blocks
+// goes through that chain and rounds the same query rows again.
 constexpr int kScoreThreads = 256;
 constexpr int kScorePages = kScoreThreads / 32 * 16;
 constexpr int kScoreRows = 64;  // of shared memory at a time

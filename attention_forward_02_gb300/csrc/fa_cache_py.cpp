@@ -4,8 +4,9 @@
 // stream of its own, another device than the current one, an argument that does
 // not pass) is handed back, and cache.py goes through it, which also words the
 // error.  What it saves is time on the host, which is most of a small call: a
-// fa_decode_cache of one short sequence takes 11 us in place of 28 (two launches
-// of about 2 us among them), a fa_cache_write of one token 6 in place of 13.
+// fa_decode_cache of one sequence of 500 keys takes 9.7 us in place of 26 (8.4 of
+// them on the GPU), a fa_cache_write of one token 4.2 in place of 12, a choice of
+// pages and the attention over them 22 in place of 55.
 //
 // A CPython module without state but the addresses of the library's functions,
 // which cache.py sets (bind), so that either build of the library can be used.
