@@ -8,20 +8,32 @@ C ABI (include/fa.h) of the in-tree CUDA library on the current torch stream;
 (split-KV).  ``FACache`` is a paged KV cache held in 8 bits with a scale for each
 page and head: ``fa_cache_write`` appends tokens to it, ``fa_cache_read`` reads
 them back, ``fa_decode_cache`` attends to it (grouped query heads, ragged
-lengths) and ``fa_cache_select`` chooses the pages that it reads.
+lengths) and ``fa_cache_select`` chooses the pages that it reads.  ``FACache4``
+is one held in 4 bits (``fa_cache4_write``, ``fa_cache4_read``,
+``fa_decode_cache4``).  ``fa_cache_plan`` and ``fa_cache_trim`` keep the page
+tables of either on the GPU, and ``fa_rope`` turns query and key rows to their
+positions (and gradients back).
 PyTorch only supplies device memory and the stream; every step of the
 computation runs in the library's kernel.  There is no CPU or eager fallback:
 without the built library, or off a CUDA device, calls raise ``FAError``.
 """
-from ._lib import (FA_BF16, FA_E4M3, FA_FP16, FA_INT8, CacheDesc, FAError, fa1_fwd_raw,
+from ._lib import (FA_BF16, FA_E4M3, FA_FP16, FA_INT8, Cache4Desc, CacheDesc, FAError, RopeDesc,
+                   RopeRows, fa1_fwd_raw,
                    fa1_fwd_workspace_size, fa_abi_version, fa_bwd_raw, fa_bwd_workspace_size,
+                   fa_cache4_read_raw, fa_cache4_write_raw, fa_cache_plan_raw,
                    fa_cache_read_raw, fa_cache_select_raw, fa_cache_select_workspace_size,
-                   fa_cache_write_raw, fa_decode_cache_raw, fa_decode_cache_workspace_size,
+                   fa_cache_trim_raw, fa_cache_write_raw, fa_decode_cache4_raw,
+                   fa_decode_cache4_workspace_size, fa_decode_cache_raw,
+                   fa_decode_cache_workspace_size,
                    fa_decode_raw, fa_decode_workspace_size, fa_fwd_raw, fa_last_device_status,
-                   fa_selftest_bounds_check, fa_selftest_wait_timeout, fa_status_str, lib_path,
+                   fa_rope_raw, fa_selftest_bounds_check, fa_selftest_wait_timeout, fa_status_str, lib_path,
                    load, load_checked)
 
-_CACHE_NAMES = ("FACache", "fa_cache_write", "fa_cache_read", "fa_cache_select", "fa_decode_cache")
+# names of the modules that need torch at their import, which this one does not
+_LAZY = {"cache": ("FACache", "fa_cache_write", "fa_cache_read", "fa_cache_select", "fa_decode_cache"),
+         "cache4": ("FACache4", "fa_cache4_write", "fa_cache4_read", "fa_decode_cache4"),
+         "pages": ("FAPagePool", "FAPlan", "fa_cache_plan", "fa_cache_trim"),
+         "rope": ("FARope", "fa_rope")}
 
 __all__ = ["fa_fwd", "fa_fwd_raw", "fa1_fwd", "fa1_fwd_raw", "fa1_fwd_workspace_size",
            "fa_bwd", "fa_bwd_raw", "fa_bwd_workspace_size",
@@ -29,17 +41,23 @@ __all__ = ["fa_fwd", "fa_fwd_raw", "fa1_fwd", "fa1_fwd_raw", "fa1_fwd_workspace_
            "FACache", "fa_cache_write", "fa_cache_read", "fa_cache_select", "fa_decode_cache",
            "fa_cache_write_raw", "fa_cache_read_raw", "fa_cache_select_raw", "fa_decode_cache_raw",
            "fa_cache_select_workspace_size", "fa_decode_cache_workspace_size", "CacheDesc",
+           "FACache4", "fa_cache4_write", "fa_cache4_read", "fa_decode_cache4", "Cache4Desc",
+           "fa_cache4_write_raw", "fa_cache4_read_raw", "fa_decode_cache4_raw",
+           "fa_decode_cache4_workspace_size",
+           "FAPagePool", "FAPlan", "fa_cache_plan", "fa_cache_trim", "fa_cache_plan_raw", "fa_cache_trim_raw",
+           "FARope", "fa_rope", "fa_rope_raw", "RopeDesc", "RopeRows",
            "fa_last_device_status", "fa_selftest_wait_timeout", "fa_selftest_bounds_check",
            "fa_status_str", "fa_abi_version", "FAError", "load", "load_checked", "lib_path"]
 
 
 def __getattr__(name):
-    # the cache's module needs torch at its import, this one does not
-    if name in _CACHE_NAMES:
-        from . import cache
-        for n in _CACHE_NAMES:
-            globals()[n] = getattr(cache, n)
-        return globals()[name]
+    for module, names in _LAZY.items():
+        if name in names:
+            from importlib import import_module
+            found = import_module("." + module, __name__)
+            for n in names:
+                globals()[n] = getattr(found, n)
+            return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 

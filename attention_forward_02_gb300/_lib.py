@@ -25,7 +25,8 @@ FA_INT8 = 1
 EXPORTS = ("fa_fwd", "fa1_fwd_workspace_size", "fa1_fwd", "fa1_fwd_noalloc", "fa_bwd_workspace_size",
            "fa_bwd", "fa_decode_workspace_size", "fa_decode", "fa_cache_write", "fa_cache_read",
            "fa_decode_cache_workspace_size", "fa_decode_cache", "fa_cache_select_workspace_size",
-           "fa_cache_select", "fa_last_device_status",
+           "fa_cache_select", "fa_rope", "fa_cache_plan", "fa_cache_trim", "fa_cache4_write",
+           "fa_cache4_read", "fa_decode_cache4_workspace_size", "fa_decode_cache4", "fa_last_device_status",
            "fa_selftest_wait_timeout", "fa_selftest_bounds_check", "fa_checked_build",
            "fa_status_str", "fa_abi_version")
 
@@ -40,6 +41,25 @@ class CacheDesc(ctypes.Structure):
                 ("k_mean_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int),
                 ("heads", ctypes.c_int), ("page", ctypes.c_int), ("d", ctypes.c_int),
                 ("format", ctypes.c_int)]
+
+
+class Cache4Desc(ctypes.Structure):
+    """fa_cache4_t of include/fa.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("heads", ctypes.c_int),
+                ("page", ctypes.c_int), ("d", ctypes.c_int)]
+
+
+class RopeDesc(ctypes.Structure):
+    """fa_rope_t of include/fa.h."""
+    _fields_ = [("turns", ctypes.c_void_p), ("pairs", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("factor", ctypes.c_float)]
+
+
+class RopeRows(ctypes.Structure):
+    """fa_rope_rows_t of include/fa.h."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p)] + [
+        (name, ctypes.c_longlong) for name in ("x_batch", "x_head", "x_row", "y_batch", "y_head", "y_row")] + [
+        ("heads", ctypes.c_int)]
 
 
 class FAError(RuntimeError):
@@ -110,6 +130,21 @@ def _open(path):
     lib.fa_cache_select.restype = i
     lib.fa_cache_select.argtypes = [cp, vp, ll, ll, ll, vp, vp, ll, i, vp, i, i, i, vp,
                                     ctypes.c_size_t, i, i, i, i, i, vp]
+    lib.fa_rope.restype = i
+    lib.fa_rope.argtypes = [cp, cp, cp, vp, ll, i, i, i, i, i, vp]
+    lib.fa_cache_plan.restype = i
+    lib.fa_cache_plan.argtypes = [vp, i, vp, vp, ll, i, vp, vp, vp, vp, vp, vp, vp, i, i, i, vp]
+    lib.fa_cache_trim.restype = i
+    lib.fa_cache_trim.argtypes = [vp, i, vp, vp, ll, i, vp, vp, vp, i, i, vp]
+    lib.fa_cache4_write.restype = i
+    lib.fa_cache4_write.argtypes = [cp, vp, vp, ll, ll, ll, ll, vp, i, i, vp]
+    lib.fa_cache4_read.restype = i
+    lib.fa_cache4_read.argtypes = [cp, vp, vp, vp, vp, ll, i, i, i, i, vp]
+    lib.fa_decode_cache4_workspace_size.restype = ctypes.c_size_t
+    lib.fa_decode_cache4_workspace_size.argtypes = [i, i, i, i, i]
+    lib.fa_decode_cache4.restype = i
+    lib.fa_decode_cache4.argtypes = [cp, vp, ll, ll, ll, vp, vp, vp, vp, ll, i, vp, ctypes.c_size_t, i, i, i, f, i,
+                                     i, vp]
     lib.fa_last_device_status.restype = i
     lib.fa_last_device_status.argtypes = [vp]
     lib.fa_selftest_wait_timeout.restype = i
@@ -191,6 +226,41 @@ def fa_cache_select_workspace_size(B, Hkv, Nq, max_pages):
 def fa_cache_select_raw(*args):
     """Direct call of the page-selecting entry point; returns the status."""
     return load().fa_cache_select(*args)
+
+
+def fa_rope_raw(*args):
+    """Direct call of the rotary entry point (arguments as in include/fa.h, the structs a RopeDesc and
+    RopeRows); returns the status."""
+    return load().fa_rope(*args)
+
+
+def fa_cache_plan_raw(*args):
+    """Direct call of the planning entry point; returns the status."""
+    return load().fa_cache_plan(*args)
+
+
+def fa_cache_trim_raw(*args):
+    """Direct call of the entry point that gives pages back; returns the status."""
+    return load().fa_cache_trim(*args)
+
+
+def fa_cache4_write_raw(*args):
+    """Direct call of the 4-bit cache's writing entry point (the cache a Cache4Desc); returns the status."""
+    return load().fa_cache4_write(*args)
+
+
+def fa_cache4_read_raw(*args):
+    """Direct call of the 4-bit cache's reading entry point; returns the status."""
+    return load().fa_cache4_read(*args)
+
+
+def fa_decode_cache4_workspace_size(B, Hq, Hkv, Nq, d):
+    return load().fa_decode_cache4_workspace_size(B, Hq, Hkv, Nq, d)
+
+
+def fa_decode_cache4_raw(*args):
+    """Direct call of the decoding entry point over the 4-bit cache; returns the status."""
+    return load().fa_decode_cache4(*args)
 
 
 def fa_last_device_status(stream=None):

@@ -1,6 +1,7 @@
 """Build the sm_103a CUDA library in-tree (attention_forward_02_gb300/_build/).
 
-Four translation units (forward, backward, decoding, the paged cache), one -gencode
+Seven translation units (forward, backward, decoding, the 8-bit and the 4-bit paged
+cache, page tables, rotary positions), one -gencode
 (compute_103a -> sm_103a), static cudart, no link against libcuda (the TMA
 encoder is fetched through the runtime's driver entry-point query).  The same
 units are compiled a second time with FA_BOUNDS_CHECK into the checked
@@ -25,11 +26,14 @@ LIB = os.path.join(OUT_DIR, LIB_NAME)
 # The same sources with the device-side address checks compiled in
 # (FA_BOUNDS_CHECK; see include/fa.h): a test build, never the product path.
 LIB_CHECKED = os.path.join(OUT_DIR, "libfa_gb300_checked.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("fa_fwd.cu", "fa_bwd.cu", "fa_decode.cu", "fa_cache.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("fa_fwd.cu", "fa_bwd.cu", "fa_decode.cu", "fa_cache.cu", "fa_cache4.cu",
+                                             "fa_pages.cu", "fa_rope.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_fwd_kernel.cuh", "fa1_fwd_kernel.cuh",
                                                   "fa_bwd_kernel.cuh", "fa_decode_kernel.cuh", "fa_decode_tc_kernel.cuh",
                                                   "fa_cache_kernel.cuh", "fa_cache_decode_kernel.cuh",
-                                                  "fa_common.cuh",
+                                                  "fa_cache4_kernel.cuh", "fa_cache4_decode_kernel.cuh",
+                                                  "fa_pages_kernel.cuh", "fa_rope_kernel.cuh",
+                                                  "fa_cache_host.h", "fa_common.cuh",
                                                   "fa_host.h", "sm100_ptx.cuh")] + [
     os.path.join(INCLUDE, "fa.h")]
 BINDING_NAME = "_fa_cache_py"

@@ -11,6 +11,7 @@
 
 #include "fa.h"
 #include "fa_cache_decode_kernel.cuh"
+#include "fa_cache_host.h"
 #include "fa_cache_kernel.cuh"
 #include "fa_host.h"
 
@@ -19,11 +20,8 @@ namespace {
 using fa::cache::Batch;
 using fa::cache::Cache;
 using fa::cache::Queries;
-using fa_host::kMaxDevices;
-using fa_host::overlaps;
+using namespace fa_host;
 
-constexpr int kMaxNq = 16;
-constexpr int kMaxBatch = 65535;  // a grid's y and z extent
 // Units of a segment that one block may take whole: one launch in place of two,
 // but the units one after the other.  8 KV heads, e4m3, whole / shared out, us on the
 // GPU (in a graph):
@@ -87,25 +85,6 @@ void init_cache(CacheState &st)
     if (st.err == cudaSuccess) st.err = set_smem_attrs<128>();
 }
 
-// How the R query rows of a KV head are laid out: tiles of 8 rows a warp, warps of
-// a block along the rows (the others take keys), rows a block.  Rows beyond 64 go
-// to further row groups, which read the codes again.
-// Sixteen rows a warp share one conversion of the codes, where two warps of eight
-// convert them twice; they need Q in shared memory.  16 x 16,384 keys (mean 8,700)
-// of 8 heads, sixteen a warp against eight: 16 rows, d = 128, int8 83 / 89 us, e4m3
-// 82 / 75; d = 64 47 / 55 and 44 / 47; 64 rows, d = 128 233 / 285 and 216 / 229,
-// d = 64 126 / 177 and 113 / 142.  Up to 8 rows the second eight would be padding.
-struct Shape {
-    int tiles, row_warps, rows_block;
-};
-Shape shape_of(int R)
-{
-    if (R <= 8)
-        return {1, 1, 8};
-    const int row_warps = R <= 16 ? 1 : R <= 32 ? 2 : 4;
-    return {2, row_warps, 16 * row_warps};
-}
-
 // A code buffer as [num_pages * heads, page, d] bytes: boxes of `box` rows of
 // `width` columns, each row swizzled by its width.
 fa_status_t encode_codes(fa_host::EncodeTiledFn encode, CUtensorMap *map, void *codes, const fa_cache_t *c, int width,
@@ -126,9 +105,6 @@ fa_status_t encode_codes(fa_host::EncodeTiledFn encode, CUtensorMap *map, void *
                : FA_ERR_CUDA;
 }
 
-// Bytes of the plan at the workspace's start (a 64-bit number, and one a sequence).
-size_t plan_bytes(int B) { return (static_cast<size_t>(B) + 2) / 2 * 16; }
-
 // The current device's status word and SM count.
 fa_status_t device(CacheState **out, int *num_sms, fa_host::EncodeTiledFn *encoder = nullptr)
 {
@@ -147,21 +123,6 @@ fa_status_t device(CacheState **out, int *num_sms, fa_host::EncodeTiledFn *encod
         return FA_ERR_CUDA;
     *out = &st;
     return FA_OK;
-}
-
-uintptr_t u(const void *p) { return reinterpret_cast<uintptr_t>(p); }
-
-struct Range {
-    uintptr_t at;
-    size_t bytes;
-};
-
-bool any_overlap(const Range &a, const Range *others, int count)
-{
-    for (int i = 0; i < count; ++i)
-        if (a.at && others[i].at && a.bytes && others[i].bytes && overlaps(a.at, a.bytes, others[i].at, others[i].bytes))
-            return true;
-    return false;
 }
 
 // Checks of a cache that need no device; fills its six buffers' ranges.
@@ -193,17 +154,6 @@ fa_status_t check_cache(const fa_cache_t *c, Range (&r)[kCacheRanges])
     return FA_OK;
 }
 
-fa_status_t check_batch(const int *seq_lens, const int *table, long long table_stride, int max_pages, int B, int page)
-{
-    if (!seq_lens || !table || max_pages < 1 || table_stride < max_pages)
-        return FA_ERR_INVALID_ARG;
-    if (B > kMaxBatch || static_cast<long long>(max_pages) * page > 0x7fffffffLL)
-        return FA_ERR_UNSUPPORTED;
-    if ((u(seq_lens) | u(table)) & 3u)
-        return FA_ERR_MISALIGNED;
-    return FA_OK;
-}
-
 Cache device_cache(const fa_cache_t *c)
 {
     int log2_page = 4;
@@ -213,51 +163,6 @@ Cache device_cache(const fa_cache_t *c)
             reinterpret_cast<int8_t *>(c->k_mean), c->k_mean_scale, c->num_pages, c->heads, c->page, log2_page};
 }
 
-// Strides of an input with rows of d values, in elements.
-bool strides_ok(long long a, long long b, long long c = 0) { return a >= 0 && b >= 0 && c >= 0; }
-bool strides_aligned(long long a, long long b, long long c = 0) { return ((a | b | c) & 7) == 0; }
-
-// Checks of the queries of fa_decode_cache and fa_cache_select.
-fa_status_t check_queries(const fa_cache_t *cache, const void *q, long long &sb, long long &sh, long long &sr, int B,
-                          int Hq, int Nq, int causal, fa_dtype_t dtype, Range *r)
-{
-    sb = B == 1 ? 0 : sb;  // the stride of a dimension of one means nothing
-    sh = Hq == 1 ? 0 : sh;
-    sr = Nq == 1 ? 0 : sr;
-    if (causal != 0 && causal != 1)
-        return FA_ERR_INVALID_ARG;
-    if (dtype != FA_FP16 && dtype != FA_BF16)
-        return FA_ERR_UNSUPPORTED;
-    if (Nq < 1 || Nq > kMaxNq)
-        return FA_ERR_UNSUPPORTED;
-    if (Hq % cache->heads != 0 || !q || !strides_ok(sb, sh, sr))
-        return FA_ERR_INVALID_ARG;
-    if (u(q) & 15u || !strides_aligned(sb, sh, sr))
-        return FA_ERR_MISALIGNED;
-    *r = {u(q), static_cast<size_t>((B - 1) * sb + (Hq - 1) * sh + (Nq - 1) * sr + cache->d) * 2};
-    return FA_OK;
-}
-
-// Launch of a kernel that may begin before the one ahead of it has ended (it
-// waits for that one itself).
-template <typename... P, typename... A>
-bool launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A &...args)
-{
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess;
-}
-
-fa_status_t launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
-
 // f(T, C) with the 16-bit type and the code type.
 template <typename F>
 fa_status_t by_types(fa_dtype_t dtype, int format, F f)
@@ -265,16 +170,6 @@ fa_status_t by_types(fa_dtype_t dtype, int format, F f)
     if (dtype == FA_FP16)
         return format == FA_E4M3 ? f(__half(), fa::cache::E4M3()) : f(__half(), fa::cache::I8());
     return format == FA_E4M3 ? f(__nv_bfloat16(), fa::cache::E4M3()) : f(__nv_bfloat16(), fa::cache::I8());
-}
-
-template <int D>
-struct Dim {
-    static constexpr int value = D;
-};
-template <typename F>
-fa_status_t by_dim(int d, F f)
-{
-    return d == 32 ? f(Dim<32>()) : d == 64 ? f(Dim<64>()) : d == 96 ? f(Dim<96>()) : f(Dim<128>());
 }
 
 }  // namespace
@@ -447,7 +342,7 @@ fa_status_t fa_decode_cache(const fa_cache_t *cache, const void *q, long long q_
     if ((s = check_batch(seq_lens, page_table, table_stride, max_pages, B, cache->page)) != FA_OK)
         return s;
     Range in[4];
-    if ((s = check_queries(cache, q, q_batch_stride, q_head_stride, q_row_stride, B, Hq, Nq, causal, dtype, in)) != FA_OK)
+    if ((s = check_queries(cache->heads, cache->d, q, q_batch_stride, q_head_stride, q_row_stride, B, Hq, Nq, causal, dtype, in)) != FA_OK)
         return s;
     const size_t need = fa_decode_cache_workspace_size(B, Hq, cache->heads, Nq, cache->d);
     if (!o || !workspace || workspace_bytes < need)
@@ -569,7 +464,7 @@ fa_status_t fa_cache_select(const fa_cache_t *cache, const void *q, long long q_
     if ((s = check_batch(seq_lens, page_table, table_stride, max_pages, B, cache->page)) != FA_OK)
         return s;
     Range in[3];
-    if ((s = check_queries(cache, q, q_batch_stride, q_head_stride, q_row_stride, B, Hq, Nq, causal, dtype, in)) != FA_OK)
+    if ((s = check_queries(cache->heads, cache->d, q, q_batch_stride, q_head_stride, q_row_stride, B, Hq, Nq, causal, dtype, in)) != FA_OK)
         return s;
     const size_t need = fa_cache_select_workspace_size(B, cache->heads, Nq, max_pages);
     if (!pages || !workspace || workspace_bytes < need)

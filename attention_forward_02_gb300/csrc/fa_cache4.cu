@@ -1,0 +1,250 @@
+// fa_cache4.cu -- host side of the 4-bit paged KV cache declared in include/fa.h:
+// argument checks and the launches of writing, reading back and decoding attention.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <functional>
+#include <mutex>
+
+#include "fa.h"
+#include "fa_cache4_decode_kernel.cuh"
+#include "fa_cache4_kernel.cuh"
+#include "fa_cache_host.h"
+#include "fa_host.h"
+
+namespace {
+
+using namespace fa_host;
+using fa::cache4::Batch;
+using fa::cache4::Cache4;
+
+struct Cache4State {
+    std::once_flag once;
+    cudaError_t err = cudaErrorUnknown;
+    unsigned int *status = nullptr;
+};
+Cache4State g_cache4[kMaxDevices];
+
+void init_cache4(Cache4State &st)
+{
+    void *p = nullptr;
+    st.err = cudaGetSymbolAddress(&p, fa::g_fa_status);
+    st.status = static_cast<unsigned int *>(p);
+}
+
+// The current device's state and SM count.
+fa_status_t device(Cache4State **out, int *num_sms)
+{
+    EncodeTiledFn encode = nullptr;
+    const fa_status_t s = encoder(&encode, num_sms);
+    if (s != FA_OK)
+        return s;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+        return FA_ERR_CUDA;
+    Cache4State &st = g_cache4[dev];
+    std::call_once(st.once, init_cache4, std::ref(st));
+    if (st.err != cudaSuccess)
+        return FA_ERR_CUDA;
+    *out = &st;
+    return FA_OK;
+}
+
+// Checks of a cache that need no device; its memory.
+fa_status_t check_cache(const fa_cache4_t *c, Range *own)
+{
+    if (!c || c->num_pages < 1 || c->heads < 1)
+        return FA_ERR_INVALID_ARG;
+    if ((c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) ||
+        (c->d != 32 && c->d != 64 && c->d != 96 && c->d != 128) || c->heads > kMaxBatch / 2 ||
+        static_cast<long long>(c->num_pages) * c->heads > 0x7fffffffLL ||
+        static_cast<long long>(c->num_pages) * c->page > 0x7fffffffLL)
+        return FA_ERR_UNSUPPORTED;
+    if (!c->data)
+        return FA_ERR_INVALID_ARG;
+    if (u(c->data) & 15u)
+        return FA_ERR_MISALIGNED;
+    *own = {u(c->data), static_cast<size_t>(c->num_pages) * c->heads * (2 * fa::cache4::half_block(c->page, c->d))};
+    return FA_OK;
+}
+
+Cache4 device_cache(const fa_cache4_t *c)
+{
+    int log2_page = 4;
+    while ((1 << log2_page) < c->page)
+        ++log2_page;
+    return {static_cast<uint8_t *>(c->data), c->num_pages, c->heads, c->page, log2_page};
+}
+
+template <typename F>
+fa_status_t by_type(fa_dtype_t dtype, F f)
+{
+    return dtype == FA_FP16 ? f(__half()) : f(__nv_bfloat16());
+}
+
+}  // namespace
+
+namespace fa_host {
+
+fa_status_t take_cache4_status(unsigned int *word)
+{
+    *word = 0;
+    const unsigned int zero = 0;
+    if (cudaMemcpyFromSymbol(word, fa::g_fa_status, sizeof(*word)) != cudaSuccess)
+        return FA_ERR_CUDA;
+    if (cudaMemcpyToSymbol(fa::g_fa_status, &zero, sizeof(zero)) != cudaSuccess)
+        return FA_ERR_CUDA;
+    return FA_OK;
+}
+
+}  // namespace fa_host
+
+extern "C" {
+
+fa_status_t fa_cache4_write(const fa_cache4_t *cache, const void *k, const void *v, long long k_token_stride,
+                            long long k_head_stride, long long v_token_stride, long long v_head_stride,
+                            const int *slots, int T, fa_dtype_t dtype, void *stream)
+{
+    Range own;
+    fa_status_t s = check_cache(cache, &own);
+    if (s != FA_OK)
+        return s;
+    if (T < 0)
+        return FA_ERR_INVALID_ARG;
+    if (dtype != FA_FP16 && dtype != FA_BF16)
+        return FA_ERR_UNSUPPORTED;
+    if (T == 0)
+        return FA_OK;  // empty problem
+    if (T == 1)        // the stride of a dimension of one means nothing
+        k_token_stride = v_token_stride = 0;
+    if (cache->heads == 1)
+        k_head_stride = v_head_stride = 0;
+    if (!k || !v || !slots || !strides_ok(k_token_stride, k_head_stride) || !strides_ok(v_token_stride, v_head_stride))
+        return FA_ERR_INVALID_ARG;
+    if ((u(k) | u(v)) & 15u || u(slots) & 3u || !strides_aligned(k_token_stride, k_head_stride) ||
+        !strides_aligned(v_token_stride, v_head_stride))
+        return FA_ERR_MISALIGNED;
+    const Range in[3] = {
+        {u(k), static_cast<size_t>((T - 1) * k_token_stride + (cache->heads - 1) * k_head_stride + cache->d) * 2},
+        {u(v), static_cast<size_t>((T - 1) * v_token_stride + (cache->heads - 1) * v_head_stride + cache->d) * 2},
+        {u(slots), static_cast<size_t>(T) * 4}};
+    if (any_overlap(own, in, 3))
+        return FA_ERR_INVALID_ARG;
+    Cache4State *st = nullptr;
+    if ((s = device(&st, nullptr)) != FA_OK)
+        return s;
+    const fa::cache4::Rows4 rows = {
+        {k, v}, {k_token_stride, v_token_stride}, {k_head_stride, v_head_stride}, slots, T};
+    const int tokens = fa::cache4::kWriteThreads / (cache->d / fa::cache4::kGroup);
+    const dim3 grid((T + tokens - 1) / tokens, cache->heads);
+    return by_type(dtype, [&](auto t) {
+        fa::cache4::fa_cache4_write_kernel<decltype(t)>
+            <<<grid, fa::cache4::kWriteThreads, 0, static_cast<cudaStream_t>(stream)>>>(device_cache(cache), rows, cache->d,
+                                                                                       st->status);
+        return launched();
+    });
+}
+
+fa_status_t fa_cache4_read(const fa_cache4_t *cache, void *k, void *v, const int *seq_lens, const int *page_table,
+                           long long table_stride, int max_pages, int B, int N, fa_dtype_t dtype, void *stream)
+{
+    Range own;
+    fa_status_t s = check_cache(cache, &own);
+    if (s != FA_OK)
+        return s;
+    if (B < 0 || N < 0)
+        return FA_ERR_INVALID_ARG;
+    if (dtype != FA_FP16 && dtype != FA_BF16)
+        return FA_ERR_UNSUPPORTED;
+    if (B == 0 || N == 0)
+        return FA_OK;  // empty problem
+    if ((s = check_batch(seq_lens, page_table, table_stride, max_pages, B, cache->page)) != FA_OK)
+        return s;
+    if (!k || !v)
+        return FA_ERR_INVALID_ARG;
+    if ((u(k) | u(v)) & 15u)
+        return FA_ERR_MISALIGNED;
+    constexpr int kPerBlock = fa::cache4::kReadThreads * fa::cache4::kReadSteps;
+    const long long chunks = (static_cast<long long>(N) * (cache->d / fa::cache4::kGroup) + kPerBlock - 1) / kPerBlock;
+    const long long blocks = chunks * B * cache->heads;
+    if (blocks > 0x7fffffffLL)
+        return FA_ERR_UNSUPPORTED;
+    const size_t bytes = static_cast<size_t>(B) * cache->heads * N * cache->d * 2;
+    const Range out[2] = {{u(k), bytes}, {u(v), bytes}};
+    const Range in[3] = {own,
+                         {u(seq_lens), static_cast<size_t>(B) * 4},
+                         {u(page_table), (static_cast<size_t>(B - 1) * table_stride + max_pages) * 4}};
+    if (any_overlap(out[0], in, 3) || any_overlap(out[1], in, 3) || any_overlap(out[0], out + 1, 1))
+        return FA_ERR_INVALID_ARG;
+    Cache4State *st = nullptr;
+    if ((s = device(&st, nullptr)) != FA_OK)
+        return s;
+    const Batch batch = {seq_lens, page_table, table_stride, max_pages, cache->num_pages, st->status};
+    return by_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        fa::cache4::fa_cache4_read_kernel<T>
+            <<<dim3(static_cast<unsigned>(blocks), 2), fa::cache4::kReadThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+                device_cache(cache), batch, static_cast<T *>(k), static_cast<T *>(v), N, cache->d, static_cast<int>(chunks));
+        return launched();
+    });
+}
+
+size_t fa_decode_cache4_workspace_size(int B, int Hq, int Hkv, int Nq, int d)
+{
+    return fa_decode_cache_workspace_size(B, Hq, Hkv, Nq, d);
+}
+
+fa_status_t fa_decode_cache4(const fa_cache4_t *cache, const void *q, long long q_batch_stride, long long q_head_stride,
+                             long long q_row_stride, void *o, float *lse, const int *seq_lens, const int *page_table,
+                             long long table_stride, int max_pages, void *workspace, size_t workspace_bytes, int B, int Hq,
+                             int Nq, float scale, int causal, fa_dtype_t dtype, void *stream)
+{
+    Range own;
+    fa_status_t s = check_cache(cache, &own);
+    if (s != FA_OK)
+        return s;
+    if (B < 0 || Hq < 0 || !std::isfinite(scale))
+        return FA_ERR_INVALID_ARG;
+    if (scale < 0.f)
+        return FA_ERR_UNSUPPORTED;
+    if (B == 0 || Hq == 0)
+        return FA_OK;  // empty problem
+    if ((s = check_batch(seq_lens, page_table, table_stride, max_pages, B, cache->page)) != FA_OK)
+        return s;
+    Range in[4] = {own};
+    if ((s = check_queries(cache->heads, cache->d, q, q_batch_stride, q_head_stride, q_row_stride, B, Hq, Nq, causal, dtype,
+                           in + 1)) != FA_OK)
+        return s;
+    const size_t need = fa_decode_cache4_workspace_size(B, Hq, cache->heads, Nq, cache->d);
+    if (!o || !workspace || workspace_bytes < need)
+        return FA_ERR_INVALID_ARG;
+    if ((u(o) | u(workspace)) & 15u || u(lse) & 3u)
+        return FA_ERR_MISALIGNED;
+    const long long rows = static_cast<long long>(B) * Hq * Nq;
+    if (rows > 0x7fffffffLL)
+        return FA_ERR_UNSUPPORTED;
+    in[2] = {u(seq_lens), static_cast<size_t>(B) * 4};
+    in[3] = {u(page_table), (static_cast<size_t>(B - 1) * table_stride + max_pages) * 4};
+    const Range out[3] = {{u(o), static_cast<size_t>(rows) * cache->d * 2},
+                          {u(lse), static_cast<size_t>(rows) * 4},
+                          {u(workspace), need}};
+    for (int i = 0; i < 3; ++i)
+        if (any_overlap(out[i], in, 4) || any_overlap(out[i], out, i))
+            return FA_ERR_INVALID_ARG;
+    Cache4State *st = nullptr;
+    if ((s = device(&st, nullptr)) != FA_OK)
+        return s;
+    const Batch batch = {seq_lens, page_table, table_stride, max_pages, cache->num_pages, st->status};
+    const fa::cache::Queries qs = {q, q_batch_stride, q_head_stride, q_row_stride, Hq / cache->heads, Nq, causal};
+    return by_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        fa::cache4::fa_cache4_decode_simple_kernel<T>
+            <<<static_cast<unsigned>(rows), fa::cache4::kSimpleThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+                device_cache(cache), batch, qs, cache->d, scale, static_cast<T *>(o), lse);
+        return launched();
+    });
+}
+
+}  // extern "C"

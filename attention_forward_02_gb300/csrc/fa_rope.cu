@@ -1,0 +1,182 @@
+// fa_rope.cu -- host side of fa_rope declared in include/fa.h: argument checks
+// and the launch.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "fa.h"
+#include "fa_host.h"
+#include "fa_rope_kernel.cuh"
+
+namespace {
+
+using fa_host::overlaps;
+
+uintptr_t u(const void *p) { return reinterpret_cast<uintptr_t>(p); }
+
+// A tensor of rows: its address, and (stride, extent) of batch, rows and heads.
+struct View {
+    uintptr_t at;
+    long long batch, row, head;
+    int B, N, H, d;
+
+    size_t bytes() const
+    {
+        return static_cast<size_t>((B - 1) * batch + (N - 1) * row + (H - 1) * head + d) * 2;
+    }
+    size_t heads_bytes() const { return static_cast<size_t>((H - 1) * head + d) * 2; }
+    // No element twice: each stride of a dimension spans the smaller ones.
+    bool distinct() const
+    {
+        long long stride[3] = {batch, row, head}, span = d;
+        int extent[3] = {B, N, H};
+        for (int i = 0; i < 3; ++i)
+            for (int j = i + 1; j < 3; ++j)
+                if (stride[j] < stride[i]) {
+                    const long long s = stride[i];
+                    stride[i] = stride[j];
+                    stride[j] = s;
+                    const int e = extent[i];
+                    extent[i] = extent[j];
+                    extent[j] = e;
+                }
+        for (int i = 0; i < 3; ++i) {
+            if (extent[i] == 1)
+                continue;
+            if (stride[i] < span)
+                return false;
+            span += (extent[i] - 1) * stride[i];
+        }
+        return true;
+    }
+};
+
+// No element in common: different memory, or heads side by side in the rows of one buffer.
+bool apart(const View &a, const View &b)
+{
+    if (!overlaps(a.at, a.bytes(), b.at, b.bytes()))
+        return true;
+    if ((a.B > 1 && a.batch != b.batch) || (a.N > 1 && a.row != b.row))
+        return false;
+    const View &lo = a.at <= b.at ? a : b, &hi = a.at <= b.at ? b : a;
+    const uintptr_t gap = hi.at - lo.at;
+    const size_t both = static_cast<size_t>(gap) + hi.heads_bytes();
+    const bool rows = a.N == 1 || both <= static_cast<size_t>(a.row) * 2;
+    const bool batches = a.B == 1 || both <= static_cast<size_t>(a.batch) * 2;
+    // rows of both lie within a row's distance: those of one batch follow one another without meeting
+    const bool nested = a.B == 1 || a.N == 1 || static_cast<long long>(a.N) * a.row <= a.batch ||
+                        static_cast<long long>(a.B) * a.batch <= a.row;
+    return gap >= lo.heads_bytes() && rows && batches && nested;
+}
+
+// A stride: not negative, and small enough for the sums here.
+bool fine(long long s) { return s >= 0 && s < 1ll << 40; }
+
+// Checks rows and fills their views; strides of dimensions of one become 0.
+fa_status_t check_rows(fa_rope_rows_t &r, int B, int N, int d, View *x, View *y)
+{
+    long long *all[6] = {&r.x_batch, &r.y_batch, &r.x_row, &r.y_row, &r.x_head, &r.y_head};
+    const int extent[3] = {B, N, r.heads};
+    for (int i = 0; i < 6; ++i)
+        if (extent[i / 2] == 1)
+            *all[i] = 0;
+    for (const long long *s : all)
+        if (!fine(*s))
+            return FA_ERR_INVALID_ARG;
+    if (!r.x || !r.y)
+        return FA_ERR_INVALID_ARG;
+    long long bits = 0;
+    for (const long long *s : all)
+        bits |= *s;
+    if ((u(r.x) | u(r.y)) & 15u || bits & 7)
+        return FA_ERR_MISALIGNED;
+    *x = {u(r.x), r.x_batch, r.x_row, r.x_head, B, N, r.heads, d};
+    *y = {u(r.y), r.y_batch, r.y_row, r.y_head, B, N, r.heads, d};
+    const bool in_place = r.x == r.y && r.x_batch == r.y_batch && r.x_row == r.y_row && r.x_head == r.y_head;
+    if (!y->distinct() || !(in_place || apart(*x, *y)))
+        return FA_ERR_INVALID_ARG;
+    return FA_OK;
+}
+
+template <typename T>
+void launch(bool interleaved, const fa::rope::Rows &q, const fa::rope::Rows &k, const fa::rope::Turn &turn,
+            const int *positions, long long stride, int N, int units, int slots, unsigned threads, cudaStream_t stream)
+{
+    const unsigned blocks = (threads + fa::rope::kThreads - 1) / fa::rope::kThreads;
+    if (interleaved)
+        fa::rope::fa_rope_kernel<T, true>
+            <<<blocks, fa::rope::kThreads, 0, stream>>>(q, k, turn, positions, stride, N, units, slots, threads);
+    else
+        fa::rope::fa_rope_kernel<T, false>
+            <<<blocks, fa::rope::kThreads, 0, stream>>>(q, k, turn, positions, stride, N, units, slots, threads);
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status_t fa_rope(const fa_rope_t *rope, const fa_rope_rows_t *q, const fa_rope_rows_t *k, const int *positions,
+                    long long position_stride, int B, int N, int d, int backward, fa_dtype_t dtype, void *stream)
+{
+    if (!rope || !q || B < 0 || N < 0 || q->heads < 0 || (k && k->heads < 0) || (backward != 0 && backward != 1) ||
+        !std::isfinite(rope->factor) || (rope->interleaved != 0 && rope->interleaved != 1) || rope->pairs < 1)
+        return FA_ERR_INVALID_ARG;
+    if ((d != 32 && d != 64 && d != 96 && d != 128) || (dtype != FA_FP16 && dtype != FA_BF16) || rope->pairs % 4 != 0 ||
+        rope->pairs > d / 2)
+        return FA_ERR_UNSUPPORTED;
+    const bool some_q = q->heads > 0, some_k = k && k->heads > 0;
+    if (B == 0 || N == 0 || (!some_q && !some_k))
+        return FA_OK;  // empty problem
+    if (!rope->turns || (positions && !fine(position_stride)))
+        return FA_ERR_INVALID_ARG;
+    if (u(rope->turns) & 7u || u(positions) & 3u)
+        return FA_ERR_MISALIGNED;
+    if (B == 1)
+        position_stride = 0;
+    fa_rope_rows_t rows[2] = {*q, k ? *k : fa_rope_rows_t()};
+    View x[2], y[2];
+    const uintptr_t at[2] = {u(rope->turns), u(positions)};
+    const size_t bytes[2] = {static_cast<size_t>(rope->pairs) * 8,
+                             positions ? static_cast<size_t>((B - 1) * position_stride + N) * 4 : 0};
+    for (int i = 0; i < 2; ++i) {
+        if (!(i ? some_k : some_q))
+            continue;
+        const fa_status_t s = check_rows(rows[i], B, N, d, &x[i], &y[i]);
+        if (s != FA_OK)
+            return s;
+        for (int j = 0; j < 2; ++j)
+            if (bytes[j] && overlaps(y[i].at, y[i].bytes(), at[j], bytes[j]))
+                return FA_ERR_INVALID_ARG;
+    }
+    if (some_q && some_k && !(apart(y[0], y[1]) && apart(y[0], x[1]) && apart(y[1], x[0])))
+        return FA_ERR_INVALID_ARG;
+    int sms = 0;
+    fa_host::EncodeTiledFn encode = nullptr;
+    const fa_status_t s = fa_host::encoder(&encode, &sms);
+    if (s != FA_OK)
+        return s;
+    // Heads a thread: all of them where rows are many, fewer where the GPU would not be full.
+    const long long rows_units = static_cast<long long>(B) * N * (d / 8);
+    const int heads = (some_q ? rows[0].heads : 0) + (some_k ? rows[1].heads : 0);
+    int slots = 1;
+    while (slots < heads && rows_units * slots < static_cast<long long>(sms) * 1024)
+        slots *= 2;
+    if (rows_units * slots > 0x7fffffffLL)
+        return FA_ERR_UNSUPPORTED;
+    fa::rope::Rows r[2];
+    for (int i = 0; i < 2; ++i)
+        r[i] = {rows[i].x,      rows[i].y,     rows[i].x_batch, rows[i].x_head, rows[i].x_row,
+                rows[i].y_batch, rows[i].y_head, rows[i].y_row,   (i ? some_k : some_q) ? rows[i].heads : 0};
+    const fa::rope::Turn turn = {rope->turns, rope->pairs, rope->factor, backward == 1};
+    const unsigned threads = static_cast<unsigned>(rows_units * slots);
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (dtype == FA_FP16)
+        launch<__half>(rope->interleaved, r[0], r[1], turn, positions, position_stride, N, d / 8, slots, threads, cs);
+    else
+        launch<__nv_bfloat16>(rope->interleaved, r[0], r[1], turn, positions, position_stride, N, d / 8, slots, threads, cs);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

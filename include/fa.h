@@ -35,7 +35,7 @@
 extern "C" {
 #endif
 
-#define FA_ABI_VERSION 5
+#define FA_ABI_VERSION 6
 
 #if defined(__GNUC__)
 #define FA_API __attribute__((visibility("default")))
@@ -408,6 +408,188 @@ FA_API fa_status_t fa_cache_select(const fa_cache_t *cache, const void *q, long 
                                    int keep_first, int keep_last, void *workspace,
                                    size_t workspace_bytes, int B, int Hq, int Nq, int causal,
                                    fa_dtype_t dtype, void *stream);
+
+/*
+ * Rotary positions.
+ *
+ * The first 2 * pairs channels of a head turn in pairs: with w_i the angle a position
+ * of pair i, a row at position p has its channels (a, b) of the pair replaced by
+ *     a' = factor (a cos(p w_i) - b sin(p w_i)),  b' = factor (b cos(p w_i) + a sin(p w_i));
+ * the other channels stay.  Angles are held as fractions of a turn in 64-bit fixed point:
+ * p times turns[i], taken modulo 2^64, is the turn's fraction at p, so that far positions
+ * lose nothing (off by at most p 2^-65 of a turn).  Frequencies scaled for long contexts are
+ * other `turns`; the pages have no counterpart.
+ */
+typedef struct {
+    const unsigned long long *turns; /* [pairs] on the device, 8-byte aligned: w_i / (2 pi) * 2^64
+                                        modulo 2^64 (two's complement for negative w_i) */
+    int pairs;                       /* a multiple of 4, 4 .. d / 2 */
+    int interleaved;                 /* 0: channel c pairs with c + pairs; 1: 2 c with 2 c + 1 */
+    float factor;                    /* of the turned channels; finite */
+} fa_rope_t;
+
+/* Rows in and rows out: element (b, h, i, c) of x at b * x_batch + h * x_head + i * x_row + c,
+   of y likewise (strides in elements, multiples of 8, not negative; that of a dimension of one
+   is ignored); both 16-byte aligned. */
+typedef struct {
+    const void *x;
+    void *y;
+    long long x_batch, x_head, x_row;
+    long long y_batch, y_head, y_row;
+    int heads;
+} fa_rope_rows_t;
+
+/*
+ * fa_rope -- turn query and key rows to their positions (asynchronous), or, with
+ * backward = 1, the gradients of turned rows to those of the rows before (the transpose:
+ * sin with the other sign).
+ *
+ *  rope     : host struct; its turns on the device.
+ *  q, k     : host structs; k may be NULL.  y may be x with the same strides (in place);
+ *             otherwise outputs overlap nothing, themselves among it.  Rows of one buffer
+ *             side by side, as a fused projection gives them, do not count as overlapping.
+ *  positions: int32 on the device, that of row i of batch b at b * position_stride + i
+ *             (position_stride 0: one row of them for the whole batch), or NULL: row i is
+ *             at position i.  A row at a negative position stays as it is (padding).
+ *  B, N     : batch and rows a head (packed tokens: B = 1, N tokens); 0, like no heads, is an
+ *             empty problem.
+ *  d        : head dimension, 32, 64, 96 or 128.
+ *  backward : 0 or 1.
+ * Computed in fp32 and rounded once to `dtype`.
+ */
+FA_API fa_status_t fa_rope(const fa_rope_t *rope, const fa_rope_rows_t *q, const fa_rope_rows_t *k,
+                           const int *positions, long long position_stride, int B, int N, int d,
+                           int backward, fa_dtype_t dtype, void *stream);
+
+/*
+ * Page tables and slot maps from lengths.
+ *
+ * The free pages of a paged cache (of either kind) lie in a ring of num_pages page numbers:
+ * with counts[0] pages taken and counts[1] given back so far (a full pool starts with 0 and
+ * num_pages), the free ones are ring[x mod num_pages] for counts[0] <= x < counts[1].  Pages
+ * are taken from the front and given back behind the end, so the one that was given back
+ * first is used first.  Everything is read and written on the device: a captured graph
+ * follows it.
+ */
+
+/*
+ * fa_cache_plan -- find room for a step's new tokens (asynchronous).
+ *
+ * Sequence b has seq_lens[b] tokens and gets new_lens[b] more, whose rows follow one another
+ * in the step's packed buffers: row cu_seqlens[b] + i is its token at position seq_lens[b] + i.
+ * It needs ceil((seq_lens[b] + new_lens[b]) / page) - ceil(seq_lens[b] / page) pages, taken in
+ * the sequences' order.  It is refused where the free pages do not reach (then so are all
+ * behind it that need any), and where it does not fit the page table or the T rows; a
+ * refused one takes no page and its rows have no slot.
+ *
+ *  ring, num_pages, counts : the pool; counts is [2] int64.  num_pages * page < 2^31.
+ *  page_table : [B, max_pages] int32, rows table_stride apart.  The places of the pages
+ *               taken are written, no others.
+ *  seq_lens, new_lens : [B] int32.  Negative ones count as no new tokens, and refuse the sequence.
+ *  cu_seqlens : [B + 1] int32, written: where each sequence's rows begin, refused or not.
+ *  ends       : [B] int32, written: seq_lens[b] + new_lens[b], or seq_lens[b] if refused.
+ *  positions, slots : [T] int32, written: of each row its position and its slot in the cache,
+ *               page number * page + place in the page (fa_cache4_write); -1 for rows of
+ *               refused sequences and behind the last one.
+ *  counts_out : [2] int64, written: the pool's counts afterwards.  It may be counts; where it
+ *               is another buffer the pool stays as it was, and another plan may take its place.
+ *  page       : tokens a page, 16, 32, 64 or 128.
+ *  B          : at most 16,384 sequences; 0 is an empty problem (nothing is written).
+ *  T          : rows of positions and slots; may be 0.
+ * Reported as FA_ERR_BOUNDS by fa_last_device_status: negative lengths, sequences that do not fit
+ * the page table or the T rows, counts that are none, and a place of the table below a
+ * sequence's end that holds no page (its rows get no slot).  Too few free pages are no error:
+ * `ends` says who was served.
+ * Buffers that are written overlap nothing but, as above, counts.
+ */
+FA_API fa_status_t fa_cache_plan(const int *ring, int num_pages, const long long *counts,
+                                 int *page_table, long long table_stride, int max_pages,
+                                 const int *seq_lens, const int *new_lens, int *cu_seqlens, int *ends,
+                                 int *positions, int *slots, long long *counts_out, int page, int B,
+                                 int T, void *stream);
+
+/*
+ * fa_cache_trim -- cut sequences and give the pages behind their new ends back
+ * (asynchronous): rejected speculative tokens, or, cut to 0, a sequence that is done.
+ *
+ * Places ceil(keep_lens[b] / page) .. ceil(seq_lens[b] / page) - 1 of row b of the table go to
+ * the ring's end, in the sequences' order; what the table holds there means nothing afterwards.
+ * A sequence with keep_lens[b] negative or above seq_lens[b], or seq_lens[b] behind the page
+ * table, gives nothing back and is reported as FA_ERR_BOUNDS; so is one whose pages the ring has
+ * no room for (pages given back twice), with all that follow it, and a place that holds no page
+ * number (it goes to the ring as it is; whatever takes it later skips it).
+ *
+ *  ring       : written behind its end.  Other arguments as for fa_cache_plan.
+ */
+FA_API fa_status_t fa_cache_trim(int *ring, int num_pages, const long long *counts,
+                                 const int *page_table, long long table_stride, int max_pages,
+                                 const int *seq_lens, const int *keep_lens, long long *counts_out,
+                                 int page, int B, void *stream);
+
+/*
+ * The 4-bit paged KV cache.
+ *
+ * As the 8-bit one, K and V of many sequences in pages of `page` tokens, but 4.5 bits a
+ * value: 16 neighbouring channels of a token and head share a scale, so that every token
+ * stands by itself and a write changes nothing written before.
+ *  - Scale: an unsigned number of 5 exponent and 3 fraction bits (bias 15, subnormal ones
+ *    too), one byte: the eight bits below the sign of an fp16, whose other bits are zero.
+ *    It is amax / 6 rounded to the nearest (ties to even), amax the largest finite magnitude
+ *    of the 16 values; at most 10,240 (0xE2), so that every value fits fp16.
+ *  - Code: x / scale rounded to the nearest (ties to even) of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (numbers
+ *    0 .. 7: a float of 2 exponent bits and 1 fraction bit), beyond 6 to 6, with the sign in bit
+ *    3; NaN becomes 0 and so does all where the scale is 0.
+ * The value code * scale is exact in fp16 and in bf16.  Values beyond 61,440 saturate.
+ *
+ * A page and head is one block of 9 / 8 page * d bytes: codes of K [page, d / 2] (channel 2 c in
+ * the low half of byte c), scales of K [page, d / 16], codes of V, scales of V.
+ */
+typedef struct {
+    void *data;    /* [num_pages, heads] blocks, 16-byte aligned */
+    int num_pages; /* >= 1; num_pages * page < 2^31 */
+    int heads;     /* KV heads */
+    int page;      /* tokens a page: 16, 32, 64 or 128 */
+    int d;         /* head dimension: 32, 64, 96 or 128 */
+} fa_cache4_t;
+
+/*
+ * fa_cache4_write -- write rows to slots of the cache (asynchronous).
+ *
+ *  k, v    : T rows; strides and alignment as for fa_cache_write.  Read only.
+ *  slots   : [T] int32 on the device: page number * page + place in the page of each row
+ *            (fa_cache_plan).  Rows with a negative slot are left out; a slot behind the
+ *            cache is left out and reported as FA_ERR_BOUNDS.  Of rows with the same slot any
+ *            one, or parts of several, are written.
+ *  T       : rows; 0 is an empty problem.
+ *  dtype   : type of k and v.
+ */
+FA_API fa_status_t fa_cache4_write(const fa_cache4_t *cache, const void *k, const void *v,
+                                   long long k_token_stride, long long k_head_stride,
+                                   long long v_token_stride, long long v_head_stride,
+                                   const int *slots, int T, fa_dtype_t dtype, void *stream);
+
+/*
+ * fa_cache4_read -- the first N positions of every sequence in 16 bits (asynchronous), zeros
+ * behind their ends: as fa_cache_read, exact in either type.
+ */
+FA_API fa_status_t fa_cache4_read(const fa_cache4_t *cache, void *k, void *v, const int *seq_lens,
+                                  const int *page_table, long long table_stride, int max_pages,
+                                  int B, int N, fa_dtype_t dtype, void *stream);
+
+/* Bytes of device workspace fa_decode_cache4 needs; 0 for invalid sizes. */
+FA_API size_t fa_decode_cache4_workspace_size(int B, int Hq, int Hkv, int Nq, int d);
+
+/*
+ * fa_decode_cache4 -- decoding attention over the 4-bit cache (asynchronous): arguments,
+ * results, masks and reports as for fa_decode_cache over all pages.  Bytes above 0xE2 are no
+ * scales; what rows that see such a key get is not said.
+ */
+FA_API fa_status_t fa_decode_cache4(const fa_cache4_t *cache, const void *q, long long q_batch_stride,
+                                    long long q_head_stride, long long q_row_stride, void *o,
+                                    float *lse, const int *seq_lens, const int *page_table,
+                                    long long table_stride, int max_pages, void *workspace,
+                                    size_t workspace_bytes, int B, int Hq, int Nq, float scale,
+                                    int causal, fa_dtype_t dtype, void *stream);
 
 /*
  * fa_last_device_status -- synchronise `stream`, read and clear the device
