@@ -27,11 +27,39 @@ struct Cache4State {
 };
 Cache4State g_cache4[kMaxDevices];
 
+// Units of a segment that one block may take whole, as for the 8-bit cache.
+constexpr long long kWholeUnits = 8;
+
+template <int D, int NT, typename T>
+constexpr auto decode_kernel()
+{
+    return fa::cache4::fa_cache4_decode_kernel<D, NT, D <= 64 ? 2 : 1, T>;
+}
+
+template <int D>
+cudaError_t set_smem_attrs()
+{
+    const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    constexpr int bytes = fa::cache4::Dec4Cfg<D>::SMEM;
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, 1, __half>(), a, bytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(decode_kernel<D, 2, __half>(), a, bytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(decode_kernel<D, 1, __nv_bfloat16>(), a, bytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(decode_kernel<D, 2, __nv_bfloat16>(), a, bytes);
+    return e;
+}
+
 void init_cache4(Cache4State &st)
 {
     void *p = nullptr;
     st.err = cudaGetSymbolAddress(&p, fa::g_fa_status);
     st.status = static_cast<unsigned int *>(p);
+    if (st.err == cudaSuccess) st.err = set_smem_attrs<32>();
+    if (st.err == cudaSuccess) st.err = set_smem_attrs<64>();
+    if (st.err == cudaSuccess) st.err = set_smem_attrs<96>();
+    if (st.err == cudaSuccess) st.err = set_smem_attrs<128>();
 }
 
 // The current device's state and SM count.
@@ -234,16 +262,63 @@ fa_status_t fa_decode_cache4(const fa_cache4_t *cache, const void *q, long long 
         if (any_overlap(out[i], in, 4) || any_overlap(out[i], out, i))
             return FA_ERR_INVALID_ARG;
     Cache4State *st = nullptr;
-    if ((s = device(&st, nullptr)) != FA_OK)
+    int sms = 0;
+    if ((s = device(&st, &sms)) != FA_OK)
         return s;
     const Batch batch = {seq_lens, page_table, table_stride, max_pages, cache->num_pages, st->status};
-    const fa::cache::Queries qs = {q, q_batch_stride, q_head_stride, q_row_stride, Hq / cache->heads, Nq, causal};
-    return by_type(dtype, [&](auto t) {
-        using T = decltype(t);
-        fa::cache4::fa_cache4_decode_simple_kernel<T>
-            <<<static_cast<unsigned>(rows), fa::cache4::kSimpleThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-                device_cache(cache), batch, qs, cache->d, scale, static_cast<T *>(o), lse);
-        return launched();
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const Cache4 c = device_cache(cache);
+    fa::cache::Work w = {};
+    w.cache = {c.data, nullptr, nullptr, nullptr, nullptr, nullptr, c.num_pages, c.heads, c.page, c.log2_page};
+    w.batch = batch;
+    w.q = {q, q_batch_stride, q_head_stride, q_row_stride, Hq / cache->heads, Nq, causal};
+    w.B = B;
+    w.R = w.q.G * Nq;
+    const Shape shape = shape_of(w.R);
+    w.row_warps = shape.row_warps;
+    const int rows_block = shape.rows_block;
+    w.groups = (w.R + rows_block - 1) / rows_block;
+    w.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    w.plan = static_cast<long long *>(workspace);
+    const size_t part_rows = static_cast<size_t>(2 * fa::cache::kMaxBlocks) * rows_block;
+    w.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan_bytes(B));
+    w.part_m = w.part_o + part_rows * cache->d;
+    w.part_l = w.part_m + part_rows;
+    return by_dim(cache->d, [&](auto dim) {
+        constexpr int D = decltype(dim)::value;
+        using F = fa::cache4::Dec4Cfg<D>;
+        const int box = cache->page < F::STEP ? cache->page : F::STEP;
+        w.log2_box = box == 128 ? 7 : box == 64 ? 6 : box == 32 ? 5 : 4;
+        const long long segments = static_cast<long long>(B) * cache->heads * w.groups;
+        const long long units = (static_cast<long long>(max_pages) * cache->page - 1) / F::STEP + 1;  // of one, at most
+        long long blocks = static_cast<long long>(sms) * F::BLOCKS;
+        if (blocks > fa::cache::kMaxBlocks)
+            blocks = fa::cache::kMaxBlocks;
+        w.whole = units <= kWholeUnits && segments <= blocks;
+        if (w.whole)
+            blocks = segments;
+        else if (segments * units < blocks)
+            blocks = segments * units;
+        return by_type(dtype, [&](auto t) {
+            using T = decltype(t);
+            if (!launch_dependent(shape.tiles == 1 ? decode_kernel<D, 1, T>() : decode_kernel<D, 2, T>(),
+                                  static_cast<unsigned>(blocks), fa::cache::kDecThreads, F::SMEM, cs, w,
+                                  static_cast<T *>(o), lse))
+                return FA_ERR_CUDA;
+            if (w.whole)
+                return launched();
+            constexpr int kWarps = fa::cache::kCombineThreads / 32;
+            const bool second =
+                blocks <= segments * fa::cache::kCombineEach
+                    ? launch_dependent(fa::cache::fa_cache_combine_kernel<D, T, 1>,
+                                       static_cast<unsigned>((rows + kWarps - 1) / kWarps), fa::cache::kCombineThreads, 0,
+                                       cs, w, static_cast<T *>(o), lse, rows_block, rows)
+                    : launch_dependent(fa::cache::fa_cache_combine_kernel<D, T, kWarps>, static_cast<unsigned>(rows),
+                                       fa::cache::kCombineThreads, 0, cs, w, static_cast<T *>(o), lse, rows_block, rows);
+            if (!second)
+                return FA_ERR_CUDA;
+            return launched();
+        });
     });
 }
 

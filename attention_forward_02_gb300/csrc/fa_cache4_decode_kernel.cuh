@@ -1,100 +1,717 @@
 // fa_cache4_decode_kernel.cuh -- decoding attention over the 4-bit paged cache on
 // sm_103a: O = softmax(scale q K^T) V over the keys of a sequence.
+//
+// Built as the one over the 8-bit cache (fa_cache_decode_kernel.cuh): units of a stage's
+// keys dealt out in equal runs to a persistent grid, one warp that copies, four that
+// compute with mma.m16n8k16 on fp16, keys as rows and query rows as columns, parts
+// merged by fa_cache_combine_kernel.  What differs:
+//  - A page and head is one block of bytes, so that a copy is one bulk copy (four where a
+//    page is larger than a stage).  It is not swizzled: of a tile's 16 rows, row r stands for
+//    the key r ^ (r >> 2 & 1), and then the reads of K are free of bank conflicts and those
+//    of V at most two-way.
+//  - Codes become fp16 by cvt (two at a time), times their scale: both exact.  For V the codes
+//    of two keys are put side by side first, even channels in one word and odd in another.
+//  - Scales belong to keys and channels, so none enters the softmax: P's reference is a plain
+//    running maximum (2^kAim under it, as there).
+//
+// What bounds it: 16 keys of d = 128 are 2,304 bytes, for which HBM takes some 100 clocks of
+// an SM, while the tile costs a warp some 300 instructions, 75 clocks of the SM's four
+// schedulers.  Both are near one another, so that instructions count.
 #pragma once
 
 #include "fa_cache4_kernel.cuh"
+#include "fa_cache_decode_kernel.cuh"
 
 namespace fa {
 namespace cache4 {
 
-using cache::Queries;
+using cache::kAim;
+using cache::kDecThreads;
+using cache::kDecWarps;
+using cache::kFirst;
+using cache::kHeadPart;
+using cache::kLast;
+using cache::kMost;
+using cache::kNoKey;
+using cache::kTailPart;
+using cache::kTile;
+using cache::Work;
 
-// A block a query row: a thread a key for the scores of 128 keys, a thread a channel for
-// the values.
-constexpr int kSimpleThreads = 128;
+// As DecCfg of the 8-bit cache, whose stages have the same keys (the merge counts in them).
+template <int D>
+struct Dec4Cfg {
+    static constexpr int LOG2_STEP = cache::DecCfg<D>::LOG2_STEP;
+    static constexpr int STEP = 1 << LOG2_STEP;
+    static constexpr int SUBS = STEP / kTile;
+    static constexpr int STAGE = STEP * D / 8 * 9;  // bytes
+    static constexpr int BLOCKS = D == 32 ? 4 : 3;  // an SM
+    static constexpr int STAGES = 5;
+    static constexpr int OROW = D + 4;
+    static constexpr int META_OFF = STAGES * STAGE;
+    static constexpr int MERGE_OFF = META_OFF + STAGES * 64;
+    static constexpr int ML_OFF = MERGE_OFF + kDecWarps * 8 * OROW * 4;
+    static constexpr int BAR_OFF = ML_OFF + kDecWarps * 8 * 8;
+    static constexpr int FLAG_OFF = BAR_OFF + 16 * STAGES + 16;
+    static constexpr int SMEM = FLAG_OFF + 16 + 16 * kDecWarps + 128;  // and room to align the ring
+    static_assert(STAGE % 128 == 0, "alignment of the ring");
+};
 
-template <typename T>
-__global__ void __launch_bounds__(kSimpleThreads)
-    fa_cache4_decode_simple_kernel(Cache4 cache, Batch batch, Queries q, int d, float scale, T *__restrict__ out,
-                                   float *__restrict__ lse)
+// What the computing warps know of a stage.
+struct __align__(16) Stage4 {
+    int key0[8];  // position of each tile's first key, or kNoKey
+    int flags, b, head, group, pad[4];
+};
+static_assert(sizeof(Stage4) == 64, "stage record");
+
+// Words of eight consecutive channels of a key's K that a thread has: D / 4 channels from
+// c * D / 4 on; their scales' bytes.
+template <int D>
+__device__ __forceinline__ void load_k(uint32_t codes, uint32_t scales, int row, int c, uint32_t (&w)[D / 32],
+                                       uint32_t (&by)[D / 32])
 {
-    __shared__ float qs[128], p[kSimpleThreads], red[kSimpleThreads / 32];
-    const int t = threadIdx.x;
-    const int rows = cache.heads * q.G * q.Nq;
-    const int b = blockIdx.x / rows, row = blockIdx.x % rows;
-    const int hq = row / q.Nq, i = row % q.Nq, h = hq / q.G;
-    const int len = batch.length(b, cache.log2_page);
-    if (row == 0 && t == 0)
-        batch.check_length(b, cache.log2_page);
-    const int ctx = cache::context(q, len, i);
-    if (t < d)
-        qs[t] = static_cast<float>(
-            static_cast<const T *>(q.q)[b * q.batch_stride + hq * q.head_stride + i * q.row_stride + t]);
-    const int half = half_block(cache.page, d);
-    float m = -INFINITY, l = 0.f, acc = 0.f;
-    for (int k0 = 0; k0 < ctx; k0 += kSimpleThreads) {
+    const uint32_t at = codes + row * (D / 2) + c * (D / 8), s = scales + row * (D / 16);
+    if constexpr (D == 128) {
+        cache::load_words<4>(w, at);
+        const uint32_t b = load_u16(s + 2 * c);
+        by[0] = by[1] = (b & 255u) * 0x800080u;
+        by[2] = by[3] = (b >> 8) * 0x800080u;
+    } else if constexpr (D == 96) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            cache::load_words<1>(w + i, at + 4 * i);
+        const uint32_t lo = load_u8(s + (3 * c >> 1)) * 0x800080u, hi = load_u8(s + (3 * c >> 1) + 1) * 0x800080u;
+        by[0] = lo;
+        by[1] = c & 1 ? hi : lo;
+        by[2] = hi;
+    } else if constexpr (D == 64) {
+        cache::load_words<2>(w, at);
+        by[0] = by[1] = load_u8(s + c) * 0x800080u;
+    } else {
+        cache::load_words<1>(w, at);
+        by[0] = load_u8(s + (c >> 1)) * 0x800080u;
+    }
+}
+
+// A thread's channels of a key's V: v_column's, eight to a word (four in the last of d = 32 and
+// 96), and the scale byte of each word.
+template <int D>
+__device__ __forceinline__ void load_v(uint32_t codes, uint32_t scales, int row, int g, uint32_t (&w)[(D + 63) / 64],
+                                       uint32_t (&s)[(D + 63) / 64])
+{
+    const uint32_t at = codes + row * (D / 2), st = scales + row * (D / 16);
+    if constexpr (D == 128) {
+        cache::load_words<2>(w, at + 8 * g);
+        s[0] = s[1] = load_u8(st + g);
+    } else if constexpr (D == 96) {
+        cache::load_words<1>(w, at + 4 * g);
+        w[1] = load_u16(at + 32 + 2 * g);
+        s[0] = load_u8(st + (g >> 1));
+        s[1] = load_u8(st + 4 + (g >> 2));
+    } else if constexpr (D == 64) {
+        cache::load_words<1>(w, at + 4 * g);
+        s[0] = load_u8(st + (g >> 1));
+    } else {
+        w[0] = load_u16(at + 2 * g);
+        s[0] = load_u8(st + (g >> 2));
+    }
+}
+
+__device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b)
+{
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&x);
+}
+
+template <int D, int NT, int J, typename T>
+__global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
+    fa_cache4_decode_kernel(const __grid_constant__ Work w, T *__restrict__ out, float *__restrict__ lse)
+{
+    using F = Dec4Cfg<D>;
+    constexpr int S = F::STAGES;
+    constexpr int KW = D / 16;           // steps of the first product
+    constexpr int VW = D / 32;           // fours of channels of a thread
+    constexpr int VX = (D + 63) / 64;    // words of them
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ long long scan[kDecWarps + 1];
+    __shared__ long long begin[2];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sbase = (raw + 127u) & ~127u;
+    uint8_t *smem = smem_raw + (sbase - raw);
+    auto full = [&](int s) -> uint32_t { return sbase + F::BAR_OFF + 8u * s; };
+    auto empty = [&](int s) -> uint32_t { return sbase + F::BAR_OFF + 8u * (S + s); };
+    const uint32_t merged = sbase + F::BAR_OFF + 16u * S;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + F::FLAG_OFF);
+    Stage4 *meta = reinterpret_cast<Stage4 *>(smem + F::META_OFF);
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    constexpr int ROWS = 8 * NT;  // query rows a warp
+    const int rows_block = ROWS * w.row_warps;
+    const int log2_page = w.cache.log2_page;
+
+    if (t == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), kDecWarps);
+        }
+        mbar_init(merged, kDecWarps);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    cache::wait_ahead();
+    cache::let_next();
+
+    // ---- this block's run of units ----
+    int all;            // units of this block
+    int b;              // its first sequence
+    long long off = 0;  // ... and the unit of that sequence it begins with
+    int head = 0, group = 0;  // with `whole`, its segment
+    if (w.whole) {
+        int x = blockIdx.x;
+        group = x % w.groups;
+        x /= w.groups;
+        head = x % w.cache.heads;
+        b = x / w.cache.heads;
+        if (t == 0 && group == 0 && head == 0)
+            w.batch.check_length(b, log2_page);
+        // a segment without keys has a unit all the same, and writes its rows in it
+        all = max(1, cache::units_of<F::LOG2_STEP>(w, w.batch.length(b, log2_page), 0));
+        __syncthreads();  // the barriers are set
+    } else {
+        const int each = (w.B + kDecThreads - 1) / kDecThreads;
+        const int b0 = min(w.B, t * each), b1 = min(w.B, b0 + each);
+        long long sum = 0;
+        for (int x = b0; x < b1; ++x)
+            sum += cache::units_of_sequence<F::LOG2_STEP>(w, x);
+        long long incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += y;
+        }
+        if (lane == 31)
+            scan[warp] = incl;
         __syncthreads();
-        const int key = k0 + t;
-        float s = -INFINITY;
-        if (key < ctx) {
-            const int pg = batch.page(b, key >> cache.log2_page);
-            if (pg < 0) {
-                batch.bad();
-            } else {
-                const uint8_t *block = cache.data + (static_cast<size_t>(pg) * cache.heads + h) * (2 * half);
-                const int r = key & (cache.page - 1);
-                s = 0.f;
-                for (int g = 0; g < d / kGroup; ++g) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(block + r * (d / 2) + 8 * g);
-                    const uint32_t by = scale_pair(block[cache.page * (d / 2) + r * (d / kGroup) + g]);
-                    uint32_t x[2][4];
-                    halves8(w.x, x[0]);
-                    halves8(w.y, x[1]);
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 y = __half22float2(__hmul2(*reinterpret_cast<const __half2 *>(&x[j >> 2][j & 3]),
-                                                                *reinterpret_cast<const __half2 *>(&by)));
-                        s = fmaf(y.x, qs[kGroup * g + 2 * j], s);
-                        s = fmaf(y.y, qs[kGroup * g + 2 * j + 1], s);
-                    }
-                }
-                s *= scale;
+        long long total = 0;
+        for (int x = 0; x < kDecWarps + 1; ++x) {
+            if (x < warp)
+                incl += scan[x];
+            total += scan[x];
+        }
+        const long long share = max(1ll, (total + gridDim.x - 1) / gridDim.x);
+        const long long first_unit = share * blockIdx.x;
+        long long at = incl - sum;
+        if (blockIdx.x == 0) {
+            if (t == 0)
+                w.plan[0] = share;
+            long long y = at;
+            for (int x = b0; x < b1; ++x) {
+                w.plan[1 + x] = y;
+                w.batch.check_length(x, log2_page);
+                y += cache::units_of_sequence<F::LOG2_STEP>(w, x);
             }
         }
-        float top = s;
-        for (int o = 16; o > 0; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if ((t & 31) == 0)
-            red[t >> 5] = top;
+        if (first_unit >= at && first_unit < incl) {
+            int x = b0;
+            for (; x + 1 < b1; ++x) {
+                const long long n = cache::units_of_sequence<F::LOG2_STEP>(w, x);
+                if (first_unit < at + n)
+                    break;
+                at += n;
+            }
+            begin[0] = x;
+            begin[1] = first_unit - at;
+        }
         __syncthreads();
-        for (int x = 0; x < kSimpleThreads / 32; ++x)
-            top = fmaxf(top, red[x]);
-        const float next = fmaxf(m, top), ref = next == -INFINITY ? 0.f : next;
-        const float alpha = expf(m - ref);
-        p[t] = expf(s - ref);
-        __syncthreads();
-        l *= alpha;
-        acc *= alpha;
-        m = next;
-        const int n = min(kSimpleThreads, ctx - k0);
-        for (int x = 0; x < n; ++x) {
-            l += p[x];
-            const int pg = batch.page(b, (k0 + x) >> cache.log2_page);
-            if (t < d && pg >= 0) {
-                const uint8_t *block = cache.data + (static_cast<size_t>(pg) * cache.heads + h) * (2 * half) + half;
-                const int r = (k0 + x) & (cache.page - 1);
-                uint32_t y[4];
-                halves8(block[r * (d / 2) + t / 2], y);
-                const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&y[0]));
-                const uint32_t by = scale_pair(block[cache.page * (d / 2) + r * (d / kGroup) + t / kGroup]);
-                acc = fmaf(p[x] * __half2float(__ushort_as_half(by & 0xFFFFu)), t & 1 ? z.y : z.x, acc);
+        if (first_unit >= total)
+            return;
+        b = static_cast<int>(begin[0]);
+        off = begin[1];
+        all = static_cast<int>(min(share, total - first_unit));
+    }
+
+    const int box = 1 << w.log2_box, box_bytes = box * (D / 8 * 9);
+    if (warp == kDecWarps) {
+        // ---------------- the warp that loads ----------------
+        int len = 0, units = 0, unit = 0;
+        auto open_sequence = [&]() {
+            len = b < w.B ? w.batch.length(b, log2_page) : 0;
+            units = cache::units_of<F::LOG2_STEP>(w, len, 0);
+        };
+        open_sequence();
+        if (w.whole) {
+            units = all;
+        } else {
+            // off < units * heads * groups here: 32 bits hold it unless a sequence's work is vast
+            const int seg = off >> 31 ? static_cast<int>(off / units) : static_cast<int>(off) / units;
+            head = seg / w.groups;
+            group = seg % w.groups;
+            unit = static_cast<int>(off - static_cast<long long>(seg) * units);
+        }
+        const int log2_boxes = F::LOG2_STEP - w.log2_box;  // boxes of a stage: 1 to 8
+        const int batch_units = 32 >> log2_boxes;
+        const size_t page_bytes = static_cast<size_t>(w.cache.page) * (D / 8 * 9);
+        const uint64_t policy = l2_policy_evict_first();
+        bool opened = true, ok = true;  // opened: the next unit is this block's first of its segment
+        const unsigned stage_lanes = (1u << (1 << log2_boxes)) - 1u;
+        int done = 0, s = 0;
+        uint32_t phase = 0;  // of the ring's round
+        while (done < all && ok) {
+            // lane l: page of the l-th of the next 32 boxes of this segment
+            const int here = min(min(batch_units, units - unit), all - done);
+            const int key = (unit << F::LOG2_STEP) + lane * box;
+            int p = -1;
+            if ((lane >> log2_boxes) < here && key < len) {
+                p = w.batch.page(b, key >> log2_page);
+                if (p < 0)
+                    w.batch.bad();
+            }
+            const uint8_t *src = w.cache.k + (static_cast<size_t>(max(p, 0)) * w.cache.heads + head) * page_bytes;
+            const unsigned alive = __ballot_sync(0xffffffffu, p >= 0);
+            // lane l < SUBS writes the record of a stage's tile l: the lane that has its box
+            const int tile_lane = (lane * kTile) >> w.log2_box, tile_key = (lane * kTile) & (box - 1);
+            for (int u = 0; u < here; ++u, ++done) {
+                if (done >= S && !(ok = wait_warp(empty(s), phase ^ 1u, abort_flag)))
+                    break;
+                const int first_lane = u << log2_boxes;
+                const bool mine = (lane >> log2_boxes) == u;
+                const bool ended = unit + 1 == units || done + 1 == all;
+                // the copies first (their bytes may arrive before they are expected: the phase
+                // waits for the arrival below), then the record
+                if (mine && p >= 0) {
+                    const uint32_t dst = sbase + s * F::STAGE + (lane - first_lane) * box_bytes;
+                    if (w.cache.page == box) {
+                        bulk_load(dst, src, box_bytes, full(s), policy);
+                    } else {  // a part of the page: rows of its four arrays
+                        const int y = key & (w.cache.page - 1);
+                        const uint32_t half = box_bytes / 2, from = static_cast<uint32_t>(page_bytes / 2);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            bulk_load(dst + i * half, src + i * from + y * (D / 2), box * (D / 2), full(s), policy);
+                            bulk_load(dst + i * half + box * (D / 2), src + i * from + w.cache.page * (D / 2) + y * (D / 16),
+                                      box * (D / 16), full(s), policy);
+                        }
+                    }
+                }
+                Stage4 *m = meta + s;
+                const int from = (first_lane + tile_lane) & 31;
+                const int t0 = __shfl_sync(0xffffffffu, key, from) + tile_key;
+                if (lane < F::SUBS)
+                    m->key0[lane] = (alive >> from & 1u) && t0 < len ? t0 : kNoKey;
+                int flags = (opened ? kFirst : 0) | (ended ? kLast : 0);
+                if (ended) {
+                    // did this block have the segment from its first to its last unit?
+                    if (unit > done)
+                        flags |= kHeadPart;  // it began before this block's run
+                    else if (unit + 1 < units)
+                        flags |= kTailPart;
+                }
+                if (lane == 0) {
+                    m->flags = flags;
+                    if (opened) {
+                        m->b = b;
+                        m->head = head;
+                        m->group = group;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_expect_tx(full(s), __popc(alive >> first_lane & stage_lanes) * box_bytes);
+                opened = ended;
+                ++unit;
+                if (++s == S) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (unit == units && done < all) {  // on to the next segment
+                unit = 0;
+                if (++group == w.groups) {
+                    group = 0;
+                    if (++head == w.cache.heads) {
+                        head = 0;
+                        do {
+                            ++b;
+                            open_sequence();
+                        } while (units == 0 && b < w.B);
+                    }
+                }
+            }
+        }
+        // the computing warps wait for every copy; after a failed wait this one does
+        if (!ok)
+            for (int x = 0; x < S; ++x)
+                if (done > x)
+                    drain_bounded(full(x), ((done - 1 - x) / S) & 1);
+        return;
+    }
+
+    // ---------------- the warps that compute ----------------
+    const int g = lane >> 2, c = lane & 3;
+    const int g_row = g ^ (g >> 2), v_row = 2 * c, v_swap = c >> 1;  // a tile's rows of this thread's keys
+    const int key_warps = kDecWarps / w.row_warps;
+    const int wk = warp % key_warps, wr = warp / key_warps;
+    // Q^T operand: of query rows g (+ 8), their d in the order of the thread's K
+    // words; in registers for eight rows, for sixteen in the warp's merge area
+    uint32_t qb[NT == 1 ? KW : 1][2];
+    const uint32_t q_own = sbase + F::MERGE_OFF + warp * (8 * F::OROW * 4) + lane * 16;
+    static_assert(KW * 512 <= 8 * F::OROW * 4, "sixteen rows of Q fit the merge area");
+    float qf[NT][2];      // per query row 2 c, 2 c + 1 (+ 8): scale to log2 units
+    uint32_t behind = 0;  // ... keys that it sees beyond `least`, a byte each
+    float m[NT][2], l[NT][2], acc[D / 16][NT][4];
+    int least = 0, most = 0;  // keys that all rows see (negative: the first ones see none), that any row sees
+    auto limit = [&](int nt, int u) -> int { return least + static_cast<int>((behind >> (8 * (2 * nt + u))) & 255u); };
+    int4 *segment = reinterpret_cast<int4 *>(smem + F::FLAG_OFF + 16) + warp;  // b, head, group
+    uint32_t merges = 0;
+    // a barrier of the computing warps whose wait is bounded
+    auto meet = [&]() -> bool {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(merged);
+        return wait_warp(merged, merges++ & 1u, abort_flag);
+    };
+    bool fresh = true;   // some row may have no reference yet
+    uint32_t unset = 0;  // ... a bit each of the thread's
+    int slot = S - 1;
+    uint32_t phase = 1;
+    for (int done = 0; done < all; ++done) {
+        if (++slot == S)
+            slot = 0;
+        if (slot == 0)
+            phase ^= 1u;
+        if (!wait_warp(full(slot), phase, abort_flag))
+            return;
+        const Stage4 *info = meta + slot;
+        const int flags = info->flags;
+
+        if (flags & kFirst) {
+            const int b_seg = info->b;
+            head = info->head;
+            group = info->group;
+            if (lane == 0)
+                *segment = make_int4(b_seg, head, group, 0);
+            __syncwarp();
+            most = w.batch.length(b_seg, log2_page);
+            least = w.q.causal ? most - w.q.Nq + 1 : most;
+            behind = 0;
+            fresh = true;
+            unset = (1u << (2 * NT)) - 1u;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int row = group * rows_block + wr * ROWS + nt * 8 + g;
+                const int hq = row / w.q.Nq, qi = row % w.q.Nq;
+                const T *src = static_cast<const T *>(w.q.q) + b_seg * w.q.batch_stride +
+                               static_cast<long long>(head * w.q.G + hq) * w.q.head_stride + qi * w.q.row_stride + c * (D / 4);
+                uint2 x[KW];
+                float top = 0.f;
+#pragma unroll
+                for (int s = 0; s < KW; ++s) {
+                    x[s] = make_uint2(0, 0);
+                    if (row < w.R)
+                        x[s] = *reinterpret_cast<const uint2 *>(src + 4 * s);
+                }
+#pragma unroll
+                for (int s = 0; s < KW; ++s) {
+                    const float2 y = DTypeTraits<T>::unpack(x[s].x), z = DTypeTraits<T>::unpack(x[s].y);
+                    const float f[4] = {fabsf(y.x), fabsf(y.y), fabsf(z.x), fabsf(z.y)};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (f[u] <= 3.402823466e38f)
+                            top = fmaxf(top, f[u]);
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int e = top > 0.f ? max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -100) : 0;
+                const float by = cache::pow2f(-e);
+#pragma unroll
+                for (int s = 0; s < KW; ++s) {
+                    const float2 y = DTypeTraits<T>::unpack(x[s].x), z = DTypeTraits<T>::unpack(x[s].y);
+                    const uint32_t q0 = DTypeTraits<__half>::pack(y.x * by, y.y * by);
+                    const uint32_t q1 = DTypeTraits<__half>::pack(z.x * by, z.y * by);
+                    if constexpr (NT == 1) {
+                        qb[s][0] = q0;
+                        qb[s][1] = q1;
+                    } else {
+                        cache::store_pair(q_own + s * 512 + nt * 8, q0, q1);
+                    }
+                }
+                const int extra = w.q.causal ? qi : 0;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    qf[nt][u] = cache::pow2f(__shfl_sync(0xffffffffu, e, 8 * c + 4 * u)) * w.scale_log2;
+                    behind |= __shfl_sync(0xffffffffu, extra, 8 * c + 4 * u) << (8 * (2 * nt + u));
+                    m[nt][u] = 0.f;
+                    l[nt][u] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        acc[j][nt][u] = 0.f;
+            }
+        }
+
+        for (int set = wk; set < F::SUBS / J; set += key_warps) {
+            // J tiles at once: one look at the reference, and twice the independent work
+            const int sub0 = set * J;
+            const bool last_set = set + key_warps >= F::SUBS / J;
+            int key0[J];
+            uint32_t at[J];  // the tile's codes of K
+            int nearest = kNoKey, farthest = 0;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                key0[j] = info->key0[sub0 + j];
+                nearest = min(nearest, key0[j]);
+                farthest = max(farthest, key0[j]);
+                const int row = (sub0 + j) * kTile;
+                at[j] = sbase + slot * F::STAGE + (row >> w.log2_box) * box_bytes + (row & (box - 1)) * (D / 2);
+            }
+            if (nearest == kNoKey) {
+                if (last_set) {
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(empty(slot));
+                }
+                continue;
+            }
+            // from a tile's codes to its scales: the rest of the box's codes, and the scales before it
+            const uint32_t half = box_bytes / 2;
+            auto scales_of = [&](int j) -> uint32_t {
+                const int row = ((sub0 + j) * kTile) & (box - 1);
+                return at[j] + (box - row) * (D / 2) + row * (D / 16);
+            };
+            // ---- S^T = K Q^T ----
+            float e[J][NT][4];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                uint32_t kw[2][D / 32], by[2][D / 32];
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    load_k<D>(at[j], scales_of(j), g_row + 8 * r, c, kw[r], by[r]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        e[j][nt][u] = 0.f;
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    uint32_t h[2][4];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        halves8(kw[r][x], h[r]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            h[r][i] = times(h[r][i], by[r][x]);
+                    }
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int s = 2 * x + y;
+                        if constexpr (NT == 1) {
+                            cache::mma_f16(e[j][0], h[0][2 * y], h[1][2 * y], h[0][2 * y + 1], h[1][2 * y + 1], qb[s][0],
+                                           qb[s][1]);
+                        } else {
+                            uint32_t z[4];
+                            cache::load_words<4>(z, q_own + s * 512);
+                            cache::mma_f16(e[j][0], h[0][2 * y], h[1][2 * y], h[0][2 * y + 1], h[1][2 * y + 1], z[0], z[1]);
+                            cache::mma_f16(e[j][1], h[0][2 * y], h[1][2 * y], h[0][2 * y + 1], h[1][2 * y + 1], z[2], z[3]);
+                        }
+                    }
+                }
+            }
+            // ---- exponents of P, masks; does any outgrow its reference? ----
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        e[j][nt][u] = fmaf(e[j][nt][u], qf[nt][u & 1], -m[nt][u & 1]);
+            const bool masked = farthest + kTile > least;
+            if (masked) {
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (key0[j] + g_row + 8 * (u >> 1) >= limit(nt, u & 1))
+                                e[j][nt][u] = -INFINITY;
+            }
+            bool grown = fresh;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        grown |= !(e[j][nt][u] <= kMost);
+            if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t bit = 1u << (2 * nt + u);
+                        float top = -INFINITY;  // over the reference, which is 0 as long as it is not set
+#pragma unroll
+                        for (int j = 0; j < J; ++j)
+                            top = fmaxf(top, fmaxf(e[j][nt][u], e[j][nt][u + 2]));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        const float over = top - kAim;
+                        const float up = unset & bit ? (top == -INFINITY ? 0.f : over) : fmaxf(over, 0.f);
+                        const float alpha = unset & bit ? 1.f : cache::ex2(-up);
+                        if (top > -INFINITY)
+                            unset &= ~bit;
+                        m[nt][u] += up;
+                        l[nt][u] *= alpha;
+#pragma unroll
+                        for (int j = 0; j < J; ++j) {
+                            e[j][nt][u] -= up;
+                            e[j][nt][u + 2] -= up;
+                        }
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            acc[j][nt][u] *= alpha;
+                            acc[j][nt][u + 2] *= alpha;
+                        }
+                    }
+                fresh = __any_sync(0xffffffffu, unset != 0);
+            }
+            // ---- P, and O^T += V^T P^T ----
+            uint32_t pb[J][NT][2];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float(&p)[4] = e[j][nt];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        p[u] = cache::ex2(p[u]);
+                        l[nt][u & 1] += p[u];
+                    }
+                    pb[j][nt][0] = cache::transpose8(DTypeTraits<__half>::pack(p[0], p[1]));
+                    pb[j][nt][1] = cache::transpose8(DTypeTraits<__half>::pack(p[2], p[3]));
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                uint32_t vw[4][VX], vs[4][VX];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    load_v<D>(at[j] + half, scales_of(j) + half, (v_row + ((r & 1) ^ v_swap)) + 8 * (r >> 1), g, vw[r], vs[r]);
+                if (j == J - 1 && last_set) {  // the stage's bytes are in registers
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(empty(slot));
+                }
+                if (masked) {
+                    // bytes behind the last key are whatever the page held: codes are finite, a scale
+                    // need not be
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (key0[j] + (v_row + ((r & 1) ^ v_swap)) + 8 * (r >> 1) >= most)
+#pragma unroll
+                            for (int x = 0; x < VX; ++x)
+                                vs[r][x] = 0;
+                }
+#pragma unroll
+                for (int x = 0; x < VX; ++x) {
+                    // the channels of a word, of keys 2 c and 2 c + 1, and of the two 8 behind them
+                    const bool half_word = x == VX - 1 && D % 64 != 0;
+                    uint32_t even[2][4], odd[2][4];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t a = vw[2 * r][x], z = vw[2 * r + 1][x];
+                        const uint32_t by = (vs[2 * r][x] | vs[2 * r + 1][x] << 16) << 7;
+                        halves8((a & 0x0F0F0F0Fu) | (z << 4 & 0xF0F0F0F0u), even[r]);
+                        halves8((a >> 4 & 0x0F0F0F0Fu) | (z & 0xF0F0F0F0u), odd[r]);
+#pragma unroll
+                        for (int i = 0; i < (half_word ? 2 : 4); ++i) {
+                            even[r][i] = times(even[r][i], by);
+                            odd[r][i] = times(odd[r][i], by);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < (half_word ? 2 : 4); ++i)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            cache::mma_f16(acc[4 * x + i][nt], even[0][i], odd[0][i], even[1][i], odd[1][i], pb[j][nt][0],
+                                           pb[j][nt][1]);
+                }
+            }
+        }
+
+        if (flags & kLast) {
+            // ---- merge the warps of each row group, eight rows a warp at a time;
+            // write the rows, or the block's part ----
+            float *mo = reinterpret_cast<float *>(smem + F::MERGE_OFF);
+            float *mm = reinterpret_cast<float *>(smem + F::ML_OFF), *ml = mm + kDecWarps * 8;
+            const int b_seg = segment->x;
+            head = segment->y;
+            group = segment->z;
+            const bool part = flags & (kHeadPart | kTailPart);
+            const long long place = 2ll * blockIdx.x + (flags & kTailPart ? 1 : 0);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float sum = l[nt][u];
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                    const int row = warp * 8 + 2 * c + u;
+                    if (g == 0) {
+                        mm[row] = unset >> (2 * nt + u) & 1u ? -INFINITY : m[nt][u];
+                        ml[row] = sum;
+                    }
+#pragma unroll
+                    for (int x = 0; x < VW; ++x)
+                        *reinterpret_cast<float4 *>(mo + row * F::OROW + cache::v_column<D>(g, x)) =
+                            make_float4(acc[2 * x][nt][u], acc[2 * x][nt][u + 2], acc[2 * x + 1][nt][u],
+                                        acc[2 * x + 1][nt][u + 2]);
+                }
+                if (!meet())
+                    return;
+                for (int x = t; x < 8 * w.row_warps * (D / 2); x += 32 * kDecWarps) {
+                    const int r8 = x / (D / 2), d = 2 * (x % (D / 2));
+                    const int row = r8 / 8 * ROWS + nt * 8 + r8 % 8;  // of the block
+                    const int abs_row = group * rows_block + row;
+                    if (abs_row >= w.R)
+                        continue;
+                    const int from = (r8 / 8) * key_warps * 8 + r8 % 8;  // of its first warp
+                    float top = -INFINITY;
+                    for (int y = 0; y < key_warps; ++y)
+                        top = fmaxf(top, mm[from + y * 8]);
+                    float2 o = make_float2(0.f, 0.f);
+                    float sum = 0.f;
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    for (int y = 0; y < key_warps; ++y) {
+                        const float f = cache::ex2(mm[from + y * 8] - ref);
+                        const float2 z = *reinterpret_cast<const float2 *>(mo + (from + y * 8) * F::OROW + d);
+                        o.x = fmaf(z.x, f, o.x);
+                        o.y = fmaf(z.y, f, o.y);
+                        sum = fmaf(ml[from + y * 8], f, sum);
+                    }
+                    if (part) {
+                        const long long pr = place * rows_block + row;
+                        *reinterpret_cast<float2 *>(w.part_o + pr * D + d) = o;
+                        if (d == 0) {
+                            w.part_m[pr] = top;
+                            w.part_l[pr] = sum;
+                        }
+                    } else {
+                        const long long orow = (static_cast<long long>(b_seg) * w.cache.heads + head) * w.R + abs_row;
+                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                        *reinterpret_cast<uint32_t *>(out + orow * D + d) = DTypeTraits<T>::pack(o.x * inv, o.y * inv);
+                        if (d == 0 && lse != nullptr)
+                            lse[orow] = sum == 0.f ? -INFINITY : (ref + __log2f(sum)) * 0.6931471805599453f;
+                    }
+                }
+                if (!meet())  // the area is free: for the next rows, for the next segment's Q
+                    return;
             }
         }
     }
-    const long long orow = static_cast<long long>(b) * rows + row;
-    if (t < d)
-        out[orow * d + t] = static_cast<T>(l > 0.f ? acc / l : 0.f);
-    if (t == 0 && lse != nullptr)
-        lse[orow] = l > 0.f ? m + logf(l) : -INFINITY;
 }
 
 }  // namespace cache4

@@ -29,6 +29,21 @@ struct Cache4 {
 // Bytes of K (or V) of a page and head.
 __host__ __device__ __forceinline__ int half_block(int page, int d) { return page * d / 16 * 9; }
 
+__device__ __forceinline__ uint32_t load_u8(uint32_t addr)
+{
+    uint32_t x = 0;
+    if (smem_ok(addr, 1, 1))
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+    return x;
+}
+__device__ __forceinline__ uint32_t load_u16(uint32_t addr)
+{
+    uint32_t x = 0;
+    if (smem_ok(addr, 2, 2))
+        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+    return x;
+}
+
 // A scale byte's value, in both halves of a pair.
 __device__ __forceinline__ uint32_t scale_pair(uint32_t byte) { return (byte << 7) | (byte << 23); }
 

@@ -201,6 +201,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
         : "memory");
 }
 
+// The same with an L2 policy.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar, uint64_t policy)
+{
+    if (!smem_ok(dst, bytes, 16) || !smem_ok(bar, 8, 8))
+        return;
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "l"(policy)
+        : "memory");
+}
+
 // Tensor store shared -> global of one box (rows outside the tensor are not
 // written), tracked by the issuing thread's bulk async-group.
 __device__ __forceinline__ void tma_store_3d(const void *tmap, uint32_t src, int x, int y, int z)
