@@ -30,10 +30,12 @@ Cache4State g_cache4[kMaxDevices];
 // Units of a segment that one block may take whole, as for the 8-bit cache.
 constexpr long long kWholeUnits = 8;
 
+// Two 16-key tiles a warp at once, or, with sixteen query rows, where their registers
+// would spill, one.
 template <int D, int NT, typename T>
 constexpr auto decode_kernel()
 {
-    return fa::cache4::fa_cache4_decode_kernel<D, NT, D <= 64 ? 2 : 1, T>;
+    return fa::cache4::fa_cache4_decode_kernel<D, NT, NT == 1 || D <= 64 ? 2 : 1, T>;
 }
 
 template <int D>
@@ -302,7 +304,7 @@ fa_status_t fa_decode_cache4(const fa_cache4_t *cache, const void *q, long long 
         return by_type(dtype, [&](auto t) {
             using T = decltype(t);
             if (!launch_dependent(shape.tiles == 1 ? decode_kernel<D, 1, T>() : decode_kernel<D, 2, T>(),
-                                  static_cast<unsigned>(blocks), fa::cache::kDecThreads, F::SMEM, cs, w,
+                                  static_cast<unsigned>(blocks), F::THREADS, F::SMEM, cs, w,
                                   static_cast<T *>(o), lse))
                 return FA_ERR_CUDA;
             if (w.whole)
@@ -310,10 +312,10 @@ fa_status_t fa_decode_cache4(const fa_cache4_t *cache, const void *q, long long 
             constexpr int kWarps = fa::cache::kCombineThreads / 32;
             const bool second =
                 blocks <= segments * fa::cache::kCombineEach
-                    ? launch_dependent(fa::cache::fa_cache_combine_kernel<D, T, 1>,
+                    ? launch_dependent(fa::cache::fa_cache_combine_kernel<D, T, 1, F::LOG2_STEP, F::OPEN>,
                                        static_cast<unsigned>((rows + kWarps - 1) / kWarps), fa::cache::kCombineThreads, 0,
                                        cs, w, static_cast<T *>(o), lse, rows_block, rows)
-                    : launch_dependent(fa::cache::fa_cache_combine_kernel<D, T, kWarps>, static_cast<unsigned>(rows),
+                    : launch_dependent(fa::cache::fa_cache_combine_kernel<D, T, kWarps, F::LOG2_STEP, F::OPEN>, static_cast<unsigned>(rows),
                                        fa::cache::kCombineThreads, 0, cs, w, static_cast<T *>(o), lse, rows_block, rows);
             if (!second)
                 return FA_ERR_CUDA;

@@ -26,8 +26,6 @@ namespace fa {
 namespace cache4 {
 
 using cache::kAim;
-using cache::kDecThreads;
-using cache::kDecWarps;
 using cache::kFirst;
 using cache::kHeadPart;
 using cache::kLast;
@@ -37,22 +35,26 @@ using cache::kTailPart;
 using cache::kTile;
 using cache::Work;
 
-// As DecCfg of the 8-bit cache, whose stages have the same keys (the merge counts in them).
+// As DecCfg of the 8-bit cache.
 template <int D>
 struct Dec4Cfg {
-    static constexpr int LOG2_STEP = cache::DecCfg<D>::LOG2_STEP;
+    static constexpr int LOG2_STEP = 7;
     static constexpr int STEP = 1 << LOG2_STEP;
     static constexpr int SUBS = STEP / kTile;
     static constexpr int STAGE = STEP * D / 8 * 9;  // bytes
+    static constexpr int WARPS = 4;              // that compute
+    static constexpr int THREADS = 32 * (WARPS + 1);
     static constexpr int BLOCKS = D == 32 ? 4 : 3;  // an SM
-    static constexpr int STAGES = 5;
+    static constexpr int STAGES = D == 128 ? 3 : D == 96 ? 4 : 5;
+    static constexpr int OPEN = 2;                  // units that a segment's begin and end cost
+    static_assert(SUBS >= 2 * WARPS, "every warp has two tiles of a stage");
     static constexpr int OROW = D + 4;
     static constexpr int META_OFF = STAGES * STAGE;
     static constexpr int MERGE_OFF = META_OFF + STAGES * 64;
-    static constexpr int ML_OFF = MERGE_OFF + kDecWarps * 8 * OROW * 4;
-    static constexpr int BAR_OFF = ML_OFF + kDecWarps * 8 * 8;
+    static constexpr int ML_OFF = MERGE_OFF + WARPS * 8 * OROW * 4;
+    static constexpr int BAR_OFF = ML_OFF + WARPS * 8 * 8;
     static constexpr int FLAG_OFF = BAR_OFF + 16 * STAGES + 16;
-    static constexpr int SMEM = FLAG_OFF + 16 + 16 * kDecWarps + 128;  // and room to align the ring
+    static constexpr int SMEM = FLAG_OFF + 16 + 16 * WARPS + 128;  // and room to align the ring
     static_assert(STAGE % 128 == 0, "alignment of the ring");
 };
 
@@ -62,6 +64,7 @@ struct __align__(16) Stage4 {
     int flags, b, head, group, pad[4];
 };
 static_assert(sizeof(Stage4) == 64, "stage record");
+constexpr int kEnd = 32;  // the block's last stage
 
 // Words of eight consecutive channels of a key's K that a thread has: D / 4 channels from
 // c * D / 4 on; their scales' bytes.
@@ -123,7 +126,7 @@ __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b)
 }
 
 template <int D, int NT, int J, typename T>
-__global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
+__global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
     fa_cache4_decode_kernel(const __grid_constant__ Work w, T *__restrict__ out, float *__restrict__ lse)
 {
     using F = Dec4Cfg<D>;
@@ -132,7 +135,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
     constexpr int VW = D / 32;           // fours of channels of a thread
     constexpr int VX = (D + 63) / 64;    // words of them
     extern __shared__ uint8_t smem_raw[];
-    __shared__ long long scan[kDecWarps + 1];
+    __shared__ long long scan[F::WARPS + 1];
     __shared__ long long begin[2];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sbase = (raw + 127u) & ~127u;
@@ -150,9 +153,9 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
     if (t == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), kDecWarps);
+            mbar_init(empty(s), F::WARPS);
         }
-        mbar_init(merged, kDecWarps);
+        mbar_init(merged, F::WARPS);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -160,9 +163,9 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
     cache::let_next();
 
     // ---- this block's run of units ----
-    int all;            // units of this block
+    int left = 0;       // its length
     int b;              // its first sequence
-    long long off = 0;  // ... and the unit of that sequence it begins with
+    long long off = 0;  // ... and where in that sequence it begins
     int head = 0, group = 0;  // with `whole`, its segment
     if (w.whole) {
         int x = blockIdx.x;
@@ -172,15 +175,13 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
         b = x / w.cache.heads;
         if (t == 0 && group == 0 && head == 0)
             w.batch.check_length(b, log2_page);
-        // a segment without keys has a unit all the same, and writes its rows in it
-        all = max(1, cache::units_of<F::LOG2_STEP>(w, w.batch.length(b, log2_page), 0));
         __syncthreads();  // the barriers are set
     } else {
-        const int each = (w.B + kDecThreads - 1) / kDecThreads;
+        const int each = (w.B + F::THREADS - 1) / F::THREADS;
         const int b0 = min(w.B, t * each), b1 = min(w.B, b0 + each);
         long long sum = 0;
         for (int x = b0; x < b1; ++x)
-            sum += cache::units_of_sequence<F::LOG2_STEP>(w, x);
+            sum += cache::units_of_sequence<F::LOG2_STEP, F::OPEN>(w, x);
         long long incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -192,12 +193,13 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
             scan[warp] = incl;
         __syncthreads();
         long long total = 0;
-        for (int x = 0; x < kDecWarps + 1; ++x) {
+        for (int x = 0; x < F::WARPS + 1; ++x) {
             if (x < warp)
                 incl += scan[x];
             total += scan[x];
         }
-        const long long share = max(1ll, (total + gridDim.x - 1) / gridDim.x);
+        // longer than a segment's begin, so that every run has a unit (the last one ends with one)
+        const long long share = max(F::OPEN + 1ll, (total + gridDim.x - 1) / gridDim.x);
         const long long first_unit = share * blockIdx.x;
         long long at = incl - sum;
         if (blockIdx.x == 0) {
@@ -207,13 +209,13 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
             for (int x = b0; x < b1; ++x) {
                 w.plan[1 + x] = y;
                 w.batch.check_length(x, log2_page);
-                y += cache::units_of_sequence<F::LOG2_STEP>(w, x);
+                y += cache::units_of_sequence<F::LOG2_STEP, F::OPEN>(w, x);
             }
         }
         if (first_unit >= at && first_unit < incl) {
             int x = b0;
             for (; x + 1 < b1; ++x) {
-                const long long n = cache::units_of_sequence<F::LOG2_STEP>(w, x);
+                const long long n = cache::units_of_sequence<F::LOG2_STEP, F::OPEN>(w, x);
                 if (first_unit < at + n)
                     break;
                 at += n;
@@ -226,11 +228,11 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
             return;
         b = static_cast<int>(begin[0]);
         off = begin[1];
-        all = static_cast<int>(min(share, total - first_unit));
+        left = static_cast<int>(min(share, total - first_unit));
     }
 
     const int box = 1 << w.log2_box, box_bytes = box * (D / 8 * 9);
-    if (warp == kDecWarps) {
+    if (warp == F::WARPS) {
         // ---------------- the warp that loads ----------------
         int len = 0, units = 0, unit = 0;
         auto open_sequence = [&]() {
@@ -239,25 +241,31 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
         };
         open_sequence();
         if (w.whole) {
-            units = all;
+            units = left = max(1, units);  // without keys it has a unit all the same, and writes its rows in it
         } else {
-            // off < units * heads * groups here: 32 bits hold it unless a sequence's work is vast
-            const int seg = off >> 31 ? static_cast<int>(off / units) : static_cast<int>(off) / units;
+            // off < (units + OPEN) * heads * groups here: 32 bits hold it unless a sequence's work is vast
+            const int span = units + F::OPEN;
+            const int seg = off >> 31 ? static_cast<int>(off / span) : static_cast<int>(off) / span;
             head = seg / w.groups;
             group = seg % w.groups;
-            unit = static_cast<int>(off - static_cast<long long>(seg) * units);
+            unit = static_cast<int>(off - static_cast<long long>(seg) * span) - F::OPEN;
+            left += min(unit, 0);  // what is left of the segment's begin
+            unit = max(unit, 0);
         }
         const int log2_boxes = F::LOG2_STEP - w.log2_box;  // boxes of a stage: 1 to 8
         const int batch_units = 32 >> log2_boxes;
         const size_t page_bytes = static_cast<size_t>(w.cache.page) * (D / 8 * 9);
         const uint64_t policy = l2_policy_evict_first();
         bool opened = true, ok = true;  // opened: the next unit is this block's first of its segment
+        bool begun = unit == 0;         // this block has the segment's first unit
         const unsigned stage_lanes = (1u << (1 << log2_boxes)) - 1u;
         int done = 0, s = 0;
         uint32_t phase = 0;  // of the ring's round
-        while (done < all && ok) {
+        while (left > 0 && ok) {
             // lane l: page of the l-th of the next 32 boxes of this segment
-            const int here = min(min(batch_units, units - unit), all - done);
+            const int here = min(min(batch_units, units - unit), left);
+            if (here <= 0)  // lengths that changed under the call: the other warps' waits will give up
+                break;
             const int key = (unit << F::LOG2_STEP) + lane * box;
             int p = -1;
             if ((lane >> log2_boxes) < here && key < len) {
@@ -274,7 +282,9 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
                     break;
                 const int first_lane = u << log2_boxes;
                 const bool mine = (lane >> log2_boxes) == u;
-                const bool ended = unit + 1 == units || done + 1 == all;
+                --left;
+                const bool last = left == 0 || (unit + 1 == units && left <= F::OPEN);
+                const bool ended = unit + 1 == units || last;
                 // the copies first (their bytes may arrive before they are expected: the phase
                 // waits for the arrival below), then the record
                 if (mine && p >= 0) {
@@ -297,14 +307,12 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
                 const int t0 = __shfl_sync(0xffffffffu, key, from) + tile_key;
                 if (lane < F::SUBS)
                     m->key0[lane] = (alive >> from & 1u) && t0 < len ? t0 : kNoKey;
-                int flags = (opened ? kFirst : 0) | (ended ? kLast : 0);
-                if (ended) {
-                    // did this block have the segment from its first to its last unit?
-                    if (unit > done)
-                        flags |= kHeadPart;  // it began before this block's run
-                    else if (unit + 1 < units)
-                        flags |= kTailPart;
-                }
+                int flags = (opened ? kFirst : 0) | (ended ? kLast : 0) | (last ? kEnd : 0);
+                // does this block have the segment from its first to its last unit?
+                if (ended && !begun)
+                    flags |= kHeadPart;  // it began before this block's run
+                else if (ended && unit + 1 < units)
+                    flags |= kTailPart;
                 if (lane == 0) {
                     m->flags = flags;
                     if (opened) {
@@ -323,8 +331,9 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
                     phase ^= 1u;
                 }
             }
-            if (unit == units && done < all) {  // on to the next segment
+            if (unit == units && (left -= F::OPEN) > 0) {  // on to the next segment
                 unit = 0;
+                begun = true;
                 if (++group == w.groups) {
                     group = 0;
                     if (++head == w.cache.heads) {
@@ -348,7 +357,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
     // ---------------- the warps that compute ----------------
     const int g = lane >> 2, c = lane & 3;
     const int g_row = g ^ (g >> 2), v_row = 2 * c, v_swap = c >> 1;  // a tile's rows of this thread's keys
-    const int key_warps = kDecWarps / w.row_warps;
+    const int key_warps = F::WARPS / w.row_warps;
     const int wk = warp % key_warps, wr = warp / key_warps;
     // Q^T operand: of query rows g (+ 8), their d in the order of the thread's K
     // words; in registers for eight rows, for sixteen in the warp's merge area
@@ -373,7 +382,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
     uint32_t unset = 0;  // ... a bit each of the thread's
     int slot = S - 1;
     uint32_t phase = 1;
-    for (int done = 0; done < all; ++done) {
+    for (int flags = 0; !(flags & kEnd);) {
         if (++slot == S)
             slot = 0;
         if (slot == 0)
@@ -381,7 +390,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
         if (!wait_warp(full(slot), phase, abort_flag))
             return;
         const Stage4 *info = meta + slot;
-        const int flags = info->flags;
+        flags = info->flags;
 
         if (flags & kFirst) {
             const int b_seg = info->b;
@@ -395,20 +404,26 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
             behind = 0;
             fresh = true;
             unset = (1u << (2 * NT)) - 1u;
+            uint2 rows_q[NT][KW];
+            int extra[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int row = group * rows_block + wr * ROWS + nt * 8 + g;
                 const int hq = row / w.q.Nq, qi = row % w.q.Nq;
+                extra[nt] = w.q.causal ? qi : 0;
                 const T *src = static_cast<const T *>(w.q.q) + b_seg * w.q.batch_stride +
                                static_cast<long long>(head * w.q.G + hq) * w.q.head_stride + qi * w.q.row_stride + c * (D / 4);
-                uint2 x[KW];
-                float top = 0.f;
 #pragma unroll
                 for (int s = 0; s < KW; ++s) {
-                    x[s] = make_uint2(0, 0);
+                    rows_q[nt][s] = make_uint2(0, 0);
                     if (row < w.R)
-                        x[s] = *reinterpret_cast<const uint2 *>(src + 4 * s);
+                        rows_q[nt][s] = *reinterpret_cast<const uint2 *>(src + 4 * s);
                 }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint2(&x)[KW] = rows_q[nt];
+                float top = 0.f;
 #pragma unroll
                 for (int s = 0; s < KW; ++s) {
                     const float2 y = DTypeTraits<T>::unpack(x[s].x), z = DTypeTraits<T>::unpack(x[s].y);
@@ -434,11 +449,10 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
                         cache::store_pair(q_own + s * 512 + nt * 8, q0, q1);
                     }
                 }
-                const int extra = w.q.causal ? qi : 0;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     qf[nt][u] = cache::pow2f(__shfl_sync(0xffffffffu, e, 8 * c + 4 * u)) * w.scale_log2;
-                    behind |= __shfl_sync(0xffffffffu, extra, 8 * c + 4 * u) << (8 * (2 * nt + u));
+                    behind |= __shfl_sync(0xffffffffu, extra[nt], 8 * c + 4 * u) << (8 * (2 * nt + u));
                     m[nt][u] = 0.f;
                     l[nt][u] = 0.f;
                 }
@@ -519,12 +533,17 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
             }
             // ---- exponents of P, masks; does any outgrow its reference? ----
 #pragma unroll
-            for (int j = 0; j < J; ++j)
+            for (int nt = 0; nt < NT; ++nt) {
+                const float2 by = make_float2(qf[nt][0], qf[nt][1]), from = make_float2(-m[nt][0], -m[nt][1]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int j = 0; j < J; ++j)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        e[j][nt][u] = fmaf(e[j][nt][u], qf[nt][u & 1], -m[nt][u & 1]);
+                    for (int u = 0; u < 4; u += 2) {
+                        const float2 x = ffma2(make_float2(e[j][nt][u], e[j][nt][u + 1]), by, from);
+                        e[j][nt][u] = x.x;
+                        e[j][nt][u + 1] = x.y;
+                    }
+            }
             const bool masked = farthest + kTile > least;
             if (masked) {
 #pragma unroll
@@ -536,15 +555,15 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
                             if (key0[j] + g_row + 8 * (u >> 1) >= limit(nt, u & 1))
                                 e[j][nt][u] = -INFINITY;
             }
-            bool grown = fresh;
+            float highest = fresh ? INFINITY : -INFINITY;  // NaN moves no reference
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        grown |= !(e[j][nt][u] <= kMost);
-            if (__any_sync(0xffffffffu, grown)) {
+                    for (int u = 0; u < 4; u += 2)
+                        highest = fmax3(highest, e[j][nt][u], e[j][nt][u + 1]);
+            if (__any_sync(0xffffffffu, highest > kMost)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -585,10 +604,12 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
                 for (int nt = 0; nt < NT; ++nt) {
                     float(&p)[4] = e[j][nt];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
+                    for (int u = 0; u < 4; ++u)
                         p[u] = cache::ex2(p[u]);
-                        l[nt][u & 1] += p[u];
-                    }
+                    const float2 sum = fadd2(make_float2(l[nt][0], l[nt][1]),
+                                             fadd2(make_float2(p[0], p[1]), make_float2(p[2], p[3])));
+                    l[nt][0] = sum.x;
+                    l[nt][1] = sum.y;
                     pb[j][nt][0] = cache::transpose8(DTypeTraits<__half>::pack(p[0], p[1]));
                     pb[j][nt][1] = cache::transpose8(DTypeTraits<__half>::pack(p[2], p[3]));
                 }
@@ -645,7 +666,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
             // ---- merge the warps of each row group, eight rows a warp at a time;
             // write the rows, or the block's part ----
             float *mo = reinterpret_cast<float *>(smem + F::MERGE_OFF);
-            float *mm = reinterpret_cast<float *>(smem + F::ML_OFF), *ml = mm + kDecWarps * 8;
+            float *mm = reinterpret_cast<float *>(smem + F::ML_OFF), *ml = mm + F::WARPS * 8;
             const int b_seg = segment->x;
             head = segment->y;
             group = segment->z;
@@ -672,29 +693,35 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
                 }
                 if (!meet())
                     return;
-                for (int x = t; x < 8 * w.row_warps * (D / 2); x += 32 * kDecWarps) {
-                    const int r8 = x / (D / 2), d = 2 * (x % (D / 2));
+                for (int x = t; x < 8 * w.row_warps * (D / 4); x += 32 * F::WARPS) {
+                    const int r8 = x / (D / 4), d = 4 * (x % (D / 4));
                     const int row = r8 / 8 * ROWS + nt * 8 + r8 % 8;  // of the block
                     const int abs_row = group * rows_block + row;
                     if (abs_row >= w.R)
                         continue;
                     const int from = (r8 / 8) * key_warps * 8 + r8 % 8;  // of its first warp
-                    float top = -INFINITY;
-                    for (int y = 0; y < key_warps; ++y)
-                        top = fmaxf(top, mm[from + y * 8]);
-                    float2 o = make_float2(0.f, 0.f);
-                    float sum = 0.f;
-                    const float ref = top == -INFINITY ? 0.f : top;
-                    for (int y = 0; y < key_warps; ++y) {
-                        const float f = cache::ex2(mm[from + y * 8] - ref);
-                        const float2 z = *reinterpret_cast<const float2 *>(mo + (from + y * 8) * F::OROW + d);
-                        o.x = fmaf(z.x, f, o.x);
-                        o.y = fmaf(z.y, f, o.y);
-                        sum = fmaf(ml[from + y * 8], f, sum);
+                    float f[F::WARPS], top = -INFINITY, sum = 0.f;
+#pragma unroll
+                    for (int y = 0; y < F::WARPS; ++y) {
+                        f[y] = y < key_warps ? mm[from + y * 8] : -INFINITY;
+                        top = fmaxf(top, f[y]);
                     }
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int y = 0; y < F::WARPS; ++y)
+                        if (y < key_warps) {
+                            const float4 z = *reinterpret_cast<const float4 *>(mo + (from + y * 8) * F::OROW + d);
+                            f[y] = cache::ex2(f[y] - ref);
+                            o.x = fmaf(z.x, f[y], o.x);
+                            o.y = fmaf(z.y, f[y], o.y);
+                            o.z = fmaf(z.z, f[y], o.z);
+                            o.w = fmaf(z.w, f[y], o.w);
+                            sum = fmaf(ml[from + y * 8], f[y], sum);
+                        }
                     if (part) {
                         const long long pr = place * rows_block + row;
-                        *reinterpret_cast<float2 *>(w.part_o + pr * D + d) = o;
+                        *reinterpret_cast<float4 *>(w.part_o + pr * D + d) = o;
                         if (d == 0) {
                             w.part_m[pr] = top;
                             w.part_l[pr] = sum;
@@ -702,7 +729,8 @@ __global__ void __launch_bounds__(kDecThreads, Dec4Cfg<D>::BLOCKS)
                     } else {
                         const long long orow = (static_cast<long long>(b_seg) * w.cache.heads + head) * w.R + abs_row;
                         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                        *reinterpret_cast<uint32_t *>(out + orow * D + d) = DTypeTraits<T>::pack(o.x * inv, o.y * inv);
+                        *reinterpret_cast<uint2 *>(out + orow * D + d) = make_uint2(
+                            DTypeTraits<T>::pack(o.x * inv, o.y * inv), DTypeTraits<T>::pack(o.z * inv, o.w * inv));
                         if (d == 0 && lse != nullptr)
                             lse[orow] = sum == 0.f ? -INFINITY : (ref + __log2f(sum)) * 0.6931471805599453f;
                     }

@@ -189,13 +189,16 @@ __device__ __forceinline__ int units_of(const Work &w, int len, int i)
     }
     return keys > 0 ? ((keys - 1) >> LOG2_STEP) + 1 : 0;
 }
-template <int LOG2_STEP>
+// Those of sequence b; a segment that has any counts OPEN more.
+template <int LOG2_STEP, int OPEN = 0>
 __device__ __forceinline__ long long units_of_sequence(const Work &w, int b)
 {
     const int len = w.batch.length(b, w.cache.log2_page);
     long long n = 0;
-    for (int i = 0; i < (w.pages ? w.q.Nq : 1); ++i)
-        n += units_of<LOG2_STEP>(w, len, i);
+    for (int i = 0; i < (w.pages ? w.q.Nq : 1); ++i) {
+        const int units = units_of<LOG2_STEP>(w, len, i);
+        n += units > 0 ? units + OPEN : 0;
+    }
     return n * w.cache.heads * w.groups;
 }
 
@@ -920,8 +923,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::BLOCKS)
 }
 
 // Merges the parts of every segment that more than one block has, SPLIT warps a
-// query row; writes the rows of segments without keys.
-template <int D, typename T, int SPLIT>
+// query row; writes the rows of segments without keys.  Units are of 2^LOG2_STEP keys, and
+// the first of a segment lies OPEN behind its begin.
+template <int D, typename T, int SPLIT, int LOG2_STEP = DecCfg<D>::LOG2_STEP, int OPEN = 0>
 __global__ void __launch_bounds__(kCombineThreads)
     fa_cache_combine_kernel(const __grid_constant__ Work w, T *__restrict__ out, float *__restrict__ lse, int rows_block,
                             long long rows)
@@ -942,7 +946,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     const int i = static_cast<int>(x % queries), b = static_cast<int>(x / queries);
     const int group = row / rows_block;
     const int len = w.batch.length(b, w.cache.log2_page);
-    const int units = units_of<DecCfg<D>::LOG2_STEP>(w, len, i);
+    const int units = units_of<LOG2_STEP>(w, len, i);
     const long long orow =
         w.pages ? ((static_cast<long long>(b) * w.cache.heads + head) * w.q.G + row) * w.q.Nq + i
                 : (static_cast<long long>(b) * w.cache.heads + head) * w.R + row;
@@ -957,9 +961,11 @@ __global__ void __launch_bounds__(kCombineThreads)
     wait_ahead();
     const long long share = w.plan[0];
     long long first = w.plan[1 + b];
-    for (int y = 0; y < i; ++y)
-        first += static_cast<long long>(units_of<DecCfg<D>::LOG2_STEP>(w, len, y)) * w.cache.heads * w.groups;
-    first += (static_cast<long long>(head) * w.groups + group) * units;
+    for (int y = 0; y < i; ++y) {
+        const int n = units_of<LOG2_STEP>(w, len, y);
+        first += static_cast<long long>(n > 0 ? n + OPEN : 0) * w.cache.heads * w.groups;
+    }
+    first += (static_cast<long long>(head) * w.groups + group) * (units + OPEN) + OPEN;
     const int x0 = static_cast<int>(first / share), x1 = static_cast<int>((first + units - 1) / share);
     if (x0 == x1)
         return;  // one block had it all, and has written it
