@@ -30,27 +30,31 @@ Cache4State g_cache4[kMaxDevices];
 // Units of a segment that one block may take whole, as for the 8-bit cache.
 constexpr long long kWholeUnits = 8;
 
-// Two 16-key tiles a warp at once, or, with sixteen query rows, where their registers
-// would spill, one.
-template <int D, int NT, typename T>
+// Warps of 4, 8 or 16 query rows; two 16-key tiles at once or, with sixteen rows of more
+// than 64 channels, where their registers would spill, one.
+template <int D, int ROWS, typename T>
 constexpr auto decode_kernel()
 {
-    return fa::cache4::fa_cache4_decode_kernel<D, NT, NT == 1 || D <= 64 ? 2 : 1, T>;
+    return fa::cache4::fa_cache4_decode_kernel<D, ROWS, ROWS <= 8 || D <= 64 ? 2 : 1, T>;
 }
 
-template <int D>
-cudaError_t set_smem_attrs()
+template <int D, typename T>
+cudaError_t set_smem_attr()
 {
     const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
     constexpr int bytes = fa::cache4::Dec4Cfg<D>::SMEM;
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, 1, __half>(), a, bytes);
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, 4, T>(), a, bytes);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decode_kernel<D, 2, __half>(), a, bytes);
+        e = cudaFuncSetAttribute(decode_kernel<D, 8, T>(), a, bytes);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decode_kernel<D, 1, __nv_bfloat16>(), a, bytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decode_kernel<D, 2, __nv_bfloat16>(), a, bytes);
+        e = cudaFuncSetAttribute(decode_kernel<D, 16, T>(), a, bytes);
     return e;
+}
+template <int D>
+cudaError_t set_smem_attrs()
+{
+    const cudaError_t e = set_smem_attr<D, __half>();
+    return e == cudaSuccess ? set_smem_attr<D, __nv_bfloat16>() : e;
 }
 
 void init_cache4(Cache4State &st)
@@ -303,7 +307,9 @@ fa_status_t fa_decode_cache4(const fa_cache4_t *cache, const void *q, long long 
             blocks = segments * units;
         return by_type(dtype, [&](auto t) {
             using T = decltype(t);
-            if (!launch_dependent(shape.tiles == 1 ? decode_kernel<D, 1, T>() : decode_kernel<D, 2, T>(),
+            if (!launch_dependent(w.R <= 4              ? decode_kernel<D, 4, T>()
+                                  : shape.tiles == 1 ? decode_kernel<D, 8, T>()
+                                                     : decode_kernel<D, 16, T>(),
                                   static_cast<unsigned>(blocks), F::THREADS, F::SMEM, cs, w,
                                   static_cast<T *>(o), lse))
                 return FA_ERR_CUDA;

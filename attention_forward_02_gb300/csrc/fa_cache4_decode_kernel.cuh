@@ -50,7 +50,7 @@ struct Dec4Cfg {
     static_assert(SUBS >= 2 * WARPS, "every warp has two tiles of a stage");
     static constexpr int OROW = D + 4;
     static constexpr int META_OFF = STAGES * STAGE;
-    static constexpr int MERGE_OFF = META_OFF + STAGES * 64;
+    static constexpr int MERGE_OFF = META_OFF + STAGES * 32;
     static constexpr int ML_OFF = MERGE_OFF + WARPS * 8 * OROW * 4;
     static constexpr int BAR_OFF = ML_OFF + WARPS * 8 * 8;
     static constexpr int FLAG_OFF = BAR_OFF + 16 * STAGES + 16;
@@ -58,64 +58,73 @@ struct Dec4Cfg {
     static_assert(STAGE % 128 == 0, "alignment of the ring");
 };
 
-// What the computing warps know of a stage.
+// What the computing warps know of a stage: flags, with a bit from kBoxes on for every box that
+// was copied, and the unit's number within the sequence; b .. group with kFirst.
 struct __align__(16) Stage4 {
-    int key0[8];  // position of each tile's first key, or kNoKey
-    int flags, b, head, group, pad[4];
+    int flags, unit, b, head, group, pad[3];
 };
-static_assert(sizeof(Stage4) == 64, "stage record");
+static_assert(sizeof(Stage4) == 32, "stage record");
 constexpr int kEnd = 32;  // the block's last stage
+constexpr int kBoxes = 8;
 
 // Words of eight consecutive channels of a key's K that a thread has: D / 4 channels from
-// c * D / 4 on; their scales' bytes.
+// c * D / 4 on; their scales, as pairs.  `codes` and `scales` are where its first ones lie.
 template <int D>
-__device__ __forceinline__ void load_k(uint32_t codes, uint32_t scales, int row, int c, uint32_t (&w)[D / 32],
-                                       uint32_t (&by)[D / 32])
+__device__ __forceinline__ uint32_t k_scale_offset(int c)
 {
-    const uint32_t at = codes + row * (D / 2) + c * (D / 8), s = scales + row * (D / 16);
-    if constexpr (D == 128) {
-        cache::load_words<4>(w, at);
-        const uint32_t b = load_u16(s + 2 * c);
-        by[0] = by[1] = (b & 255u) * 0x800080u;
-        by[2] = by[3] = (b >> 8) * 0x800080u;
-    } else if constexpr (D == 96) {
+    return D == 128 ? 2 * c : D == 96 ? 3 * c >> 1 : D == 64 ? c : c >> 1;
+}
+template <int D>
+__device__ __forceinline__ void load_k(uint32_t codes, uint32_t scales, int c, uint32_t (&w)[D / 32], uint32_t (&by)[D / 32])
+{
+    if constexpr (D == 96) {
 #pragma unroll
         for (int i = 0; i < 3; ++i)
-            cache::load_words<1>(w + i, at + 4 * i);
-        const uint32_t lo = load_u8(s + (3 * c >> 1)) * 0x800080u, hi = load_u8(s + (3 * c >> 1) + 1) * 0x800080u;
+            cache::load_words<1>(w + i, codes + 4 * i);
+        const uint32_t lo = load_u8(scales) * 0x800080u, hi = load_u8(scales + 1) * 0x800080u;
         by[0] = lo;
         by[1] = c & 1 ? hi : lo;
         by[2] = hi;
-    } else if constexpr (D == 64) {
-        cache::load_words<2>(w, at);
-        by[0] = by[1] = load_u8(s + c) * 0x800080u;
     } else {
-        cache::load_words<1>(w, at);
-        by[0] = load_u8(s + (c >> 1)) * 0x800080u;
+        cache::load_words<D / 32>(w, codes);
+        by[0] = load_u8(scales) * 0x800080u;
+        if constexpr (D == 64)
+            by[1] = by[0];
+        if constexpr (D == 128) {
+            by[1] = by[0];
+            by[2] = by[3] = load_u8(scales + 1) * 0x800080u;
+        }
     }
 }
 
 // A thread's channels of a key's V: v_column's, eight to a word (four in the last of d = 32 and
-// 96), and the scale byte of each word.
+// 96), and the scale byte of each word; as above.
 template <int D>
-__device__ __forceinline__ void load_v(uint32_t codes, uint32_t scales, int row, int g, uint32_t (&w)[(D + 63) / 64],
+__device__ __forceinline__ uint32_t v_code_offset(int g)
+{
+    return D == 128 ? 8 * g : D == 32 ? 2 * g : 4 * g;
+}
+template <int D>
+__device__ __forceinline__ uint32_t v_scale_offset(int g)
+{
+    return D == 128 ? g : D == 32 ? g >> 2 : g >> 1;
+}
+template <int D>
+__device__ __forceinline__ void load_v(uint32_t codes, uint32_t scales, int g, uint32_t (&w)[(D + 63) / 64],
                                        uint32_t (&s)[(D + 63) / 64])
 {
-    const uint32_t at = codes + row * (D / 2), st = scales + row * (D / 16);
+    s[0] = load_u8(scales);
     if constexpr (D == 128) {
-        cache::load_words<2>(w, at + 8 * g);
-        s[0] = s[1] = load_u8(st + g);
+        cache::load_words<2>(w, codes);
+        s[1] = s[0];
     } else if constexpr (D == 96) {
-        cache::load_words<1>(w, at + 4 * g);
-        w[1] = load_u16(at + 32 + 2 * g);
-        s[0] = load_u8(st + (g >> 1));
-        s[1] = load_u8(st + 4 + (g >> 2));
+        cache::load_words<1>(w, codes);
+        w[1] = load_u16(codes + 32 - 2 * g);
+        s[1] = load_u8(scales + 4 + (g >> 2) - (g >> 1));
     } else if constexpr (D == 64) {
-        cache::load_words<1>(w, at + 4 * g);
-        s[0] = load_u8(st + (g >> 1));
+        cache::load_words<1>(w, codes);
     } else {
-        w[0] = load_u16(at + 2 * g);
-        s[0] = load_u8(st + (g >> 2));
+        w[0] = load_u16(codes);
     }
 }
 
@@ -125,13 +134,16 @@ __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b)
     return *reinterpret_cast<const uint32_t *>(&x);
 }
 
-template <int D, int NT, int J, typename T>
+template <int D, int ROWS, int J, typename T>
 __global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
     fa_cache4_decode_kernel(const __grid_constant__ Work w, T *__restrict__ out, float *__restrict__ lse)
 {
     using F = Dec4Cfg<D>;
     constexpr int S = F::STAGES;
-    constexpr int KW = D / 16;           // steps of the first product
+    constexpr int NT = ROWS == 16 ? 2 : 1;          // tiles of eight columns
+    constexpr bool PAIRS = ROWS == 4;               // columns are four rows twice
+    constexpr int KW = D / 16;                      // steps of the first product
+    constexpr int TILES = PAIRS ? D / 32 : D / 16;  // of O^T
     constexpr int VW = D / 32;           // fours of channels of a thread
     constexpr int VX = (D + 63) / 64;    // words of them
     extern __shared__ uint8_t smem_raw[];
@@ -146,8 +158,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + F::FLAG_OFF);
     Stage4 *meta = reinterpret_cast<Stage4 *>(smem + F::META_OFF);
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    constexpr int ROWS = 8 * NT;  // query rows a warp
-    const int rows_block = ROWS * w.row_warps;
+    const int rows_block = 8 * NT * w.row_warps;
     const int log2_page = w.cache.log2_page;
 
     if (t == 0) {
@@ -275,8 +286,6 @@ __global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
             }
             const uint8_t *src = w.cache.k + (static_cast<size_t>(max(p, 0)) * w.cache.heads + head) * page_bytes;
             const unsigned alive = __ballot_sync(0xffffffffu, p >= 0);
-            // lane l < SUBS writes the record of a stage's tile l: the lane that has its box
-            const int tile_lane = (lane * kTile) >> w.log2_box, tile_key = (lane * kTile) & (box - 1);
             for (int u = 0; u < here; ++u, ++done) {
                 if (done >= S && !(ok = wait_warp(empty(s), phase ^ 1u, abort_flag)))
                     break;
@@ -302,28 +311,23 @@ __global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
                         }
                     }
                 }
-                Stage4 *m = meta + s;
-                const int from = (first_lane + tile_lane) & 31;
-                const int t0 = __shfl_sync(0xffffffffu, key, from) + tile_key;
-                if (lane < F::SUBS)
-                    m->key0[lane] = (alive >> from & 1u) && t0 < len ? t0 : kNoKey;
                 int flags = (opened ? kFirst : 0) | (ended ? kLast : 0) | (last ? kEnd : 0);
                 // does this block have the segment from its first to its last unit?
                 if (ended && !begun)
                     flags |= kHeadPart;  // it began before this block's run
                 else if (ended && unit + 1 < units)
                     flags |= kTailPart;
+                const unsigned copied = alive >> first_lane & stage_lanes;
                 if (lane == 0) {
-                    m->flags = flags;
+                    Stage4 *m = meta + s;
+                    *reinterpret_cast<int2 *>(&m->flags) = make_int2(flags | static_cast<int>(copied << kBoxes), unit);
                     if (opened) {
                         m->b = b;
                         m->head = head;
                         m->group = group;
                     }
+                    mbar_arrive_expect_tx(full(s), __popc(copied) * box_bytes);
                 }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_expect_tx(full(s), __popc(alive >> first_lane & stage_lanes) * box_bytes);
                 opened = ended;
                 ++unit;
                 if (++s == S) {
@@ -366,7 +370,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
     static_assert(KW * 512 <= 8 * F::OROW * 4, "sixteen rows of Q fit the merge area");
     float qf[NT][2];      // per query row 2 c, 2 c + 1 (+ 8): scale to log2 units
     uint32_t behind = 0;  // ... keys that it sees beyond `least`, a byte each
-    float m[NT][2], l[NT][2], acc[D / 16][NT][4];
+    float m[NT][2], l[NT][2], acc[TILES][NT][4];
     int least = 0, most = 0;  // keys that all rows see (negative: the first ones see none), that any row sees
     auto limit = [&](int nt, int u) -> int { return least + static_cast<int>((behind >> (8 * (2 * nt + u))) & 255u); };
     int4 *segment = reinterpret_cast<int4 *>(smem + F::FLAG_OFF + 16) + warp;  // b, head, group
@@ -378,6 +382,27 @@ __global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
             mbar_arrive(merged);
         return wait_warp(merged, merges++ & 1u, abort_flag);
     };
+    // where in a stage a tile's codes and scales of K begin; those of V lie half a box behind
+    auto place = [&](int sub) -> uint2 {
+        const int row = sub * kTile, in_box = row & (box - 1);
+        const uint32_t at = (row >> w.log2_box) * box_bytes;
+        return make_uint2(at + in_box * (D / 2), at + box * (D / 2) + in_box * (D / 16));
+    };
+    uint2 own[J];  // of this warp's tiles, with eight rows a block the same in every stage
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+        own[j] = place(wk * J + j);
+    const unsigned all_boxes = (1u << (F::STEP >> w.log2_box)) - 1u;
+    const uint32_t half = box_bytes / 2;
+    const uint32_t k_codes = g_row * (D / 2) + c * (D / 8), k_scales = g_row * (D / 16) + k_scale_offset<D>(c);
+    uint32_t v_codes[2], v_scales[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        v_codes[r] = half + (v_row + (r ^ v_swap)) * (D / 2) + v_code_offset<D>(g);
+        v_scales[r] = half + (v_row + (r ^ v_swap)) * (D / 16) + v_scale_offset<D>(g);
+    }
+    // bytes of a key pair's P that a column of first (second) channels takes of the first and second key
+    const uint32_t of_first = g < 4 ? 0x4410u : 0x1044u, of_second = g < 4 ? 0x4432u : 0x3244u;
     bool fresh = true;   // some row may have no reference yet
     uint32_t unset = 0;  // ... a bit each of the thread's
     int slot = S - 1;
@@ -390,7 +415,8 @@ __global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
         if (!wait_warp(full(slot), phase, abort_flag))
             return;
         const Stage4 *info = meta + slot;
-        flags = info->flags;
+        const int2 what = *reinterpret_cast<const int2 *>(&info->flags);
+        flags = what.x;
 
         if (flags & kFirst) {
             const int b_seg = info->b;
@@ -408,7 +434,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
             int extra[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const int row = group * rows_block + wr * ROWS + nt * 8 + g;
+                const int row = group * rows_block + wr * (8 * NT) + nt * 8 + (PAIRS ? g & 3 : g);
                 const int hq = row / w.q.Nq, qi = row % w.q.Nq;
                 extra[nt] = w.q.causal ? qi : 0;
                 const T *src = static_cast<const T *>(w.q.q) + b_seg * w.q.batch_stride +
@@ -457,29 +483,34 @@ __global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
                     l[nt][u] = 0.f;
                 }
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j)
+                for (int j = 0; j < TILES; ++j)
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
                         acc[j][nt][u] = 0.f;
             }
         }
 
+        const uint32_t base = sbase + slot * F::STAGE;
         for (int set = wk; set < F::SUBS / J; set += key_warps) {
             // J tiles at once: one look at the reference, and twice the independent work
-            const int sub0 = set * J;
-            const bool last_set = set + key_warps >= F::SUBS / J;
+            const int sub0 = set * J, first = (what.y << F::LOG2_STEP) + sub0 * kTile;
+            const bool last_set = NT == 1 || set + key_warps >= F::SUBS / J;
             int key0[J];
-            uint32_t at[J];  // the tile's codes of K
-            int nearest = kNoKey, farthest = 0;
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                key0[j] = info->key0[sub0 + j];
-                nearest = min(nearest, key0[j]);
-                farthest = max(farthest, key0[j]);
-                const int row = (sub0 + j) * kTile;
-                at[j] = sbase + slot * F::STAGE + (row >> w.log2_box) * box_bytes + (row & (box - 1)) * (D / 2);
+            for (int j = 0; j < J; ++j)
+                key0[j] = first + j * kTile;
+            bool masked = first + J * kTile > least, some = first < most;
+            if (static_cast<unsigned>(flags) >> kBoxes != all_boxes) {  // the end, or a page with a bad number
+                masked = true;
+                some = false;
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    if (!(flags >> (kBoxes + ((sub0 + j) * kTile >> w.log2_box)) & 1))
+                        key0[j] = kNoKey;
+                    some |= key0[j] < most;
+                }
             }
-            if (nearest == kNoKey) {
+            if (!some) {
                 if (last_set) {
                     __syncwarp();
                     if (lane == 0)
@@ -487,47 +518,58 @@ __global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
                 }
                 continue;
             }
-            // from a tile's codes to its scales: the rest of the box's codes, and the scales before it
-            const uint32_t half = box_bytes / 2;
-            auto scales_of = [&](int j) -> uint32_t {
-                const int row = ((sub0 + j) * kTile) & (box - 1);
-                return at[j] + (box - row) * (D / 2) + row * (D / 16);
-            };
-            // ---- S^T = K Q^T ----
-            float e[J][NT][4];
+            uint32_t codes[J], scales[J];
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                uint32_t kw[2][D / 32], by[2][D / 32];
+                const uint2 at = NT == 1 ? own[j] : place(sub0 + j);
+                codes[j] = base + at.x;
+                scales[j] = base + at.y;
+            }
+            // ---- S^T = K Q^T ----
+            float e[J][NT][4];
+            {
+                uint32_t kw[J][2][D / 32], by[J][2][D / 32];
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    load_k<D>(at[j], scales_of(j), g_row + 8 * r, c, kw[r], by[r]);
+                for (int j = 0; j < J; ++j)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int r = 0; r < 2; ++r)
+                        load_k<D>(codes[j] + k_codes + r * (8 * D / 2), scales[j] + k_scales + r * (8 * D / 16), c, kw[j][r],
+                                  by[j][r]);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        e[j][nt][u] = 0.f;
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            e[j][nt][u] = 0.f;
 #pragma unroll
                 for (int x = 0; x < D / 32; ++x) {
-                    uint32_t h[2][4];
+                    uint32_t h[J][2][4];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        halves8(kw[r][x], h[r]);
+                    for (int j = 0; j < J; ++j)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            h[r][i] = times(h[r][i], by[r][x]);
-                    }
+                        for (int r = 0; r < 2; ++r) {
+                            halves8(kw[j][r][x], h[j][r]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                h[j][r][i] = times(h[j][r][i], by[j][r][x]);
+                        }
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const int s = 2 * x + y;
+                        uint32_t z[2 * NT];
                         if constexpr (NT == 1) {
-                            cache::mma_f16(e[j][0], h[0][2 * y], h[1][2 * y], h[0][2 * y + 1], h[1][2 * y + 1], qb[s][0],
-                                           qb[s][1]);
+                            z[0] = qb[s][0];
+                            z[1] = qb[s][1];
                         } else {
-                            uint32_t z[4];
                             cache::load_words<4>(z, q_own + s * 512);
-                            cache::mma_f16(e[j][0], h[0][2 * y], h[1][2 * y], h[0][2 * y + 1], h[1][2 * y + 1], z[0], z[1]);
-                            cache::mma_f16(e[j][1], h[0][2 * y], h[1][2 * y], h[0][2 * y + 1], h[1][2 * y + 1], z[2], z[3]);
                         }
+#pragma unroll
+                        for (int j = 0; j < J; ++j)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                cache::mma_f16(e[j][nt], h[j][0][2 * y], h[j][1][2 * y], h[j][0][2 * y + 1], h[j][1][2 * y + 1],
+                                               z[2 * nt], z[2 * nt + 1]);
                     }
                 }
             }
@@ -544,7 +586,6 @@ __global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
                         e[j][nt][u + 1] = x.y;
                     }
             }
-            const bool masked = farthest + kTile > least;
             if (masked) {
 #pragma unroll
                 for (int j = 0; j < J; ++j)
@@ -589,7 +630,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
                             e[j][nt][u + 2] -= up;
                         }
 #pragma unroll
-                        for (int j = 0; j < D / 16; ++j) {
+                        for (int j = 0; j < TILES; ++j) {
                             acc[j][nt][u] *= alpha;
                             acc[j][nt][u + 2] *= alpha;
                         }
@@ -619,7 +660,8 @@ __global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
                 uint32_t vw[4][VX], vs[4][VX];
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    load_v<D>(at[j] + half, scales_of(j) + half, (v_row + ((r & 1) ^ v_swap)) + 8 * (r >> 1), g, vw[r], vs[r]);
+                    load_v<D>(codes[j] + v_codes[r & 1] + (r >> 1) * (8 * D / 2), scales[j] + v_scales[r & 1] + (r >> 1) * (8 * D / 16), g,
+                              vw[r], vs[r]);
                 if (j == J - 1 && last_set) {  // the stage's bytes are in registers
                     __syncwarp();
                     if (lane == 0)
@@ -635,29 +677,54 @@ __global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
                             for (int x = 0; x < VX; ++x)
                                 vs[r][x] = 0;
                 }
-#pragma unroll
-                for (int x = 0; x < VX; ++x) {
-                    // the channels of a word, of keys 2 c and 2 c + 1, and of the two 8 behind them
-                    const bool half_word = x == VX - 1 && D % 64 != 0;
-                    uint32_t even[2][4], odd[2][4];
+                if constexpr (PAIRS) {
+                    // a pair's two channels as two terms of the product, each with the key's weight for its
+                    // own columns and 0 for the other's
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const uint32_t a = vw[2 * r][x], z = vw[2 * r + 1][x];
-                        const uint32_t by = (vs[2 * r][x] | vs[2 * r + 1][x] << 16) << 7;
-                        halves8((a & 0x0F0F0F0Fu) | (z << 4 & 0xF0F0F0F0u), even[r]);
-                        halves8((a >> 4 & 0x0F0F0F0Fu) | (z & 0xF0F0F0F0u), odd[r]);
+                        const uint32_t b0 = __byte_perm(pb[j][0][r], 0, of_first), b1 = __byte_perm(pb[j][0][r], 0, of_second);
 #pragma unroll
-                        for (int i = 0; i < (half_word ? 2 : 4); ++i) {
-                            even[r][i] = times(even[r][i], by);
-                            odd[r][i] = times(odd[r][i], by);
+                        for (int x = 0; x < VX; ++x) {
+                            const bool half_word = x == VX - 1 && D % 64 != 0;
+                            uint32_t h[2][4];
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                halves8(vw[2 * r + y][x], h[y]);
+#pragma unroll
+                                for (int i = 0; i < (half_word ? 2 : 4); ++i)
+                                    h[y][i] = times(h[y][i], vs[2 * r + y][x] * 0x800080u);
+                            }
+#pragma unroll
+                            for (int i = 0; i < (half_word ? 1 : 2); ++i)
+                                cache::mma_f16(acc[2 * x + i][0], h[0][2 * i], h[0][2 * i + 1], h[1][2 * i], h[1][2 * i + 1], b0,
+                                               b1);
                         }
                     }
+                } else {
 #pragma unroll
-                    for (int i = 0; i < (half_word ? 2 : 4); ++i)
+                    for (int x = 0; x < VX; ++x) {
+                        // the channels of a word, of keys 2 c and 2 c + 1, and of the two 8 behind them
+                        const bool half_word = x == VX - 1 && D % 64 != 0;
+                        uint32_t even[2][4], odd[2][4];
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            cache::mma_f16(acc[4 * x + i][nt], even[0][i], odd[0][i], even[1][i], odd[1][i], pb[j][nt][0],
-                                           pb[j][nt][1]);
+                        for (int r = 0; r < 2; ++r) {
+                            const uint32_t a = vw[2 * r][x], z = vw[2 * r + 1][x];
+                            const uint32_t by = vs[2 * r][x] * 0x80u + vs[2 * r + 1][x] * 0x800000u;
+                            halves8((a & 0x0F0F0F0Fu) | (z << 4 & 0xF0F0F0F0u), even[r]);
+                            halves8((a >> 4 & 0x0F0F0F0Fu) | (z & 0xF0F0F0F0u), odd[r]);
+#pragma unroll
+                            for (int i = 0; i < (half_word ? 2 : 4); ++i) {
+                                even[r][i] = times(even[r][i], by);
+                                odd[r][i] = times(odd[r][i], by);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < (half_word ? 2 : 4); ++i)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                cache::mma_f16(acc[4 * x + i][nt], even[0][i], odd[0][i], even[1][i], odd[1][i], pb[j][nt][0],
+                                               pb[j][nt][1]);
+                    }
                 }
             }
         }
@@ -685,17 +752,27 @@ __global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
                         mm[row] = unset >> (2 * nt + u) & 1u ? -INFINITY : m[nt][u];
                         ml[row] = sum;
                     }
+                    if constexpr (PAIRS) {
+                        // rows 2 (c & 1), + 1; channels: those of v_column, first ones at c < 2, second at c >= 2
+                        float *to = mo + (warp * 8 + 2 * (c & 1) + u) * F::OROW + (c >> 1);
 #pragma unroll
-                    for (int x = 0; x < VW; ++x)
-                        *reinterpret_cast<float4 *>(mo + row * F::OROW + cache::v_column<D>(g, x)) =
-                            make_float4(acc[2 * x][nt][u], acc[2 * x][nt][u + 2], acc[2 * x + 1][nt][u],
-                                        acc[2 * x + 1][nt][u + 2]);
+                        for (int x = 0; x < VW; ++x) {
+                            to[cache::v_column<D>(g, x)] = acc[x][0][u];
+                            to[cache::v_column<D>(g, x) + 2] = acc[x][0][u + 2];
+                        }
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < VW; ++x)
+                            *reinterpret_cast<float4 *>(mo + row * F::OROW + cache::v_column<D>(g, x)) =
+                                make_float4(acc[2 * x][nt][u], acc[2 * x][nt][u + 2], acc[2 * x + 1][nt][u],
+                                            acc[2 * x + 1][nt][u + 2]);
+                    }
                 }
                 if (!meet())
                     return;
                 for (int x = t; x < 8 * w.row_warps * (D / 4); x += 32 * F::WARPS) {
                     const int r8 = x / (D / 4), d = 4 * (x % (D / 4));
-                    const int row = r8 / 8 * ROWS + nt * 8 + r8 % 8;  // of the block
+                    const int row = r8 / 8 * (8 * NT) + nt * 8 + r8 % 8;  // of the block
                     const int abs_row = group * rows_block + row;
                     if (abs_row >= w.R)
                         continue;
