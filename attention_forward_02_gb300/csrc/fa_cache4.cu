@@ -30,31 +30,27 @@ Cache4State g_cache4[kMaxDevices];
 // Units of a segment that one block may take whole, as for the 8-bit cache.
 constexpr long long kWholeUnits = 8;
 
-// Warps of 4, 8 or 16 query rows; two 16-key tiles at once or, with sixteen rows of more
-// than 64 channels, where their registers would spill, one.
 template <int D, int ROWS, typename T>
 constexpr auto decode_kernel()
 {
-    return fa::cache4::fa_cache4_decode_kernel<D, ROWS, ROWS <= 8 || D <= 64 ? 2 : 1, T>;
+    return fa::cache4::fa_cache4_decode_kernel<D, ROWS, T>;
 }
 
-template <int D, typename T>
+template <int D, int ROWS>
 cudaError_t set_smem_attr()
 {
     const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    constexpr int bytes = fa::cache4::Dec4Cfg<D>::SMEM;
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, 4, T>(), a, bytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decode_kernel<D, 8, T>(), a, bytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decode_kernel<D, 16, T>(), a, bytes);
-    return e;
+    constexpr int bytes = fa::cache4::Dec4Cfg<D, ROWS>::SMEM;
+    const cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, ROWS, __half>(), a, bytes);
+    return e == cudaSuccess ? cudaFuncSetAttribute(decode_kernel<D, ROWS, __nv_bfloat16>(), a, bytes) : e;
 }
 template <int D>
 cudaError_t set_smem_attrs()
 {
-    const cudaError_t e = set_smem_attr<D, __half>();
-    return e == cudaSuccess ? set_smem_attr<D, __nv_bfloat16>() : e;
+    cudaError_t e = set_smem_attr<D, 4>();
+    if (e == cudaSuccess)
+        e = set_smem_attr<D, 8>();
+    return e == cudaSuccess ? set_smem_attr<D, 16>() : e;
 }
 
 void init_cache4(Cache4State &st)
@@ -174,10 +170,10 @@ fa_status_t fa_cache4_write(const fa_cache4_t *cache, const void *k, const void 
     const int tokens = fa::cache4::kWriteThreads / (cache->d / fa::cache4::kGroup);
     const dim3 grid((T + tokens - 1) / tokens, cache->heads);
     return by_type(dtype, [&](auto t) {
-        fa::cache4::fa_cache4_write_kernel<decltype(t)>
-            <<<grid, fa::cache4::kWriteThreads, 0, static_cast<cudaStream_t>(stream)>>>(device_cache(cache), rows, cache->d,
-                                                                                       st->status);
-        return launched();
+        return launch_dependent(fa::cache4::fa_cache4_write_kernel<decltype(t)>, grid, fa::cache4::kWriteThreads, 0,
+                                static_cast<cudaStream_t>(stream), device_cache(cache), rows, cache->d, st->status)
+                   ? launched()
+                   : FA_ERR_CUDA;
     });
 }
 
@@ -218,10 +214,11 @@ fa_status_t fa_cache4_read(const fa_cache4_t *cache, void *k, void *v, const int
     const Batch batch = {seq_lens, page_table, table_stride, max_pages, cache->num_pages, st->status};
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
-        fa::cache4::fa_cache4_read_kernel<T>
-            <<<dim3(static_cast<unsigned>(blocks), 2), fa::cache4::kReadThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-                device_cache(cache), batch, static_cast<T *>(k), static_cast<T *>(v), N, cache->d, static_cast<int>(chunks));
-        return launched();
+        return launch_dependent(fa::cache4::fa_cache4_read_kernel<T>, dim3(static_cast<unsigned>(blocks), 2),
+                                fa::cache4::kReadThreads, 0, static_cast<cudaStream_t>(stream), device_cache(cache), batch,
+                                static_cast<T *>(k), static_cast<T *>(v), N, cache->d, static_cast<int>(chunks))
+                   ? launched()
+                   : FA_ERR_CUDA;
     });
 }
 
@@ -292,41 +289,43 @@ fa_status_t fa_decode_cache4(const fa_cache4_t *cache, const void *q, long long 
     w.part_l = w.part_m + part_rows;
     return by_dim(cache->d, [&](auto dim) {
         constexpr int D = decltype(dim)::value;
-        using F = fa::cache4::Dec4Cfg<D>;
-        const int box = cache->page < F::STEP ? cache->page : F::STEP;
-        w.log2_box = box == 128 ? 7 : box == 64 ? 6 : box == 32 ? 5 : 4;
-        const long long segments = static_cast<long long>(B) * cache->heads * w.groups;
-        const long long units = (static_cast<long long>(max_pages) * cache->page - 1) / F::STEP + 1;  // of one, at most
-        long long blocks = static_cast<long long>(sms) * F::BLOCKS;
-        if (blocks > fa::cache::kMaxBlocks)
-            blocks = fa::cache::kMaxBlocks;
-        w.whole = units <= kWholeUnits && segments <= blocks;
-        if (w.whole)
-            blocks = segments;
-        else if (segments * units < blocks)
-            blocks = segments * units;
-        return by_type(dtype, [&](auto t) {
-            using T = decltype(t);
-            if (!launch_dependent(w.R <= 4              ? decode_kernel<D, 4, T>()
-                                  : shape.tiles == 1 ? decode_kernel<D, 8, T>()
-                                                     : decode_kernel<D, 16, T>(),
-                                  static_cast<unsigned>(blocks), F::THREADS, F::SMEM, cs, w,
-                                  static_cast<T *>(o), lse))
-                return FA_ERR_CUDA;
+        const auto with_rows = [&](auto warp_rows) {
+            constexpr int ROWS = decltype(warp_rows)::value;
+            using F = fa::cache4::Dec4Cfg<D, ROWS>;
+            const int box = cache->page < F::STEP ? cache->page : F::STEP;
+            w.log2_box = box == 128 ? 7 : box == 64 ? 6 : box == 32 ? 5 : 4;
+            const long long segments = static_cast<long long>(B) * cache->heads * w.groups;
+            const long long units = (static_cast<long long>(max_pages) * cache->page - 1) / F::STEP + 1;  // of one, at most
+            long long blocks = static_cast<long long>(sms) * F::BLOCKS;
+            if (blocks > fa::cache::kMaxBlocks)
+                blocks = fa::cache::kMaxBlocks;
+            w.whole = units <= kWholeUnits && segments <= blocks;
             if (w.whole)
+                blocks = segments;
+            else if (segments * units < blocks)
+                blocks = segments * units;
+            return by_type(dtype, [&](auto t) {
+                using T = decltype(t);
+                if (!launch_dependent(decode_kernel<D, ROWS, T>(), static_cast<unsigned>(blocks), F::THREADS, F::SMEM, cs, w,
+                                      static_cast<T *>(o), lse))
+                    return FA_ERR_CUDA;
+                if (w.whole)
+                    return launched();
+                constexpr int kWarps = fa::cache::kCombineThreads / 32;
+                const bool second =
+                    blocks <= segments * fa::cache::kCombineEach
+                        ? launch_dependent(fa::cache::fa_cache_combine_kernel<D, T, 1, F::LOG2_STEP, F::OPEN>,
+                                           static_cast<unsigned>((rows + kWarps - 1) / kWarps), fa::cache::kCombineThreads,
+                                           0, cs, w, static_cast<T *>(o), lse, rows_block, rows)
+                        : launch_dependent(fa::cache::fa_cache_combine_kernel<D, T, kWarps, F::LOG2_STEP, F::OPEN>,
+                                           static_cast<unsigned>(rows), fa::cache::kCombineThreads, 0, cs, w,
+                                           static_cast<T *>(o), lse, rows_block, rows);
+                if (!second)
+                    return FA_ERR_CUDA;
                 return launched();
-            constexpr int kWarps = fa::cache::kCombineThreads / 32;
-            const bool second =
-                blocks <= segments * fa::cache::kCombineEach
-                    ? launch_dependent(fa::cache::fa_cache_combine_kernel<D, T, 1, F::LOG2_STEP, F::OPEN>,
-                                       static_cast<unsigned>((rows + kWarps - 1) / kWarps), fa::cache::kCombineThreads, 0,
-                                       cs, w, static_cast<T *>(o), lse, rows_block, rows)
-                    : launch_dependent(fa::cache::fa_cache_combine_kernel<D, T, kWarps, F::LOG2_STEP, F::OPEN>, static_cast<unsigned>(rows),
-                                       fa::cache::kCombineThreads, 0, cs, w, static_cast<T *>(o), lse, rows_block, rows);
-            if (!second)
-                return FA_ERR_CUDA;
-            return launched();
-        });
+            });
+        };
+        return w.R <= 4 ? with_rows(Dim<4>()) : w.R <= 8 ? with_rows(Dim<8>()) : with_rows(Dim<16>());
     });
 }
 

@@ -35,8 +35,8 @@ using cache::kTailPart;
 using cache::kTile;
 using cache::Work;
 
-// As DecCfg of the 8-bit cache.
-template <int D>
+// As DecCfg of the 8-bit cache, for warps of ROWS query rows.
+template <int D, int ROWS>
 struct Dec4Cfg {
     static constexpr int LOG2_STEP = 7;
     static constexpr int STEP = 1 << LOG2_STEP;
@@ -44,10 +44,11 @@ struct Dec4Cfg {
     static constexpr int STAGE = STEP * D / 8 * 9;  // bytes
     static constexpr int WARPS = 4;              // that compute
     static constexpr int THREADS = 32 * (WARPS + 1);
-    static constexpr int BLOCKS = D == 32 ? 4 : 3;  // an SM
-    static constexpr int STAGES = D == 128 ? 3 : D == 96 ? 4 : 5;
+    static constexpr int BLOCKS = D == 32 ? 4 : D >= 96 && ROWS == 16 ? 2 : 3;  // an SM
+    static constexpr int STAGES = D == 128 && BLOCKS == 3 ? 3 : D == 96 && BLOCKS == 3 ? 4 : 5;
+    static constexpr int J = 2;                     // tiles of a warp at once
     static constexpr int OPEN = 2;                  // units that a segment's begin and end cost
-    static_assert(SUBS >= 2 * WARPS, "every warp has two tiles of a stage");
+    static_assert(SUBS >= J * WARPS, "every warp has tiles of a stage");
     static constexpr int OROW = D + 4;
     static constexpr int META_OFF = STAGES * STAGE;
     static constexpr int MERGE_OFF = META_OFF + STAGES * 32;
@@ -134,12 +135,12 @@ __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b)
     return *reinterpret_cast<const uint32_t *>(&x);
 }
 
-template <int D, int ROWS, int J, typename T>
-__global__ void __launch_bounds__(Dec4Cfg<D>::THREADS, Dec4Cfg<D>::BLOCKS)
+template <int D, int ROWS, typename T>
+__global__ void __launch_bounds__(Dec4Cfg<D, ROWS>::THREADS, Dec4Cfg<D, ROWS>::BLOCKS)
     fa_cache4_decode_kernel(const __grid_constant__ Work w, T *__restrict__ out, float *__restrict__ lse)
 {
-    using F = Dec4Cfg<D>;
-    constexpr int S = F::STAGES;
+    using F = Dec4Cfg<D, ROWS>;
+    constexpr int S = F::STAGES, J = F::J;
     constexpr int NT = ROWS == 16 ? 2 : 1;          // tiles of eight columns
     constexpr bool PAIRS = ROWS == 4;               // columns are four rows twice
     constexpr int KW = D / 16;                      // steps of the first product

@@ -158,6 +158,8 @@ __device__ __forceinline__ void write_block(const uint4 (&raw)[2], uint8_t *code
 template <typename T>
 __global__ void __launch_bounds__(kWriteThreads) fa_cache4_write_kernel(Cache4 cache, Rows4 in, int d, unsigned int *status)
 {
+    cache::wait_ahead();
+    cache::let_next();
     const int groups = d / kGroup;
     const int tokens = kWriteThreads / groups;
     const int lane = threadIdx.x / groups, g = threadIdx.x % groups;
@@ -200,6 +202,8 @@ __global__ void __launch_bounds__(kReadThreads)
     fa_cache4_read_kernel(Cache4 cache, Batch batch, T *__restrict__ k, T *__restrict__ v, int N, int d, int chunks)
 {
     // blockIdx.x = (b * heads + h) * chunks + chunk; y: K or V
+    cache::wait_ahead();
+    cache::let_next();
     const int which = blockIdx.y;
     const long long bh = blockIdx.x / chunks;
     const int chunk = blockIdx.x % chunks;

@@ -140,8 +140,16 @@ fa_status_t fa_cache_plan(const int *ring, int num_pages, const long long *count
     using namespace fa::pages;
     const Pool pool = {const_cast<int *>(ring), num_pages, counts, counts_out};
     const Lengths in = {seq_lens, new_lens, B, log2_of(page)};
-    fa_cache_plan_kernel<<<kBlocks, kThreads, smem_bytes(B), static_cast<cudaStream_t>(stream)>>>(
-        pool, in, page_table, table_stride, max_pages, cu_seqlens, ends, positions, slots, T, st->status);
+    const Rows rows = {positions, slots, T};
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (!launch_dependent(fa_cache_plan_kernel, 1, kThreads, smem_bytes(B), cs, pool, in, page_table, table_stride, max_pages,
+                          cu_seqlens, ends, rows, st->status))
+        return FA_ERR_CUDA;
+    constexpr int kPerBlock = kRowThreads * kRows;
+    if (T > kOwnRows &&
+        !launch_dependent(fa_cache_rows_kernel, static_cast<unsigned>((T + kPerBlock - 1ll) / kPerBlock), kRowThreads, 0, cs,
+                          in, page_table, table_stride, num_pages, cu_seqlens, ends, rows, st->status))
+        return FA_ERR_CUDA;
     return launched();
 }
 
@@ -171,9 +179,10 @@ fa_status_t fa_cache_trim(int *ring, int num_pages, const long long *counts, con
     using namespace fa::pages;
     const Pool pool = {ring, num_pages, counts, counts_out};
     const Lengths in = {seq_lens, keep_lens, B, log2_of(page)};
-    fa_cache_trim_kernel<<<kBlocks, kThreads, smem_bytes(B), static_cast<cudaStream_t>(stream)>>>(
-        pool, in, page_table, table_stride, max_pages, st->status);
-    return launched();
+    return launch_dependent(fa_cache_trim_kernel, 1, kThreads, smem_bytes(B), static_cast<cudaStream_t>(stream), pool,
+                            in, page_table, table_stride, max_pages, st->status)
+               ? launched()
+               : FA_ERR_CUDA;
 }
 
 }  // extern "C"

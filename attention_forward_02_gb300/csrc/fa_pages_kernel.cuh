@@ -4,20 +4,21 @@
 // need(b) = pages(len + n) - pages(len); prefix sums of n place a sequence's rows, those of
 // need its pages in the ring.  What bounds it is no traffic (8 bytes a row) but a chain:
 // lengths, two sums over the batch, then per row a search for its sequence, its page, its
-// slot.  So one launch of one cluster does all: every block takes the sums over the whole
-// batch by itself (a few words a thread), which costs less than a second launch, and the
-// rows and pages are shared out among the blocks.  The searches run in shared memory.
+// slot.  So one block does all of a step: sums over the batch, pages and, of up to kOwnRows
+// rows, positions and slots, by searches in shared memory.  More rows (prompts) go to a
+// second launch, which reads what the first has written.
 #pragma once
 
-#include "fa_common.cuh"
+#include "fa_cache_kernel.cuh"
 
 namespace fa {
 namespace pages {
 
-constexpr int kThreads = 512;
-constexpr int kBlocks = 8;  // one cluster
+constexpr int kThreads = 1024;
 constexpr int kMaxBatch = 16384;
-constexpr int kRows = 4;    // neighbouring rows a thread
+constexpr int kRows = 4;       // neighbouring rows a thread
+constexpr int kOwnRows = 4096;  // that the first launch takes
+constexpr int kRowThreads = 256;
 
 // Dynamic shared memory: [B + 1] first rows, [B] pages up to and with a sequence.
 inline __host__ __device__ size_t smem_bytes(int B) { return static_cast<size_t>(2 * B + 1) * 4; }
@@ -32,11 +33,26 @@ struct Lengths {
     const int *had, *other;  // tokens; new ones, or those to keep
     int B, log2_page;
 };
+struct Rows {
+    int *positions, *slots;
+    int T;
 
-__device__ __forceinline__ void cluster_meet()
-{
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
+    // Rows t0 .. t0 + kRows - 1 at once where they lie so.
+    __device__ void write(long long t0, const int (&p)[kRows], const int (&s)[kRows]) const
+    {
+        if (t0 + kRows <= T && ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slots)) & 15) == 0) {
+            *reinterpret_cast<int4 *>(positions + t0) = make_int4(p[0], p[1], p[2], p[3]);
+            *reinterpret_cast<int4 *>(slots + t0) = make_int4(s[0], s[1], s[2], s[3]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kRows; ++u)
+                if (t0 + u < T) {
+                    positions[t0 + u] = p[u];
+                    slots[t0 + u] = s[u];
+                }
+        }
+    }
+};
 
 // Inclusive sum over the block's threads of x, and the block's total.
 __device__ __forceinline__ long long block_scan(long long x, long long *warps, long long &total)
@@ -52,15 +68,19 @@ __device__ __forceinline__ long long block_scan(long long x, long long *warps, l
     if (lane == 31)
         warps[warp] = x;
     __syncthreads();
-    total = 0;
+    // every warp sums the warps' totals by itself
+    long long y = warps[lane];
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp)
-            x += warps[w];
-        total += warps[w];
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o)
+            y += z;
     }
-    return x;
+    total = __shfl_sync(0xffffffffu, y, 31);
+    const long long before = __shfl_sync(0xffffffffu, y, (warp + 31) & 31);
+    return warp ? x + before : x;
 }
+static_assert(kThreads == 1024, "a warp has a lane for each warp's total");
 
 // First i of [0, n) with a[i] > x; n if there is none.
 __device__ __forceinline__ int first_above(const int *a, int n, int x)
@@ -84,58 +104,59 @@ __device__ __forceinline__ long long pages_of(long long tokens, int log2_page)
     return (tokens + (1 << log2_page) - 1) >> log2_page;
 }
 
-// Free pages, and where in the ring the x-th of them lies.
+// Free pages, and where in the ring the x-th of them lies.  One thread divides.
 struct Ring {
-    int size;
     unsigned begin, end;  // places of the first page and of the first behind the last
-    int free;
-    bool bad;
-    __device__ explicit Ring(const Pool &p) : size(p.size)
+    int free, bad;
+    __device__ void read(const Pool &p)
     {
         const long long taken = p.counts[0], given = p.counts[1];
         bad = taken < 0 || given < taken || given - taken > p.size;
         free = bad ? 0 : static_cast<int>(given - taken);
         begin = bad ? 0 : static_cast<unsigned>(taken % p.size);
-        end = bad ? 0 : static_cast<unsigned>(given % p.size);
-    }
-    // x < size
-    __device__ int place(unsigned from, int x) const
-    {
-        const unsigned at = from + static_cast<unsigned>(x);
-        return static_cast<int>(at < static_cast<unsigned>(size) ? at : at - size);
+        end = begin + static_cast<unsigned>(free);
+        end = end < static_cast<unsigned>(p.size) ? end : end - p.size;
     }
 };
+// x < size
+__device__ __forceinline__ int place(int size, unsigned from, int x)
+{
+    const unsigned at = from + static_cast<unsigned>(x);
+    return static_cast<int>(at < static_cast<unsigned>(size) ? at : at - size);
+}
 
-__global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads)
-    fa_cache_plan_kernel(Pool pool, Lengths in, int *__restrict__ table, long long table_stride, int max_pages,
-                         int *__restrict__ cu_seqlens, int *__restrict__ ends, int *__restrict__ positions,
-                         int *__restrict__ slots, int T, unsigned int *status)
+__global__ void __launch_bounds__(kThreads)
+    fa_cache_plan_kernel(Pool pool, Lengths in, int *table, long long table_stride, int max_pages, int *cu_seqlens, int *ends,
+                         Rows rows, unsigned int *status)
 {
     extern __shared__ int smem[];
     __shared__ long long warps[kThreads / 32];
+    __shared__ Ring ring;
     __shared__ int taken_all;
     int *cu = smem, *until = smem + in.B + 1;
-    const int t = threadIdx.x, wide = kThreads * kBlocks;
-    const int mine = blockIdx.x * kThreads + t;
-    const Ring ring(pool);
+    const int t = threadIdx.x;
     const int log2_page = in.log2_page;
     const long long cap = static_cast<long long>(max_pages) << log2_page;
-    bool bad = ring.bad && mine == 0;
-    if (t == 0)
+    cache::wait_ahead();
+    cache::let_next();
+    if (t == kThreads - 1) {  // a thread that has no sequence in a batch of fewer
+        ring.read(pool);
         taken_all = 0;
+    }
     // this thread's sequences, one after the other
     const int each = (in.B + kThreads - 1) / kThreads;
     const int b0 = min(in.B, t * each), b1 = min(in.B, b0 + each);
-    long long rows = 0, total;
+    long long count = 0, total;
     for (int b = b0; b < b1; ++b)
-        rows += max(0, in.had[b] < 0 ? 0 : in.other[b]);
-    const long long first_row = block_scan(rows, warps, total) - rows;
+        count += in.had[b] < 0 ? 0 : max(0, in.other[b]);
+    const long long first_row = block_scan(count, warps, total) - count;
     const int all_rows = up_to(total);
+    bool bad = t == 0 && (ring.bad || total > 0x7fffffff);
     long long row = first_row, need = 0;
     auto needs = [&](int b, long long begin, int &n) -> long long {  // -1: it does not fit
         const long long had = in.had[b];
         n = had < 0 ? 0 : max(0, in.other[b]);
-        if (had < 0 || in.other[b] < 0 || had + n > cap || begin + n > T)
+        if (had < 0 || in.other[b] < 0 || had + n > cap || begin + n > rows.T)
             return -1;
         return pages_of(had + n, log2_page) - pages_of(had, log2_page);
     };
@@ -144,106 +165,171 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads)
         need += max(0ll, needs(b, row, n));
         row += n;
     }
-    long long pages = block_scan(need, warps, total) - need;
+    const long long first_page = block_scan(need, warps, total) - need;
+    long long pages = first_page;
     row = first_row;
     for (int b = b0; b < b1; ++b) {
         int n;
         const long long more = needs(b, row, n);
         pages += max(0ll, more);
         const bool served = more == 0 || (more > 0 && pages <= ring.free);
-        cu[b] = up_to(row);
+        cu[b] = cu_seqlens[b] = up_to(row);
         until[b] = up_to(pages);
         if (served && more > 0)
             atomicMax(&taken_all, until[b]);
-        if (b / each % kBlocks == blockIdx.x) {  // its outputs are this block's to write
-            cu_seqlens[b] = up_to(row);
-            ends[b] = served ? in.had[b] + n : in.had[b];
-            bad |= more < 0;
-        }
+        ends[b] = served ? in.had[b] + n : in.had[b];
+        bad |= more < 0;
         row += n;
     }
     if (t == 0)
-        cu[in.B] = all_rows;
-    if (mine == 0) {
-        cu_seqlens[in.B] = all_rows;
-        bad |= total > 0x7fffffff;
-    }
+        cu[in.B] = cu_seqlens[in.B] = all_rows;
     __syncthreads();
     const int taken = taken_all;
     // the pages taken: those of refused sequences come behind them
-    for (int j = mine; j < taken; j += wide) {
+    for (int j = t; j < taken; j += kThreads) {
         const int b = first_above(until, in.B, j);
         const int before = b > 0 ? until[b - 1] : 0;
         const long long at = pages_of(in.had[b], log2_page) + (j - before);
-        table[b * table_stride + at] = pool.ring[ring.place(ring.begin, j)];
+        table[b * table_stride + at] = pool.ring[place(pool.size, ring.begin, j)];
     }
-    // the rows
-    for (long long t0 = static_cast<long long>(mine) * kRows; t0 < T; t0 += static_cast<long long>(wide) * kRows) {
+    const int own = rows.T <= kOwnRows ? rows.T : 0;
+    for (long long t0 = static_cast<long long>(t) * kRows; t0 < own; t0 += kThreads * kRows) {
+        // their sequences and positions, then the pages of all of them at once, then their slots
         int b = t0 < all_rows ? first_above(cu + 1, in.B, static_cast<int>(t0)) : in.B;
         int p[kRows], s[kRows];
+        const int *from[kRows];
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
             const int at = static_cast<int>(t0) + u;  // behind T it is written nowhere
             p[u] = s[u] = -1;
+            from[u] = nullptr;
             while (b < in.B && at >= cu[b + 1])
                 ++b;
-            if (b >= in.B || t0 + u >= T)
+            if (b >= in.B || at >= rows.T)
                 continue;
             const long long had = in.had[b];
             const int before = b > 0 ? until[b - 1] : 0;
             const int n = cu[b + 1] - cu[b];
             // a row has a sequence with n > 0: it was refused if it did not fit, or its pages did not
-            if (had + n > cap || cu[b + 1] > T || (until[b] > before && until[b] > ring.free))
+            if (had + n > cap || cu[b + 1] > rows.T || (until[b] > before && until[b] > ring.free))
                 continue;
-            const int pos = static_cast<int>(had) + at - cu[b];
-            const long long column = pos >> log2_page, old = pages_of(had, log2_page);
-            const int page = column < old ? table[b * table_stride + column]
-                                          : pool.ring[ring.place(ring.begin, before + static_cast<int>(column - old))];
-            p[u] = pos;
-            if (page >= 0 && page < pool.size)
-                s[u] = (page << log2_page) + (pos & ((1 << log2_page) - 1));
-            else
-                bad = true;
+            p[u] = static_cast<int>(had) + at - cu[b];
+            const int column = p[u] >> log2_page, old = static_cast<int>(pages_of(had, log2_page));
+            from[u] = column < old ? table + b * table_stride + column
+                                   : pool.ring + place(pool.size, ring.begin, before + column - old);
         }
-        if (t0 + kRows <= T && ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slots)) & 15) == 0) {
-            *reinterpret_cast<int4 *>(positions + t0) = make_int4(p[0], p[1], p[2], p[3]);
-            *reinterpret_cast<int4 *>(slots + t0) = make_int4(s[0], s[1], s[2], s[3]);
-        } else {
+        int page[kRows];
 #pragma unroll
-            for (int u = 0; u < kRows; ++u)
-                if (t0 + u < T) {
-                    positions[t0 + u] = p[u];
-                    slots[t0 + u] = s[u];
-                }
-        }
+        for (int u = 0; u < kRows; ++u)
+            page[u] = from[u] ? *from[u] : 0;
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+            if (from[u]) {
+                if (page[u] >= 0 && page[u] < pool.size)
+                    s[u] = (page[u] << log2_page) + (p[u] & ((1 << log2_page) - 1));
+                else
+                    bad = true;
+            }
+        rows.write(t0, p, s);
     }
     if (bad)
         atomicOr(status, kStatusBounds);
-    const long long counts0 = pool.counts[0], counts1 = pool.counts[1];
-    cluster_meet();  // every block has read the counts, which may be the ones that are written
-    if (mine == 0) {
+    if (t == kThreads - 1) {  // which has read the counts, if they are the ones that are written
+        const long long counts0 = pool.counts[0], counts1 = pool.counts[1];
         pool.out[0] = counts0 + taken;
         pool.out[1] = counts1;
     }
 }
 
-__global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads)
-    fa_cache_trim_kernel(Pool pool, Lengths in, const int *__restrict__ table, long long table_stride, int max_pages,
+// The rows of more than kOwnRows, a warp 32 * kRows of them: from cu_seqlens, ends (a
+// sequence with new rows and no new end was refused) and the page table.
+__global__ void __launch_bounds__(kRowThreads)
+    fa_cache_rows_kernel(Lengths in, const int *table, long long table_stride, int num_pages, const int *cu_seqlens,
+                         const int *ends, Rows rows, unsigned int *status)
+{
+    cache::wait_ahead();
+    cache::let_next();
+    const int lane = threadIdx.x & 31;
+    const long long w0 = (static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5)) * (32 * kRows);
+    if (w0 >= rows.T)
+        return;
+    const int *until = cu_seqlens + 1;  // until[b]: the first row behind sequence b
+    // the sequences of the warp's first row and of its last: 32 borders a look
+    int lo[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int x = static_cast<int>(min(w0 + (i ? 32 * kRows - 1 : 0), static_cast<long long>(rows.T) - 1));
+        int n = in.B;  // first above x in [lo, lo + n], as first_above
+        while (n > 0) {
+            const int step = (n + 31) / 32, at = min(lane * step + step - 1, n - 1);
+            const unsigned above = __ballot_sync(0xffffffffu, until[lo[i] + at] > x);
+            if (!above) {
+                lo[i] += n;
+                break;
+            }
+            const int first = __ffs(above) - 1;  // the border is in this lane's step, before its last
+            const int left = first * step, right = min(left + step - 1, n - 1);
+            lo[i] += left;
+            n = right - left;
+        }
+    }
+    const long long t0 = w0 + lane * kRows;
+    if (t0 >= rows.T)
+        return;
+    int b = lo[0] + first_above(until + lo[0], lo[1] - lo[0], static_cast<int>(t0));
+    int p[kRows], s[kRows];
+    const int *from[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+        const int at = static_cast<int>(t0) + u;
+        p[u] = s[u] = -1;
+        from[u] = nullptr;
+        while (b < in.B && at >= until[b])
+            ++b;
+        if (b >= in.B || at >= rows.T)
+            continue;
+        const int had = in.had[b];
+        if (ends[b] == had)
+            continue;
+        p[u] = had + at - cu_seqlens[b];
+        from[u] = table + b * table_stride + (p[u] >> in.log2_page);
+    }
+    int page[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+        page[u] = from[u] ? *from[u] : 0;
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+        if (from[u]) {
+            if (page[u] >= 0 && page[u] < num_pages)
+                s[u] = (page[u] << in.log2_page) + (p[u] & ((1 << in.log2_page) - 1));
+            else
+                bad = true;
+        }
+    rows.write(t0, p, s);
+    if (bad)
+        atomicOr(status, kStatusBounds);
+}
+
+__global__ void __launch_bounds__(kThreads)
+    fa_cache_trim_kernel(Pool pool, Lengths in, const int *table, long long table_stride, int max_pages,
                          unsigned int *status)
 {
     extern __shared__ int smem[];
     __shared__ long long warps[kThreads / 32];
+    __shared__ Ring ring;
     __shared__ int back_all;
     int *until = smem;
-    const int t = threadIdx.x, wide = kThreads * kBlocks;
-    const int mine = blockIdx.x * kThreads + t;
-    const Ring ring(pool);
+    const int t = threadIdx.x;
     const int log2_page = in.log2_page;
     const long long cap = static_cast<long long>(max_pages) << log2_page;
-    const int room = ring.bad ? 0 : ring.size - ring.free;
-    bool bad = ring.bad && mine == 0;
-    if (t == 0)
+    cache::wait_ahead();
+    cache::let_next();
+    if (t == kThreads - 1) {
+        ring.read(pool);
         back_all = 0;
+    }
     const int each = (in.B + kThreads - 1) / kThreads;
     const int b0 = min(in.B, t * each), b1 = min(in.B, b0 + each);
     auto gives = [&](int b) -> long long {  // -1: lengths that are none
@@ -254,29 +340,29 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads)
     for (int b = b0; b < b1; ++b)
         sum += max(0ll, gives(b));
     long long pages = block_scan(sum, warps, total) - sum;
+    const int room = ring.bad ? 0 : pool.size - ring.free;
+    bool bad = t == 0 && ring.bad;
     for (int b = b0; b < b1; ++b) {
         const long long n = gives(b);
         pages += max(0ll, n);
         until[b] = up_to(pages);
         if (n > 0 && pages <= room)
             atomicMax(&back_all, until[b]);
-        if (mine == t)
-            bad |= n < 0 || (n > 0 && pages > room);
+        bad |= n < 0 || (n > 0 && pages > room);
     }
     __syncthreads();
     const int back = back_all;
-    for (int j = mine; j < back; j += wide) {
+    for (int j = t; j < back; j += kThreads) {
         const int b = first_above(until, in.B, j);
         const int before = b > 0 ? until[b - 1] : 0;
         const int page = table[b * table_stride + pages_of(in.other[b], log2_page) + (j - before)];
         bad |= page < 0 || page >= pool.size;
-        pool.ring[ring.place(ring.end, j)] = page;
+        pool.ring[place(pool.size, ring.end, j)] = page;
     }
     if (bad)
         atomicOr(status, kStatusBounds);
-    const long long counts0 = pool.counts[0], counts1 = pool.counts[1];
-    cluster_meet();  // every block has read the counts, which may be the ones that are written
-    if (mine == 0) {
+    if (t == kThreads - 1) {
+        const long long counts0 = pool.counts[0], counts1 = pool.counts[1];
         pool.out[0] = counts0;
         pool.out[1] = counts1 + back;
     }

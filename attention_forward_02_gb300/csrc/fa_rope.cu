@@ -7,14 +7,13 @@
 #include <cstdint>
 
 #include "fa.h"
+#include "fa_cache_host.h"
 #include "fa_host.h"
 #include "fa_rope_kernel.cuh"
 
 namespace {
 
-using fa_host::overlaps;
-
-uintptr_t u(const void *p) { return reinterpret_cast<uintptr_t>(p); }
+using namespace fa_host;
 
 // A tensor of rows: its address, and (stride, extent) of batch, rows and heads.
 struct View {
@@ -101,16 +100,12 @@ fa_status_t check_rows(fa_rope_rows_t &r, int B, int N, int d, View *x, View *y)
 }
 
 template <typename T>
-void launch(bool interleaved, const fa::rope::Rows &q, const fa::rope::Rows &k, const fa::rope::Turn &turn,
+bool launch(bool interleaved, const fa::rope::Rows &q, const fa::rope::Rows &k, const fa::rope::Turn &turn,
             const int *positions, long long stride, int N, int units, int slots, unsigned threads, cudaStream_t stream)
 {
     const unsigned blocks = (threads + fa::rope::kThreads - 1) / fa::rope::kThreads;
-    if (interleaved)
-        fa::rope::fa_rope_kernel<T, true>
-            <<<blocks, fa::rope::kThreads, 0, stream>>>(q, k, turn, positions, stride, N, units, slots, threads);
-    else
-        fa::rope::fa_rope_kernel<T, false>
-            <<<blocks, fa::rope::kThreads, 0, stream>>>(q, k, turn, positions, stride, N, units, slots, threads);
+    return launch_dependent(interleaved ? fa::rope::fa_rope_kernel<T, true> : fa::rope::fa_rope_kernel<T, false>, blocks,
+                            fa::rope::kThreads, 0, stream, q, k, turn, positions, stride, N, units, slots, threads);
 }
 
 }  // namespace
@@ -172,11 +167,12 @@ fa_status_t fa_rope(const fa_rope_t *rope, const fa_rope_rows_t *q, const fa_rop
     const fa::rope::Turn turn = {rope->turns, rope->pairs, rope->factor, backward == 1};
     const unsigned threads = static_cast<unsigned>(rows_units * slots);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (dtype == FA_FP16)
-        launch<__half>(rope->interleaved, r[0], r[1], turn, positions, position_stride, N, d / 8, slots, threads, cs);
-    else
-        launch<__nv_bfloat16>(rope->interleaved, r[0], r[1], turn, positions, position_stride, N, d / 8, slots, threads, cs);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    const bool done =
+        dtype == FA_FP16
+            ? launch<__half>(rope->interleaved, r[0], r[1], turn, positions, position_stride, N, d / 8, slots, threads, cs)
+            : launch<__nv_bfloat16>(rope->interleaved, r[0], r[1], turn, positions, position_stride, N, d / 8, slots, threads,
+                                    cs);
+    return done ? launched() : FA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -12,7 +12,7 @@
 // angle and fp64 would be slow.  Its upper 32 bits, in half turns, go to sincospif.
 #pragma once
 
-#include "fa_common.cuh"
+#include "fa_cache_kernel.cuh"
 
 namespace fa {
 namespace rope {
@@ -38,9 +38,11 @@ struct Turn {
 // channels, or, interleaved, of pairs 0, 1 and 2, 3.
 template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads)
-    fa_rope_kernel(Rows q, Rows k, Turn turn, const int *__restrict__ positions, long long position_stride, int N,
+    fa_rope_kernel(Rows q, Rows k, Turn turn, const int *positions, long long position_stride, int N,
                    int units, int slots, unsigned threads)
 {
+    cache::wait_ahead();
+    cache::let_next();
     const unsigned i = blockIdx.x * kThreads + threadIdx.x;
     if (i >= threads)
         return;
