@@ -7,7 +7,7 @@ encoder is fetched through the runtime's driver entry-point query).  The same
 units are compiled a second time with FA_BOUNDS_CHECK into the checked
 build (libfa_gb300_checked.so, device-side address checks; a test build).  All
 of them compile in parallel, and beside them, with g++, the small CPython module
-that shortens the host's way to the cache's entry points (fa_cache_py.cpp).
+that shortens the host's way to the entry points around the caches (fa_cache_py.cpp).
 """
 import os
 import shutil

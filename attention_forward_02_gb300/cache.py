@@ -91,7 +91,9 @@ def _quick():
         if _module:
             _module.bind(*(cast(f, c_void_p).value for f in (
                 lib.fa_cache_write, lib.fa_cache_read, lib.fa_decode_cache, lib.fa_decode_cache_workspace_size,
-                lib.fa_cache_select, lib.fa_cache_select_workspace_size)))
+                lib.fa_cache_select, lib.fa_cache_select_workspace_size, lib.fa_cache4_write, lib.fa_cache4_read,
+                lib.fa_decode_cache4, lib.fa_decode_cache4_workspace_size, lib.fa_cache_plan, lib.fa_cache_trim,
+                lib.fa_rope)))
         _bound = lib
     return _module
 

@@ -16,7 +16,7 @@ import torch
 
 from ._lib import (FAError, fa_cache4_read_raw, fa_cache4_write_raw, fa_decode_cache4_raw,
                    fa_decode_cache4_workspace_size)
-from .cache import _CODES, _check_batch, _code, _elsewhere, _int, _output, _stream, _there, _workspace
+from .cache import _CODES, _check_batch, _code, _elsewhere, _int, _output, _quick, _stream, _there, _workspace
 
 
 class FACache4(NamedTuple):
@@ -63,6 +63,12 @@ def _describe(cache):
 def fa_cache4_write(cache, k, v, slots, stream=None):
     """Write rows k, v [T, heads, d] (any strides that keep rows of d contiguous) to slots [T] (int32: page
     number * page + place in the page, as ``fa_cache_plan`` gives them; rows with a negative one are left out)."""
+    if stream is None and type(cache) is FACache4 and (quick := _quick()):
+        done = quick.write4(cache, k, v, slots)
+        if done is not None:
+            if done:
+                raise FAError(done, "fa_cache4_write")
+            return
     desc, heads, d, index = _describe(cache)
     if _elsewhere(index, stream):
         with _there(index, stream):
@@ -84,6 +90,14 @@ def fa_cache4_read(cache, page_table, seq_lens, N, dtype=torch.bfloat16, k=None,
     """The first N positions of every sequence as 16-bit k, v [B, heads, N, d], exact in either type, zeros behind
     seq_lens[b] (which are no mask: attention that sees them counts them as keys of score 0).
     k, v: optional preallocated outputs (their dtype counts then).  Returns (k, v)."""
+    if stream is None and type(cache) is FACache4 and dtype in _CODES and (quick := _quick()):
+        given = k if k is not None else v
+        done = quick.read4(cache, page_table, seq_lens, N,
+                           (dtype if given is None else getattr(given, "dtype", None)) is torch.float16, k, v)
+        if type(done) is tuple:
+            return done
+        if done is not None:
+            raise FAError(done, "fa_cache4_read")
     desc, heads, d, index = _describe(cache)
     if _elsewhere(index, stream):
         with _there(index, stream):
@@ -113,6 +127,13 @@ def fa_decode_cache4(q, cache, page_table, seq_lens, o=None, lse=None, scale=Non
     keep rows contiguous) to the cache; seq_lens counts the queries' own tokens.  causal puts the queries at the
     end of the sequence.  scale defaults to 1/sqrt(d).  Returns (o, lse); a row without keys has o = 0,
     lse = -inf."""
+    if stream is None and type(cache) is FACache4 and (quick := _quick()):
+        done = quick.decode4(q, cache, page_table, seq_lens, o, lse, scale if scale is None else float(scale),
+                             True if causal else False, True if return_lse else False, workspace)
+        if type(done) is tuple:
+            return done
+        if done is not None:
+            raise FAError(done, "fa_decode_cache4")
     desc, heads, d, index = _describe(cache)
     if _elsewhere(index, stream):
         with _there(index, stream):

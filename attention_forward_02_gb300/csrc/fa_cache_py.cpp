@@ -1,9 +1,9 @@
-// fa_cache_py.cpp -- the usual call of the 8-bit cache's Python functions, in
-// C++: the same checks as attention_forward_02_gb300/cache.py, the outputs'
-// allocation and the call of the C ABI.  A call that is anything but usual (a
-// stream of its own, another device than the current one, an argument that does
-// not pass) is handed back, and cache.py goes through it, which also words the
-// error.  What it saves is time on the host, which is most of a small call: a
+// fa_cache_py.cpp -- the usual call of the paged caches', the page plan's and the
+// rotary positions' Python functions, in C++: the same checks as cache.py, cache4.py,
+// pages.py and rope.py of the package, the outputs' allocation and the call of the C
+// ABI.  A call that is anything but usual (a stream of its own, another device than the
+// current one, an argument that does not pass) is handed back, and the Python function
+// goes through it, which also words the error.  What it saves is time on the host, which is most of a small call: a
 // fa_decode_cache of one sequence of 500 keys takes 9.7 us in place of 26 (8.4 of
 // them on the GPU), a fa_cache_write of one token 4.2 in place of 12, a choice of
 // pages and the attention over them 22 in place of 55.
@@ -33,6 +33,13 @@ struct Library {
     decltype(&fa_decode_cache_workspace_size) decode_workspace;
     decltype(&fa_cache_select) select;
     decltype(&fa_cache_select_workspace_size) select_workspace;
+    decltype(&fa_cache4_write) write4;
+    decltype(&fa_cache4_read) read4;
+    decltype(&fa_decode_cache4) decode4;
+    decltype(&fa_decode_cache4_workspace_size) decode4_workspace;
+    decltype(&fa_cache_plan) plan;
+    decltype(&fa_cache_trim) trim;
+    decltype(&fa_rope) rope;
 };
 Library lib = {};
 
@@ -325,23 +332,286 @@ PyObject *py_select(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
-// bind(write, read, decode, decode_workspace_size, select, select_workspace_size): their addresses
+bool describe4(PyObject *cache, int device, fa_cache4_t &c)
+{
+    if (!PyTuple_Check(cache) || PyTuple_GET_SIZE(cache) != 1)
+        return false;
+    const Tensor *t = plain(PyTuple_GET_ITEM(cache, 0), device);
+    if (!t || t->dim() != 4 || t->scalar_type() != at::kByte || !t->is_contiguous() || t->size(3) % 36 != 0 ||
+        !to_int(t->size(0), c.num_pages) || !to_int(t->size(1), c.heads) || !to_int(t->size(2), c.page) ||
+        !to_int(t->size(3) / 9 * 8, c.d))
+        return false;
+    c.data = t->data_ptr();
+    return true;
+}
+
+// write4(cache, k, v, slots)
+PyObject *py_write4(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        if (n != 4 || !lib.write4)
+            return handed_back();
+        const int device = c10::cuda::current_device();
+        fa_cache4_t c;
+        fa_dtype_t type, vtype;
+        int T;
+        if (!describe4(a[0], device, c))
+            return handed_back();
+        const Tensor *k = rows(a[1], device, 3, c.d, type), *v = rows(a[2], device, 3, c.d, vtype);
+        if (!k || !v || type != vtype || k->sizes() != v->sizes() || k->size(1) != c.heads || !to_int(k->size(0), T))
+            return handed_back();
+        const Tensor *slots = exact(a[3], device, at::kInt, {k->size(0)});
+        if (!slots)
+            return handed_back();
+        return PyLong_FromLong(lib.write4(&c, k->data_ptr(), v->data_ptr(), k->stride(0), k->stride(1), v->stride(0),
+                                          v->stride(1), static_cast<const int *>(slots->data_ptr()), T, type,
+                                          stream_of(device)));
+    });
+}
+
+// read4(cache, page_table, seq_lens, N, fp16?, k, v)
+PyObject *py_read4(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        if (n != 7 || !lib.read4 || !PyLong_Check(a[3]))
+            return handed_back();
+        const int device = c10::cuda::current_device();
+        fa_cache4_t c;
+        Batch b;
+        int N;
+        if (!describe4(a[0], device, c) || !describe_batch(a[1], a[2], device, b) || !to_int(PyLong_AsLongLong(a[3]), N)) {
+            PyErr_Clear();
+            return handed_back();
+        }
+        const fa_dtype_t type = a[4] == Py_True ? FA_FP16 : FA_BF16;
+        const int64_t shape[4] = {b.B, c.heads, N, c.d};
+        Tensor k, v;
+        if (!output(a[5], shape, scalar_of(type), device, k) || !output(a[6], shape, scalar_of(type), device, v))
+            return handed_back();
+        const fa_status_t s = lib.read4(&c, k.data_ptr(), v.data_ptr(), b.lens, b.table, b.stride, b.pages, b.B, N, type,
+                                        stream_of(device));
+        if (s != FA_OK)
+            return PyLong_FromLong(s);
+        PyObject *pk = a[5] == Py_None ? THPVariable_Wrap(k) : Py_NewRef(a[5]);
+        PyObject *pv = a[6] == Py_None ? THPVariable_Wrap(v) : Py_NewRef(a[6]);
+        return Py_BuildValue("(NN)", pk, pv);
+    });
+}
+
+// decode4(q, cache, page_table, seq_lens, o, lse, scale, causal, return_lse, workspace)
+PyObject *py_decode4(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        if (n != 10 || !lib.decode4 || (a[6] != Py_None && !PyFloat_Check(a[6])) || !PyBool_Check(a[7]) ||
+            !PyBool_Check(a[8]))
+            return handed_back();
+        const int device = c10::cuda::current_device();
+        fa_cache4_t c;
+        Batch b;
+        fa_dtype_t type;
+        int Hq, Nq;
+        if (!describe4(a[1], device, c) || !describe_batch(a[2], a[3], device, b))
+            return handed_back();
+        const Tensor *q = rows(a[0], device, 4, c.d, type);
+        if (!q || q->size(0) != b.B || !to_int(q->size(1), Hq) || !to_int(q->size(2), Nq) || c.heads < 1 || Hq % c.heads)
+            return handed_back();
+        const double scale = a[6] == Py_None ? 1.0 / std::sqrt(static_cast<double>(c.d)) : PyFloat_AS_DOUBLE(a[6]);
+        const int64_t shape[4] = {b.B, Hq, Nq, c.d};
+        Tensor o, lse, ws;
+        if (!output(a[4], shape, q->scalar_type(), device, o))
+            return handed_back();
+        const bool with_lse = a[5] != Py_None || a[8] == Py_True;
+        if (with_lse && !output(a[5], at::IntArrayRef(shape, 3), at::kFloat, device, lse))
+            return handed_back();
+        if (!workspace_of(a[9], lib.decode4_workspace(b.B, Hq, c.heads, Nq, c.d), device, ws))
+            return handed_back();
+        const fa_status_t s =
+            lib.decode4(&c, q->data_ptr(), q->stride(0), q->stride(1), q->stride(2), o.data_ptr(),
+                        with_lse ? static_cast<float *>(lse.data_ptr()) : nullptr, b.lens, b.table, b.stride, b.pages,
+                        ws.data_ptr(), ws.nbytes(), b.B, Hq, Nq, static_cast<float>(scale), a[7] == Py_True, type,
+                        stream_of(device));
+        if (s != FA_OK)
+            return PyLong_FromLong(s);
+        PyObject *po = a[4] == Py_None ? THPVariable_Wrap(o) : Py_NewRef(a[4]);
+        PyObject *pl = !with_lse ? Py_NewRef(Py_None) : a[5] == Py_None ? THPVariable_Wrap(lse) : Py_NewRef(a[5]);
+        return Py_BuildValue("(NN)", po, pl);
+    });
+}
+
+// The pool of a plan or a trim, their lengths, and where the counts go.
+struct PoolArgs {
+    Tensor ring, counts, out;
+    Batch b;
+    const Tensor *other;
+    int num_pages, page;
+};
+
+bool describe_pool(PyObject *pool, PyObject *table, PyObject *lens, PyObject *other, PyObject *page, PyObject *out, int device,
+                   PoolArgs &x)
+{
+    if (!PyTuple_Check(pool) || PyTuple_GET_SIZE(pool) != 2 || !PyLong_Check(page))
+        return false;
+    const Tensor *ring = plain(PyTuple_GET_ITEM(pool, 0), device);
+    const Tensor *counts = exact(PyTuple_GET_ITEM(pool, 1), device, at::kLong, {2});
+    const Tensor *to = out == Py_None ? counts : exact(out, device, at::kLong, {2});
+    if (!ring || !counts || !to || ring->dim() != 1 || ring->scalar_type() != at::kInt || !ring->is_contiguous() ||
+        !to_int(ring->size(0), x.num_pages) || !to_int(PyLong_AsLongLong(page), x.page) ||
+        !describe_batch(table, lens, device, x.b))
+        return false;
+    x.other = exact(other, device, at::kInt, {x.b.B});
+    if (!x.other)
+        return false;
+    x.ring = *ring;
+    x.counts = *counts;
+    x.out = *to;
+    return true;
+}
+
+// plan(pool, page_table, seq_lens, new_lens, page, T, counts): the four tensors of a new plan
+PyObject *py_plan(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        if (n != 7 || !lib.plan || !PyLong_Check(a[5]))
+            return handed_back();
+        const int device = c10::cuda::current_device();
+        PoolArgs x;
+        int T;
+        if (!describe_pool(a[0], a[1], a[2], a[3], a[4], a[6], device, x) || !to_int(PyLong_AsLongLong(a[5]), T) ||
+            x.b.B == 0) {
+            PyErr_Clear();
+            return handed_back();
+        }
+        Tensor cu = empty({x.b.B + 1ll}, at::kInt, device), ends = empty({x.b.B}, at::kInt, device);
+        Tensor positions = empty({T}, at::kInt, device), slots = empty({T}, at::kInt, device);
+        auto ints = [](const Tensor &t) { return static_cast<int *>(t.data_ptr()); };
+        const fa_status_t s =
+            lib.plan(ints(x.ring), x.num_pages, static_cast<const long long *>(x.counts.data_ptr()),
+                     const_cast<int *>(x.b.table), x.b.stride, x.b.pages, x.b.lens, ints(*x.other), ints(cu), ints(ends),
+                     ints(positions), ints(slots), static_cast<long long *>(x.out.data_ptr()), x.page, x.b.B, T,
+                     stream_of(device));
+        if (s != FA_OK)
+            return PyLong_FromLong(s);
+        return Py_BuildValue("(NNNN)", THPVariable_Wrap(cu), THPVariable_Wrap(ends), THPVariable_Wrap(positions),
+                             THPVariable_Wrap(slots));
+    });
+}
+
+// trim(pool, page_table, seq_lens, keep_lens, page, counts)
+PyObject *py_trim(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        if (n != 6 || !lib.trim)
+            return handed_back();
+        const int device = c10::cuda::current_device();
+        PoolArgs x;
+        if (!describe_pool(a[0], a[1], a[2], a[3], a[4], a[5], device, x)) {
+            PyErr_Clear();
+            return handed_back();
+        }
+        return PyLong_FromLong(lib.trim(static_cast<int *>(x.ring.data_ptr()), x.num_pages,
+                                        static_cast<const long long *>(x.counts.data_ptr()), x.b.table, x.b.stride,
+                                        x.b.pages, x.b.lens, static_cast<const int *>(x.other->data_ptr()),
+                                        static_cast<long long *>(x.out.data_ptr()), x.page, x.b.B, stream_of(device)));
+    });
+}
+
+// rope(q, k, rope, positions, backward, q_out, k_out): (q, k) turned
+PyObject *py_rope(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        if (n != 7 || !lib.rope || !PyTuple_Check(a[2]) || PyTuple_GET_SIZE(a[2]) != 3 || !PyBool_Check(a[4]))
+            return handed_back();
+        const int device = c10::cuda::current_device();
+        const Tensor *turns = plain(PyTuple_GET_ITEM(a[2], 0), device);
+        PyObject *interleaved = PyTuple_GET_ITEM(a[2], 1), *factor = PyTuple_GET_ITEM(a[2], 2);
+        fa_rope_t rope;
+        if (!turns || turns->dim() != 1 || turns->scalar_type() != at::kLong || !turns->is_contiguous() ||
+            !PyBool_Check(interleaved) || !PyFloat_Check(factor) || !to_int(turns->size(0), rope.pairs))
+            return handed_back();
+        rope.turns = static_cast<const unsigned long long *>(turns->data_ptr());
+        rope.interleaved = interleaved == Py_True;
+        rope.factor = static_cast<float>(PyFloat_AS_DOUBLE(factor));
+        const Tensor *x[2] = {plain(a[0], device), a[1] == Py_None ? nullptr : plain(a[1], device)};
+        if (!x[0] || (x[0]->dim() != 3 && x[0]->dim() != 4) || (a[1] == Py_None ? a[6] != Py_None : !x[1]))
+            return handed_back();
+        const int dim = static_cast<int>(x[0]->dim()), tokens = dim == 3 ? 0 : 2;
+        const int64_t d = x[0]->size(dim - 1);
+        int B = 1, N, width;
+        if (!to_int(x[0]->size(tokens), N) || (dim == 4 && !to_int(x[0]->size(0), B)) || !to_int(d, width))
+            return handed_back();
+        fa_rope_rows_t r[2];
+        Tensor y[2];
+        fa_dtype_t type = FA_FP16;
+        for (int i = 0; i < (x[1] ? 2 : 1); ++i) {
+            fa_dtype_t own;
+            const Tensor *t = rows(a[i], device, dim, width, own);
+            if (!t || (i && (own != type || t->size(0) != x[0]->size(0) || t->size(tokens) != N)))
+                return handed_back();
+            type = own;
+            PyObject *given = a[5 + i];
+            if (given == Py_None) {
+                y[i] = empty(t->sizes(), t->scalar_type(), device);
+            } else {
+                fa_dtype_t as;
+                const Tensor *o = rows(given, device, dim, width, as);
+                if (!o || as != own || o->sizes() != t->sizes())
+                    return handed_back();
+                y[i] = *o;
+            }
+            r[i].x = t->data_ptr();
+            r[i].y = y[i].data_ptr();
+            r[i].x_batch = dim == 4 ? t->stride(0) : 0;
+            r[i].y_batch = dim == 4 ? y[i].stride(0) : 0;
+            r[i].x_head = t->stride(1);
+            r[i].y_head = y[i].stride(1);
+            r[i].x_row = t->stride(tokens);
+            r[i].y_row = y[i].stride(tokens);
+            if (!to_int(t->size(1), r[i].heads))
+                return handed_back();
+        }
+        const int *positions = nullptr;
+        int64_t stride = 0;
+        if (a[3] != Py_None) {
+            const Tensor *p = plain(a[3], device);
+            if (!p || p->scalar_type() != at::kInt || p->dim() < 1 || p->dim() > dim - 2 || p->size(p->dim() - 1) != N ||
+                (p->dim() == 2 && p->size(0) != B) || (p->stride(p->dim() - 1) != 1 && N > 1))
+                return handed_back();
+            positions = static_cast<const int *>(p->data_ptr());
+            stride = p->dim() == 2 ? p->stride(0) : 0;
+        }
+        const fa_status_t s = lib.rope(&rope, &r[0], x[1] ? &r[1] : nullptr, positions, stride, B, N, width, a[4] == Py_True,
+                                       type, stream_of(device));
+        if (s != FA_OK)
+            return PyLong_FromLong(s);
+        PyObject *pq = a[5] == Py_None ? THPVariable_Wrap(y[0]) : Py_NewRef(a[5]);
+        PyObject *pk = !x[1] ? Py_NewRef(Py_None) : a[6] == Py_None ? THPVariable_Wrap(y[1]) : Py_NewRef(a[6]);
+        return Py_BuildValue("(NN)", pq, pk);
+    });
+}
+
+// bind(the library's functions' addresses, in the order of Library)
+constexpr int kFunctions = 13;
+static_assert(sizeof(Library) == kFunctions * sizeof(void *), "an address each");
 PyObject *py_bind(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    void *p[6];
-    if (n != 6) {
-        PyErr_SetString(PyExc_TypeError, "six addresses");
+    void *p[kFunctions];
+    if (n != kFunctions) {
+        PyErr_SetString(PyExc_TypeError, "an address for each function");
         return nullptr;
     }
-    for (int i = 0; i < 6; ++i)
+    for (int i = 0; i < kFunctions; ++i)
         if (!(p[i] = PyLong_AsVoidPtr(a[i]))) {
             if (!PyErr_Occurred())
                 PyErr_SetString(PyExc_ValueError, "an address is zero");
             return nullptr;
         }
-    lib = {reinterpret_cast<decltype(lib.write)>(p[0]),  reinterpret_cast<decltype(lib.read)>(p[1]),
-           reinterpret_cast<decltype(lib.decode)>(p[2]), reinterpret_cast<decltype(lib.decode_workspace)>(p[3]),
-           reinterpret_cast<decltype(lib.select)>(p[4]), reinterpret_cast<decltype(lib.select_workspace)>(p[5])};
+    lib = {reinterpret_cast<decltype(lib.write)>(p[0]),     reinterpret_cast<decltype(lib.read)>(p[1]),
+           reinterpret_cast<decltype(lib.decode)>(p[2]),    reinterpret_cast<decltype(lib.decode_workspace)>(p[3]),
+           reinterpret_cast<decltype(lib.select)>(p[4]),    reinterpret_cast<decltype(lib.select_workspace)>(p[5]),
+           reinterpret_cast<decltype(lib.write4)>(p[6]),    reinterpret_cast<decltype(lib.read4)>(p[7]),
+           reinterpret_cast<decltype(lib.decode4)>(p[8]),   reinterpret_cast<decltype(lib.decode4_workspace)>(p[9]),
+           reinterpret_cast<decltype(lib.plan)>(p[10]),     reinterpret_cast<decltype(lib.trim)>(p[11]),
+           reinterpret_cast<decltype(lib.rope)>(p[12])};
     Py_RETURN_NONE;
 }
 
@@ -351,8 +621,10 @@ constexpr PyMethodDef method(const char *name, F f)
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef methods[] = {method("bind", py_bind),     method("write", py_write),   method("read", py_read),
-                         method("decode", py_decode), method("select", py_select), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {method("bind", py_bind),       method("write", py_write),   method("read", py_read),
+                         method("decode", py_decode),   method("select", py_select), method("write4", py_write4),
+                         method("read4", py_read4),     method("decode4", py_decode4), method("plan", py_plan),
+                         method("trim", py_trim),       method("rope", py_rope),     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fa_cache_py", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -15,7 +15,7 @@ from typing import NamedTuple
 import torch
 
 from ._lib import FAError, fa_cache_plan_raw, fa_cache_trim_raw
-from .cache import _check_batch, _elsewhere, _int, _output, _stream, _there
+from .cache import _check_batch, _elsewhere, _int, _output, _quick, _stream, _there
 
 
 class FAPagePool(NamedTuple):
@@ -67,6 +67,12 @@ def fa_cache_plan(pool, page_table, seq_lens, new_lens, page, T, counts=None, pl
     reach for is refused, with all behind it that need any.
     counts: where the pool's counts afterwards go (default: the pool's own; with another tensor the pool stays as it
     was, and another plan may take this one's place).  plan: preallocated outputs.  Returns the plan."""
+    if stream is None and plan is None and type(pool) is FAPagePool and (quick := _quick()):
+        done = quick.plan(pool, page_table, seq_lens, new_lens, page, T, counts)
+        if type(done) is tuple:
+            return FAPlan._make(done)
+        if done is not None:
+            raise FAError(done, "fa_cache_plan")
     index, B, stride, P = _check(pool, page_table, seq_lens, new_lens, "new_lens", counts)
     if _elsewhere(index, stream):
         with _there(index, stream):
@@ -100,6 +106,12 @@ def fa_cache_plan(pool, page_table, seq_lens, new_lens, page, T, counts=None, pl
 def fa_cache_trim(pool, page_table, seq_lens, keep_lens, page, counts=None, stream=None):
     """Cut sequences of seq_lens[b] tokens to keep_lens[b] (0: done) and give the pages behind back to the pool.
     The caller's lengths become keep_lens afterwards.  counts: as for ``fa_cache_plan``."""
+    if stream is None and type(pool) is FAPagePool and (quick := _quick()):
+        done = quick.trim(pool, page_table, seq_lens, keep_lens, page, counts)
+        if done is not None:
+            if done:
+                raise FAError(done, "fa_cache_trim")
+            return
     index, B, stride, P = _check(pool, page_table, seq_lens, keep_lens, "keep_lens", counts)
     if _elsewhere(index, stream):
         with _there(index, stream):

@@ -11,7 +11,7 @@ from typing import NamedTuple
 import torch
 
 from ._lib import FAError, RopeDesc, RopeRows, fa_rope_raw
-from .cache import _CODES, _elsewhere, _int, _stream, _there
+from .cache import _CODES, _elsewhere, _int, _quick, _stream, _there
 
 
 def _scaled(rot, base, scaling, factor, trained, fast, slow):
@@ -110,6 +110,12 @@ def fa_rope(q, k, rope, positions=None, backward=False, q_out=None, k_out=None, 
     None counts rows from 0; a row at a negative one stays as it is.  backward: gradients with respect to turned
     rows in, those with respect to the rows before out.  q_out, k_out: optional outputs, q and k themselves among
     them.  Returns (q, k) turned; computed in fp32 and rounded once."""
+    if stream is None and type(rope) is FARope and (quick := _quick()):
+        done = quick.rope(q, k, rope, positions, True if backward else False, q_out, k_out)
+        if type(done) is tuple:
+            return done
+        if done is not None:
+            raise FAError(done, "fa_rope")
     index = q.get_device() if isinstance(q, torch.Tensor) else -1
     if index < 0:
         raise FAError(1, "q must be a CUDA tensor")
