@@ -193,7 +193,10 @@ __global__ void __launch_bounds__(kWriteThreads) fa_cache4_write_kernel(Cache4 c
 // Reading back
 //
 // A block of 16 channels (8 code bytes, a scale byte) in, 32 bytes out a thread and
-// step; bound by the bytes it writes.
+// step; bound by the bytes it writes, so that they leave in one 32-byte store, a whole
+// sector (two of 16 bytes, which leave a warp in half sectors, take 8 x 16,384 tokens of 8
+// heads of 128, 656 MB, from 98.5 to 117.7 us on the GPU; outputs on odd 16 bytes have
+// them).  98 % of the measured copy rate; four steps a thread 98.8 us.
 constexpr int kReadThreads = 256;
 constexpr int kReadSteps = 2;
 
@@ -214,6 +217,7 @@ __global__ void __launch_bounds__(kReadThreads)
     if (chunk == 0 && h == 0 && which == 0 && threadIdx.x == 0)
         batch.check_length(b, cache.log2_page);
     T *out = (which ? v : k) + bh * N * d;
+    const bool whole = (reinterpret_cast<uintptr_t>(out) & 31) == 0;  // d is a multiple of 16 values: every block is then
     const int half = half_block(cache.page, d);
     const long long first = static_cast<long long>(chunk) * (kReadThreads * kReadSteps) + threadIdx.x;
     uint2 c[kReadSteps];
@@ -257,8 +261,14 @@ __global__ void __launch_bounds__(kReadThreads)
             }
         }
         uint4 *dst = reinterpret_cast<uint4 *>(out + at * kGroup);
-        __stcs(dst, make_uint4(r[0], r[1], r[2], r[3]));
-        __stcs(dst + 1, make_uint4(r[4], r[5], r[6], r[7]));
+        if (whole) {
+            asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]), "r"(r[1]),
+                         "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                         : "memory");
+        } else {
+            __stcs(dst, make_uint4(r[0], r[1], r[2], r[3]));
+            __stcs(dst + 1, make_uint4(r[4], r[5], r[6], r[7]));
+        }
     }
 }
 

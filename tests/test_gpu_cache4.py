@@ -183,6 +183,22 @@ def test_read_bad_pages_and_given_outputs():
     assert status() == 6
 
 
+def test_read_into_outputs_on_odd_16_bytes():
+    """Rows that begin 16 bytes behind a 32-byte border, one output or both."""
+    page, d, N = 32, 96, 50
+    table, pool = pages_for([50, 20], page, 1)
+    ref = Ref(pool, 2, page, d)
+    n = 2 * 2 * N * d
+    want = ref.read(table, [50, 20], N, torch.bfloat16)
+    for shift_k, shift_v in ((8, 0), (0, 8), (8, 8)):
+        bufs = [torch.full((n + 16,), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        k, v = (x[s:s + n].view(2, 2, N, d) for x, s in zip(bufs, (shift_k, shift_v)))
+        fa.fa_cache4_read(ref.to(DEV), table.to(DEV), i32([50, 20]), N, k=k, v=v)
+        assert torch.equal(k.cpu(), want[0]) and torch.equal(v.cpu(), want[1])
+        for x, s in zip(bufs, (shift_k, shift_v)):
+            assert (x[:s] == 7).all() and (x[s + n:] == 7).all()
+
+
 # ---------------------------------------------------------------------------
 # attention
 
