@@ -27,7 +27,16 @@ struct Cache4State {
 };
 Cache4State g_cache4[kMaxDevices];
 
-// Units of a segment that one block may take whole, as for the 8-bit cache.
+// Units (128 keys) of a segment that one block may take whole: one launch in place of two,
+// but the units one after the other.  8 KV heads of 4 rows, whole / shared out, us on the
+// GPU (in a graph):
+//                      1 unit       4 units      8 units      12 units
+//   d = 128, 1 seq.    4.1 / 6.5    6.2 / 8.6    9.1 / 8.7    12.1 / 8.8
+//            16        4.4 / 6.8    6.6 / 9.9    9.7 / 11.0   13.0 / 11.5
+//            56        6.0 / 8.2    10.1 / 14.5  15.2 / 17.8  20.4 / 21.0
+//   d = 64,  1         3.5 / 5.7    5.2 / 7.5    7.3 / 7.5    9.6 / 7.8
+//            56        4.4 / 6.8    6.8 / 10.7   10.1 / 12.7  14.2 / 15.6
+//   d = 32,  16        3.6 / 5.8    5.1 / 7.9    7.2 / 8.1    9.3 / 8.3
 constexpr long long kWholeUnits = 8;
 
 template <int D, int ROWS, typename T>
