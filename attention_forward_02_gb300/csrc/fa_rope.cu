@@ -70,6 +70,14 @@ bool apart(const View &a, const View &b)
     return gap >= lo.heads_bytes() && rows && batches && nested;
 }
 
+// Units of rows an SM below which a block shares its rows' sines (few heads share too little),
+// and up to which, with a thread a unit, a row's heads are shared out: so that every SM has
+// something, and, which leaves sixteen heads a thread, so that the last threads to start are few.
+// Without the latter a second wave of few threads takes as long as the first: 12,000 rows of 40
+// heads of 128 43.9 us on the GPU and 40.5 with it, 2 x 10,334 rows of 96 heads of 64 88.7 and
+// 80.0, 30,000 97.2 and 94.0 (half as many units: 41.2, 79.6, 96.9).
+constexpr int kFewUnits = 256, kFewHeads = 16, kUnits = 512, kManyUnits = 4096;
+
 // A stride: not negative, and small enough for the sums here.
 bool fine(long long s) { return s >= 0 && s < 1ll << 40; }
 
@@ -97,15 +105,6 @@ fa_status_t check_rows(fa_rope_rows_t &r, int B, int N, int d, View *x, View *y)
     if (!y->distinct() || !(in_place || apart(*x, *y)))
         return FA_ERR_INVALID_ARG;
     return FA_OK;
-}
-
-template <typename T>
-bool launch(bool interleaved, const fa::rope::Rows &q, const fa::rope::Rows &k, const fa::rope::Turn &turn,
-            const int *positions, long long stride, int N, int units, int slots, unsigned threads, cudaStream_t stream)
-{
-    const unsigned blocks = (threads + fa::rope::kThreads - 1) / fa::rope::kThreads;
-    return launch_dependent(interleaved ? fa::rope::fa_rope_kernel<T, true> : fa::rope::fa_rope_kernel<T, false>, blocks,
-                            fa::rope::kThreads, 0, stream, q, k, turn, positions, stride, N, units, slots, threads);
 }
 
 }  // namespace
@@ -152,27 +151,43 @@ fa_status_t fa_rope(const fa_rope_t *rope, const fa_rope_rows_t *q, const fa_rop
     const fa_status_t s = fa_host::encoder(&encode, &sms);
     if (s != FA_OK)
         return s;
-    // Heads a thread: all of them where rows are many, fewer where the GPU would not be full.
-    const long long rows_units = static_cast<long long>(B) * N * (d / 8);
+    const long long total = static_cast<long long>(B) * N;
     const int heads = (some_q ? rows[0].heads : 0) + (some_k ? rows[1].heads : 0);
-    int slots = 1;
-    while (slots < heads && rows_units * slots < static_cast<long long>(sms) * 1024)
-        slots *= 2;
-    if (rows_units * slots > 0x7fffffffLL)
+    const int units = d / 8, places = fa::rope::kThreads / units;  // of a block: rows times slots
+    if (total * units > 0x7fffffffLL / 2)
         return FA_ERR_UNSUPPORTED;
     fa::rope::Rows r[2];
     for (int i = 0; i < 2; ++i)
         r[i] = {rows[i].x,      rows[i].y,     rows[i].x_batch, rows[i].x_head, rows[i].x_row,
                 rows[i].y_batch, rows[i].y_head, rows[i].y_row,   (i ? some_k : some_q) ? rows[i].heads : 0};
     const fa::rope::Turn turn = {rope->turns, rope->pairs, rope->factor, backward == 1};
-    const unsigned threads = static_cast<unsigned>(rows_units * slots);
-    cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const bool done =
-        dtype == FA_FP16
-            ? launch<__half>(rope->interleaved, r[0], r[1], turn, positions, position_stride, N, d / 8, slots, threads, cs)
-            : launch<__nv_bfloat16>(rope->interleaved, r[0], r[1], turn, positions, position_stride, N, d / 8, slots, threads,
-                                    cs);
-    return done ? launched() : FA_ERR_CUDA;
+    fa::rope::Shape shape = {positions, position_stride, static_cast<unsigned>(N), static_cast<unsigned>(total), units, 1};
+    dim3 grid(1);
+    const bool few = total * units < static_cast<long long>(sms) * kFewUnits && heads >= kFewHeads;
+    if (few) {
+        while (shape.slots < 8 && 4 * shape.slots < heads && 2 * shape.slots <= places)
+            shape.slots *= 2;
+        const int per_block = places / shape.slots;
+        grid.x = static_cast<unsigned>((total + per_block - 1) / per_block);
+        while (static_cast<long long>(grid.y) * shape.slots < heads && static_cast<long long>(grid.x) * grid.y < sms)
+            grid.y *= 2;
+    } else {
+        // more threads than the GPU holds at once, but sixteen heads for each pair's sine, if there are so many
+        const auto below = [&](int per_sm) { return total * units * shape.slots < static_cast<long long>(sms) * per_sm; };
+        while ((shape.slots < heads && below(kUnits)) || (heads >= 16 * shape.slots && below(kManyUnits)))
+            shape.slots *= 2;
+        grid.x = static_cast<unsigned>((total * units * shape.slots + fa::rope::kThreads - 1) / fa::rope::kThreads);
+    }
+    const auto of_type = [&](auto t) {
+        using T = decltype(t);
+        using namespace fa::rope;
+        const auto kernel = few ? (rope->interleaved ? fa_rope_rows_kernel<T, true> : fa_rope_rows_kernel<T, false>)
+                                : (rope->interleaved ? fa_rope_kernel<T, true> : fa_rope_kernel<T, false>);
+        return launch_dependent(kernel, grid, kThreads, 0, static_cast<cudaStream_t>(stream), r[0], r[1], turn, shape)
+                   ? launched()
+                   : FA_ERR_CUDA;
+    };
+    return dtype == FA_FP16 ? of_type(__half()) : of_type(__nv_bfloat16());
 }
 
 }  // extern "C"
