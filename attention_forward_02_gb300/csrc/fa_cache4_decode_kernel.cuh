@@ -11,12 +11,30 @@
 //    of V at most two-way.
 //  - Codes become fp16 by cvt (two at a time), times their scale: both exact.  For V the codes
 //    of two keys are put side by side first, even channels in one word and odd in another.
+//    Up to four rows a head this is not needed: the eight columns of a product are then four
+//    rows twice, and the two channels that a byte holds two terms of it, each with the key's
+//    weight in one half of the columns and 0 in the other (PAIRS; 124 -> 113 us for the
+//    64 sequences below).
 //  - Scales belong to keys and channels, so none enters the softmax: P's reference is a plain
 //    running maximum (2^kAim under it, as there).
+//  - A segment's begin and end (its queries' rows, the merge of its warps) cost a block about
+//    as much as OPEN units, and count so when the runs are dealt out: the slowest block was
+//    12 to 26 % over the mean before (OPEN 0, 1, 2, 3: 130, 128, 125, 128 us for those 64
+//    sequences, 70, 67, 66, 66 for the 16 of 16 rows).
 //
-// What bounds it: 16 keys of d = 128 are 2,304 bytes, for which HBM takes some 100 clocks of
-// an SM, while the tile costs a warp some 300 instructions, 75 clocks of the SM's four
-// schedulers.  Both are near one another, so that instructions count.
+// What bounds it: instructions.  16 keys of d = 128 are 2,304 bytes, for which HBM takes some
+// 100 clocks of an SM.  A tile costs a warp 260 instructions (four rows) to 350 (sixteen),
+// and pipes that take two clocks an instruction: 64 conversions on that of logic, 64
+// scalings on the multiplying one, and products of 8.4 clocks, 16 (32) a tile; the three
+// overlap only in part (32 + 32 + 8 of them take 105 clocks of a scheduler, each kind alone
+// 62).  Without copies the 64 sequences took 122 us where they took 124 with them.
+//
+// Measured on the GPU, d = 128, 8 KV heads: 64 sequences of up to 16,384 keys, 4 rows a head,
+// 675 MB: 112.5 us, 6.0 TB/s, 88 % of the measured copy rate; 16 of them 41 (4 rows), 45 (8)
+// and 61 (16, two blocks an SM: 168 registers); one of 131,072 keys, 8 rows, 151 MB: 37;
+// some 10 us of these are start, merge and end.  d = 64, 32 heads of a row, 8 x up to 8,000
+// keys, 78 MB: 25; d = 96 and 32: 53 and 36 % of the copy rate, the softmax's instructions
+// being the same for fewer bytes.
 #pragma once
 
 #include "fa_cache4_kernel.cuh"
@@ -42,7 +60,7 @@ struct Dec4Cfg {
     static constexpr int STEP = 1 << LOG2_STEP;
     static constexpr int SUBS = STEP / kTile;
     static constexpr int STAGE = STEP * D / 8 * 9;  // bytes
-    static constexpr int WARPS = 4;              // that compute
+    static constexpr int WARPS = 4;                 // that compute
     static constexpr int THREADS = 32 * (WARPS + 1);
     static constexpr int BLOCKS = D == 32 ? 4 : D >= 96 && ROWS == 16 ? 2 : 3;  // an SM
     static constexpr int STAGES = D == 128 && BLOCKS == 3 ? 3 : D == 96 && BLOCKS == 3 ? 4 : 5;
@@ -66,7 +84,7 @@ struct __align__(16) Stage4 {
 };
 static_assert(sizeof(Stage4) == 32, "stage record");
 constexpr int kEnd = 32;  // the block's last stage
-constexpr int kBoxes = 8;
+constexpr int kBoxes = 8;  // number of the first box's bit
 
 // Words of eight consecutive channels of a key's K that a thread has: D / 4 channels from
 // c * D / 4 on; their scales, as pairs.  `codes` and `scales` are where its first ones lie.
@@ -145,8 +163,8 @@ __global__ void __launch_bounds__(Dec4Cfg<D, ROWS>::THREADS, Dec4Cfg<D, ROWS>::B
     constexpr bool PAIRS = ROWS == 4;               // columns are four rows twice
     constexpr int KW = D / 16;                      // steps of the first product
     constexpr int TILES = PAIRS ? D / 32 : D / 16;  // of O^T
-    constexpr int VW = D / 32;           // fours of channels of a thread
-    constexpr int VX = (D + 63) / 64;    // words of them
+    constexpr int VW = D / 32;                      // fours of channels of a thread
+    constexpr int VX = (D + 63) / 64;               // words of them
     extern __shared__ uint8_t smem_raw[];
     __shared__ long long scan[F::WARPS + 1];
     __shared__ long long begin[2];

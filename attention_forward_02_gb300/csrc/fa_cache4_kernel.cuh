@@ -102,6 +102,10 @@ __device__ __forceinline__ float scale_of(float amax)
 // x = X 2^i, X < 2^11, and scale = S 2^j, S < 2^4, the quotient is off a border k / 4 by
 // (4 X 2^i - k S 2^j) / (4 S 2^j), which for X > 100 is no less than 1 / 4 / X > 2^-13 (i < j - 1
 // there, and both terms multiples of 4 2^i), and for a smaller X no less than 2^-11.
+//
+// 58,800 tokens of 8 heads of 128 (308 MB) take 50.8 us on the GPU from fp16, 89 % of the
+// measured copy rate: 185 instructions a block of channels keep the schedulers 71 % busy, which
+// leaves the loads too few; 32-byte loads change nothing.  256 tokens take 2.0 us.
 constexpr int kWriteThreads = 256;
 
 struct Rows4 {

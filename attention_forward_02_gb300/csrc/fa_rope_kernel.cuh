@@ -6,7 +6,7 @@
 // What bounds it: each 16-bit value is read once and written once, six flops a pair beside
 // it, so HBM does.  Sine and cosine depend on the row's position and the pair only.  With
 // many rows a thread computes those of four pairs of one row and goes through its heads
-// with them: 58,800 rows of 40 heads of 128 take 179.5 us on the GPU, 1.2 GB, 99 % of the
+// with them: 58,800 rows of 40 heads of 128 take 180 us on the GPU, 1.2 GB, 98 % of the
 // measured copy rate.  With few rows the heads have to be shared out among threads, and a
 // block computes its rows' sines once for all of them.  40 heads of 128, bf16, sines a
 // block / a thread, us on the GPU:

@@ -469,7 +469,7 @@ FA_API fa_status_t fa_rope(const fa_rope_t *rope, const fa_rope_rows_t *q, const
  * num_pages), the free ones are ring[x mod num_pages] for counts[0] <= x < counts[1].  Pages
  * are taken from the front and given back behind the end, so the one that was given back
  * first is used first.  Everything is read and written on the device: a captured graph
- * follows it.
+ * follows it.  Calls that share a pool or a page table must not run concurrently.
  */
 
 /*
@@ -582,7 +582,8 @@ FA_API size_t fa_decode_cache4_workspace_size(int B, int Hq, int Hkv, int Nq, in
 /*
  * fa_decode_cache4 -- decoding attention over the 4-bit cache (asynchronous): arguments,
  * results, masks and reports as for fa_decode_cache over all pages.  Bytes above 0xE2 are no
- * scales; what rows that see such a key get is not said.
+ * scales: what the rows of a KV head get of a key with such a byte that any of them sees is not
+ * said.  (Behind the last key they mean nothing.)
  */
 FA_API fa_status_t fa_decode_cache4(const fa_cache4_t *cache, const void *q, long long q_batch_stride,
                                     long long q_head_stride, long long q_row_stride, void *o,

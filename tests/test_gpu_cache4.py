@@ -332,6 +332,48 @@ def test_scores_of_any_size(by):
     attend(ref, table, lens, q, True)
 
 
+@pytest.mark.parametrize("G,Nq", [(4, 1), (8, 1), (4, 4)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_queries_that_are_not_finite(G, Nq, bad):
+    """A row with such a channel is NaN (or nothing); the other rows of its KV head, causal ones among them, are as ever."""
+    lens, d = [300, 41], 64
+    table, pool = pages_for(lens, 32, 4)
+    ref = Ref(pool, 2, 32, d)
+    q = normal((2, 2 * G, Nq, d), "bf16", 3)
+    want = attend_bounds(ref, q, table, lens, d ** -0.5, True)
+    x = q.clone()
+    x[:, 1, Nq - 1, 5], x[:, G + 2, 0, 9] = bad, bad
+    o, lse = fa.fa_decode_cache4(x.to(DEV), ref.to(DEV), table.to(DEV), i32(lens), causal=True)
+    hit = torch.zeros(2, 2 * G, Nq, dtype=torch.bool)
+    hit[:, 1, Nq - 1], hit[:, G + 2, 0] = True, True
+    assert not torch.isfinite(lse.cpu()[hit]).any()
+    o, lse = o.cpu().double(), lse.cpu().double()
+    assert ((o - want[0]).abs() <= want[2])[~hit].all() and ((lse - want[1]).abs() <= want[3])[~hit].all()
+
+
+@pytest.mark.parametrize("R", [1, 2, 3, 4, 5, 8, 9, 16, 17, 32, 33, 64, 65, 100])
+def test_every_layout_of_rows(R):
+    """One KV head with R query heads: four, eight and sixteen rows a warp, warps along the rows, groups of 64."""
+    lens, d = [1500, 0, 77, 400], 128
+    table, pool = pages_for(lens, 64, R)
+    ref = Ref(pool, 1, 64, d, seed=R)
+    attend(ref, table, lens, normal((4, R, 1, d), "fp16", R))
+    attend(ref, table[2:], lens[2:], normal((2, R, 1, d), "fp16", R))
+
+
+def test_more_segments_than_blocks():
+    """Short sequences, more of them with their heads than blocks: runs over many whole segments."""
+    lens = [(37 * b) % 140 for b in range(200)]
+    table, pool = pages_for(lens, 16, 2)
+    ref = Ref(pool, 4, 16, 32, seed=1)
+    attend(ref, table, lens, normal((200, 8, 1, 32), "bf16", 2))
+    lens = [1] * 700 + [0] * 20 + [300] * 3
+    table, pool = pages_for(lens, 128, 2)
+    ref = Ref(pool, 1, 128, 64, seed=1)
+    attend(ref, table, lens, normal((723, 1, 2, 64), "fp16", 2), True)
+    assert status() == 0
+
+
 def test_query_strides_scale_and_given_outputs():
     d, lens = 128, [90, 200]
     table, pool = pages_for(lens, 64, 4)
