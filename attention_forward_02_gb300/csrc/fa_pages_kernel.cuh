@@ -187,8 +187,9 @@ __global__ void __launch_bounds__(kThreads)
         cu[in.B] = cu_seqlens[in.B] = all_rows;
     __syncthreads();
     const int taken = taken_all;
-    // the pages taken: those of refused sequences come behind them
-    for (int j = t; j < taken; j += kThreads) {
+    // the pages taken: those of refused sequences come behind them; the last threads begin with them,
+    // the first ones with the rows
+    for (int j = kThreads - 1 - t; j < taken; j += kThreads) {
         const int b = first_above(until, in.B, j);
         const int before = b > 0 ? until[b - 1] : 0;
         const long long at = pages_of(in.had[b], log2_page) + (j - before);

@@ -98,6 +98,24 @@ def test_both_ways_agree(monkeypatch):
         assert x.dtype == y.dtype and x.shape == y.shape and torch.equal(x, y)
 
 
+def test_outputs_of_one_allocation():
+    """Contiguous, apart from one another, on 16-byte borders, and in place of their memory when written to."""
+    rope, lens = fa.FARope.new(32), i32([0, 0, 0])
+    x = torch.randn(5, 7, 32, device=DEV, dtype=torch.float16)
+    pool, table = fa.FAPagePool.full(9), torch.zeros(3, 4, dtype=torch.int32, device=DEV)
+    plan = fa.fa_cache_plan(pool, table, lens, i32([3, 1, 2]), 16, 7)
+    cache = fa.FACache4(torch.zeros(9, 3, 16, 36, dtype=torch.uint8, device=DEV))
+    for group in (fa.fa_rope(x, x[:, :3], rope), fa.fa_cache4_read(cache, table, plan.ends, 5), plan):
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for t in group)
+        assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+        for t in group:
+            assert t.is_contiguous() and t.data_ptr() % 16 == 0 and not t.requires_grad
+            others = [u.clone() for u in group if u is not t]
+            t.add_(1).view(-1)[-1:].zero_()
+            assert all(torch.equal(u, v) for u, v in zip(others, [u for u in group if u is not t]))
+            assert t.storage_offset() * t.element_size() + t.nbytes <= t.untyped_storage().nbytes()
+
+
 def test_streams_and_empty_calls_go_the_longer_way():
     rope = fa.FARope.new(64)
     x = torch.randn(5, 2, 64, device=DEV, dtype=torch.float16)
