@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <functional>
@@ -11,6 +12,7 @@
 #include "fa.h"
 #include "fa_cache4_decode_kernel.cuh"
 #include "fa_cache4_kernel.cuh"
+#include "fa_cache4_short_kernel.cuh"
 #include "fa_cache_host.h"
 #include "fa_host.h"
 
@@ -39,6 +41,22 @@ Cache4State g_cache4[kMaxDevices];
 //   d = 32,  16        3.6 / 5.8    5.1 / 7.9    7.2 / 8.1    9.3 / 8.3
 constexpr long long kWholeUnits = 8;
 
+// More segments than resident blocks go to a warp each where they are bounded to this many
+// units, one more for every segment a block, kWholeUnits at most.  Up to 8 rows; a warp each /
+// shared out, us on the GPU (in a graph), contexts of up to
+//                                   1 unit        3 units        4 units        6 units        8 units
+//   d = 128,   512 segments, 4 rows 6.3 / 10.5    13.4 / 13.7    16.9 / 13.9    24.1 / 17.5    31.2 / 18.9
+//             1024                  7.7 / 15.0    16.4 / 20.6    20.7 / 22.1    29.2 / 25.1    38.1 / 27.8
+//             2048                  11.7 / 24.4   23.8 / 32.1    30.3 / 36.0    42.6 / 41.3    54.2 / 48.7
+//             4096                  18.6 / 41.3   36.7 / 56.5    46.7 / 63.7    64.4 / 76.1    78.0 / 85.0
+//                          8 rows   20.8 / 51.0   40.3 / 68.4    51.3 / 76.1    71.2 / 90.1    86.1 / 100
+//   d = 64,    512           1 row  5.2 / 8.3     10.8 / 10.5    13.8 / 11.3    19.4 / 12.4    25.2 / 13.8
+//             4096                  12.8 / 26.0   25.4 / 37.2    32.2 / 40.8    43.5 / 50.0    56.4 / 57.0
+//   d = 32,   1024           4 rows 5.3 / 9.8     11.1 / 13.1    13.8 / 13.7    19.6 / 15.4    25.4 / 17.4
+// With no more segments than blocks a block each is ahead from 2 units on: 384 of up to 300
+// keys 8.1 where a warp each takes 11.4.
+constexpr long long kShortUnits = 2;
+
 template <int D, int ROWS, typename T>
 constexpr auto decode_kernel()
 {
@@ -50,8 +68,17 @@ cudaError_t set_smem_attr()
 {
     const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
     constexpr int bytes = fa::cache4::Dec4Cfg<D, ROWS>::SMEM;
-    const cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, ROWS, __half>(), a, bytes);
-    return e == cudaSuccess ? cudaFuncSetAttribute(decode_kernel<D, ROWS, __nv_bfloat16>(), a, bytes) : e;
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, ROWS, __half>(), a, bytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(decode_kernel<D, ROWS, __nv_bfloat16>(), a, bytes);
+    if constexpr (ROWS <= 8) {
+        constexpr int own = fa::cache4::Short4Cfg<D, ROWS>::SMEM;
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(fa::cache4::fa_cache4_short_kernel<D, ROWS, __half>, a, own);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(fa::cache4::fa_cache4_short_kernel<D, ROWS, __nv_bfloat16>, a, own);
+    }
+    return e;
 }
 template <int D>
 cudaError_t set_smem_attrs()
@@ -121,6 +148,25 @@ template <typename F>
 fa_status_t by_type(fa_dtype_t dtype, F f)
 {
     return dtype == FA_FP16 ? f(__half()) : f(__nv_bfloat16());
+}
+
+// A warp for each of the segments, of up to eight rows.
+template <int D, int ROWS>
+fa_status_t launch_short(const fa::cache::Work &w, long long segments, void *o, float *lse, fa_dtype_t dtype, cudaStream_t cs)
+{
+    if constexpr (ROWS > 8) {
+        return FA_ERR_UNSUPPORTED;
+    } else {
+        using S = fa::cache4::Short4Cfg<D, ROWS>;
+        const unsigned blocks = static_cast<unsigned>((segments + S::WARPS - 1) / S::WARPS);
+        return by_type(dtype, [&](auto t) {
+            using T = decltype(t);
+            return launch_dependent(fa::cache4::fa_cache4_short_kernel<D, ROWS, T>, blocks, S::THREADS, S::SMEM, cs, w,
+                                    static_cast<T *>(o), lse)
+                       ? launched()
+                       : FA_ERR_CUDA;
+        });
+    }
 }
 
 }  // namespace
@@ -308,6 +354,8 @@ fa_status_t fa_decode_cache4(const fa_cache4_t *cache, const void *q, long long 
             long long blocks = static_cast<long long>(sms) * F::BLOCKS;
             if (blocks > fa::cache::kMaxBlocks)
                 blocks = fa::cache::kMaxBlocks;
+            if (ROWS <= 8 && segments > blocks && units <= std::min(kWholeUnits, kShortUnits + segments / blocks))
+                return launch_short<D, ROWS>(w, segments, o, lse, dtype, cs);
             w.whole = units <= kWholeUnits && segments <= blocks;
             if (w.whole)
                 blocks = segments;

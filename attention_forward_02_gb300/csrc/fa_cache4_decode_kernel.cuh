@@ -4,7 +4,8 @@
 // Built as the one over the 8-bit cache (fa_cache_decode_kernel.cuh): units of a stage's
 // keys dealt out in equal runs to a persistent grid, one warp that copies, four that
 // compute with mma.m16n8k16 on fp16, keys as rows and query rows as columns, parts
-// merged by fa_cache_combine_kernel.  What differs:
+// merged by fa_cache_combine_kernel.  (Many short segments: fa_cache4_short_kernel.cuh.)  What
+// differs:
 //  - A page and head is one block of bytes, so that a copy is one bulk copy (four where a
 //    page is larger than a stage).  It is not swizzled: of a tile's 16 rows, row r stands for
 //    the key r ^ (r >> 2 & 1), and then the reads of K are free of bank conflicts and those
@@ -30,28 +31,22 @@
 // 62).  Without copies the 64 sequences took 122 us where they took 124 with them.
 //
 // Measured on the GPU, d = 128, 8 KV heads: 64 sequences of up to 16,384 keys, 4 rows a head,
-// 675 MB: 112.5 us, 6.0 TB/s, 88 % of the measured copy rate; 16 of them 41 (4 rows), 45 (8)
+// 675 MB: 113 us, 6.0 TB/s, 88 % of the measured copy rate; 16 of them 41 (4 rows), 45 (8)
 // and 61 (16, two blocks an SM: 168 registers); one of 131,072 keys, 8 rows, 151 MB: 37;
 // some 10 us of these are start, merge and end.  d = 64, 32 heads of a row, 8 x up to 8,000
 // keys, 78 MB: 25; d = 96 and 32: 53 and 36 % of the copy rate, the softmax's instructions
 // being the same for fewer bytes.
 #pragma once
 
-#include "fa_cache4_kernel.cuh"
-#include "fa_cache_decode_kernel.cuh"
+#include "fa_cache4_running.cuh"
 
 namespace fa {
 namespace cache4 {
 
-using cache::kAim;
 using cache::kFirst;
 using cache::kHeadPart;
 using cache::kLast;
-using cache::kMost;
-using cache::kNoKey;
 using cache::kTailPart;
-using cache::kTile;
-using cache::Work;
 
 // As DecCfg of the 8-bit cache, for warps of ROWS query rows.
 template <int D, int ROWS>
@@ -86,85 +81,15 @@ static_assert(sizeof(Stage4) == 32, "stage record");
 constexpr int kEnd = 32;  // the block's last stage
 constexpr int kBoxes = 8;  // number of the first box's bit
 
-// Words of eight consecutive channels of a key's K that a thread has: D / 4 channels from
-// c * D / 4 on; their scales, as pairs.  `codes` and `scales` are where its first ones lie.
-template <int D>
-__device__ __forceinline__ uint32_t k_scale_offset(int c)
-{
-    return D == 128 ? 2 * c : D == 96 ? 3 * c >> 1 : D == 64 ? c : c >> 1;
-}
-template <int D>
-__device__ __forceinline__ void load_k(uint32_t codes, uint32_t scales, int c, uint32_t (&w)[D / 32], uint32_t (&by)[D / 32])
-{
-    if constexpr (D == 96) {
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-            cache::load_words<1>(w + i, codes + 4 * i);
-        const uint32_t lo = load_u8(scales) * 0x800080u, hi = load_u8(scales + 1) * 0x800080u;
-        by[0] = lo;
-        by[1] = c & 1 ? hi : lo;
-        by[2] = hi;
-    } else {
-        cache::load_words<D / 32>(w, codes);
-        by[0] = load_u8(scales) * 0x800080u;
-        if constexpr (D == 64)
-            by[1] = by[0];
-        if constexpr (D == 128) {
-            by[1] = by[0];
-            by[2] = by[3] = load_u8(scales + 1) * 0x800080u;
-        }
-    }
-}
-
-// A thread's channels of a key's V: v_column's, eight to a word (four in the last of d = 32 and
-// 96), and the scale byte of each word; as above.
-template <int D>
-__device__ __forceinline__ uint32_t v_code_offset(int g)
-{
-    return D == 128 ? 8 * g : D == 32 ? 2 * g : 4 * g;
-}
-template <int D>
-__device__ __forceinline__ uint32_t v_scale_offset(int g)
-{
-    return D == 128 ? g : D == 32 ? g >> 2 : g >> 1;
-}
-template <int D>
-__device__ __forceinline__ void load_v(uint32_t codes, uint32_t scales, int g, uint32_t (&w)[(D + 63) / 64],
-                                       uint32_t (&s)[(D + 63) / 64])
-{
-    s[0] = load_u8(scales);
-    if constexpr (D == 128) {
-        cache::load_words<2>(w, codes);
-        s[1] = s[0];
-    } else if constexpr (D == 96) {
-        cache::load_words<1>(w, codes);
-        w[1] = load_u16(codes + 32 - 2 * g);
-        s[1] = load_u8(scales + 4 + (g >> 2) - (g >> 1));
-    } else if constexpr (D == 64) {
-        cache::load_words<1>(w, codes);
-    } else {
-        w[0] = load_u16(codes);
-    }
-}
-
-__device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b)
-{
-    const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&x);
-}
-
 template <int D, int ROWS, typename T>
 __global__ void __launch_bounds__(Dec4Cfg<D, ROWS>::THREADS, Dec4Cfg<D, ROWS>::BLOCKS)
     fa_cache4_decode_kernel(const __grid_constant__ Work w, T *__restrict__ out, float *__restrict__ lse)
 {
     using F = Dec4Cfg<D, ROWS>;
     constexpr int S = F::STAGES, J = F::J;
-    constexpr int NT = ROWS == 16 ? 2 : 1;          // tiles of eight columns
-    constexpr bool PAIRS = ROWS == 4;               // columns are four rows twice
-    constexpr int KW = D / 16;                      // steps of the first product
-    constexpr int TILES = PAIRS ? D / 32 : D / 16;  // of O^T
-    constexpr int VW = D / 32;                      // fours of channels of a thread
-    constexpr int VX = (D + 63) / 64;               // words of them
+    using R = Running<D, ROWS, T>;
+    constexpr int NT = R::NT;
+    constexpr int VW = D / 32;  // fours of channels of a thread
     extern __shared__ uint8_t smem_raw[];
     __shared__ long long scan[F::WARPS + 1];
     __shared__ long long begin[2];
@@ -379,19 +304,10 @@ __global__ void __launch_bounds__(Dec4Cfg<D, ROWS>::THREADS, Dec4Cfg<D, ROWS>::B
 
     // ---------------- the warps that compute ----------------
     const int g = lane >> 2, c = lane & 3;
-    const int g_row = g ^ (g >> 2), v_row = 2 * c, v_swap = c >> 1;  // a tile's rows of this thread's keys
     const int key_warps = F::WARPS / w.row_warps;
     const int wk = warp % key_warps, wr = warp / key_warps;
-    // Q^T operand: of query rows g (+ 8), their d in the order of the thread's K
-    // words; in registers for eight rows, for sixteen in the warp's merge area
-    uint32_t qb[NT == 1 ? KW : 1][2];
-    const uint32_t q_own = sbase + F::MERGE_OFF + warp * (8 * F::OROW * 4) + lane * 16;
-    static_assert(KW * 512 <= 8 * F::OROW * 4, "sixteen rows of Q fit the merge area");
-    float qf[NT][2];      // per query row 2 c, 2 c + 1 (+ 8): scale to log2 units
-    uint32_t behind = 0;  // ... keys that it sees beyond `least`, a byte each
-    float m[NT][2], l[NT][2], acc[TILES][NT][4];
-    int least = 0, most = 0;  // keys that all rows see (negative: the first ones see none), that any row sees
-    auto limit = [&](int nt, int u) -> int { return least + static_cast<int>((behind >> (8 * (2 * nt + u))) & 255u); };
+    static_assert(R::KW * 512 <= 8 * F::OROW * 4, "sixteen rows of Q fit the merge area");
+    R run(lane, sbase + F::MERGE_OFF + warp * (8 * F::OROW * 4) + lane * 16);
     int4 *segment = reinterpret_cast<int4 *>(smem + F::FLAG_OFF + 16) + warp;  // b, head, group
     uint32_t merges = 0;
     // a barrier of the computing warps whose wait is bounded
@@ -413,17 +329,13 @@ __global__ void __launch_bounds__(Dec4Cfg<D, ROWS>::THREADS, Dec4Cfg<D, ROWS>::B
         own[j] = place(wk * J + j);
     const unsigned all_boxes = (1u << (F::STEP >> w.log2_box)) - 1u;
     const uint32_t half = box_bytes / 2;
-    const uint32_t k_codes = g_row * (D / 2) + c * (D / 8), k_scales = g_row * (D / 16) + k_scale_offset<D>(c);
+    const uint32_t k_codes = run.key_row * (D / 2) + c * (D / 8), k_scales = run.key_row * (D / 16) + k_scale_offset<D>(c);
     uint32_t v_codes[2], v_scales[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        v_codes[r] = half + (v_row + (r ^ v_swap)) * (D / 2) + v_code_offset<D>(g);
-        v_scales[r] = half + (v_row + (r ^ v_swap)) * (D / 16) + v_scale_offset<D>(g);
+        v_codes[r] = half + run.v_row[r] * (D / 2) + v_code_offset<D>(g);
+        v_scales[r] = half + run.v_row[r] * (D / 16) + v_scale_offset<D>(g);
     }
-    // bytes of a key pair's P that a column of first (second) channels takes of the first and second key
-    const uint32_t of_first = g < 4 ? 0x4410u : 0x1044u, of_second = g < 4 ? 0x4432u : 0x3244u;
-    bool fresh = true;   // some row may have no reference yet
-    uint32_t unset = 0;  // ... a bit each of the thread's
     int slot = S - 1;
     uint32_t phase = 1;
     for (int flags = 0; !(flags & kEnd);) {
@@ -444,69 +356,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, ROWS>::THREADS, Dec4Cfg<D, ROWS>::B
             if (lane == 0)
                 *segment = make_int4(b_seg, head, group, 0);
             __syncwarp();
-            most = w.batch.length(b_seg, log2_page);
-            least = w.q.causal ? most - w.q.Nq + 1 : most;
-            behind = 0;
-            fresh = true;
-            unset = (1u << (2 * NT)) - 1u;
-            uint2 rows_q[NT][KW];
-            int extra[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int row = group * rows_block + wr * (8 * NT) + nt * 8 + (PAIRS ? g & 3 : g);
-                const int hq = row / w.q.Nq, qi = row % w.q.Nq;
-                extra[nt] = w.q.causal ? qi : 0;
-                const T *src = static_cast<const T *>(w.q.q) + b_seg * w.q.batch_stride +
-                               static_cast<long long>(head * w.q.G + hq) * w.q.head_stride + qi * w.q.row_stride + c * (D / 4);
-#pragma unroll
-                for (int s = 0; s < KW; ++s) {
-                    rows_q[nt][s] = make_uint2(0, 0);
-                    if (row < w.R)
-                        rows_q[nt][s] = *reinterpret_cast<const uint2 *>(src + 4 * s);
-                }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const uint2(&x)[KW] = rows_q[nt];
-                float top = 0.f;
-#pragma unroll
-                for (int s = 0; s < KW; ++s) {
-                    const float2 y = DTypeTraits<T>::unpack(x[s].x), z = DTypeTraits<T>::unpack(x[s].y);
-                    const float f[4] = {fabsf(y.x), fabsf(y.y), fabsf(z.x), fabsf(z.y)};
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (f[u] <= 3.402823466e38f)
-                            top = fmaxf(top, f[u]);
-                }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int e = top > 0.f ? max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -100) : 0;
-                const float by = cache::pow2f(-e);
-#pragma unroll
-                for (int s = 0; s < KW; ++s) {
-                    const float2 y = DTypeTraits<T>::unpack(x[s].x), z = DTypeTraits<T>::unpack(x[s].y);
-                    const uint32_t q0 = DTypeTraits<__half>::pack(y.x * by, y.y * by);
-                    const uint32_t q1 = DTypeTraits<__half>::pack(z.x * by, z.y * by);
-                    if constexpr (NT == 1) {
-                        qb[s][0] = q0;
-                        qb[s][1] = q1;
-                    } else {
-                        cache::store_pair(q_own + s * 512 + nt * 8, q0, q1);
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    qf[nt][u] = cache::pow2f(__shfl_sync(0xffffffffu, e, 8 * c + 4 * u)) * w.scale_log2;
-                    behind |= __shfl_sync(0xffffffffu, extra[nt], 8 * c + 4 * u) << (8 * (2 * nt + u));
-                    m[nt][u] = 0.f;
-                    l[nt][u] = 0.f;
-                }
-#pragma unroll
-                for (int j = 0; j < TILES; ++j)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        acc[j][nt][u] = 0.f;
-            }
+            run.open(w, b_seg, head, group * rows_block + wr * (8 * NT), w.batch.length(b_seg, log2_page));
         }
 
         const uint32_t base = sbase + slot * F::STAGE;
@@ -518,7 +368,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, ROWS>::THREADS, Dec4Cfg<D, ROWS>::B
 #pragma unroll
             for (int j = 0; j < J; ++j)
                 key0[j] = first + j * kTile;
-            bool masked = first + J * kTile > least, some = first < most;
+            bool masked = first + J * kTile > run.least, some = first < run.most;
             if (static_cast<unsigned>(flags) >> kBoxes != all_boxes) {  // the end, or a page with a bad number
                 masked = true;
                 some = false;
@@ -526,7 +376,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, ROWS>::THREADS, Dec4Cfg<D, ROWS>::B
                 for (int j = 0; j < J; ++j) {
                     if (!(flags >> (kBoxes + ((sub0 + j) * kTile >> w.log2_box)) & 1))
                         key0[j] = kNoKey;
-                    some |= key0[j] < most;
+                    some |= key0[j] < run.most;
                 }
             }
             if (!some) {
@@ -544,207 +394,32 @@ __global__ void __launch_bounds__(Dec4Cfg<D, ROWS>::THREADS, Dec4Cfg<D, ROWS>::B
                 codes[j] = base + at.x;
                 scales[j] = base + at.y;
             }
-            // ---- S^T = K Q^T ----
             float e[J][NT][4];
             {
-                uint32_t kw[J][2][D / 32], by[J][2][D / 32];
+                uint32_t kw[J][2][D / 32], ks[J][2][R::KS];
 #pragma unroll
                 for (int j = 0; j < J; ++j)
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
-                        load_k<D>(codes[j] + k_codes + r * (8 * D / 2), scales[j] + k_scales + r * (8 * D / 16), c, kw[j][r],
-                                  by[j][r]);
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            e[j][nt][u] = 0.f;
-#pragma unroll
-                for (int x = 0; x < D / 32; ++x) {
-                    uint32_t h[J][2][4];
-#pragma unroll
-                    for (int j = 0; j < J; ++j)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            halves8(kw[j][r][x], h[j][r]);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                h[j][r][i] = times(h[j][r][i], by[j][r][x]);
-                        }
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int s = 2 * x + y;
-                        uint32_t z[2 * NT];
-                        if constexpr (NT == 1) {
-                            z[0] = qb[s][0];
-                            z[1] = qb[s][1];
-                        } else {
-                            cache::load_words<4>(z, q_own + s * 512);
-                        }
-#pragma unroll
-                        for (int j = 0; j < J; ++j)
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                cache::mma_f16(e[j][nt], h[j][0][2 * y], h[j][1][2 * y], h[j][0][2 * y + 1], h[j][1][2 * y + 1],
-                                               z[2 * nt], z[2 * nt + 1]);
-                    }
-                }
+                        load_k<D>(codes[j] + k_codes + r * (8 * D / 2), scales[j] + k_scales + r * (8 * D / 16), kw[j][r],
+                                  ks[j][r]);
+                run.template scores<J>(kw, ks, e);
             }
-            // ---- exponents of P, masks; does any outgrow its reference? ----
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float2 by = make_float2(qf[nt][0], qf[nt][1]), from = make_float2(-m[nt][0], -m[nt][1]);
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int u = 0; u < 4; u += 2) {
-                        const float2 x = ffma2(make_float2(e[j][nt][u], e[j][nt][u + 1]), by, from);
-                        e[j][nt][u] = x.x;
-                        e[j][nt][u + 1] = x.y;
-                    }
-            }
-            if (masked) {
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            if (key0[j] + g_row + 8 * (u >> 1) >= limit(nt, u & 1))
-                                e[j][nt][u] = -INFINITY;
-            }
-            float highest = fresh ? INFINITY : -INFINITY;  // NaN moves no reference
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int u = 0; u < 4; u += 2)
-                        highest = fmax3(highest, e[j][nt][u], e[j][nt][u + 1]);
-            if (__any_sync(0xffffffffu, highest > kMost)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t bit = 1u << (2 * nt + u);
-                        float top = -INFINITY;  // over the reference, which is 0 as long as it is not set
-#pragma unroll
-                        for (int j = 0; j < J; ++j)
-                            top = fmaxf(top, fmaxf(e[j][nt][u], e[j][nt][u + 2]));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        const float over = top - kAim;
-                        const float up = unset & bit ? (top == -INFINITY ? 0.f : over) : fmaxf(over, 0.f);
-                        const float alpha = unset & bit ? 1.f : cache::ex2(-up);
-                        if (top > -INFINITY)
-                            unset &= ~bit;
-                        m[nt][u] += up;
-                        l[nt][u] *= alpha;
-#pragma unroll
-                        for (int j = 0; j < J; ++j) {
-                            e[j][nt][u] -= up;
-                            e[j][nt][u + 2] -= up;
-                        }
-#pragma unroll
-                        for (int j = 0; j < TILES; ++j) {
-                            acc[j][nt][u] *= alpha;
-                            acc[j][nt][u + 2] *= alpha;
-                        }
-                    }
-                fresh = __any_sync(0xffffffffu, unset != 0);
-            }
-            // ---- P, and O^T += V^T P^T ----
             uint32_t pb[J][NT][2];
+            run.template weights<J>(e, key0, masked, pb);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float(&p)[4] = e[j][nt];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        p[u] = cache::ex2(p[u]);
-                    const float2 sum = fadd2(make_float2(l[nt][0], l[nt][1]),
-                                             fadd2(make_float2(p[0], p[1]), make_float2(p[2], p[3])));
-                    l[nt][0] = sum.x;
-                    l[nt][1] = sum.y;
-                    pb[j][nt][0] = cache::transpose8(DTypeTraits<__half>::pack(p[0], p[1]));
-                    pb[j][nt][1] = cache::transpose8(DTypeTraits<__half>::pack(p[2], p[3]));
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                uint32_t vw[4][VX], vs[4][VX];
+                uint32_t vw[4][R::VX], vs[4][R::VX];
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    load_v<D>(codes[j] + v_codes[r & 1] + (r >> 1) * (8 * D / 2), scales[j] + v_scales[r & 1] + (r >> 1) * (8 * D / 16), g,
-                              vw[r], vs[r]);
+                    load_v<D>(codes[j] + v_codes[r & 1] + (r >> 1) * (8 * D / 2),
+                              scales[j] + v_scales[r & 1] + (r >> 1) * (8 * D / 16), g, vw[r], vs[r]);
                 if (j == J - 1 && last_set) {  // the stage's bytes are in registers
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(empty(slot));
                 }
-                if (masked) {
-                    // bytes behind the last key are whatever the page held: codes are finite, a scale
-                    // need not be
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (key0[j] + (v_row + ((r & 1) ^ v_swap)) + 8 * (r >> 1) >= most)
-#pragma unroll
-                            for (int x = 0; x < VX; ++x)
-                                vs[r][x] = 0;
-                }
-                if constexpr (PAIRS) {
-                    // a pair's two channels as two terms of the product, each with the key's weight for its
-                    // own columns and 0 for the other's
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const uint32_t b0 = __byte_perm(pb[j][0][r], 0, of_first), b1 = __byte_perm(pb[j][0][r], 0, of_second);
-#pragma unroll
-                        for (int x = 0; x < VX; ++x) {
-                            const bool half_word = x == VX - 1 && D % 64 != 0;
-                            uint32_t h[2][4];
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                halves8(vw[2 * r + y][x], h[y]);
-#pragma unroll
-                                for (int i = 0; i < (half_word ? 2 : 4); ++i)
-                                    h[y][i] = times(h[y][i], vs[2 * r + y][x] * 0x800080u);
-                            }
-#pragma unroll
-                            for (int i = 0; i < (half_word ? 1 : 2); ++i)
-                                cache::mma_f16(acc[2 * x + i][0], h[0][2 * i], h[0][2 * i + 1], h[1][2 * i], h[1][2 * i + 1], b0,
-                                               b1);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int x = 0; x < VX; ++x) {
-                        // the channels of a word, of keys 2 c and 2 c + 1, and of the two 8 behind them
-                        const bool half_word = x == VX - 1 && D % 64 != 0;
-                        uint32_t even[2][4], odd[2][4];
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const uint32_t a = vw[2 * r][x], z = vw[2 * r + 1][x];
-                            const uint32_t by = vs[2 * r][x] * 0x80u + vs[2 * r + 1][x] * 0x800000u;
-                            halves8((a & 0x0F0F0F0Fu) | (z << 4 & 0xF0F0F0F0u), even[r]);
-                            halves8((a >> 4 & 0x0F0F0F0Fu) | (z & 0xF0F0F0F0u), odd[r]);
-#pragma unroll
-                            for (int i = 0; i < (half_word ? 2 : 4); ++i) {
-                                even[r][i] = times(even[r][i], by);
-                                odd[r][i] = times(odd[r][i], by);
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < (half_word ? 2 : 4); ++i)
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                cache::mma_f16(acc[4 * x + i][nt], even[0][i], odd[0][i], even[1][i], odd[1][i], pb[j][nt][0],
-                                               pb[j][nt][1]);
-                    }
-                }
+                run.values(vw, vs, pb[j], key0[j], masked);
             }
         }
 
@@ -762,29 +437,29 @@ __global__ void __launch_bounds__(Dec4Cfg<D, ROWS>::THREADS, Dec4Cfg<D, ROWS>::B
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    float sum = l[nt][u];
+                    float sum = run.l[nt][u];
                     sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                     const int row = warp * 8 + 2 * c + u;
                     if (g == 0) {
-                        mm[row] = unset >> (2 * nt + u) & 1u ? -INFINITY : m[nt][u];
+                        mm[row] = run.unset >> (2 * nt + u) & 1u ? -INFINITY : run.m[nt][u];
                         ml[row] = sum;
                     }
-                    if constexpr (PAIRS) {
+                    if constexpr (R::PAIRS) {
                         // rows 2 (c & 1), + 1; channels: those of v_column, first ones at c < 2, second at c >= 2
                         float *to = mo + (warp * 8 + 2 * (c & 1) + u) * F::OROW + (c >> 1);
 #pragma unroll
                         for (int x = 0; x < VW; ++x) {
-                            to[cache::v_column<D>(g, x)] = acc[x][0][u];
-                            to[cache::v_column<D>(g, x) + 2] = acc[x][0][u + 2];
+                            to[cache::v_column<D>(g, x)] = run.acc[x][0][u];
+                            to[cache::v_column<D>(g, x) + 2] = run.acc[x][0][u + 2];
                         }
                     } else {
 #pragma unroll
                         for (int x = 0; x < VW; ++x)
                             *reinterpret_cast<float4 *>(mo + row * F::OROW + cache::v_column<D>(g, x)) =
-                                make_float4(acc[2 * x][nt][u], acc[2 * x][nt][u + 2], acc[2 * x + 1][nt][u],
-                                            acc[2 * x + 1][nt][u + 2]);
+                                make_float4(run.acc[2 * x][nt][u], run.acc[2 * x][nt][u + 2], run.acc[2 * x + 1][nt][u],
+                                            run.acc[2 * x + 1][nt][u + 2]);
                     }
                 }
                 if (!meet())

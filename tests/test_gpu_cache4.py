@@ -374,6 +374,40 @@ def test_more_segments_than_blocks():
     assert status() == 0
 
 
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("G,Nq", [(1, 1), (4, 1), (1, 3), (8, 1), (2, 4), (5, 1)])
+def test_a_warp_a_segment(d, page, G, Nq):
+    """More segments than any grid of blocks, of up to 256 keys: what lies behind the last key is no number."""
+    lens = [0, 1, 2, 3, 15, 16, 17, 31, 32, 33, 63, 64, 65, 255, 256] + [(53 * b) % 257 for b in range(155)]
+    table, pool = pages_for(lens, page, 5)
+    ref = Ref(pool, 4, page, d, seed=6)
+    for b, n in enumerate(lens):
+        if n % page:
+            last = table[b, n // page].long()
+            ref.k_scale[last, :, n % page:] = 0xFF
+            ref.v_scale[last, :, n % page:] = 0xFF
+    attend(ref, table, lens, normal((170, 4 * G, Nq, d), "bf16" if G > 2 else "fp16", 7), Nq > 1)
+    assert status() == 0
+
+
+def test_a_warp_a_segment_of_many_pages():
+    lens = [1 + 11 * b % 600 for b in range(400)]
+    table, pool = pages_for(lens, 16, 3)
+    ref = Ref(pool, 4, 16, 64, seed=4)
+    attend(ref, table, lens, normal((400, 8, 1, 64), "fp16", 5))
+    assert status() == 0
+
+
+def test_a_warp_a_segment_bad_pages_and_lengths():
+    lens = [100, 60, 33, -4, 10 ** 6] + [20] * 700
+    table, pool = pages_for([min(n, 112) for n in lens], 16, 4)
+    ref = Ref(pool, 1, 16, 128)
+    table[0, 2], table[1, 0], table[2, :], table[3:5, 3], table[9, 1] = pool, -1, 2 ** 31 - 1, -2 ** 31, -1
+    attend(ref, table, lens, normal((705, 8, 1, 128), "fp16", 1))
+    assert status() == 6
+
+
 def test_query_strides_scale_and_given_outputs():
     d, lens = 128, [90, 200]
     table, pool = pages_for(lens, 64, 4)

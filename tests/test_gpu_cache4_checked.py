@@ -1,5 +1,5 @@
-"""The checked build over the new operators: attention over the 4-bit cache at every page size and head dimension, whole
-segments and shared ones, and the calls around it."""
+"""The checked build: attention over the 4-bit cache at every page size and head dimension, segments of a block, of
+several and of a warp, and the calls around it."""
 import pytest
 import torch
 
@@ -31,6 +31,20 @@ def test_attention(checked, d, page, G, Nq):
         n = torch.tensor(lens, dtype=torch.int32).cuda()
         o, lse = fa.fa_decode_cache4(q.cuda(), ref.to("cuda"), table.cuda(), n, causal=True)
         within(o, lse, attend_bounds(ref, q, table, lens, d ** -0.5, True))
+
+
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("G,Nq", [(2, 2), (3, 2)])
+def test_attention_of_many_segments(checked, d, page, G, Nq):
+    import attention_forward_02_gb300 as fa
+    lens = [(71 * b) % 257 for b in range(335)]
+    table, pool = pages_for(lens, page, 1)
+    ref = Ref(pool, 2, page, d, 2)
+    q = torch.randn(len(lens), 2 * G, Nq, d, generator=torch.Generator().manual_seed(3)).half()
+    n = torch.tensor(lens, dtype=torch.int32).cuda()
+    o, lse = fa.fa_decode_cache4(q.cuda(), ref.to("cuda"), table.cuda(), n, causal=True)
+    within(o, lse, attend_bounds(ref, q, table, lens, d ** -0.5, True))
 
 
 def test_around_it(checked):

@@ -45,6 +45,20 @@ def test_tokens(d, rot, interleaved, dtype, backward):
     assert torch.equal(x, before)
 
 
+@pytest.mark.parametrize("d,rot", [(32, 32), (32, 8), (64, 64), (64, 16), (96, 96), (96, 24), (128, 128), (128, 56)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,Hq,H", [(1, 32, 8), (3, 29, 5), (9, 64, 8), (40, 24, 3), (200, 16, 1)])
+@pytest.mark.parametrize("backward", [False, True])
+def test_few_tokens_of_many_heads(d, rot, interleaved, T, Hq, H, backward):
+    rope = fa.FARope.new(rot, interleaved=interleaved)
+    x = normal((T, Hq + H, d), "bf16", d + rot).to(DEV)
+    pos = torch.tensor([[131071, -1, 2 ** 31 - 1, 0, 5][t % 5] if t % 3 else t for t in range(T)], dtype=torch.int32)
+    y = torch.full_like(x, 7.0)
+    fa.fa_rope(x[:, :Hq], x[:, Hq:], rope, pos.to(DEV), q_out=y[:, :Hq], k_out=y[:, Hq:], backward=backward)
+    check(y.transpose(0, 1)[None], x.transpose(0, 1)[None], rope, pos[None], backward)
+    assert torch.equal(y[pos.to(DEV) < 0], x[pos.to(DEV) < 0]) and torch.equal(y[..., rot:], x[..., rot:])
+
+
 @pytest.mark.parametrize("B,Hq,H,N,d", [(1, 1, 1, 1, 128), (2, 3, 3, 65, 64), (3, 8, 1, 7, 32), (1, 40, 8, 1, 128),
                                         (2, 5, 0, 33, 96), (1, 0, 4, 9, 64), (4, 128, 2, 1, 128), (1, 2, 2, 1500, 128)])
 @pytest.mark.parametrize("kind", ["none", "row", "each"])
