@@ -29,7 +29,7 @@ struct Cache4State {
 };
 Cache4State g_cache4[kMaxDevices];
 
-// Units (128 keys) of a segment that one block may take whole: one launch in place of two,
+// Units of 128 keys of a segment that one block may take whole: one launch in place of two,
 // but the units one after the other.  8 KV heads of 4 rows, whole / shared out, us on the
 // GPU (in a graph):
 //                      1 unit       4 units      8 units      12 units
@@ -351,12 +351,13 @@ fa_status_t fa_decode_cache4(const fa_cache4_t *cache, const void *q, long long 
             w.log2_box = box == 128 ? 7 : box == 64 ? 6 : box == 32 ? 5 : 4;
             const long long segments = static_cast<long long>(B) * cache->heads * w.groups;
             const long long units = (static_cast<long long>(max_pages) * cache->page - 1) / F::STEP + 1;  // of one, at most
+            const long long bound = (static_cast<long long>(max_pages) * cache->page + 127) / 128;  // units of 128 keys
             long long blocks = static_cast<long long>(sms) * F::BLOCKS;
             if (blocks > fa::cache::kMaxBlocks)
                 blocks = fa::cache::kMaxBlocks;
-            if (ROWS <= 8 && segments > blocks && units <= std::min(kWholeUnits, kShortUnits + segments / blocks))
+            if (ROWS <= 8 && segments > blocks && bound <= std::min(kWholeUnits, kShortUnits + segments / blocks))
                 return launch_short<D, ROWS>(w, segments, o, lse, dtype, cs);
-            w.whole = units <= kWholeUnits && segments <= blocks;
+            w.whole = bound <= kWholeUnits && segments <= blocks;
             if (w.whole)
                 blocks = segments;
             else if (segments * units < blocks)

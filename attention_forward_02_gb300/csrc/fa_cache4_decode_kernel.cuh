@@ -22,6 +22,10 @@
 //    as much as OPEN units, and count so when the runs are dealt out: the slowest block was
 //    12 to 26 % over the mean before (OPEN 0, 1, 2, 3: 130, 128, 125, 128 us for those 64
 //    sequences, 70, 67, 66, 66 for the 16 of 16 rows).
+//  - Two stages of 128 keys hide what latency there is (three: 113.5 us, two 115.1), so the
+//    16-row warps of d = 128, two blocks an SM, take stages of 256: half the visits to the
+//    ring (61.0 -> 58.4 us; 32 and 64 rows a head as before, and d = 96 and 64 up to 5 %
+//    slower in short contexts, so there not).
 //
 // What bounds it: instructions.  16 keys of d = 128 are 2,304 bytes, for which HBM takes some
 // 100 clocks of an SM.  A tile costs a warp 260 instructions (four rows) to 350 (sixteen),
@@ -32,7 +36,7 @@
 //
 // Measured on the GPU, d = 128, 8 KV heads: 64 sequences of up to 16,384 keys, 4 rows a head,
 // 675 MB: 113 us, 6.0 TB/s, 88 % of the measured copy rate; 16 of them 41 (4 rows), 45 (8)
-// and 61 (16, two blocks an SM: 168 registers); one of 131,072 keys, 8 rows, 151 MB: 37;
+// and 58 (16, two blocks an SM: 168 registers); one of 131,072 keys, 8 rows, 151 MB: 37;
 // some 10 us of these are start, merge and end.  d = 64, 32 heads of a row, 8 x up to 8,000
 // keys, 78 MB: 25; d = 96 and 32: 53 and 36 % of the copy rate, the softmax's instructions
 // being the same for fewer bytes.
@@ -51,16 +55,16 @@ using cache::kTailPart;
 // As DecCfg of the 8-bit cache, for warps of ROWS query rows.
 template <int D, int ROWS>
 struct Dec4Cfg {
-    static constexpr int LOG2_STEP = 7;
+    static constexpr int LOG2_STEP = D == 128 && ROWS == 16 ? 8 : 7;
     static constexpr int STEP = 1 << LOG2_STEP;
     static constexpr int SUBS = STEP / kTile;
     static constexpr int STAGE = STEP * D / 8 * 9;  // bytes
     static constexpr int WARPS = 4;                 // that compute
     static constexpr int THREADS = 32 * (WARPS + 1);
     static constexpr int BLOCKS = D == 32 ? 4 : D >= 96 && ROWS == 16 ? 2 : 3;  // an SM
-    static constexpr int STAGES = D == 128 && BLOCKS == 3 ? 3 : D == 96 && BLOCKS == 3 ? 4 : 5;
+    static constexpr int STAGES = D == 128 ? (ROWS == 16 ? 2 : 3) : D == 96 && BLOCKS == 3 ? 4 : 5;
     static constexpr int J = 2;                     // tiles of a warp at once
-    static constexpr int OPEN = 2;                  // units that a segment's begin and end cost
+    static constexpr int OPEN = 256 / STEP;         // units that a segment's begin and end cost
     static_assert(SUBS >= J * WARPS, "every warp has tiles of a stage");
     static constexpr int OROW = D + 4;
     static constexpr int META_OFF = STAGES * STAGE;
@@ -323,7 +327,8 @@ __global__ void __launch_bounds__(Dec4Cfg<D, ROWS>::THREADS, Dec4Cfg<D, ROWS>::B
         const uint32_t at = (row >> w.log2_box) * box_bytes;
         return make_uint2(at + in_box * (D / 2), at + box * (D / 2) + in_box * (D / 16));
     };
-    uint2 own[J];  // of this warp's tiles, with eight rows a block the same in every stage
+    static_assert(NT > 1 || F::SUBS == J * F::WARPS, "with eight rows a block a warp has the same tiles of every stage");
+    uint2 own[J];  // ... these
 #pragma unroll
     for (int j = 0; j < J; ++j)
         own[j] = place(wk * J + j);
