@@ -28,7 +28,7 @@
 //    slower in short contexts, so there not).
 //
 // What bounds it: instructions.  16 keys of d = 128 are 2,304 bytes, for which HBM takes some
-// 100 clocks of an SM.  A tile costs a warp 260 instructions (four rows) to 350 (sixteen),
+// 100 clocks of an SM.  A tile costs a warp 260 instructions (four rows) to 330 (sixteen),
 // and pipes that take two clocks an instruction: 64 conversions on that of logic, 64
 // scalings on the multiplying one, and products of 8.4 clocks, 16 (32) a tile; the three
 // overlap only in part (32 + 32 + 8 of them take 105 clocks of a scheduler, each kind alone

@@ -6,7 +6,8 @@
 // goes through it, which also words the error.  What it saves is time on the host, which is most of a small call: a
 // fa_decode_cache of one sequence of 500 keys takes 9.7 us in place of 26 (8.4 of
 // them on the GPU), a fa_cache_write of one token 4.2 in place of 12, a choice of
-// pages and the attention over them 22 in place of 55.
+// pages and the attention over them 22 in place of 55, a fa_rope of one token 5.1
+// (2.1 on the GPU), a fa_cache4_write of a step 2.7.
 //
 // A CPython module without state but the addresses of the library's functions,
 // which cache.py sets (bind), so that either build of the library can be used.

@@ -7,7 +7,7 @@
 // slot.  So one block does all of a step: sums over the batch, pages and, of up to kOwnRows
 // rows, positions and slots, by searches in shared memory.  More rows (prompts) go to a
 // second launch, which reads what the first has written.  On the GPU 256 sequences of 4
-// tokens take 4.4 us, and as much to give some back; 64 with 130,000 new tokens 8.3 (one
+// tokens take 4.2 us, and as much to give some back; 64 with 130,000 new tokens 8.3 (one
 // cluster of eight blocks for all of it took 22.8, the rows bound by those eight SMs).
 #pragma once
 
