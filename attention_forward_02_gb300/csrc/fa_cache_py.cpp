@@ -163,7 +163,9 @@ bool output(PyObject *given, at::IntArrayRef shape, ScalarType type, int device,
     return true;
 }
 // A contiguous tensor of its own at an element of a buffer's memory.  An allocation is 1.2 us
-// of a small call; the outputs of one share theirs.
+// of a small call; the outputs of one share theirs, up to kShared elements (two that are larger
+// are worth having apart: either may be freed before the other).
+constexpr int64_t kShared = 1 << 18;
 Tensor part(const Tensor &buffer, int64_t at, at::IntArrayRef shape)
 {
     auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(buffer.storage()), buffer.key_set(), buffer.dtype());
@@ -178,8 +180,8 @@ bool outputs(PyObject *const (&given)[2], at::IntArrayRef shape0, at::IntArrayRe
              Tensor (&t)[2])
 {
     const at::IntArrayRef shapes[2] = {shape0, shape1};
-    if (given[0] == Py_None && given[1] == Py_None) {
-        const int64_t n = c10::multiply_integers(shape0);
+    const int64_t n = c10::multiply_integers(shape0);
+    if (given[0] == Py_None && given[1] == Py_None && n + c10::multiply_integers(shape1) <= kShared) {
         const Tensor both = empty({up_to_128(n) + c10::multiply_integers(shape1)}, type, device);
         t[0] = part(both, 0, shape0);
         t[1] = part(both, up_to_128(n), shape1);
@@ -582,7 +584,7 @@ PyObject *py_rope(PyObject *, PyObject *const *a, Py_ssize_t n)
                 return handed_back();
             type = own;
             PyObject *given = a[5 + i];
-            if (given == Py_None && x[1] && a[5] == Py_None && a[6] == Py_None) {
+            if (given == Py_None && x[1] && a[5] == Py_None && a[6] == Py_None && x[0]->numel() + x[1]->numel() <= kShared) {
                 if (i == 0) {  // both in one allocation
                     const int64_t n = up_to_128(t->numel());
                     y[1] = empty({n + x[1]->numel()}, t->scalar_type(), device);

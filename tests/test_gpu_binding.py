@@ -116,6 +116,18 @@ def test_outputs_of_one_allocation():
             assert t.storage_offset() * t.element_size() + t.nbytes <= t.untyped_storage().nbytes()
 
 
+def test_large_outputs_have_memory_of_their_own():
+    """Either may be freed or saved without the other."""
+    rope = fa.FARope.new(128)
+    x = torch.randn(600, 8, 128, device=DEV, dtype=torch.float16)
+    cache = fa.FACache4(torch.zeros(9, 3, 128, 144, dtype=torch.uint8, device=DEV))
+    table = torch.zeros(1, 6, dtype=torch.int32, device=DEV)
+    for group in (fa.fa_rope(x, x[:, :3], rope), fa.fa_cache4_read(cache, table, i32([700]), 768)):
+        for t in group:
+            assert t.untyped_storage().nbytes() < 2 * t.nbytes and t.storage_offset() == 0
+        assert group[0].untyped_storage().data_ptr() != group[1].untyped_storage().data_ptr()
+
+
 def test_streams_and_empty_calls_go_the_longer_way():
     rope = fa.FARope.new(64)
     x = torch.randn(5, 2, 64, device=DEV, dtype=torch.float16)
