@@ -63,7 +63,12 @@ class FARope(NamedTuple):
             raise FAError(2, "rot must be a multiple of 8, got %s" % (rot,))
         on_channels = 1.0
         if radians is None:
-            radians, on_channels = _scaled(rot, float(base), scaling, float(factor), trained, float(fast), float(slow))
+            try:
+                radians, on_channels = _scaled(rot, float(base), scaling, float(factor), trained, float(fast), float(slow))
+            except (OverflowError, ValueError, ZeroDivisionError):
+                raise FAError(1, "these numbers give no frequencies") from None
+            if not all(math.isfinite(x) for x in (*radians, on_channels)):
+                raise FAError(1, "these numbers give no finite frequencies")
         else:
             radians = [float(x) for x in radians]
             if len(radians) != rot // 2 or not all(math.isfinite(x) for x in radians):

@@ -78,7 +78,9 @@ def test_python_refusals():
         fa.fa_rope(x, None, rope)
     for args in (dict(rot=12), dict(rot=0), dict(rot=8.0), dict(rot=8, scaling="other"), dict(rot=8, base=-1.0),
                  dict(rot=8, scaling="yarn"), dict(rot=8, scaling="linear", factor=0.0), dict(rot=8, radians=[1.0]),
-                 dict(rot=8, radians=[1.0, float("nan"), 1.0, 1.0]), dict(rot=8, scaling="bands", trained=10, fast=1.0)):
+                 dict(rot=8, radians=[1.0, float("nan"), 1.0, 1.0]), dict(rot=8, scaling="bands", trained=10, fast=1.0),
+                 dict(rot=8, base=1.0, scaling="yarn", trained=100), dict(rot=64, base=1e300, scaling="base", factor=1e300),
+                 dict(rot=8, scaling="yarn", trained=100, fast=float("inf")), dict(rot=8, base=float("nan"))):
         with pytest.raises(fa.FAError):
             fa.FARope.new(device="cpu", **args)
 
