@@ -78,8 +78,10 @@ bool apart(const View &a, const View &b)
 // 80.0, 30,000 97.2 and 94.0 (half as many units: 41.2, 79.6, 96.9).
 constexpr int kFewUnits = 256, kFewHeads = 16, kUnits = 512, kManyUnits = 4096;
 
-// A stride: not negative, and small enough for the sums here.
-bool fine(long long s) { return s >= 0 && s < 1ll << 40; }
+// A stride: not negative, and what it spans small enough for the sums here.
+bool fine(long long s, int extent) { return s >= 0 && (extent <= 1 || s <= (1ll << 40) / (extent - 1)); }
+
+constexpr int kMaxHeads = 65535;
 
 // Checks rows and fills their views; strides of dimensions of one become 0.
 fa_status_t check_rows(fa_rope_rows_t &r, int B, int N, int d, View *x, View *y)
@@ -89,8 +91,8 @@ fa_status_t check_rows(fa_rope_rows_t &r, int B, int N, int d, View *x, View *y)
     for (int i = 0; i < 6; ++i)
         if (extent[i / 2] == 1)
             *all[i] = 0;
-    for (const long long *s : all)
-        if (!fine(*s))
+    for (int i = 0; i < 6; ++i)
+        if (!fine(*all[i], extent[i / 2]))
             return FA_ERR_INVALID_ARG;
     if (!r.x || !r.y)
         return FA_ERR_INVALID_ARG;
@@ -118,12 +120,12 @@ fa_status_t fa_rope(const fa_rope_t *rope, const fa_rope_rows_t *q, const fa_rop
         !std::isfinite(rope->factor) || (rope->interleaved != 0 && rope->interleaved != 1) || rope->pairs < 1)
         return FA_ERR_INVALID_ARG;
     if ((d != 32 && d != 64 && d != 96 && d != 128) || (dtype != FA_FP16 && dtype != FA_BF16) || rope->pairs % 4 != 0 ||
-        rope->pairs > d / 2)
+        rope->pairs > d / 2 || q->heads > kMaxHeads || (k && k->heads > kMaxHeads))
         return FA_ERR_UNSUPPORTED;
     const bool some_q = q->heads > 0, some_k = k && k->heads > 0;
     if (B == 0 || N == 0 || (!some_q && !some_k))
         return FA_OK;  // empty problem
-    if (!rope->turns || (positions && !fine(position_stride)))
+    if (!rope->turns || (positions && !fine(position_stride, B)))
         return FA_ERR_INVALID_ARG;
     if (u(rope->turns) & 7u || u(positions) & 3u)
         return FA_ERR_MISALIGNED;

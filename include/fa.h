@@ -436,7 +436,7 @@ typedef struct {
     void *y;
     long long x_batch, x_head, x_row;
     long long y_batch, y_head, y_row;
-    int heads;
+    int heads; /* at most 65,535 */
 } fa_rope_rows_t;
 
 /*

@@ -33,6 +33,8 @@ def call(pairs=32, interleaved=0, factor=1.0, turns=TURNS, q=Q, qo=QO, k=K, ko=K
     (dict(d=48), 2), (dict(dtype=2), 2), (dict(pairs=30), 2), (dict(pairs=36), 2), (dict(pairs=0), 1), (dict(pairs=-4), 1),
     (dict(factor=float("nan")), 1), (dict(factor=float("inf")), 1), (dict(interleaved=2), 1), (dict(backward=2), 1),
     (dict(B=-1), 1), (dict(N=-1), 1), (dict(Hq=-1), 1), (dict(H=-1), 1),
+    (dict(Hq=65536), 2), (dict(H=2 ** 31 - 1), 2), (dict(N=2 ** 30, q_in=(64, 64, 1 << 34)), 1),
+    (dict(B=2 ** 30, pos_stride=1 << 34), 1),
     (dict(turns=0), 1), (dict(q=0), 1), (dict(qo=0), 1), (dict(k=0), 1), (dict(ko=0), 1),
     (dict(q=Q + 8), 3), (dict(qo=QO + 2), 3), (dict(turns=TURNS + 4), 3), (dict(pos=POS + 2), 3),
     (dict(q_in=(8 * 5 * 64, 5 * 64, 66)), 3), (dict(k_out=(1000, 500, 68)), 3),
