@@ -31,8 +31,9 @@ SOURCES = [os.path.join(CSRC, f) for f in ("fa_fwd.cu", "fa_bwd.cu", "fa_decode.
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_fwd_kernel.cuh", "fa1_fwd_kernel.cuh",
                                                   "fa_bwd_kernel.cuh", "fa_decode_kernel.cuh", "fa_decode_tc_kernel.cuh",
                                                   "fa_cache_kernel.cuh", "fa_cache_decode_kernel.cuh",
-                                                  "fa_cache4_kernel.cuh", "fa_cache4_running.cuh",
+                                                  "fa_cache4_kernel.cuh", "fa_cache4_run.cuh", "fa_cache4_running.cuh",
                                                   "fa_cache4_decode_kernel.cuh", "fa_cache4_short_kernel.cuh",
+                                                  "fa_cache4_tc_kernel.cuh",
                                                   "fa_pages_kernel.cuh", "fa_rope_kernel.cuh",
                                                   "fa_cache_host.h", "fa_common.cuh",
                                                   "fa_host.h", "sm100_ptx.cuh")] + [

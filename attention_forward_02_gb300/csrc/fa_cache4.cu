@@ -13,6 +13,7 @@
 #include "fa_cache4_decode_kernel.cuh"
 #include "fa_cache4_kernel.cuh"
 #include "fa_cache4_short_kernel.cuh"
+#include "fa_cache4_tc_kernel.cuh"
 #include "fa_cache_host.h"
 #include "fa_host.h"
 
@@ -81,6 +82,14 @@ cudaError_t set_smem_attr()
     return e;
 }
 template <int D>
+cudaError_t set_tc_smem_attr()
+{
+    const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    constexpr int bytes = fa::cache4::Tc4Cfg<D>::SMEM;
+    const cudaError_t e = cudaFuncSetAttribute(fa::cache4::fa_cache4_tc_kernel<D, __half>, a, bytes);
+    return e == cudaSuccess ? cudaFuncSetAttribute(fa::cache4::fa_cache4_tc_kernel<D, __nv_bfloat16>, a, bytes) : e;
+}
+template <int D>
 cudaError_t set_smem_attrs()
 {
     cudaError_t e = set_smem_attr<D, 4>();
@@ -98,6 +107,8 @@ void init_cache4(Cache4State &st)
     if (st.err == cudaSuccess) st.err = set_smem_attrs<64>();
     if (st.err == cudaSuccess) st.err = set_smem_attrs<96>();
     if (st.err == cudaSuccess) st.err = set_smem_attrs<128>();
+    if (st.err == cudaSuccess) st.err = set_tc_smem_attr<96>();
+    if (st.err == cudaSuccess) st.err = set_tc_smem_attr<128>();
 }
 
 // The current device's state and SM count.
@@ -342,30 +353,22 @@ fa_status_t fa_decode_cache4(const fa_cache4_t *cache, const void *q, long long 
     w.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan_bytes(B));
     w.part_m = w.part_o + part_rows * cache->d;
     w.part_l = w.part_m + part_rows;
+    const long long segments = static_cast<long long>(B) * cache->heads * w.groups;
+    const long long bound = (static_cast<long long>(max_pages) * cache->page + 127) / 128;  // units of 128 keys
     return by_dim(cache->d, [&](auto dim) {
         constexpr int D = decltype(dim)::value;
-        const auto with_rows = [&](auto warp_rows) {
-            constexpr int ROWS = decltype(warp_rows)::value;
-            using F = fa::cache4::Dec4Cfg<D, ROWS>;
+        // A kernel of F's runs: its grid, its launch, and the merge's.
+        const auto run = [&](auto config, int per_sm, const auto &launch) {
+            using F = decltype(config);
             const int box = cache->page < F::STEP ? cache->page : F::STEP;
             w.log2_box = box == 128 ? 7 : box == 64 ? 6 : box == 32 ? 5 : 4;
-            const long long segments = static_cast<long long>(B) * cache->heads * w.groups;
             const long long units = (static_cast<long long>(max_pages) * cache->page - 1) / F::STEP + 1;  // of one, at most
-            const long long bound = (static_cast<long long>(max_pages) * cache->page + 127) / 128;  // units of 128 keys
-            long long blocks = static_cast<long long>(sms) * F::BLOCKS;
-            if (blocks > fa::cache::kMaxBlocks)
-                blocks = fa::cache::kMaxBlocks;
-            if (ROWS <= 8 && segments > blocks && bound <= std::min(kWholeUnits, kShortUnits + segments / blocks))
-                return launch_short<D, ROWS>(w, segments, o, lse, dtype, cs);
+            long long blocks = std::min<long long>(static_cast<long long>(sms) * per_sm, fa::cache::kMaxBlocks);
             w.whole = bound <= kWholeUnits && segments <= blocks;
-            if (w.whole)
-                blocks = segments;
-            else if (segments * units < blocks)
-                blocks = segments * units;
+            blocks = w.whole ? segments : std::min(blocks, segments * units);
             return by_type(dtype, [&](auto t) {
                 using T = decltype(t);
-                if (!launch_dependent(decode_kernel<D, ROWS, T>(), static_cast<unsigned>(blocks), F::THREADS, F::SMEM, cs, w,
-                                      static_cast<T *>(o), lse))
+                if (!launch(t, static_cast<unsigned>(blocks)))
                     return FA_ERR_CUDA;
                 if (w.whole)
                     return launched();
@@ -378,11 +381,29 @@ fa_status_t fa_decode_cache4(const fa_cache4_t *cache, const void *q, long long 
                         : launch_dependent(fa::cache::fa_cache_combine_kernel<D, T, kWarps, F::LOG2_STEP, F::OPEN>,
                                            static_cast<unsigned>(rows), fa::cache::kCombineThreads, 0, cs, w,
                                            static_cast<T *>(o), lse, rows_block, rows);
-                if (!second)
-                    return FA_ERR_CUDA;
-                return launched();
+                return second ? launched() : FA_ERR_CUDA;
             });
         };
+        const auto with_rows = [&](auto warp_rows) {
+            constexpr int ROWS = decltype(warp_rows)::value;
+            using F = fa::cache4::Dec4Cfg<D, ROWS>;
+            const long long blocks = std::min<long long>(static_cast<long long>(sms) * F::BLOCKS, fa::cache::kMaxBlocks);
+            if (ROWS <= 8 && segments > blocks && bound <= std::min(kWholeUnits, kShortUnits + segments / blocks))
+                return launch_short<D, ROWS>(w, segments, o, lse, dtype, cs);
+            return run(F(), F::BLOCKS, [&](auto t, unsigned grid) {
+                using T = decltype(t);
+                return launch_dependent(decode_kernel<D, ROWS, T>(), grid, F::THREADS, F::SMEM, cs, w, static_cast<T *>(o), lse);
+            });
+        };
+        if constexpr (D >= 96) {
+            using F = fa::cache4::Tc4Cfg<D>;
+            if (w.R > F::ROWS / 2)  // both sides' figures are at the kernel
+                return run(F(), 1, [&](auto t, unsigned grid) {
+                    using T = decltype(t);
+                    return launch_dependent(fa::cache4::fa_cache4_tc_kernel<D, T>, grid, F::THREADS, F::SMEM, cs, w,
+                                            static_cast<T *>(o), lse);
+                });
+        }
         return w.R <= 4 ? with_rows(Dim<4>()) : w.R <= 8 ? with_rows(Dim<8>()) : with_rows(Dim<16>());
     });
 }

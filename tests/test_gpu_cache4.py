@@ -361,6 +361,86 @@ def test_every_layout_of_rows(R):
     attend(ref, table[2:], lens[2:], normal((2, R, 1, d), "fp16", R))
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d", [96, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("G,Nq", [(33, 1), (12, 3), (16, 4), (9, 16), (4, 10)])
+def test_many_rows(dtype, d, page, G, Nq):
+    """Groups of 64 rows, whole segments and shared ones, the last group not full."""
+    for lens in ([3000, 0, 1, 129, 700], [300, 128, 5], [40] * 90):
+        table, pool = pages_for(lens, page, 5)
+        ref = Ref(pool, 2, page, d, seed=6)
+        attend(ref, table, lens, normal((len(lens), 2 * G, Nq, d), dtype, 7), Nq > 1)
+    assert status() == 0
+
+
+@pytest.mark.parametrize("d", [96, 128])
+@pytest.mark.parametrize("by", [0.0, 8.0, 300.0])
+def test_many_rows_scores_of_any_size(d, by):
+    lens = [1500, 140]
+    table, pool = pages_for(lens, 16, 4)
+    ref = Ref(pool, 2, 16, d, seed=7, lowest=0x40, highest=0x78)
+    q = normal((2, 20, 2, d), "bf16", 3, by)
+    attend(ref, table, lens, q, True)
+    at = torch.arange(1500)                  # keys that grow along the sequence
+    ref.k_scale[table[0, at // 16].long(), :, at % 16] = (0x40 + 0x38 * (at / 1500.0)).long()[:, None, None].expand(-1, 2, d // 16)
+    attend(ref, table, lens, q, True)
+
+
+@pytest.mark.parametrize("d", [96, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_many_rows_queries_that_are_not_finite(d, bad):
+    lens, G, Nq = [300, 41], 20, 2
+    table, pool = pages_for(lens, 32, 4)
+    ref = Ref(pool, 2, 32, d)
+    q = normal((2, 2 * G, Nq, d), "bf16", 3)
+    want = attend_bounds(ref, q, table, lens, d ** -0.5, True)
+    x = q.clone()
+    x[:, 1, Nq - 1, 5], x[:, G + 12, 0, 9] = bad, bad
+    o, lse = fa.fa_decode_cache4(x.to(DEV), ref.to(DEV), table.to(DEV), i32(lens), causal=True)
+    hit = torch.zeros(2, 2 * G, Nq, dtype=torch.bool)
+    hit[:, 1, Nq - 1], hit[:, G + 12, 0] = True, True
+    assert not torch.isfinite(lse.cpu()[hit]).any()
+    o, lse = o.cpu().double(), lse.cpu().double()
+    assert ((o - want[0]).abs() <= want[2])[~hit].all() and ((lse - want[1]).abs() <= want[3])[~hit].all()
+
+
+@pytest.mark.parametrize("d", [96, 128])
+@pytest.mark.parametrize("page", [16, 64, 128])
+def test_many_rows_what_lies_behind_the_end(d, page):
+    """... and pages that are none, and lengths that are cut."""
+    lens, G, Nq = [1, 37, 130, 1000, 10 ** 6], 10, 4
+    short = [min(n, 1100) for n in lens]
+    table, pool = pages_for(short, page, 2)
+    ref = Ref(pool, 2, page, d, seed=1)
+    for b, n in enumerate(short):
+        if n % page:
+            last = table[b, n // page].long()
+            for x in (ref.k_scale, ref.v_scale):
+                x[last, :, n % page:] = 0xFF
+    if short[-1] % page:                        # cut to the table's places, the last of which hold none
+        ref.k_scale[table[-1, short[-1] // page].long()] = 0x60
+        ref.v_scale[table[-1, short[-1] // page].long()] = 0x60
+    table[3, 2], table[3, 0] = -1, 2 ** 31 - 1
+    attend(ref, table, lens, normal((5, 2 * G, Nq, d), "fp16", 2), True)
+    assert status() == 6
+
+
+def test_many_rows_twice_the_same_and_on_two_streams():
+    lens = [3000, 17, 900, 64]
+    table, pool = pages_for(lens, 32, 4)
+    ref = Ref(pool, 4, 32, 128)
+    cache, t, n = ref.to(DEV), table.to(DEV), i32(lens)
+    q = normal((4, 64, 4, 128), "bf16", 1).to(DEV)
+    want = fa.fa_decode_cache4(q, cache, t, n, causal=True)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [[fa.fa_decode_cache4(q, cache, t, n, causal=True, stream=s) for _ in range(5)] for s in streams]
+    torch.cuda.synchronize()
+    for o, lse in outs[0] + outs[1]:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
 def test_more_segments_than_blocks():
     """Short sequences, more of them with their heads than blocks: runs over many whole segments."""
     lens = [(37 * b) % 140 for b in range(200)]
