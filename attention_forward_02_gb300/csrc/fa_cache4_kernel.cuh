@@ -1,6 +1,6 @@
 // fa_cache4_kernel.cuh -- the 4-bit paged KV cache on sm_103a: writing rows into
 // its slots and reading sequences back.  The attention over it is in
-// fa_cache4_decode_kernel.cuh.
+// fa_cache4_decode_kernel.cuh, fa_cache4_short_kernel.cuh and fa_cache4_tc_kernel.cuh.
 //
 // Sixteen channels of a token share a scale of 5 exponent and 3 fraction bits; the
 // byte is bits 14 .. 7 of an fp16, so that a shift decodes it.  Codes are e2m1, which

@@ -106,7 +106,7 @@ __device__ __forceinline__ bool find_run(const Work &w, Run &r)
     return true;
 }
 
-// The warp that loads.  base: of the ring of F::STAGES stages; full0: barriers of full stages, and
+// The warp that loads.  sbase: of the ring of F::STAGES stages; full0: barriers of full stages, and
 // behind them of empty ones.
 template <typename F>
 __device__ __forceinline__ void load_run(const Work &w, const Run &r, uint32_t sbase, Stage4 *meta, uint32_t full0,

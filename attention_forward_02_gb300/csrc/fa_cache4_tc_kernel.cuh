@@ -17,8 +17,8 @@
 // P^T is, and with eight warps for both one after the other a unit took a tenth longer.
 //
 // What bounds it: the chain of a unit.  Converting, product, softmax, product take some 6,000
-// clocks, and two units under way make about 2,900 each; HBM would need 800, shared memory, through
-// which every converted byte goes twice, 1,000.  The softmax alone (S^T from TMEM, a barrier of
+// clocks, and two units under way make about 2,900 each, in which 1,700 instructions of a scheduler
+// issue; HBM would need 800, shared memory, through which every converted byte goes twice, 1,000.  The softmax alone (S^T from TMEM, a barrier of
 // four warps for the references, P^T back) is 1,700.
 //
 // Measured on the GPU, 8 KV heads, 64 rows a head, this kernel / the other, us: d = 128, 16
