@@ -223,11 +223,10 @@ __device__ __forceinline__ void load_run(const Work &w, const Run &r, uint32_t s
             }
         }
     }
-    // the computing warps wait for every copy; after a failed wait this one does
-    if (!ok)
-        for (int x = 0; x < S; ++x)
-            if (done > x)
-                drain_bounded(full0 + 8u * x, ((done - 1 - x) / S) & 1);
+    // the block does not end before its copies, whatever made the other warps leave
+    for (int x = 0; x < S; ++x)
+        if (done > x)
+            drain_bounded(full0 + 8u * x, ((done - 1 - x) / S) & 1);
 }
 
 }  // namespace cache4
