@@ -81,13 +81,13 @@ cudaError_t set_smem_attr()
     }
     return e;
 }
-template <int D>
+template <int D, int ROWS>
 cudaError_t set_tc_smem_attr()
 {
     const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    constexpr int bytes = fa::cache4::Tc4Cfg<D>::SMEM;
-    const cudaError_t e = cudaFuncSetAttribute(fa::cache4::fa_cache4_tc_kernel<D, __half>, a, bytes);
-    return e == cudaSuccess ? cudaFuncSetAttribute(fa::cache4::fa_cache4_tc_kernel<D, __nv_bfloat16>, a, bytes) : e;
+    constexpr int bytes = fa::cache4::Tc4Cfg<D, ROWS>::SMEM;
+    const cudaError_t e = cudaFuncSetAttribute(fa::cache4::fa_cache4_tc_kernel<D, ROWS, __half>, a, bytes);
+    return e == cudaSuccess ? cudaFuncSetAttribute(fa::cache4::fa_cache4_tc_kernel<D, ROWS, __nv_bfloat16>, a, bytes) : e;
 }
 template <int D>
 cudaError_t set_smem_attrs()
@@ -107,8 +107,9 @@ void init_cache4(Cache4State &st)
     if (st.err == cudaSuccess) st.err = set_smem_attrs<64>();
     if (st.err == cudaSuccess) st.err = set_smem_attrs<96>();
     if (st.err == cudaSuccess) st.err = set_smem_attrs<128>();
-    if (st.err == cudaSuccess) st.err = set_tc_smem_attr<96>();
-    if (st.err == cudaSuccess) st.err = set_tc_smem_attr<128>();
+    if (st.err == cudaSuccess) st.err = set_tc_smem_attr<96, 64>();
+    if (st.err == cudaSuccess) st.err = set_tc_smem_attr<128, 64>();
+    if (st.err == cudaSuccess) st.err = set_tc_smem_attr<128, 32>();
 }
 
 // The current device's state and SM count.
@@ -396,13 +397,20 @@ fa_status_t fa_decode_cache4(const fa_cache4_t *cache, const void *q, long long 
             });
         };
         if constexpr (D >= 96) {
-            using F = fa::cache4::Tc4Cfg<D>;
-            if (w.R > F::ROWS / 2)  // both sides' figures are at the kernel
+            const auto on_tensor_cores = [&](auto group) {
+                constexpr int ROWS = decltype(group)::value;
+                using F = fa::cache4::Tc4Cfg<D, ROWS>;
                 return run(F(), 1, [&](auto t, unsigned grid) {
                     using T = decltype(t);
-                    return launch_dependent(fa::cache4::fa_cache4_tc_kernel<D, T>, grid, F::THREADS, F::SMEM, cs, w,
+                    return launch_dependent(fa::cache4::fa_cache4_tc_kernel<D, ROWS, T>, grid, F::THREADS, F::SMEM, cs, w,
                                             static_cast<T *>(o), lse);
                 });
+            };
+            if (w.R > 32)  // both sides' figures are at the kernel
+                return on_tensor_cores(Dim<64>());
+            if constexpr (D == 128)
+                if (w.R > 16)
+                    return on_tensor_cores(Dim<32>());
         }
         return w.R <= 4 ? with_rows(Dim<4>()) : w.R <= 8 ? with_rows(Dim<8>()) : with_rows(Dim<16>());
     });

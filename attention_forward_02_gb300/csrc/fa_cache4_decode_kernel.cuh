@@ -5,7 +5,7 @@
 // keys dealt out in equal runs to a persistent grid, one warp that copies, four that
 // compute with mma.m16n8k16 on fp16, keys as rows and query rows as columns, parts
 // merged by fa_cache_combine_kernel.  (Many short segments: fa_cache4_short_kernel.cuh; more
-// than 32 rows a head: fa_cache4_tc_kernel.cuh.)  What differs:
+// than 16 rows a head, or 32: fa_cache4_tc_kernel.cuh.)  What differs:
 //  - A page and head is one block of bytes, so that a copy is one bulk copy (four where a
 //    page is larger than a stage).  It is not swizzled: of a tile's 16 rows, row r stands for
 //    the key r ^ (r >> 2 & 1), and then the reads of K are free of bank conflicts and those
@@ -24,7 +24,7 @@
 //    sequences, 70, 67, 66, 66 for the 16 of 16 rows).
 //  - Two stages of 128 keys hide what latency there is (three: 113.5 us, two 115.1), so the
 //    16-row warps of d = 128, two blocks an SM, take stages of 256: half the visits to the
-//    ring (61.0 -> 58.4 us; 32 rows a head as before, and d = 96 and 64 up to 5 %
+//    ring (61.0 -> 58.4 us; d = 96 and 64 up to 5 %
 //    slower in short contexts, so there not).
 //
 // What bounds it: instructions.  16 keys of d = 128 are 2,304 bytes, for which HBM takes some

@@ -1,32 +1,38 @@
 // fa_cache4_tc_kernel.cuh -- decoding attention over the 4-bit paged cache for more than 32 query
-// rows a KV head, with the products on tcgen05.
+// rows a KV head, at d = 128 more than 16, with the products on tcgen05.
 //
 // The kernel of fa_cache4_decode_kernel.cuh converts a tile's codes in registers, once for every
-// 16 rows.  Here they are converted once for the 64 rows of a group, into fp16 tiles of K and V
+// 16 rows.  Here they are converted once for the 32 or 64 rows of a group, into fp16 tiles of K and V
 // in shared memory, swizzled as the tensor cores read them:
-//   S^T = K Q^T     M = 128 keys, N = 64 rows, K = d; K and Q K-major
-//   O^T += V^T P^T  M = 128 (d, the columns of V behind it zero), N = 64 rows, K = 128 keys; V read
+//   S^T = K Q^T     M = 128 keys, N = rows, K = d; K and Q K-major
+//   O^T += V^T P^T  M = 128 (d, the columns of V behind it zero), N = rows, K = 128 keys; V read
 //                   MN-major, and so is P^T, a row of it a key
 // with fp32 accumulators in TMEM, S^T in two buffers.  Runs, ring, records, parts and their merge
 // are those of the other kernel; so is the softmax (P in fp16, 2^kAim under the largest weight, a
 // reference that moves only when one outgrows it).
 //
-// Warps: sixteen do the softmax, four for every 16 rows (a thread has a key of S^T, a channel of
+// Warps: eight or sixteen do the softmax, four for every 16 rows (a thread has a key of S^T, a channel of
 // O^T, and their 16 rows), four convert K and four V, one copies, two issue the products.  K and
 // V of a unit are apart: K's tile is free when its product is done, V's only when the one with
 // P^T is, and with eight warps for both one after the other a unit took a tenth longer.
 //
 // What bounds it: the chain of a unit.  Converting, product, softmax, product take some 6,000
-// clocks, and two units under way make about 2,900 each, in which 1,700 instructions of a scheduler
-// issue; HBM would need 800, shared memory, through which every converted byte goes twice, 1,000.  The softmax alone (S^T from TMEM, a barrier of
+// clocks, and two units under way make about 2,900 each (64 rows), in which 1,700 instructions of a
+// scheduler issue; HBM would need 800, shared memory, through which every converted byte goes twice, 1,000.  The softmax alone (S^T from TMEM, a barrier of
 // four warps for the references, P^T back) is 1,700.
 //
-// Measured on the GPU, 8 KV heads, 64 rows a head, this kernel / the other, us: d = 128, 16
-// sequences of up to 16,384 keys 110 / 182 (2 tiles of P^T, 2 stages: 116), one of 60,000 49 / 80, 64
-// of 2,000 86 / 115, 100 of 700 82 / 99, one of 500 14 / 21, 8 of 100 10 / 12; d = 96 107 / 156 (one tile of
-// P^T: 116), 47 / 66, 85 / 99, 83 / 83, 14 / 18, 10 / 10.  36 rows, d = 128 105 / 179, 100 of 700 74 / 86; d = 96 102 / 153,
-// 73 / 71.  With 32 rows (a group of 32) d = 128 97 / 98 and 64 of 2,000 79 / 66, with 64 and d = 64 99 / 110 and
-// 92 / 75: those stay with the other.  OPEN of 2 and 6: 120 and 118 for the first, 4: 116.
+// Measured on the GPU, 8 KV heads, this kernel / the other, us.  16 sequences of up to 16,384 keys;
+// one of 60,000; 64 of 2,000; 100 of 700; one of 500; 8 of 100:
+//   d = 128, 64 rows  110 / 182  49 / 80  87 / 115  83 / 99  14 / 21  10 / 12
+//            36       105 / 179  47 / 79  79 / 106  74 / 86  14 / 19  10 / 10
+//            32        84 / 98   38 / 48  63 / 66   58 / 58  11 / 13   8.0 / 8.6
+//            18        82 / 97   37 / 46  58 / 60   54 / 51  11 / 12   8.0 / 7.7
+//   d = 96,  64       107 / 156  47 / 66  85 / 99   83 / 83  14 / 18  10 / 10
+//            36       102 / 153  45 / 65  78 / 90   73 / 71  13 / 17  10 / 9
+//            32 (not taken) 84 / 87, 38 / 41, 63 / 57, 59 / 50, 11 / 11, 8.0 / 7.4
+//   d = 64,  64 (not taken) 99 / 110, 43 / 49, 92 / 75, 86 / 65, 13 / 14, 9 / 8
+// Of the first case: two tiles of P^T and two stages 116, one tile of P^T at d = 96 116; OPEN of 2 120,
+// of 6 118 where 4 took 116; four warps that convert 121, sixteen (32 rows) 93.
 #pragma once
 
 #include "fa_cache4_run.cuh"
@@ -35,11 +41,11 @@
 namespace fa {
 namespace cache4 {
 
-template <int D>
+template <int D, int ROWS_>
 struct Tc4Cfg {
-    static_assert(D == 96 || D == 128, "head dims 96, 128");
+    static_assert((D == 96 && ROWS_ == 64) || (D == 128 && (ROWS_ == 32 || ROWS_ == 64)), "a rule below chooses these");
     static constexpr int D_ = D;
-    static constexpr int ROWS = 64;  // of a group
+    static constexpr int ROWS = ROWS_;  // of a group
     static constexpr int LOG2_STEP = 7;
     static constexpr int STEP = 1 << LOG2_STEP;
     static constexpr int STAGE = STEP * D / 8 * 9;
@@ -48,7 +54,7 @@ struct Tc4Cfg {
     static constexpr int LOAD_WARP = SOFTMAX + CONVERT, S_WARP = LOAD_WARP + 1, O_WARP = S_WARP + 1;
     static constexpr int THREADS = 32 * (O_WARP + 1);
     static constexpr int STAGES = 3;
-    static constexpr int PS = D == 128 ? 1 : 2;  // tiles of P^T: a stage is worth more than a second one
+    static constexpr int PS = D == 128 && ROWS == 64 ? 1 : 2;  // tiles of P^T: a stage is worth more than a second one
     static constexpr int KTILE = 2 * kSwAtomBytes;  // K or V of a unit: two 64-column blocks of 128-byte rows
     static constexpr int TILE = 2 * KTILE;          // two of them
     static constexpr int BLK = ROWS * 128;      // a 64-column block of Q
@@ -73,7 +79,7 @@ struct Tc4Cfg {
     static constexpr int BARS = B_DRAIN + 2;
     static constexpr int SLOT_OFF = BAR_OFF + 8 * BARS;  // TMEM address, abort flag
     static constexpr int SMEM = SLOT_OFF + 16 + 1024;    // and room to align the tiles
-    static constexpr uint32_t TM_O = 2 * ROWS, TM_COLS = 256;
+    static constexpr uint32_t TM_O = 2 * ROWS, TM_COLS = ROWS == 64 ? 256 : 128;
     static_assert(SMEM <= 227 * 1024 && RING_OFF % 1024 == 0 && STAGE % 128 == 0, "shared memory");
 };
 
@@ -91,11 +97,11 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int col)
     return static_cast<uint32_t>((col >> 6) * BLK + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4) + (col & 7) * 2);
 }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(Tc4Cfg<D>::THREADS, 1)
+template <int D, int ROWS_, typename T>
+__global__ void __launch_bounds__(Tc4Cfg<D, ROWS_>::THREADS, 1)
     fa_cache4_tc_kernel(const __grid_constant__ Work w, T *__restrict__ out, float *__restrict__ lse)
 {
-    using F = Tc4Cfg<D>;
+    using F = Tc4Cfg<D, ROWS_>;
     constexpr int S = F::STAGES, ROWS = F::ROWS;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
