@@ -18,8 +18,9 @@
 //
 // What bounds it: the chain of a unit.  Converting, product, softmax, product take some 6,000
 // clocks, and two units under way make about 2,900 each (64 rows), in which 1,700 instructions of a
-// scheduler issue; HBM would need 800, shared memory, through which every converted byte goes twice, 1,000.  The softmax alone (S^T from TMEM, a barrier of
-// four warps for the references, P^T back) is 1,700.
+// scheduler issue; HBM would need 800, shared memory, through which every converted byte goes
+// twice, 1,000.  The softmax alone (S^T from TMEM, a barrier of four warps for the references,
+// P^T back) is 1,700.
 //
 // Measured on the GPU, 8 KV heads, this kernel / the other, us.  16 sequences of up to 16,384 keys;
 // one of 60,000; 64 of 2,000; 100 of 700; one of 500; 8 of 100:
@@ -43,7 +44,7 @@ namespace cache4 {
 
 template <int D, int ROWS_>
 struct Tc4Cfg {
-    static_assert((D == 96 && ROWS_ == 64) || (D == 128 && (ROWS_ == 32 || ROWS_ == 64)), "a rule below chooses these");
+    static_assert((D == 96 && ROWS_ == 64) || (D == 128 && (ROWS_ == 32 || ROWS_ == 64)), "what the launch chooses");
     static constexpr int D_ = D;
     static constexpr int ROWS = ROWS_;  // of a group
     static constexpr int LOG2_STEP = 7;
