@@ -25,7 +25,6 @@ struct View {
     {
         return static_cast<size_t>((B - 1) * batch + (N - 1) * row + (H - 1) * head + d) * 2;
     }
-    size_t heads_bytes() const { return static_cast<size_t>((H - 1) * head + d) * 2; }
     // No element twice: each stride of a dimension spans the smaller ones.
     bool distinct() const
     {
@@ -52,22 +51,74 @@ struct View {
     }
 };
 
-// No element in common: different memory, or heads side by side in the rows of one buffer.
+// Where an element of one tensor lies from one of another: a sum of steps, `stride` times a number
+// from lo to hi each.
+struct Step {
+    long long stride;
+    int lo, hi;
+};
+constexpr int kSteps = 6;    // three dimensions of each
+constexpr int kLooks = 4096;  // of the search below; a layout that needs more counts as overlapping
+
+// Whether `at` and steps i .. n - 1, the largest strides first, come to between -d and d; rest_lo[i]
+// and rest_hi[i] are the least and the most that steps from i on add.
+bool reaches(const Step (&step)[kSteps], const long long (&rest_lo)[kSteps + 1], const long long (&rest_hi)[kSteps + 1], int i,
+             int n, long long at, int d, int &looks)
+{
+    if (at + rest_hi[i] <= -d || at + rest_lo[i] >= d)
+        return false;
+    if (i == n || ++looks > kLooks)
+        return true;
+    for (long long x = step[i].lo; x <= step[i].hi; ++x) {
+        // on to the first number that is not too low
+        const long long short_of = -d + 1 - (at + x * step[i].stride + rest_hi[i + 1]);
+        if (short_of > 0)
+            x += (short_of + step[i].stride - 1) / step[i].stride;
+        const long long next = at + x * step[i].stride;
+        if (x > step[i].hi || next + rest_lo[i + 1] >= d)
+            return false;
+        if (reaches(step, rest_lo, rest_hi, i + 1, n, next, d, looks))
+            return true;
+    }
+    return false;
+}
+
+// No element in common.  Different memory, as a rule; else the views' elements may lie between one
+// another's: heads side by side in a row, a head's query, key and value side by side, heads of every batch.
+// Along dimensions with one stride only the distance counts, so that the search tries two or three
+// numbers for each.
 bool apart(const View &a, const View &b)
 {
     if (!overlaps(a.at, a.bytes(), b.at, b.bytes()))
         return true;
-    if ((a.B > 1 && a.batch != b.batch) || (a.N > 1 && a.row != b.row))
-        return false;
-    const View &lo = a.at <= b.at ? a : b, &hi = a.at <= b.at ? b : a;
-    const uintptr_t gap = hi.at - lo.at;
-    const size_t both = static_cast<size_t>(gap) + hi.heads_bytes();
-    const bool rows = a.N == 1 || both <= static_cast<size_t>(a.row) * 2;
-    const bool batches = a.B == 1 || both <= static_cast<size_t>(a.batch) * 2;
-    // rows of both lie within a row's distance: those of one batch follow one another without meeting
-    const bool nested = a.B == 1 || a.N == 1 || static_cast<long long>(a.N) * a.row <= a.batch ||
-                        static_cast<long long>(a.B) * a.batch <= a.row;
-    return gap >= lo.heads_bytes() && rows && batches && nested;
+    const long long of_a[3] = {a.batch, a.row, a.head}, of_b[3] = {b.batch, b.row, b.head};
+    const int ext_a[3] = {a.B, a.N, a.H}, ext_b[3] = {b.B, b.N, b.H};
+    Step step[kSteps];
+    int n = 0;
+    const auto add = [&](long long stride, int lo, int hi) {
+        if (stride == 0 || lo == hi)
+            return;
+        int i = n++;
+        for (; i > 0 && step[i - 1].stride < stride; --i)
+            step[i] = step[i - 1];
+        step[i] = {stride, lo, hi};
+    };
+    for (int i = 0; i < 3; ++i) {
+        if (of_a[i] == of_b[i]) {
+            add(of_a[i], 1 - ext_b[i], ext_a[i] - 1);
+        } else {
+            add(of_a[i], 0, ext_a[i] - 1);
+            add(of_b[i], 1 - ext_b[i], 0);
+        }
+    }
+    long long rest_lo[kSteps + 1], rest_hi[kSteps + 1];
+    rest_lo[n] = rest_hi[n] = 0;
+    for (int i = n - 1; i >= 0; --i) {
+        rest_lo[i] = rest_lo[i + 1] + step[i].lo * step[i].stride;
+        rest_hi[i] = rest_hi[i + 1] + step[i].hi * step[i].stride;
+    }
+    int looks = 0;
+    return !reaches(step, rest_lo, rest_hi, 0, n, static_cast<long long>(a.at - b.at) / 2, a.d, looks);
 }
 
 // Units of rows an SM below which a block shares its rows' sines (few heads share too little),

@@ -446,8 +446,10 @@ typedef struct {
  *
  *  rope     : host struct; its turns on the device.
  *  q, k     : host structs; k may be NULL.  y may be x with the same strides (in place);
- *             otherwise outputs overlap nothing, themselves among it.  Rows of one buffer
- *             side by side, as a fused projection gives them, do not count as overlapping.
+ *             otherwise outputs overlap nothing, themselves among it.  What counts is the elements, not
+ *             the memory between them: query and key rows of one buffer may be turned in place,
+ *             whether its rows hold all heads of q and then those of k, or each head's query, key
+ *             and value, or its batches hold the heads of q and then those of k.
  *  positions: int32 on the device, that of row i of batch b at b * position_stride + i
  *             (position_stride 0: one row of them for the whole batch), or NULL: row i is
  *             at position i.  A row at a negative position stays as it is (padding).
