@@ -539,7 +539,7 @@ PyObject *py_trim(PyObject *, PyObject *const *a, Py_ssize_t n)
             return handed_back();
         const int device = c10::cuda::current_device();
         PoolArgs x;
-        if (!describe_pool(a[0], a[1], a[2], a[3], a[4], a[5], device, x)) {
+        if (!describe_pool(a[0], a[1], a[2], a[3], a[4], a[5], device, x) || x.b.B == 0) {
             PyErr_Clear();
             return handed_back();
         }

@@ -61,12 +61,19 @@ def _check(pool, page_table, seq_lens, other, name, counts):
     return index, B, stride, P
 
 
+def _keep(own, counts):
+    """The pool's counts after an empty batch."""
+    if counts is not None:
+        counts.copy_(own)
+
+
 def fa_cache_plan(pool, page_table, seq_lens, new_lens, page, T, counts=None, plan=None, stream=None):
     """Find room for new_lens[b] more tokens of each sequence of seq_lens[b]: pages from the pool, in the sequences'
     order, into page_table [B, max_pages], and the ``FAPlan`` of T rows.  A sequence that the free pages do not
     reach for is refused, with all behind it that need any.
     counts: where the pool's counts afterwards go (default: the pool's own; with another tensor the pool stays as it
-    was, and another plan may take this one's place).  plan: preallocated outputs.  Returns the plan."""
+    was, and another plan may take this one's place).  plan: preallocated outputs.  A batch without sequences takes
+    nothing: no row has a slot, and the counts are the pool's.  Returns the plan."""
     if stream is None and plan is None and type(pool) is FAPagePool and (quick := _quick()):
         done = quick.plan(pool, page_table, seq_lens, new_lens, page, T, counts)
         if type(done) is tuple:
@@ -85,9 +92,6 @@ def fa_cache_plan(pool, page_table, seq_lens, new_lens, page, T, counts=None, pl
         rows, lens = -(-T // 4) * 4, -(-(B + 1) // 4) * 4
         buf = torch.empty(2 * rows + 2 * lens, dtype=torch.int32, device=ring.device)
         plan = FAPlan(buf[2 * rows:2 * rows + B + 1], buf[2 * rows + lens:2 * rows + lens + B], buf[:T], buf[rows:rows + T])
-        if B == 0:
-            buf.fill_(-1)
-            plan.cu_seqlens.zero_()
     elif type(plan) is FAPlan:
         for t, name, n in zip(plan, FAPlan._fields, (B + 1, B, T, T)):
             _output(t, "plan." + name, (n,), torch.int32, index)
@@ -100,6 +104,11 @@ def fa_cache_plan(pool, page_table, seq_lens, new_lens, page, T, counts=None, pl
                            _int(page, "page"), B, T, _stream(index))
     if st != 0:
         raise FAError(st, "fa_cache_plan")
+    if B == 0:  # the library writes nothing
+        plan.cu_seqlens.zero_()
+        plan.positions.fill_(-1)
+        plan.slots.fill_(-1)
+        _keep(own, counts)
     return plan
 
 
@@ -123,3 +132,5 @@ def fa_cache_trim(pool, page_table, seq_lens, keep_lens, page, counts=None, stre
                            _stream(index))
     if st != 0:
         raise FAError(st, "fa_cache_trim")
+    if B == 0:  # the library writes nothing
+        _keep(own, counts)
