@@ -212,8 +212,8 @@ fa_status_t fa_cache_write(const fa_cache_t *cache, const void *k, const void *v
         k_token_stride = v_token_stride = 0;
     if (cache->heads == 1)
         k_head_stride = v_head_stride = 0;
-    if (!k || !v || !strides_ok(k_token_stride, k_head_stride) || !strides_ok(v_token_stride, v_head_stride) ||
-        (!cu_seqlens && T % B != 0))
+    if (!k || !v || !fine(k_token_stride, T) || !fine(k_head_stride, cache->heads) || !fine(v_token_stride, T) ||
+        !fine(v_head_stride, cache->heads) || (!cu_seqlens && T % B != 0))
         return FA_ERR_INVALID_ARG;
     if ((u(k) | u(v)) & 15u || u(cu_seqlens) & 3u || !strides_aligned(k_token_stride, k_head_stride) ||
         !strides_aligned(v_token_stride, v_head_stride))

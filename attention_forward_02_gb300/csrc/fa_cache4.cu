@@ -218,7 +218,8 @@ fa_status_t fa_cache4_write(const fa_cache4_t *cache, const void *k, const void 
         k_token_stride = v_token_stride = 0;
     if (cache->heads == 1)
         k_head_stride = v_head_stride = 0;
-    if (!k || !v || !slots || !strides_ok(k_token_stride, k_head_stride) || !strides_ok(v_token_stride, v_head_stride))
+    if (!k || !v || !slots || !fine(k_token_stride, T) || !fine(k_head_stride, cache->heads) || !fine(v_token_stride, T) ||
+        !fine(v_head_stride, cache->heads))
         return FA_ERR_INVALID_ARG;
     if ((u(k) | u(v)) & 15u || u(slots) & 3u || !strides_aligned(k_token_stride, k_head_stride) ||
         !strides_aligned(v_token_stride, v_head_stride))
@@ -235,7 +236,7 @@ fa_status_t fa_cache4_write(const fa_cache4_t *cache, const void *k, const void 
     const fa::cache4::Rows4 rows = {
         {k, v}, {k_token_stride, v_token_stride}, {k_head_stride, v_head_stride}, slots, T};
     const int tokens = fa::cache4::kWriteThreads / (cache->d / fa::cache4::kGroup);
-    const dim3 grid((T + tokens - 1) / tokens, cache->heads);
+    const dim3 grid(static_cast<unsigned>((static_cast<long long>(T) + tokens - 1) / tokens), cache->heads);
     return by_type(dtype, [&](auto t) {
         return launch_dependent(fa::cache4::fa_cache4_write_kernel<decltype(t)>, grid, fa::cache4::kWriteThreads, 0,
                                 static_cast<cudaStream_t>(stream), device_cache(cache), rows, cache->d, st->status)

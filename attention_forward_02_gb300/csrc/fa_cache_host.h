@@ -54,9 +54,12 @@ inline bool any_overlap(const Range &a, const Range *others, int count)
     return false;
 }
 
+// A stride: not negative, and what it spans small enough for the sums and byte counts here.
+inline bool fine(long long s, int extent) { return s >= 0 && (extent <= 1 || s <= (1ll << 40) / (extent - 1)); }
+
 inline fa_status_t check_batch(const int *seq_lens, const int *table, long long table_stride, int max_pages, int B, int page)
 {
-    if (!seq_lens || !table || max_pages < 1 || table_stride < max_pages)
+    if (!seq_lens || !table || max_pages < 1 || table_stride < max_pages || !fine(table_stride, B))
         return FA_ERR_INVALID_ARG;
     if (B > kMaxBatch || static_cast<long long>(max_pages) * page > 0x7fffffffLL)
         return FA_ERR_UNSUPPORTED;
@@ -66,7 +69,6 @@ inline fa_status_t check_batch(const int *seq_lens, const int *table, long long 
 }
 
 // Strides of an input with rows of d values, in elements.
-inline bool strides_ok(long long a, long long b, long long c = 0) { return a >= 0 && b >= 0 && c >= 0; }
 inline bool strides_aligned(long long a, long long b, long long c = 0) { return ((a | b | c) & 7) == 0; }
 
 // Checks of the queries of a decoding call or a selection over a cache of `heads` KV heads.
@@ -82,7 +84,7 @@ inline fa_status_t check_queries(int heads, int d, const void *q, long long &sb,
         return FA_ERR_UNSUPPORTED;
     if (Nq < 1 || Nq > kMaxNq)
         return FA_ERR_UNSUPPORTED;
-    if (Hq % heads != 0 || !q || !strides_ok(sb, sh, sr))
+    if (Hq % heads != 0 || !q || !fine(sb, B) || !fine(sh, Hq) || !fine(sr, Nq))
         return FA_ERR_INVALID_ARG;
     if (u(q) & 15u || !strides_aligned(sb, sh, sr))
         return FA_ERR_MISALIGNED;

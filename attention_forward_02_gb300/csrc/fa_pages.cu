@@ -58,7 +58,8 @@ fa_status_t device(PagesState **out)
 fa_status_t check(const int *ring, int num_pages, const long long *counts, const int *table, long long table_stride,
                   int max_pages, const int *lens, const int *other, const long long *out, int page, int B)
 {
-    if (num_pages < 1 || !ring || !counts || !table || !lens || !other || !out || max_pages < 1 || table_stride < max_pages)
+    if (num_pages < 1 || !ring || !counts || !table || !lens || !other || !out || max_pages < 1 || table_stride < max_pages ||
+        !fine(table_stride, B))
         return FA_ERR_INVALID_ARG;
     if ((page != 16 && page != 32 && page != 64 && page != 128) || B > kMaxBatch ||
         static_cast<long long>(num_pages) * page > 0x7fffffffLL || static_cast<long long>(max_pages) * page > 0x7fffffffLL)
@@ -146,9 +147,9 @@ fa_status_t fa_cache_plan(const int *ring, int num_pages, const long long *count
                           cu_seqlens, ends, rows, st->status))
         return FA_ERR_CUDA;
     constexpr int kPerBlock = kRowThreads * kRows;
-    if (T > kOwnRows &&
-        !launch_dependent(fa_cache_rows_kernel, static_cast<unsigned>((T + kPerBlock - 1ll) / kPerBlock), kRowThreads, 0, cs,
-                          in, page_table, table_stride, num_pages, cu_seqlens, ends, rows, st->status))
+    const unsigned blocks = static_cast<unsigned>((static_cast<long long>(T) + kPerBlock - 1) / kPerBlock);
+    if (T > kOwnRows && !launch_dependent(fa_cache_rows_kernel, blocks, kRowThreads, 0, cs, in, page_table, table_stride,
+                                          num_pages, cu_seqlens, ends, rows, st->status))
         return FA_ERR_CUDA;
     return launched();
 }

@@ -129,9 +129,6 @@ bool apart(const View &a, const View &b)
 // 80.0, 30,000 97.2 and 94.0 (half as many units: 41.2, 79.6, 96.9).
 constexpr int kFewUnits = 256, kFewHeads = 16, kUnits = 512, kManyUnits = 4096;
 
-// A stride: not negative, and what it spans small enough for the sums here.
-bool fine(long long s, int extent) { return s >= 0 && (extent <= 1 || s <= (1ll << 40) / (extent - 1)); }
-
 constexpr int kMaxHeads = 65535;
 
 // Checks rows and fills their views; strides of dimensions of one become 0.

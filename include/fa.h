@@ -286,9 +286,10 @@ typedef struct {
  *
  *  cache   : the cache (host struct; its buffers on the device).
  *  k, v    : new rows, element (t, h, c) at t * token_stride + h * head_stride
- *            + c (strides in elements, multiples of 8, not negative; that of a
- *            dimension of one is ignored); 16-byte aligned; must not overlap
- *            the cache.  Read only.
+ *            + c (strides in elements, multiples of 8, not negative, a dimension's
+ *            span at most 2^40 elements, also of page tables; that of a dimension
+ *            of one is ignored); 16-byte aligned; must not overlap the cache.
+ *            Read only.
  *  cu_seqlens : [B + 1] int32 on the device, ascending, 0 .. T, or NULL: T / B
  *            tokens for every sequence (T a multiple of B).  Rows from
  *            cu_seqlens[B] on are ignored.
@@ -429,8 +430,8 @@ typedef struct {
 } fa_rope_t;
 
 /* Rows in and rows out: element (b, h, i, c) of x at b * x_batch + h * x_head + i * x_row + c,
-   of y likewise (strides in elements, multiples of 8, not negative; that of a dimension of one
-   is ignored); both 16-byte aligned. */
+   of y likewise (strides in elements, multiples of 8, not negative, a dimension's span at most
+   2^40 elements; that of a dimension of one is ignored); both 16-byte aligned. */
 typedef struct {
     const void *x;
     void *y;
@@ -453,8 +454,8 @@ typedef struct {
  *  positions: int32 on the device, that of row i of batch b at b * position_stride + i
  *             (position_stride 0: one row of them for the whole batch), or NULL: row i is
  *             at position i.  A row at a negative position stays as it is (padding).
- *  B, N     : batch and rows a head (packed tokens: B = 1, N tokens); 0, like no heads, is an
- *             empty problem.
+ *  B, N     : batch and rows a head (packed tokens: B = 1, N tokens), B * N * d < 2^33; 0, like no
+ *             heads, is an empty problem.
  *  d        : head dimension, 32, 64, 96 or 128.
  *  backward : 0 or 1.
  * Computed in fp32 and rounded once to `dtype`.
