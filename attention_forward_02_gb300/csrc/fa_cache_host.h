@@ -93,7 +93,7 @@ inline fa_status_t check_queries(int heads, int d, const void *q, long long &sb,
 }
 
 // Launch of a kernel that may begin before the one ahead of it has ended (it
-// waits for that one itself).
+// waits for that one itself).  A launch that fails leaves no error for a later call to find.
 template <typename... P, typename... A>
 inline bool launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A &...args)
 {
@@ -107,7 +107,10 @@ inline bool launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess;
+    if (cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess)
+        return true;
+    cudaGetLastError();
+    return false;
 }
 
 inline fa_status_t launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }

@@ -416,8 +416,10 @@ fa_status_t fa1_fwd_noalloc(const void *q, const void *k, const void *v, void *o
 fa_status_t fa_last_device_status(void *stream)
 {
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (cudaStreamSynchronize(cs) != cudaSuccess)
+    if (cudaStreamSynchronize(cs) != cudaSuccess) {
+        cudaGetLastError();  // such as a stream under capture's: not for the next call to find
         return FA_ERR_CUDA;
+    }
     unsigned int word = 0;
     const unsigned int zero = 0;
     if (cudaMemcpyFromSymbol(&word, fa::g_fa_status, sizeof(word)) != cudaSuccess)
