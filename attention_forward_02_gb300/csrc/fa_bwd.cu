@@ -181,15 +181,10 @@ fa_status_t launch(const Maps &mp, const void *o, const float *lse, const void *
 
 namespace fa_host {
 
-fa_status_t take_bwd_status(unsigned int *word)
+unsigned int *bwd_status_word()
 {
-    *word = 0;
-    const unsigned int zero = 0;
-    if (cudaMemcpyFromSymbol(word, fa::g_fa_status, sizeof(*word)) != cudaSuccess)
-        return FA_ERR_CUDA;
-    if (cudaMemcpyToSymbol(fa::g_fa_status, &zero, sizeof(zero)) != cudaSuccess)
-        return FA_ERR_CUDA;
-    return FA_OK;
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, fa::g_fa_status) == cudaSuccess ? static_cast<unsigned int *>(p) : nullptr;
 }
 
 }  // namespace fa_host

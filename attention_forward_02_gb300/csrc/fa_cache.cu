@@ -176,15 +176,10 @@ fa_status_t by_types(fa_dtype_t dtype, int format, F f)
 
 namespace fa_host {
 
-fa_status_t take_cache_status(unsigned int *word)
+unsigned int *cache_status_word()
 {
-    *word = 0;
-    const unsigned int zero = 0;
-    if (cudaMemcpyFromSymbol(word, fa::g_fa_status, sizeof(*word)) != cudaSuccess)
-        return FA_ERR_CUDA;
-    if (cudaMemcpyToSymbol(fa::g_fa_status, &zero, sizeof(zero)) != cudaSuccess)
-        return FA_ERR_CUDA;
-    return FA_OK;
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, fa::g_fa_status) == cudaSuccess ? static_cast<unsigned int *>(p) : nullptr;
 }
 
 }  // namespace fa_host

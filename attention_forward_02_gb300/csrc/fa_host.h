@@ -39,13 +39,13 @@ fa_status_t check_args(const void *q, const void *k, const void *v, const void *
                        int B, int H, int N, int d, float scale, int causal, fa_dtype_t dtype,
                        bool *empty);
 
-// Read and clear the backward / decoding / cache / pages units' device status words
-// (bit 0: a bounded wait expired; bit 2: an index outside its range); 0 when
-// nothing was recorded.
-fa_status_t take_bwd_status(unsigned int *word);
-fa_status_t take_decode_status(unsigned int *word);
-fa_status_t take_cache_status(unsigned int *word);
-fa_status_t take_cache4_status(unsigned int *word);
-fa_status_t take_pages_status(unsigned int *word);
+// Addresses of the backward / decoding / cache / pages units' status words on the
+// current device (bit 0: a bounded wait expired; bit 2: an index outside its range;
+// 0 when nothing was recorded); NULL if there is none to be had.
+unsigned int *bwd_status_word();
+unsigned int *decode_status_word();
+unsigned int *cache_status_word();
+unsigned int *cache4_status_word();
+unsigned int *pages_status_word();
 
 }  // namespace fa_host

@@ -90,15 +90,10 @@ bool separate(const Range *written, int n, const Range *read, int m)
 
 namespace fa_host {
 
-fa_status_t take_pages_status(unsigned int *word)
+unsigned int *pages_status_word()
 {
-    *word = 0;
-    const unsigned int zero = 0;
-    if (cudaMemcpyFromSymbol(word, fa::g_fa_status, sizeof(*word)) != cudaSuccess)
-        return FA_ERR_CUDA;
-    if (cudaMemcpyToSymbol(fa::g_fa_status, &zero, sizeof(zero)) != cudaSuccess)
-        return FA_ERR_CUDA;
-    return FA_OK;
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, fa::g_fa_status) == cudaSuccess ? static_cast<unsigned int *>(p) : nullptr;
 }
 
 }  // namespace fa_host
