@@ -6,12 +6,40 @@
 """
 import math
 from ctypes import byref
+from functools import lru_cache
 from typing import NamedTuple
 
 import torch
 
 from ._lib import FAError, RopeDesc, RopeRows, fa_rope_raw
 from .cache import _CODES, _elsewhere, _int, _quick, _stream, _there
+
+
+@lru_cache(maxsize=8)
+def _per_turn(bits):
+    """2^bits / (2 pi), cut to a whole number."""
+    one = 1 << (bits + 64)
+
+    def arctan(n):  # of 1 / n
+        total, term, k = 0, one // n, 1
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term //= n * n
+            k += 2
+        return total
+
+    pi = 4 * (4 * arctan(5) - arctan(239))  # Machin's formula, 64 bits to spare
+    return one * (1 << bits) // (2 * pi)
+
+
+def _turns(x):
+    """x radians as turns times 2^64, rounded to a whole number, modulo 2^64 in two's complement."""
+    mantissa, exponent = math.frexp(x)  # x = whole * 2^down, whole of 53 bits
+    whole, down = int(math.ldexp(mantissa, 53)), exponent - 53
+    bits = 256 + max(0, exponent + 255) // 256 * 256  # 128 and more behind the last one that counts
+    shift = bits - 64 - down
+    turns = (whole * _per_turn(bits) + (1 << (shift - 1))) >> shift
+    return (turns + 2 ** 63) % 2 ** 64 - 2 ** 63
 
 
 def _scaled(rot, base, scaling, factor, trained, fast, slow):
@@ -44,7 +72,7 @@ def _scaled(rot, base, scaling, factor, trained, fast, slow):
 
 class FARope(NamedTuple):
     """How positions turn heads: turns int64 [pairs], the fraction of a turn that a position turns each pair by,
-    times 2^64 (two's complement); whether neighbouring channels pair, or those half the turned part apart; and
+    times 2^64 and rounded (two's complement); whether neighbouring channels pair, or those half the turned part apart; and
     a factor on the turned channels.  Nothing is kept beside them."""
     turns: torch.Tensor
     interleaved: bool = False
@@ -73,9 +101,7 @@ class FARope(NamedTuple):
             radians = [float(x) for x in radians]
             if len(radians) != rot // 2 or not all(math.isfinite(x) for x in radians):
                 raise FAError(1, "radians must be rot / 2 finite numbers")
-        turns = [int(math.ldexp(math.fmod(x / (2 * math.pi), 1.0), 64)) for x in radians]
-        turns = [(x + 2 ** 63) % 2 ** 64 - 2 ** 63 for x in turns]
-        return cls(torch.tensor(turns, dtype=torch.int64, device=device), bool(interleaved), on_channels)
+        return cls(torch.tensor([_turns(x) for x in radians], dtype=torch.int64, device=device), bool(interleaved), on_channels)
 
 
 def _rows(x, name, index, out, like):
