@@ -417,8 +417,9 @@ FA_API fa_status_t fa_cache_select(const fa_cache_t *cache, const void *q, long 
  * of pair i, a row at position p has its channels (a, b) of the pair replaced by
  *     a' = factor (a cos(p w_i) - b sin(p w_i)),  b' = factor (b cos(p w_i) + a sin(p w_i));
  * the other channels stay.  Angles are held as fractions of a turn in 64-bit fixed point:
- * p times turns[i], taken modulo 2^64, is the turn's fraction at p, so that far positions
- * lose nothing (off by at most p 2^-65 of a turn).  Frequencies scaled for long contexts are
+ * p times turns[i], taken modulo 2^64, is the turn's fraction at p, so that far positions lose
+ * nothing but what rounding turns[i] to a whole number makes of it (|p| 2^-65 of a turn).  That
+ * fraction is then rounded to fp32 (2^-23 of itself), of which sine and cosine are taken.  Frequencies scaled for long contexts are
  * other `turns`; the pages have no counterpart.
  */
 typedef struct {
