@@ -58,6 +58,40 @@ constexpr long long kWholeUnits = 8;
 // keys 8.1 where a warp each takes 11.4.
 constexpr long long kShortUnits = 2;
 
+// More than 16 rows (d = 128; 32 at d = 96): the tcgen05 kernel has one block an SM, to which a
+// segment's begin and end cost about five units of 128 keys, so that batches of short segments are
+// faster with the other one, two blocks an SM of which each takes a segment whole.  tcgen05 / the other, us
+// on the GPU (in a graph), contexts of up to
+//                                      1 unit       2            3            4            5            6            8
+//   d = 128, 24 rows,   64 segments    8.2 / 8.5    9.5 / 9.9                 11.3 / 13.0                            15.6 / 19.7
+//                      160             16.0 / 9.6   16.1 / 11.7  18.3 / 14.1  19.6 / 15.8  20.1 / 18.0  20.8 / 21.4  23.6 / 25.3
+//                      304             17.5 / 10.3  22.0 / 12.3  25.1 / 14.8  26.4 / 17.2  26.1 / 19.3  28.2 / 21.9  31.1 / 27.0
+//                     1024             46.9 / 40.7  53.7 / 48.2  58.5 / 49.7  62.5 / 58.6  65.4 / 63.5  68.6 / 69.0  76.5 / 78.8
+//                     2048             88.1 / 69.2  98.3 / 83.5  104 / 90.8   111 / 101    117 / 110    127 / 120    142 / 141
+//            64 rows,   64             10.1 / 12.3  11.7 / 15.0               14.6 / 21.3                            20.9 / 34.2
+//                      160             22.7 / 14.1  22.7 / 18.2  25.6 / 22.6  26.7 / 27.1  27.6 / 30.5  29.5 / 37.5  33.0 / 45.4
+//                      304             25.5 / 15.6  32.0 / 19.5  37.0 / 24.7  37.7 / 28.2  38.1 / 33.5  41.2 / 38.4  44.9 / 47.4
+//                     1024             73.4 / 73.2  82.8 / 88.5  89.4 / 90.8  95.1 / 104   99.8 / 117
+//                     2048             145 / 132    158 / 159    166 / 172    177 / 190    187 / 209
+//   d = 96,  64 rows,   64             10.1 / 10.0  12.0 / 13.0               14.0 / 18.5                            20.1 / 30.2
+//            36 rows,   64             9.9 / 8.7    11.3 / 11.9               14.1 / 17.4                            19.5 / 29.1
+//                      160             20.6 / 10.1  20.8 / 13.8  23.0 / 17.5  25.0 / 21.4  25.0 / 24.3  26.6 / 30.2  29.9 / 37.0
+//                      304             22.7 / 10.8  28.8 / 15.0  33.4 / 18.5  34.6 / 22.3  34.6 / 26.1  37.2 / 31.2  40.4 / 39.1
+//                     2048             120 / 84.9   133 / 104    141 / 120    151 / 137    160 / 148    171 / 172    189 / 200
+// At d = 96 it is also behind where few units are shared out: 8 segments of 10, 16, 32, 64 units
+// 19.5 / 17.4, 20.0 / 17.9, 20.8 / 18.7, 21.5 / 22.6, 16 of 16 and 24 units 20.2 / 18.6, 20.6 / 21.9 (at d = 128 8 of 16
+// units, 17 rows 16.5 / 15.4, 32 rows 17.1 / 16.4, 64 rows 21.3 / 23.7).
+template <int D>
+bool on_tcgen05(int rows, long long segments, long long units, int sms)
+{
+    const bool more = segments > sms;
+    if (D == 96)
+        return rows > 32 && units > (more ? 5 : 1) && (units <= kWholeUnits || segments * units > 256);
+    if (rows <= 32)
+        return rows > 16 && units > (more ? 8 : 0);
+    return units > (!more ? 0 : segments <= 2 * sms ? 4 : 2);
+}
+
 template <int D, int ROWS, typename T>
 constexpr auto decode_kernel()
 {
@@ -402,11 +436,12 @@ fa_status_t fa_decode_cache4(const fa_cache4_t *cache, const void *q, long long 
                                             static_cast<T *>(o), lse);
                 });
             };
-            if (w.R > 32)  // both sides' figures are at the kernel
+            if (on_tcgen05<D>(w.R, segments, bound, sms)) {
+                if constexpr (D == 128)
+                    if (w.R <= 32)
+                        return on_tensor_cores(Dim<32>());
                 return on_tensor_cores(Dim<64>());
-            if constexpr (D == 128)
-                if (w.R > 16)
-                    return on_tensor_cores(Dim<32>());
+            }
         }
         return w.R <= 4 ? with_rows(Dim<4>()) : w.R <= 8 ? with_rows(Dim<8>()) : with_rows(Dim<16>());
     });

@@ -1,0 +1,75 @@
+"""Attention over the 4-bit cache for more than 16 rows a KV head: either kernel over batches of short and of longer
+segments, on both sides of where one takes over from the other."""
+import random
+
+import pytest
+import torch
+
+import attention_forward_02_gb300 as fa
+from cache4_util import DTYPES, Ref, attend_bounds, pages_for, within
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def attend(B, H, G, Nq, d, page, top, dtype, causal, width=0):
+    rng = random.Random(B * top + G)
+    lens = [top] + [rng.choice([0, 1, page, rng.randint(1, top), top]) for _ in range(B - 1)]
+    table, pool = pages_for(lens, page, B)
+    want = -(-top // page)
+    table = torch.nn.functional.pad(table[:, :want], (0, width), value=-7).contiguous()
+    ref = Ref(pool, H, page, d, seed=top)
+    q = torch.randn(B, H * G, Nq, d, generator=torch.Generator().manual_seed(G)).to(DTYPES[dtype])
+    o, lse = fa.fa_decode_cache4(q.to(DEV), ref.to(DEV), table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV),
+                                 causal=causal)
+    within(o, lse, attend_bounds(ref, q, table, lens, d ** -0.5, causal))
+
+
+@pytest.mark.parametrize("d,G,Nq", [(128, 17, 1), (128, 8, 4), (128, 11, 3), (128, 16, 4), (128, 20, 5), (96, 17, 2), (96, 16, 4),
+                                    (96, 13, 8)])
+@pytest.mark.parametrize("B,H,top,page", [
+    (20, 8, 128, 16), (20, 8, 600, 128), (40, 8, 250, 64), (3, 4, 100, 32), (1, 8, 1300, 16), (39, 4, 1150, 64),
+    (160, 1, 640, 32), (200, 2, 300, 128),
+])
+def test_short_segments(d, G, Nq, B, H, top, page):
+    dtype = ["fp16", "bf16"][(G + B) % 2]
+    attend(B, H, G, Nq, d, page, top, dtype, causal=bool(Nq > 1))
+
+
+@pytest.mark.parametrize("d,G", [(128, 32), (128, 64), (96, 40)])
+@pytest.mark.parametrize("page,width", [(16, 300), (128, 1)])
+def test_the_same_with_a_wide_table(d, G, page, width):
+    attend(20, 8, G, 1, d, page, 250, "bf16", False, width)
+
+
+def test_nobody_waits_for_a_slow_kernel():
+    """304 segments of one unit: with a table of one unit's width (18 us once, 11 now) well under a wide table's (18)."""
+    B, H, G, d, page = 38, 8, 32, 128, 64
+    ref = Ref(2, H, page, d)
+    cache, q = ref.to(DEV), torch.randn(B, H * G, 1, d, device=DEV).to(torch.bfloat16)
+    lens = torch.full((B,), 128, dtype=torch.int32, device=DEV)
+    wide = torch.zeros((B, 2000), dtype=torch.int32, device=DEV)
+    wide[:, 1] = 1
+    graphs = []
+    for table in (wide[:, :2], wide):
+        for _ in range(2):
+            fa.fa_decode_cache4(q, cache, table, lens)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(20):
+                fa.fa_decode_cache4(q, cache, table, lens)
+        graphs.append(graph)
+    for _ in range(5):
+        best = [float("inf")] * 2
+        for _ in range(10):
+            for i, graph in enumerate(graphs):
+                begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+                begin.record()
+                graph.replay()
+                end.record()
+                torch.cuda.synchronize()
+                best[i] = min(best[i], begin.elapsed_time(end))
+        if best[0] < 0.8 * best[1]:
+            return
+    pytest.fail("%.1f us with a narrow table, %.1f with a wide one" % (best[0] * 50, best[1] * 50))
