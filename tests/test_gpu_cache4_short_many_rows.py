@@ -42,6 +42,18 @@ def test_the_same_with_a_wide_table(d, G, page, width):
     attend(20, 8, G, 1, d, page, 250, "bf16", False, width)
 
 
+@pytest.mark.parametrize("d,G,Nq", [(128, 17, 1), (128, 16, 4), (96, 13, 3)])
+@pytest.mark.parametrize("page,top", [(16, 250), (128, 600)])
+def test_checked_build(monkeypatch, d, G, Nq, page, top):
+    """With the device-side address checks."""
+    from attention_forward_02_gb300 import _lib
+    checked, stream = _lib.load_checked(), torch.cuda.current_stream().cuda_stream
+    monkeypatch.setattr(_lib, "_lib", checked)
+    checked.fa_last_device_status(stream)
+    attend(20, 8, G, Nq, d, page, top, "bf16", True)
+    assert checked.fa_last_device_status(stream) == 0
+
+
 def test_nobody_waits_for_a_slow_kernel():
     """304 segments of one unit: with a table of one unit's width (18 us once, 11 now) well under a wide table's (18)."""
     B, H, G, d, page = 38, 8, 32, 128, 64

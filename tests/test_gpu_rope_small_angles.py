@@ -1,11 +1,12 @@
-"""Angles near zero keep their bits: slow pairs near position 0, whose sine is all that the second channel gets."""
+"""Angles near zero keep their bits: slow pairs near position 0, whose sine is all that the second channel gets.  And any
+angle against 64-bit ones."""
 import math
 
 import pytest
 import torch
 
 import attention_forward_02_gb300 as fa
-from rope_util import DTYPES
+from rope_util import DTYPES, bound, turn
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -38,3 +39,27 @@ def test_slow_pairs(dtype, rows, heads, interleaved):
     bound = fi.eps / 2 * (want.abs() + off) + off + fi.tiny * fi.eps / 2
     for h in {0, heads - 1}:
         assert ((got[:, h] - want).abs() - bound).max() <= 0
+
+
+@pytest.fixture
+def wide():
+    """rope_util.turn makes its angles in torch's default type."""
+    torch.set_default_dtype(torch.float64)
+    yield
+    torch.set_default_dtype(torch.float32)
+
+
+@pytest.mark.parametrize("d,rot,interleaved", [(128, 128, False), (64, 64, True), (96, 48, False), (32, 8, True)])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("T,heads", [(40, 3), (40, 40)])
+def test_against_angles_in_64_bits(wide, d, rot, interleaved, dtype, T, heads):
+    """rope_util.bound holds for an angle rounded twice, by 2^-24 of a half turn: with c and s its cosine and sine an output
+    a c - b s is off by |a| (1.9e-7 |s| + 3.0e-7 |c|) + |b| (1.9e-7 |c| + 3.0e-7 |s|) at most (the angle; 2 ulp of sincospif,
+    the factor and two roundings of a product and the sum), which is below 3.6e-7 < 2^-21 of |a| + |b|."""
+    rope = fa.FARope.new(rot, base=500000.0, interleaved=interleaved, scaling="yarn", factor=4.0, trained=8192)
+    x = torch.randn(T, heads, d, generator=torch.Generator().manual_seed(d)).to(DTYPES[dtype])
+    pos = torch.tensor([(0, 1, 2, 3, 131071, 2 ** 31 - 1, 4095, 12345)[t % 8] + t // 8 * (t % 8 < 4) for t in range(T)])
+    got, _ = fa.fa_rope(x.to(DEV), None, rope, pos.int().to(DEV))
+    y, mag = turn(x.transpose(0, 1)[None], [int(t) for t in rope.turns.cpu()], interleaved, rope.factor, pos[None])
+    over = (got.cpu().double().transpose(0, 1)[None] - y).abs() - bound(y, mag, DTYPES[dtype])
+    assert over.max() <= 0
