@@ -126,7 +126,9 @@ def fa_decode_cache4(q, cache, page_table, seq_lens, o=None, lse=None, scale=Non
     """Decoding attention of q [B, Hq, Nq, d] (1 <= Nq <= 16, Hq a multiple of the cache's heads, any strides that
     keep rows contiguous) to the cache; seq_lens counts the queries' own tokens.  causal puts the queries at the
     end of the sequence.  scale defaults to 1/sqrt(d).  Returns (o, lse); a row without keys has o = 0,
-    lse = -inf."""
+    lse = -inf.
+    The lengths are on the device: how the work is shared out follows the page table's width.  Where the longest
+    sequence is known to be short, its first columns are faster: page_table[:, :pages of the longest]."""
     if stream is None and type(cache) is FACache4 and (quick := _quick()):
         done = quick.decode4(q, cache, page_table, seq_lens, o, lse, scale if scale is None else float(scale),
                              True if causal else False, True if return_lse else False, workspace)

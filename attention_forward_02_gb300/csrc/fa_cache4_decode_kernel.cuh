@@ -4,8 +4,9 @@
 // Built as the one over the 8-bit cache (fa_cache_decode_kernel.cuh): units of a stage's
 // keys dealt out in equal runs to a persistent grid, one warp that copies, four that
 // compute with mma.m16n8k16 on fp16, keys as rows and query rows as columns, parts
-// merged by fa_cache_combine_kernel.  (Many short segments: fa_cache4_short_kernel.cuh; more
-// than 16 rows a head, or 32: fa_cache4_tc_kernel.cuh.)  What differs:
+// merged by fa_cache_combine_kernel.  (Many short segments of up to 8 rows:
+// fa_cache4_short_kernel.cuh; more than 16 rows a head, or 32, unless many and short:
+// fa_cache4_tc_kernel.cuh.)  What differs:
 //  - A page and head is one block of bytes, so that a copy is one bulk copy (four where a
 //    page is larger than a stage).  It is not swizzled: of a tile's 16 rows, row r stands for
 //    the key r ^ (r >> 2 & 1), and then the reads of K are free of bank conflicts and those

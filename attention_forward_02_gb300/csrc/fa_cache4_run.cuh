@@ -136,7 +136,7 @@ __device__ __forceinline__ void load_run(const Work &w, const Run &r, uint32_t s
         left += min(unit, 0);  // what is left of the segment's begin
         unit = max(unit, 0);
     }
-    const int log2_boxes = F::LOG2_STEP - w.log2_box;  // boxes of a stage: 1 to 8
+    const int log2_boxes = F::LOG2_STEP - w.log2_box;  // boxes of a stage: 1 to 16
     const int batch_units = 32 >> log2_boxes;
     const size_t page_bytes = static_cast<size_t>(w.cache.page) * (D / 8 * 9);
     const uint64_t policy = l2_policy_evict_first();

@@ -1,5 +1,6 @@
 // fa_cache4_tc_kernel.cuh -- decoding attention over the 4-bit paged cache for more than 32 query
-// rows a KV head, at d = 128 more than 16, with the products on tcgen05.
+// rows a KV head, at d = 128 more than 16, with the products on tcgen05 (but batches of short
+// segments: on_tcgen05 in fa_cache4.cu, with both sides' figures).
 //
 // The kernel of fa_cache4_decode_kernel.cuh converts a tile's codes in registers, once for every
 // 16 rows.  Here they are converted once for the 32 or 64 rows of a group, into fp16 tiles of K and V

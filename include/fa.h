@@ -585,7 +585,9 @@ FA_API size_t fa_decode_cache4_workspace_size(int B, int Hq, int Hkv, int Nq, in
 
 /*
  * fa_decode_cache4 -- decoding attention over the 4-bit cache (asynchronous): arguments,
- * results, masks and reports as for fa_decode_cache over all pages.  Bytes above 0xE2 are no
+ * results, masks and reports as for fa_decode_cache over all pages.  How the work is shared out
+ * follows max_pages, as the lengths are on the device: short contexts are faster with a max_pages
+ * that is no more than the longest one's (table_stride may be larger).  Bytes above 0xE2 are no
  * scales: what the rows of a KV head get of a key with such a byte that any of them sees is not
  * said.  (Behind the last key they mean nothing.)
  */
