@@ -6,8 +6,8 @@ import pytest
 
 import attention_forward_02_gb300 as fa
 
-# 3 and 400 decimals, summed here by Euler's series for arctan, apart from the formula that the package uses:
-# arctan(1 / n) = sum over k of 2^2k (k!)^2 / (2k + 1)! n / (n^2 + 1)^(k + 1) times n^0, pi = 20 arctan(1 / 7) + 8 arctan(3 / 79)
+# 400 decimals of pi by Euler's series, apart from the formula that the package uses: with y = x^2 / (1 + x^2)
+# arctan x = y / x (1 + 2/3 y + 2 4 / (3 5) y^2 + ...), and pi = 20 arctan(1 / 7) + 8 arctan(3 / 79)
 
 
 def euler(x, places):
